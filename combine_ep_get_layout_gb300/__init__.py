@@ -30,7 +30,9 @@ __all__ = ["EPError", "Layout", "Dispatched", "ep_layout_workspace_bytes",
            "ep_get_layout_and_dispatch",
            "ep_combine", "ep_combine_ex", "ep_fp8_packed_row_bytes", "ExpandedLayout",
            "ep_expanded_layout_workspace_bytes", "ep_get_layout_expanded",
-           "ep_dispatch_expanded", "ep_combine_expanded", "ep_selftest_bounded_waits",
+           "ep_dispatch_expanded", "ep_combine_expanded", "Routing", "ep_route",
+           "ep_route_backward", "ep_expert_product", "ep_expert_product_backward",
+           "ep_adapter_workspace_bytes", "ep_adapter_product", "ep_selftest_bounded_waits",
            "library_path"]
 
 
@@ -506,6 +508,247 @@ def ep_combine_expanded(y: torch.Tensor, layout: ExpandedLayout,
         None if bias0 is None else bias0.data_ptr(), None if bias1 is None else bias1.data_ptr(),
         out.data_ptr())
     _call(dev, "ep_combine_expanded", C.byref(args), _stream(stream, dev))
+    return out
+
+
+# ---------------------------------------- router, experts' products, adapters
+
+@dataclass
+class Routing:
+    """A batch's experts and weights, as the layouts and dispatches take them."""
+    topk_idx: torch.Tensor      # int64 [T, K], -1 = no selection
+    topk_weights: torch.Tensor  # fp32 [T, K]
+
+
+_SCORES = {"softmax": N.EP_SCORE_SOFTMAX, "sigmoid": N.EP_SCORE_SIGMOID}
+_LOGITS = {torch.float32: N.EP_LOGITS_FP32, torch.bfloat16: N.EP_LOGITS_BF16}
+_ACTIVATIONS = {None: N.EP_ACT_NONE, "swiglu": N.EP_ACT_SWIGLU}
+
+
+def _want_shape(t: torch.Tensor, name: str, shape: tuple):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _want_logits(logits: torch.Tensor, device=None) -> int:
+    """Checks the logits (rows may be apart, a row's entries may not) and
+    returns the row stride."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in _LOGITS:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [num_tokens, num_experts]")
+    T, E = logits.shape
+    _want(logits[:1].reshape(-1) if E == 1 or logits.stride(1) == 1 else logits, "logits", logits.dtype, device)
+    return logits.stride(0) if T > 1 else max(E, 1)
+
+
+def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
+             bias: Optional[torch.Tensor] = None, num_groups: int = 1, topk_groups: int = 1,
+             group_top: int = 1, renormalize: bool = True, weight_scale: float = 1.0,
+             out: Optional[Routing] = None, stream=None) -> Routing:
+    """Each token's experts and weights from the gate's logits (fp32 or bf16
+    [T, E]; rows may be a slice of wider ones).
+
+    ``score`` is "softmax" or "sigmoid".  ``bias`` (fp32 [E]) is added to the
+    scores for the choice only.  With ``num_groups`` > 1 only the experts of
+    the ``topk_groups`` best groups are offered, a group's score being the sum
+    of its ``group_top`` (1 or 2) largest keys.  ``renormalize`` divides a
+    token's weights by their sum; ``weight_scale`` multiplies them.  Experts
+    with a logit of -infinity or NaN are never chosen; missing choices are -1
+    with weight 0.  Ties go to the lowest index.
+    """
+    stride = _want_logits(logits)
+    dev = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        _want(bias, "bias", torch.float32, dev)
+        _want_shape(bias, "bias", (E,))
+    if out is None:
+        out = Routing(torch.empty((T, num_topk), dtype=torch.int64, device=dev),
+                      torch.empty((T, num_topk), dtype=torch.float32, device=dev))
+    else:
+        _want(out.topk_idx, "topk_idx", torch.int64, dev)
+        _want(out.topk_weights, "topk_weights", torch.float32, dev)
+        _want_shape(out.topk_idx, "topk_idx", (T, num_topk))
+        _want_shape(out.topk_weights, "topk_weights", (T, num_topk))
+    args = N.ep_route_args_t(
+        logits.data_ptr(), _LOGITS[logits.dtype], stride, T, E, num_topk, _SCORES[score],
+        None if bias is None else bias.data_ptr(), num_groups, topk_groups, group_top,
+        1 if renormalize else 0, weight_scale, out.topk_idx.data_ptr(), out.topk_weights.data_ptr())
+    _call(dev, "ep_route", C.byref(args), _stream(stream, dev))
+    return out
+
+
+def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
+                      score: str = "softmax", renormalize: bool = True, weight_scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of ``ep_route``'s weights for the logits ([T, E], the
+    logits' dtype), given the weights' gradient (fp32 [T, K]) and the choice.
+    The choice itself, and so the bias, has no gradient."""
+    stride = _want_logits(logits)
+    dev = logits.device
+    T, E = logits.shape
+    _want(topk_idx, "topk_idx", torch.int64, dev)
+    _want(grad_weights, "grad_weights", torch.float32, dev)
+    K = topk_idx.shape[-1]
+    _want_shape(topk_idx, "topk_idx", (T, K))
+    _want_shape(grad_weights, "grad_weights", (T, K))
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        _want(out, "out", logits.dtype, dev)
+        _want_shape(out, "out", (T, E))
+    args = N.ep_route_backward_args_t(
+        grad_weights.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], stride,
+        topk_idx.data_ptr(), T, E, K, _SCORES[score], 1 if renormalize else 0, weight_scale,
+        out.data_ptr())
+    _call(dev, "ep_route_backward", C.byref(args), _stream(stream, dev))
+    return out
+
+
+def _product_sizes(x, w, layout, activation):
+    """Checks rows and weights; (capacity, hidden, width, wide)."""
+    _want(x, "x", torch.bfloat16)
+    _want(w, "w", torch.bfloat16, x.device)
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [recv_capacity, hidden] and w [num_experts, outputs, hidden]")
+    cap, H = x.shape
+    wide = w.shape[1]
+    _want_shape(w, "w", (layout.num_experts, wide, H))
+    if activation == "swiglu" and wide % 2:
+        raise ValueError("w must have an even number of outputs with swiglu")
+    return cap, H, wide // 2 if activation == "swiglu" else wide, wide
+
+
+def ep_expert_product(x: torch.Tensor, w: torch.Tensor, layout: ExpandedLayout,
+                      activation: Optional[str] = None, out: Optional[torch.Tensor] = None,
+                      preact: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Each expert's rows times its weights.
+
+    ``x`` bf16 [cap, H] are rows grouped by expert (``ep_dispatch_expanded``
+    with dtype "bf16"), ``w`` bf16 [E, N, H].  Returns bf16 [cap, N], or with
+    ``activation="swiglu"`` [cap, N/2]: silu of the first half of the outputs
+    times the second.  ``preact`` (bf16 [cap, N]) receives the outputs before
+    the activation, which the backward pass needs.  Padding rows and rows past
+    the last are not written.  Sums are fp32.
+    """
+    act = _ACTIVATIONS[activation]
+    cap, H, width, wide = _product_sizes(x, w, layout, activation)
+    dev = x.device
+    if out is None:
+        out = torch.empty((cap, width), dtype=torch.bfloat16, device=dev)
+    else:
+        _want(out, "out", torch.bfloat16, dev)
+        _want_shape(out, "out", (cap, width))
+    if preact is not None:
+        _want(preact, "preact", torch.bfloat16, dev)
+        _want_shape(preact, "preact", (cap, wide))
+    st = layout.c_struct()
+    args = N.ep_expert_product_args_t(
+        x.data_ptr(), cap, layout.num_tokens, H, layout.num_experts, C.pointer(st), w.data_ptr(),
+        width, act, out.data_ptr(), None if preact is None else preact.data_ptr())
+    _call(dev, "ep_expert_product", C.byref(args), _stream(stream, dev))
+    return out
+
+
+def ep_expert_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                               layout: ExpandedLayout, activation: Optional[str] = None,
+                               preact: Optional[torch.Tensor] = None,
+                               grad_x: Optional[torch.Tensor] = None,
+                               grad_w: Optional[torch.Tensor] = None, need_x: bool = True,
+                               need_w: bool = True, grad_preact: Optional[torch.Tensor] = None,
+                               stream=None):
+    """(grad_x, grad_w) of ``ep_expert_product`` for the output's gradient
+    ``grad`` (bf16 [cap, width]); either is None when not needed.  With swiglu
+    ``preact`` is what the forward pass kept, and ``grad_preact`` (bf16 like
+    it, allocated when not given) receives its gradient.  Rows of ``grad_x``
+    outside the layout's are not written; ``grad_w`` of an expert without rows
+    is zero."""
+    act = _ACTIVATIONS[activation]
+    cap, H, width, wide = _product_sizes(x, w, layout, activation)
+    dev = x.device
+    _want(grad, "grad", torch.bfloat16, dev)
+    _want_shape(grad, "grad", (cap, width))
+    if act == N.EP_ACT_SWIGLU:
+        if preact is None:
+            raise ValueError("swiglu needs preact")
+        if grad_preact is None:
+            grad_preact = torch.empty((cap, wide), dtype=torch.bfloat16, device=dev)
+        for name, t in (("preact", preact), ("grad_preact", grad_preact)):
+            _want(t, name, torch.bfloat16, dev)
+            _want_shape(t, name, (cap, wide))
+    if not need_x:
+        grad_x = None
+    elif grad_x is None:
+        grad_x = torch.empty((cap, H), dtype=torch.bfloat16, device=dev)
+    if not need_w:
+        grad_w = None
+    elif grad_w is None:
+        grad_w = torch.empty(w.shape, dtype=torch.bfloat16, device=dev)
+    for name, t, shape in (("grad_x", grad_x, (cap, H)), ("grad_w", grad_w, tuple(w.shape))):
+        if t is not None:
+            _want(t, name, torch.bfloat16, dev)
+            _want_shape(t, name, shape)
+    st = layout.c_struct()
+    args = N.ep_expert_product_backward_args_t(
+        grad.data_ptr(), x.data_ptr(), w.data_ptr(), cap, layout.num_tokens, H, layout.num_experts,
+        C.pointer(st), width, act, None if preact is None else preact.data_ptr(),
+        None if grad_preact is None else grad_preact.data_ptr(),
+        None if grad_x is None else grad_x.data_ptr(), None if grad_w is None else grad_w.data_ptr())
+    _call(dev, "ep_expert_product_backward", C.byref(args), _stream(stream, dev))
+    return grad_x, grad_w
+
+
+def ep_adapter_workspace_bytes(num_rows: int, hidden: int, rank: int) -> int:
+    return int(N.load().ep_adapter_workspace_bytes(num_rows, hidden, rank))
+
+
+def ep_adapter_product(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                       adapter_idx: torch.Tensor, adapter_scale: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       error_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x w^T plus, for each row, its own adapter's low-rank term
+    ``scale[a] * (x A_a^T) B_a^T`` with a = ``adapter_idx`` (int64 [T], -1 =
+    none).  ``x`` bf16 [T, H], ``w`` bf16 [N, H], ``lora_a`` bf16 [A, r, H],
+    ``lora_b`` bf16 [A, N, r], ``adapter_scale`` fp32 [A] (1 when not given).
+    An index outside [-1, A) counts as -1 and sets EP_ERRBIT_BAD_INDEX in
+    ``error_word`` (int32 [1], if given).  Returns bf16 [T, N]."""
+    _want(x, "x", torch.bfloat16)
+    dev = x.device
+    for name, t in (("w", w), ("lora_a", lora_a), ("lora_b", lora_b)):
+        _want(t, name, torch.bfloat16, dev)
+    _want(adapter_idx, "adapter_idx", torch.int64, dev)
+    if x.dim() != 2 or w.dim() != 2 or lora_a.dim() != 3:
+        raise ValueError("x must be [rows, hidden], w [outputs, hidden], lora_a [adapters, rank, hidden]")
+    T, H = x.shape
+    width = w.shape[0]
+    A, r = lora_a.shape[:2]
+    _want_shape(w, "w", (width, H))
+    _want_shape(lora_a, "lora_a", (A, r, H))
+    _want_shape(lora_b, "lora_b", (A, width, r))
+    _want_shape(adapter_idx, "adapter_idx", (T,))
+    if adapter_scale is not None:
+        _want(adapter_scale, "adapter_scale", torch.float32, dev)
+        _want_shape(adapter_scale, "adapter_scale", (A,))
+    if error_word is not None:
+        _want(error_word, "error_word", torch.int32, dev)
+    if out is None:
+        out = torch.empty((T, width), dtype=torch.bfloat16, device=dev)
+    else:
+        _want(out, "out", torch.bfloat16, dev)
+        _want_shape(out, "out", (T, width))
+    if workspace is None:
+        workspace = torch.empty(max(ep_adapter_workspace_bytes(T, H, r), 16), dtype=torch.uint8, device=dev)
+    else:
+        _want(workspace, "workspace", torch.uint8, dev)
+    args = N.ep_adapter_product_args_t(
+        x.data_ptr(), T, H, w.data_ptr(), width, lora_a.data_ptr(), lora_b.data_ptr(), A, r,
+        adapter_idx.data_ptr(), None if adapter_scale is None else adapter_scale.data_ptr(),
+        out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        None if error_word is None else error_word.data_ptr())
+    _call(dev, "ep_adapter_product", C.byref(args), _stream(stream, dev))
     return out
 
 

@@ -35,6 +35,14 @@ EP_FP8_GROUP = 128
 EP_NOALLOC_SCRATCH_BYTES = 256 * 1024
 EP_WORK_COUNTER_WORDS = 4
 
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_LOGITS_FP32 = 0
+EP_LOGITS_BF16 = 1
+EP_ACT_NONE = 0
+EP_ACT_SWIGLU = 1
+EP_MAX_RANK = 128
+
 ABI_VERSION = 2  # EP_ABI_VERSION of the header these bindings mirror
 
 
@@ -105,6 +113,54 @@ class ep_combine_expanded_args_t(C.Structure):
     ]
 
 
+class ep_route_args_t(C.Structure):
+    _fields_ = [
+        ("logits", C.c_void_p), ("logits_type", C.c_int), ("row_stride", C.c_int64),
+        ("num_tokens", C.c_int), ("num_experts", C.c_int), ("num_topk", C.c_int),
+        ("score", C.c_int), ("bias", C.c_void_p), ("num_groups", C.c_int),
+        ("topk_groups", C.c_int), ("group_top", C.c_int), ("renormalize", C.c_int),
+        ("weight_scale", C.c_float), ("topk_idx", C.c_void_p), ("topk_weights", C.c_void_p),
+    ]
+
+
+class ep_route_backward_args_t(C.Structure):
+    _fields_ = [
+        ("grad_weights", C.c_void_p), ("logits", C.c_void_p), ("logits_type", C.c_int),
+        ("row_stride", C.c_int64), ("topk_idx", C.c_void_p), ("num_tokens", C.c_int),
+        ("num_experts", C.c_int), ("num_topk", C.c_int), ("score", C.c_int),
+        ("renormalize", C.c_int), ("weight_scale", C.c_float), ("grad_logits", C.c_void_p),
+    ]
+
+
+class ep_expert_product_args_t(C.Structure):
+    _fields_ = [
+        ("x", C.c_void_p), ("recv_capacity", C.c_int), ("num_tokens", C.c_int),
+        ("hidden", C.c_int), ("num_experts", C.c_int),
+        ("layout", C.POINTER(ep_expanded_layout_t)), ("w", C.c_void_p), ("width", C.c_int),
+        ("activation", C.c_int), ("out", C.c_void_p), ("preact", C.c_void_p),
+    ]
+
+
+class ep_expert_product_backward_args_t(C.Structure):
+    _fields_ = [
+        ("grad", C.c_void_p), ("x", C.c_void_p), ("w", C.c_void_p), ("recv_capacity", C.c_int),
+        ("num_tokens", C.c_int), ("hidden", C.c_int), ("num_experts", C.c_int),
+        ("layout", C.POINTER(ep_expanded_layout_t)), ("width", C.c_int), ("activation", C.c_int),
+        ("preact", C.c_void_p), ("grad_preact", C.c_void_p), ("grad_x", C.c_void_p),
+        ("grad_w", C.c_void_p),
+    ]
+
+
+class ep_adapter_product_args_t(C.Structure):
+    _fields_ = [
+        ("x", C.c_void_p), ("num_rows", C.c_int), ("hidden", C.c_int), ("w", C.c_void_p),
+        ("width", C.c_int), ("lora_a", C.c_void_p), ("lora_b", C.c_void_p),
+        ("num_adapters", C.c_int), ("rank", C.c_int), ("adapter_idx", C.c_void_p),
+        ("adapter_scale", C.c_void_p), ("out", C.c_void_p), ("workspace", C.c_void_p),
+        ("workspace_bytes", C.c_size_t), ("error_word", C.c_void_p),
+    ]
+
+
 # name -> (restype, argtypes); mirrors include/ep_gb300.h
 _p, _i, _sz = C.c_void_p, C.c_int, C.c_size_t
 _LP = C.POINTER(ep_layout_t)
@@ -122,6 +178,12 @@ SIGNATURES = {
     "ep_get_layout_expanded": (_i, [_p, _i, _i, _i, _i, C.POINTER(ep_expanded_layout_t), _p, _sz, _p]),
     "ep_dispatch_expanded": (_i, [C.POINTER(ep_dispatch_expanded_args_t), _p]),
     "ep_combine_expanded": (_i, [C.POINTER(ep_combine_expanded_args_t), _p]),
+    "ep_route": (_i, [C.POINTER(ep_route_args_t), _p]),
+    "ep_route_backward": (_i, [C.POINTER(ep_route_backward_args_t), _p]),
+    "ep_expert_product": (_i, [C.POINTER(ep_expert_product_args_t), _p]),
+    "ep_expert_product_backward": (_i, [C.POINTER(ep_expert_product_backward_args_t), _p]),
+    "ep_adapter_workspace_bytes": (_sz, [_i, _i, _i]),
+    "ep_adapter_product": (_i, [C.POINTER(ep_adapter_product_args_t), _p]),
     "ep_selftest_bounded_waits": (_i, [_p, _p, _p, _p]),
     "ep_status_str": (C.c_char_p, [_i]),
     "ep_last_error": (C.c_char_p, []),

@@ -491,6 +491,210 @@ typedef struct {
 } ep_combine_expanded_args_t;
 ep_status_t ep_combine_expanded(const ep_combine_expanded_args_t *args, ep_stream_t stream);
 
+/* ------------------------------------------------------------------ */
+/* Operators around the path: router, experts' products, adapters      */
+/* ------------------------------------------------------------------ */
+
+/*
+ * What lies before the dispatch and between it and the combine in a
+ * mixture-of-experts layer.  The conventions at the top hold: device
+ * pointers, nothing allocated or synchronised, host-detectable problems
+ * returned before anything is enqueued.  No counterpart in the pages, whose
+ * dispatch takes the routing as given and whose combine takes the experts'
+ * outputs as given.
+ */
+
+typedef enum {
+    EP_SCORE_SOFTMAX = 0, /* p = softmax of the token's logits  */
+    EP_SCORE_SIGMOID = 1  /* p = sigmoid of each logit          */
+} ep_score_t;
+
+typedef enum {
+    EP_LOGITS_FP32 = 0,
+    EP_LOGITS_BF16 = 1
+} ep_logits_t;
+
+/*
+ * Routing: each token's K experts and their weights, in the form that
+ * ep_get_layout* and ep_dispatch* take.  For a token with logits l:
+ *   p     softmax(l) or sigmoid(l), fp32
+ *   key   p + bias (bias NULL: p); the bias steers the choice only
+ *   groups: the experts form num_groups groups of E / num_groups; a group's
+ *         score is the sum of its group_top (1 or 2) largest keys, and only
+ *         experts of the topk_groups best groups are offered
+ *   topk_idx      the K offered experts with the largest keys, descending;
+ *                 ties, of keys and of groups, go to the lowest index
+ *   topk_weights  p of the chosen (without the bias), divided by their sum
+ *                 when renormalize != 0, times weight_scale
+ * A logit of -infinity or NaN marks an expert not offered to the token, and
+ * +infinity counts as the largest finite number.  Where fewer than K experts
+ * are offered the remaining slots are -1 with weight 0.  Without a bias, and
+ * with one group or group_top 1, the logits themselves are compared (the
+ * scores rise with them), so scores that round together stay distinct.
+ *   logits  [T] rows of E, row_stride >= E elements apart (row_stride is in
+ *           elements), fp32 (4-byte aligned) or bf16 (2-byte aligned)
+ *   bias    [E] fp32 or NULL
+ *   topk_idx [T*K] int64, topk_weights [T*K] fp32: written
+ *   T >= 0, 1 <= K <= min(E, EP_MAX_TOPK), 1 <= E <= EP_MAX_EXPERTS,
+ *   1 <= topk_groups <= num_groups <= EP_MAX_RANKS, E % num_groups == 0
+ */
+typedef struct {
+    const void *logits;
+    ep_logits_t logits_type;
+    int64_t row_stride;
+    int num_tokens;
+    int num_experts;
+    int num_topk;
+    ep_score_t score;
+    const float *bias;
+    int num_groups;
+    int topk_groups;
+    int group_top;
+    int renormalize;
+    float weight_scale;
+    int64_t *topk_idx;
+    float *topk_weights;
+} ep_route_args_t;
+ep_status_t ep_route(const ep_route_args_t *args, ep_stream_t stream);
+
+/*
+ * The gradient of ep_route's weights with respect to the logits, for the
+ * choice topk_idx (the choice itself, and so the bias, has no gradient).
+ * Slots of -1 (or outside [0, E)) contribute nothing; an expert named by two
+ * slots receives both.
+ *   grad_weights [T*K] fp32, topk_idx [T*K] int64, logits as for ep_route
+ *   grad_logits  [T*E] in the logits' type, rows E apart: written whole
+ */
+typedef struct {
+    const float *grad_weights;
+    const void *logits;
+    ep_logits_t logits_type;
+    int64_t row_stride;
+    const int64_t *topk_idx;
+    int num_tokens;
+    int num_experts;
+    int num_topk;
+    ep_score_t score;
+    int renormalize;
+    float weight_scale;
+    void *grad_logits;
+} ep_route_backward_args_t;
+ep_status_t ep_route_backward(const ep_route_backward_args_t *args, ep_stream_t stream);
+
+typedef enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_SWIGLU = 1 /* silu(first half) * second half of the outputs */
+} ep_activation_t;
+
+/*
+ * The experts' products over the rows of an expanded layout (the rows that
+ * ep_dispatch_expanded wrote in bf16): for every expert e and row s of it,
+ *   h = x[s] * w[e]^T                   fp32
+ *   out[s] = bf16(h)                    EP_ACT_NONE
+ *   out[s] = bf16(silu(h[0:width]) * h[width:2*width])   EP_ACT_SWIGLU
+ * with silu(g) = g / (1 + exp(-g)).  Padding rows and rows past the last are
+ * not written.  Rows at or past recv_capacity are skipped and set
+ * EP_ERRBIT_CAPACITY.
+ *   x       [recv_capacity * hidden] bf16
+ *   layout  num_rows_per_expert, expert_offset and error_word are used; an
+ *           expert has at most num_tokens rows (a token names it once)
+ *   w       [E * wide * hidden] bf16, wide = width, or 2 * width with
+ *           EP_ACT_SWIGLU (the gate's rows, then the others)
+ *   out     [recv_capacity * width] bf16
+ *   preact  [recv_capacity * wide] bf16 or NULL: bf16(h), what the backward
+ *           pass of EP_ACT_SWIGLU needs
+ * hidden and width are multiples of 8 in [8, EP_MAX_HIDDEN]; x, w, out and
+ * preact are 16-byte aligned.
+ */
+typedef struct {
+    const void *x;
+    int recv_capacity;
+    int num_tokens;
+    int hidden;
+    int num_experts;
+    const ep_expanded_layout_t *layout;
+    const void *w;
+    int width;
+    ep_activation_t activation;
+    void *out;
+    void *preact;
+} ep_expert_product_args_t;
+ep_status_t ep_expert_product(const ep_expert_product_args_t *args, ep_stream_t stream);
+
+/*
+ * The gradients of ep_expert_product.  With g the gradient of h (for
+ * EP_ACT_NONE `grad` itself, for EP_ACT_SWIGLU computed from `grad` and
+ * `preact` and kept in bf16 in grad_preact):
+ *   grad_x[s] = bf16(g[s] * w[e])          rows of the layout only
+ *   grad_w[e] = bf16(sum over e's rows s of g[s]^T x[s])   0 without rows
+ *   grad         [recv_capacity * width] bf16
+ *   preact       [recv_capacity * 2 * width] bf16 (EP_ACT_SWIGLU)
+ *   grad_preact  [recv_capacity * 2 * width] bf16 (EP_ACT_SWIGLU): written
+ *   grad_x       [recv_capacity * hidden] bf16 or NULL (not computed)
+ *   grad_w       [E * wide * hidden] bf16 or NULL (not computed)
+ * Sizes, alignment and the rest as for ep_expert_product.  The sums run in a
+ * fixed order: the same inputs give the same bits.
+ */
+typedef struct {
+    const void *grad;
+    const void *x;
+    const void *w;
+    int recv_capacity;
+    int num_tokens;
+    int hidden;
+    int num_experts;
+    const ep_expanded_layout_t *layout;
+    int width;
+    ep_activation_t activation;
+    const void *preact;
+    void *grad_preact;
+    void *grad_x;
+    void *grad_w;
+} ep_expert_product_backward_args_t;
+ep_status_t ep_expert_product_backward(const ep_expert_product_backward_args_t *args, ep_stream_t stream);
+
+#define EP_MAX_RANK 128 /* of a low-rank adapter */
+
+/* Bytes of device workspace ep_adapter_product needs (no initial contents;
+ * 0 for sizes it refuses). */
+size_t ep_adapter_workspace_bytes(int num_rows, int hidden, int rank);
+
+/*
+ * A shared projection with each row's own low-rank adapter beside it, for
+ * batches that serve many requests at once:
+ *   out[t] = bf16(x[t] w^T + scale[a] * (x[t] A_a^T) B_a^T), a = adapter_idx[t]
+ * without the second term where a = -1; any other a outside [0, num_adapters)
+ * counts as -1 and sets EP_ERRBIT_BAD_INDEX in error_word (if given).  Sums
+ * in fp32.  Rows may come in any order; rows of one request next to
+ * each other are faster than interleaved ones.
+ *   x [num_rows * hidden], w [width * hidden], lora_a [num_adapters * rank *
+ *   hidden], lora_b [num_adapters * width * rank], out [num_rows * width]:
+ *   bf16, 16-byte aligned; adapter_idx [num_rows] int64; adapter_scale
+ *   [num_adapters] fp32 or NULL (1)
+ *   workspace >= ep_adapter_workspace_bytes(num_rows, hidden, rank) bytes,
+ *   16-byte aligned; calls sharing one must be ordered
+ * hidden and width are multiples of 8 in [8, EP_MAX_HIDDEN], rank of 8 in
+ * [8, EP_MAX_RANK], 1 <= num_adapters <= EP_MAX_EXPERTS.
+ */
+typedef struct {
+    const void *x;
+    int num_rows;
+    int hidden;
+    const void *w;
+    int width;
+    const void *lora_a;
+    const void *lora_b;
+    int num_adapters;
+    int rank;
+    const int64_t *adapter_idx;
+    const float *adapter_scale;
+    void *out;
+    void *workspace;
+    size_t workspace_bytes;
+    uint32_t *error_word;
+} ep_adapter_product_args_t;
+ep_status_t ep_adapter_product(const ep_adapter_product_args_t *args, ep_stream_t stream);
+
 /*
  * Self-test of the bounded device waits (the pages have no counterpart: the
  * library's own guarantee that a data or hand-over problem never hangs the

@@ -1,0 +1,113 @@
+"""A shared projection with low-rank adapters against 64 bits.
+
+Tolerances, fixed before any run: fp32 sums of n products err by at most
+n * 2^-23 of the sum of absolute values (as in test_product_gpu.py); the low
+row (x A^T, times the scale) may be rounded to bf16 before it meets B, at most
+half a unit in the last of 8 binary places, 2^-8 of each of its terms; the
+result is rounded once (between the roundings of the value less and plus the
+bound, as rounding is monotone).
+"""
+import math
+
+import pytest
+import torch
+
+import combine_ep_get_layout_gb300 as ep
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def make(T, H, N, A, r, seed, spread):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    bf = torch.bfloat16
+    x = torch.randn((T, H), generator=g, device=DEV).to(bf)
+    w = (torch.randn((N, H), generator=g, device=DEV) / math.sqrt(H)).to(bf)
+    a = (torch.randn((A, r, H), generator=g, device=DEV) / math.sqrt(H)).to(bf)
+    b = (torch.randn((A, N, r), generator=g, device=DEV) / math.sqrt(r)).to(bf)
+    s = torch.rand(A, generator=g, device=DEV) + 0.5
+    if spread == "none":
+        idx = torch.full((T,), -1, device=DEV)
+    elif spread == "one":
+        idx = torch.full((T,), A - 1, device=DEV)
+    elif spread == "runs":
+        idx = (torch.arange(T, device=DEV) * A // max(T, 1)) - int(A > 1)
+    else:
+        idx = torch.randint(-1, A, (T,), generator=g, device=DEV)
+    return x, w, a, b, idx, s
+
+
+def check(x, w, a, b, idx, s, out):
+    H, r = x.shape[1], a.shape[1]
+    xd, wd = x.double(), w.double()
+    want = xd @ wd.T
+    tol = H * 2.0 ** -23 * (xd.abs() @ wd.abs().T)
+    for k in idx.unique().tolist():
+        if not 0 <= k < a.shape[0]:
+            continue
+        at = (idx == k).nonzero()[:, 0]
+        f = 1.0 if s is None else float(s[k])
+        low = f * (xd[at] @ a[k].double().T)
+        low_tol = f * H * 2.0 ** -23 * (xd[at].abs() @ a[k].double().abs().T) + 2.0 ** -8 * low.abs()
+        want[at] += low @ b[k].double().T
+        tol[at] += (low_tol + (r + H) * 2.0 ** -23 * low.abs()) @ b[k].double().abs().T
+    low, high = ((want + s * tol).to(torch.bfloat16) for s in (-1, 1))
+    assert bool(((low <= out) & (out <= high)).all()), float(((out.double() - want).abs() / (tol + 2.0 ** -8 * want.abs())).max())
+
+
+@pytest.mark.parametrize("T,H,N,A,r", [(1, 8, 8, 1, 8), (1, 4096, 512, 3, 16), (7, 200, 136, 4, 16), (32, 512, 1000, 24, 16),
+                                       (64, 256, 72, 64, 8), (130, 136, 264, 5, 24), (300, 512, 512, 9, 32),
+                                       (513, 72, 640, 2, 64), (257, 328, 128, 40, 128), (1021, 256, 1000, 40, 40),
+                                       (90, 2048, 2056, 10, 16)])
+@pytest.mark.parametrize("spread", ["rows", "runs", "one", "none"])
+def test_adapters(T, H, N, A, r, spread):
+    x, w, a, b, idx, s = make(T, H, N, A, r, T + A, spread)
+    out = ep.ep_adapter_product(x, w, a, b, idx, s)
+    check(x, w, a, b, idx, s, out)
+    again = ep.ep_adapter_product(x, w, a, b, idx, s)
+    assert torch.equal(out, again)
+    check(x, w, a, b, idx, None, ep.ep_adapter_product(x, w, a, b, idx))
+
+
+def test_bad_indices_count_as_none_and_are_flagged():
+    x, w, a, b, idx, s = make(40, 128, 64, 4, 16, 3, "rows")
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = ep.ep_adapter_product(x, w, a, b, idx, s, error_word=word)
+    assert int(word) == 0
+    bad = idx.clone()
+    bad[5], bad[17], bad[18] = 4, -2, 1 << 40
+    got = ep.ep_adapter_product(x, w, a, b, bad, s, error_word=word)
+    assert int(word) == ep.EP_ERRBIT_BAD_INDEX
+    rest = [i for i in range(40) if i not in (5, 17, 18)]
+    assert torch.equal(got[rest], want[rest])
+    check(x, w, a, b, bad, s, got)
+
+
+def test_unused_adapters_and_other_rows_do_not_leak():
+    """NaN in adapters that no row names, or in another row, reaches no row."""
+    x, w, a, b, idx, s = make(70, 128, 136, 6, 16, 4, "rows")
+    idx = torch.where(idx == 2, -1, idx)
+    want = ep.ep_adapter_product(x, w, a, b, idx, s)
+    a[2], b[2], s[2] = math.nan, math.inf, math.nan
+    got = ep.ep_adapter_product(x, w, a, b, idx, s)
+    assert torch.equal(got, want)
+    x[11] = math.nan
+    got = ep.ep_adapter_product(x, w, a, b, idx, s)
+    rest = [i for i in range(70) if i != 11]
+    assert torch.equal(got[rest], want[rest]) and torch.isnan(got[11]).all()
+
+
+def test_no_rows_and_another_stream():
+    x, w, a, b, idx, s = make(0, 64, 32, 2, 8, 5, "rows")
+    assert ep.ep_adapter_product(x, w, a, b, idx, s).shape == (0, 32)
+    x, w, a, b, idx, s = make(200, 512, 512, 8, 16, 6, "rows")
+    want = ep.ep_adapter_product(x, w, a, b, idx, s)
+    out = torch.zeros_like(want)
+    ws = torch.empty(ep.ep_adapter_workspace_bytes(200, 512, 16), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        y = x * 1.0
+        ep.ep_adapter_product(y, w, a, b, idx, s, out=out, workspace=ws)
+    st.synchronize()
+    assert torch.equal(out, want)

@@ -1,0 +1,273 @@
+"""The experts' products and their gradients against plain 64-bit products.
+
+Tolerances, fixed before any run.  A sum of n products of bf16 numbers (each
+product exact in fp32) kept in fp32 errs by at most n * 2^-23 times the sum of
+the products' absolute values S (2^-23 a step: the tensor cores may truncate
+where fp32 arithmetic rounds); the result is rounded once to bf16.  Rounding
+is monotone, so a result has to lie between the bf16 roundings of the 64-bit
+value less and plus the bound.  silu has a slope of at most 1.1.
+"""
+import math
+
+import pytest
+import torch
+
+import combine_ep_get_layout_gb300 as ep
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def rows_and_layout(T, K, E, H, align=1, seed=0, masked=0.0, only=None):
+    """A routing (distinct experts a token; `only`: the experts that may be
+    named), its expanded layout and rows; padding and unused rows are NaN."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    names = torch.arange(E, device=DEV) if only is None else torch.tensor(only, device=DEV)
+    K = min(K, len(names))
+    idx = names[torch.rand((T, len(names)), generator=g, device=DEV).argsort(1)[:, :K]]
+    idx[torch.rand((T, K), generator=g, device=DEV) < masked] = -1
+    idx = idx.contiguous()
+    lay = ep.ep_get_layout_expanded(idx, E, align)
+    cap = lay.capacity_bound()
+    x = torch.full((cap, H), math.nan, dtype=torch.bfloat16, device=DEV)
+    slot = lay.token_slot.reshape(-1).long()
+    used = slot[slot >= 0]
+    x[used] = torch.randn((len(used), H), generator=g, device=DEV).to(torch.bfloat16)
+    return lay, x, used, g
+
+
+def segments(lay):
+    return list(zip(lay.expert_offset[:-1].tolist(), lay.num_rows_per_expert.tolist()))
+
+
+def weights(g, E, N, H):
+    return (torch.randn((E, N, H), generator=g, device=DEV) / math.sqrt(H)).to(torch.bfloat16)
+
+
+def fp32_sum(a, b):
+    """(a b^T, bound of an fp32 sum's error) in 64 bits."""
+    return a.double() @ b.double().T, a.shape[1] * 2.0 ** -23 * (a.double().abs() @ b.double().abs().T)
+
+
+def close(got, want, tol):
+    low, high = ((want + s * tol).to(torch.bfloat16) for s in (-1, 1))
+    assert bool(((low <= got) & (got <= high)).all()), float(((got.double() - want).abs() / (tol + 2.0 ** -8 * want.abs())).max())
+
+
+SIZES = [
+    # T, K, E, H, width, align, masked
+    (1, 1, 1, 8, 8, 1, 0.0),
+    (1, 2, 8, 64, 72, 1, 0.0),
+    (5, 3, 16, 200, 136, 4, 0.3),
+    (40, 2, 4, 256, 128, 16, 0.0),
+    (129, 4, 4, 72, 264, 1, 0.0),
+    (300, 2, 2, 136, 520, 128, 0.0),
+    (600, 3, 5, 328, 104, 1, 0.1),
+    (257, 1, 1, 1000, 256, 1, 0.0),
+    (64, 6, 64, 512, 256, 8, 0.0),
+    (700, 8, 300, 128, 64, 1, 0.2),
+]
+
+
+@pytest.mark.parametrize("T,K,E,H,width,align,masked", SIZES)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_product(T, K, E, H, width, align, masked, act):
+    lay, x, used, g = rows_and_layout(T, K, E, H, align, T + E, masked)
+    wide = 2 * width if act else width
+    w = weights(g, E, wide, H)
+    out = torch.full((x.shape[0], width), 7.0, dtype=torch.bfloat16, device=DEV)
+    pre = torch.full((x.shape[0], wide), 7.0, dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product(x, w, lay, activation=act, out=out, preact=pre)
+    again = ep.ep_expert_product(x, w, lay, activation=act)
+    assert lay.errors() == 0
+    assert torch.equal(out[used], again[used])
+    untouched = torch.ones(x.shape[0], dtype=torch.bool, device=DEV)
+    untouched[used] = False
+    assert bool((out[untouched] == 7.0).all()) and bool((pre[untouched] == 7.0).all())
+    for e, (a, n) in enumerate(segments(lay)):
+        h, tol = fp32_sum(x[a:a + n], w[e])
+        close(pre[a:a + n], h, tol)
+        if act is None:
+            close(out[a:a + n], h, tol)
+        else:
+            gate, up, tg, tu = h[:, :width], h[:, width:], tol[:, :width], tol[:, width:]
+            s = gate * torch.sigmoid(gate)
+            close(out[a:a + n], s * up, 1.1 * tg * (up.abs() + tu) + s.abs() * tu + 1e-6 * (s * up).abs())
+
+
+@pytest.mark.parametrize("T,K,E,H,width,align,masked", SIZES)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_gradients(T, K, E, H, width, align, masked, act):
+    lay, x, used, g = rows_and_layout(T, K, E, H, align, T + 3 * E, masked)
+    wide = 2 * width if act else width
+    w = weights(g, E, wide, H)
+    grad = torch.full((x.shape[0], width), math.nan, dtype=torch.bfloat16, device=DEV)
+    grad[used] = torch.randn((len(used), width), generator=g, device=DEV).to(torch.bfloat16)
+    pre = gp = None
+    if act:
+        pre = torch.full((x.shape[0], wide), math.nan, dtype=torch.bfloat16, device=DEV)
+        ep.ep_expert_product(x, w, lay, activation=act, preact=pre)
+        gp = torch.full((x.shape[0], wide), math.nan, dtype=torch.bfloat16, device=DEV)
+    grad_x = torch.full((x.shape[0], H), 7.0, dtype=torch.bfloat16, device=DEV)
+    grad_w = torch.full((E, wide, H), math.nan, dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product_backward(grad, x, w, lay, activation=act, preact=pre, grad_x=grad_x, grad_w=grad_w,
+                                  grad_preact=gp)
+    again = ep.ep_expert_product_backward(grad, x, w, lay, activation=act, preact=pre)
+    assert torch.equal(grad_x[used], again[0][used]) and torch.equal(grad_w, again[1])
+    only_x = ep.ep_expert_product_backward(grad, x, w, lay, activation=act, preact=pre, need_w=False)
+    only_w = ep.ep_expert_product_backward(grad, x, w, lay, activation=act, preact=pre, need_x=False)
+    assert only_x[1] is None and only_w[0] is None
+    assert torch.equal(only_x[0][used], grad_x[used]) and torch.equal(only_w[1], grad_w)
+    untouched = torch.ones(x.shape[0], dtype=torch.bool, device=DEV)
+    untouched[used] = False
+    assert bool((grad_x[untouched] == 7.0).all())
+    for e, (a, n) in enumerate(segments(lay)):
+        d = grad[a:a + n]
+        if act:  # the gradient through the activation, checked by itself
+            p = pre[a:a + n].double()
+            gate, up = p[:, :width], p[:, width:]
+            sig = torch.sigmoid(gate)
+            dg = d.double() * up * sig * (1 + gate * (1 - sig))
+            close(gp[a:a + n, :width], dg, 1e-6 * (d.double() * up * sig).abs() * (1 + gate.abs()))
+            close(gp[a:a + n, width:], d.double() * gate * sig, 1e-6 * (d.double() * gate * sig).abs())
+            d = gp[a:a + n]
+        want, tol = fp32_sum(d, w[e].T)
+        close(grad_x[a:a + n], want, tol)
+        want, tol = fp32_sum(d.T, x[a:a + n].T)
+        close(grad_w[e], want, tol)
+
+
+def test_gradients_against_differences():
+    """A central difference of the 64-bit forward along random directions.
+    The kernel's gradients carry bf16 roundings of the preactivation, its
+    gradient and the results (4 of 2^-9, averaging over the sum): 2^-8 of the
+    norm of the summed terms."""
+    lay, x, used, g = rows_and_layout(30, 2, 4, 64, 1, 9)
+    width = 48
+    w = weights(g, 4, 2 * width, 64)
+    pre = torch.zeros((x.shape[0], 2 * width), dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product(x, w, lay, activation="swiglu", preact=pre)
+    grad = torch.randn((x.shape[0], width), generator=g, device=DEV).to(torch.bfloat16)
+    grad_x, grad_w = ep.ep_expert_product_backward(grad, x, w, lay, activation="swiglu", preact=pre)
+
+    def f(xx, ww):
+        total = 0.0
+        for e, (a, n) in enumerate(segments(lay)):
+            h = xx[a:a + n] @ ww[e].T
+            total = total + (torch.nn.functional.silu(h[:, :width]) * h[:, width:] * grad[a:a + n].double()).sum()
+        return float(total)
+
+    xd, wd, step = x.double(), w.double(), 1e-5
+    for _ in range(3):
+        vx = torch.randn(x.shape, generator=g, device=DEV).double()
+        vw = torch.randn(w.shape, generator=g, device=DEV).double()
+        want = (f(xd + step * vx, wd) - f(xd - step * vx, wd)) / (2 * step)
+        terms = grad_x.double() * vx
+        assert abs(float(terms.sum()) - want) <= 2.0 ** -8 * float(terms.norm()) * 4
+        want = (f(xd, wd + step * vw) - f(xd, wd - step * vw)) / (2 * step)
+        terms = grad_w.double() * vw
+        assert abs(float(terms.sum()) - want) <= 2.0 ** -8 * float(terms.norm()) * 4
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_experts_without_rows(act):
+    lay, x, used, g = rows_and_layout(50, 2, 16, 128, 1, 4, only=[3, 9, 10])
+    w = weights(g, 16, 128, 128)
+    w[0], w[15] = math.nan, math.inf  # weights that no row meets
+    width = 64 if act else 128
+    pre = torch.empty((x.shape[0], 128), dtype=torch.bfloat16, device=DEV)
+    out = ep.ep_expert_product(x, w, lay, activation=act, preact=pre)
+    assert torch.isfinite(out[used]).all()
+    grad = torch.randn((x.shape[0], width), generator=g, device=DEV).to(torch.bfloat16)
+    grad_x, grad_w = ep.ep_expert_product_backward(grad, x, w, lay, activation=act, preact=pre)
+    assert torch.isfinite(grad_x[used]).all()
+    empty = [e for e in range(16) if e not in (3, 9, 10)]
+    assert bool((grad_w[empty] == 0).all()) and bool((grad_w[3] != 0).any())
+
+
+def test_no_tokens():
+    idx = torch.empty((0, 2), dtype=torch.int64, device=DEV)
+    lay = ep.ep_get_layout_expanded(idx, 4, 1)
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    w = torch.randn((4, 32, 64), device=DEV).to(torch.bfloat16)
+    assert ep.ep_expert_product(x, w, lay).shape == (0, 32)
+    gx, gw = ep.ep_expert_product_backward(torch.empty((0, 32), dtype=torch.bfloat16, device=DEV), x, w, lay)
+    assert gx.shape == (0, 64) and bool((gw == 0).all())
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    """A row's NaN reaches its own outputs and no other row's."""
+    lay, x, used, g = rows_and_layout(90, 2, 3, 136, 1, 5)
+    w = weights(g, 3, 64, 136)
+    want = ep.ep_expert_product(x, w, lay)
+    bad = used[:5]
+    y = x.clone()
+    y[bad[0]] = math.nan
+    y[bad[1]] = math.inf
+    got = ep.ep_expert_product(y, w, lay)
+    rest = used[~torch.isin(used, bad[:2])]
+    assert torch.equal(got[rest], want[rest])
+    assert torch.isnan(got[bad[0]]).all() and not torch.isfinite(got[bad[1]]).any()
+    # an infinite gradient in one expert's row leaves the other experts' weights alone
+    grad = torch.randn((x.shape[0], 64), generator=g, device=DEV).to(torch.bfloat16)
+    _, gw = ep.ep_expert_product_backward(grad, x, w, lay, need_x=False)
+    a, n = segments(lay)[1]
+    grad[a] = math.inf
+    _, gw2 = ep.ep_expert_product_backward(grad, x, w, lay, need_x=False)
+    assert torch.equal(gw[[0, 2]], gw2[[0, 2]])
+
+
+def test_rows_past_the_capacity_are_flagged_and_skipped():
+    lay, x, used, g = rows_and_layout(64, 2, 4, 64, 1, 6)
+    w = weights(g, 4, 64, 64)
+    want = ep.ep_expert_product(x, w, lay)
+    assert lay.errors() == 0
+    cap = 70  # of 128 rows
+    out = torch.full((128, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product(x[:cap], w, lay, out=out[:cap])
+    assert lay.errors() == ep.EP_ERRBIT_CAPACITY
+    assert torch.equal(out[:cap], want[:cap]) and bool((out[cap:] == 7.0).all())
+
+
+def test_another_stream():
+    lay, x, used, g = rows_and_layout(512, 4, 8, 512, 1, 8)
+    w = weights(g, 8, 512, 512)
+    want = ep.ep_expert_product(x, w, lay, activation="swiglu")
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        y = x * 1.0
+        ep.ep_expert_product(y, w, lay, activation="swiglu", out=out)
+    s.synchronize()
+    assert torch.equal(out[used], want[used])
+
+
+def test_a_layer_end_to_end():
+    """Router, expanded layout, dispatch, both products, combine: the whole
+    layer against 64 bits.  The hidden rows are rounded to bf16 once, as the
+    reference's are, then each output and the combine once more: 3 roundings
+    of 2^-9 against the sum of absolute terms."""
+    T, H, F, E, K = 200, 128, 192, 16, 4
+    g = torch.Generator(device=DEV).manual_seed(31)
+    x = torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16)
+    gate = (torch.randn((E, H), generator=g, device=DEV) / math.sqrt(H)).to(torch.bfloat16)
+    w1, w2 = weights(g, E, 2 * F, H), weights(g, E, H, F)
+    logits = x.float() @ gate.float().T
+    r = ep.ep_route(logits, K, score="sigmoid", num_groups=4, topk_groups=2, group_top=2)
+    lay = ep.ep_get_layout_expanded(r.topk_idx, E, 8)
+    d = ep.ep_dispatch_expanded(x, r.topk_idx, r.topk_weights, lay, 4)
+    hidden = ep.ep_expert_product(d.recv_x, w1, lay, activation="swiglu")
+    y = ep.ep_expert_product(hidden, w2, lay)
+    out = ep.ep_combine_expanded(y, lay, r.topk_idx, r.topk_weights)
+    want = torch.zeros((T, H), dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(want)
+    for k in range(K):
+        e = r.topk_idx[:, k]
+        h = torch.einsum("th,tnh->tn", x.double(), w1.double()[e])
+        h = torch.nn.functional.silu(h[:, :F]) * h[:, F:]
+        p = r.topk_weights[:, k:k + 1].double()
+        want += p * torch.einsum("tf,thf->th", h, w2.double()[e])
+        size += p * torch.einsum("tf,thf->th", h.abs(), w2.double()[e].abs())
+    err = (out.double() - want).abs()
+    assert bool((err <= 3 * 2.0 ** -9 * size).all())
