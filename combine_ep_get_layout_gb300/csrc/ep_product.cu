@@ -7,208 +7,616 @@
 //   out[s]    = silu(x[s] wg^T) * (x[s] wu^T)           (gated: w[e] = [wg; wu])
 //   grad_x[s] = g[s] w[e],   grad_w[e] = sum over e's rows of g[s]^T x[s]
 //
-// with g the gradient of x w^T.  bf16 in and out, sums in fp32, rounded once.
-#include "ep_device.cuh"
+// with g the gradient of x w^T.  bf16 in and out, sums in fp32 in tensor
+// memory, rounded once.
+//
+// One kernel, four forms.  A pair of CTAs computes a tile of 256 x up to 256:
+// A, the operand with 256 rows, is the weights (so the ragged number of an
+// expert's rows meets the dimension that comes in steps of 32, not of 256),
+// B the rows:
+//   kPlain, kGated   A = w[e] (inner dimension hidden),  B = rows of x
+//   kGradX           A = w[e]^T (inner dimension wide),  B = rows of g
+//   kGradW           A = g^T, B = x^T (inner dimension the expert's rows)
+// An inner step is 64 elements, a 128-byte row of shared memory in the
+// 128-byte swizzle; the transposed operands are read with their outer
+// dimension contiguous, so nothing is ever transposed in memory.
+#include <atomic>
+
 #include "ep_ops.h"
+#include "ep_tc.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+enum Form { kPlain, kGated, kGradX, kGradW };
 
-struct Segment {
-  int first, rows;
+constexpr int kThreads = 384;        // warps: 0 copies, 1 products, 2 row ends, 4-11 results
+constexpr int kInner = 64;           // elements of an inner step
+constexpr int kABytes = 128 * 128;   // a CTA's half of A for one step
+constexpr int kMaxCols = 256;        // columns of a tile
+constexpr int kTmemCols = 512;       // two tiles: one computed, one read out
+constexpr int kMaxStages = 12;
+constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
+constexpr int kStagingBytes = 32 * kPitch;       // a result warp's 32 rows
+constexpr int kExchangeBytes = 16 * 32 * 4;      // kGated: 16 columns of a warp, fp32
+constexpr int kResultWarps = 8;
+
+struct alignas(64) Params {
+  CUtensorMap a, b, b16;  // boxes of 64 x 64; b16: 64 x 16 (rows of x or g)
+  const int32_t *rows, *offset;
+  uint32_t *error_word;
+  int E, cap;
+  int wide;      // outputs of an expert: rows of A (kPlain, kGated, kGradW), inner (kGradX)
+  int width;     // kGated: wide / 2; else the outputs of a row
+  int inner;     // length of the inner dimension (not kGradW)
+  int a_tiles;   // tiles along A
+  int b_tiles;   // kGradW: tiles along B (hidden)
+  int hidden;    // kGradW
+  uint16_t *out, *preact;
+  int stages, b_bytes;  // ring; bytes of a CTA's half of B in a stage
 };
 
-__device__ __forceinline__ Segment segment(const int32_t *offset, const int32_t *rows, int e, int cap) {
-  const int a = offset[e];
-  const int n = rows[e];
-  Segment s;
-  s.first = a;
-  s.rows = a < 0 || a >= cap ? 0 : max(0, min(n, cap - a));
-  return s;
-}
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages], ends[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem;
+};
 
-__device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+struct Tile {
+  int e, first, count;  // rows of the tile (kGradW: all rows of the expert)
+  int cols;             // columns of the product (multiple of 32)
+  int a0, b0;           // first row of A; kGradW: first column
+  int steps;
+};
 
-__device__ __forceinline__ uint16_t to_bf16(float v) { return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu); }
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ float silu_of(float g) { return g / (1.0f + expf(-g)); }
+// Walks the tiles of a pair, 32 experts at a time (a whole warp calls it).
+// Tiles are ordered by expert, then along A, then along the expert's rows, so
+// pairs that run at the same time read the same weights.
+template <Form F>
+struct Walker {
+  const Params &p;
+  int lane, chunk = -1, base = 0, total = 0;
+  int rows = 0, first = 0, prefix = 0, mine = 0;
 
-// c[i][j] += sum over k < depth of a(m0 + 4 ty + i, k) * b(n0 + 4 tx + j, k)
-template <typename A, typename B>
-__device__ __forceinline__ void tile_product(float (&c)[4][4], int depth, A a, B b, float (*sa)[kTile], float (*sb)[kTile]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int k0 = 0; k0 < depth; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-      const int r = i / kStep, k = i % kStep;
-      sa[k][r] = k0 + k < depth ? a(r, k0 + k) : 0.0f;
-      sb[k][r] = k0 + k < depth ? b(r, k0 + k) : 0.0f;
+  __device__ Walker(const Params &p_) : p(p_), lane(threadIdx.x & 31) {}
+
+  __device__ void load(int c) {
+    chunk = c;
+    const int e = c * 32 + lane;
+    rows = first = mine = 0;
+    if (e < p.E) {
+      first = p.offset[e];
+      const int n = p.rows[e];
+      rows = first < 0 || first >= p.cap ? 0 : max(0, min(n, p.cap - first));
+      if (rows != n && blockIdx.x == 0 && threadIdx.x < 32) set_error(p.error_word, EP_ERRBIT_CAPACITY);
+      mine = F == kGradW ? p.a_tiles * p.b_tiles : p.a_tiles * ceil_div(rows, kMaxCols);
     }
-    __syncthreads();
+    prefix = mine;
 #pragma unroll
-    for (int k = 0; k < kStep; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] += sa[k][4 * ty + i] * sb[k][4 * tx + j];
-    __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, prefix, o);
+      if (lane >= o) prefix += v;
+    }
+    total = __shfl_sync(0xffffffffu, prefix, 31);
   }
+
+  // The tile with this number (numbers only grow); false past the last.
+  __device__ bool find(int number, Tile &t) {
+    while (chunk < 0 || number >= base + total) {
+      base += total;
+      if ((chunk + 1) * 32 >= p.E) {
+        total = 0;
+        return false;
+      }
+      load(chunk + 1);
+    }
+    const int local = number - base;
+    const int src = __ffs(__ballot_sync(0xffffffffu, prefix > local)) - 1;
+    const int at = local - __shfl_sync(0xffffffffu, prefix - mine, src);
+    const int n = __shfl_sync(0xffffffffu, rows, src);
+    t.e = chunk * 32 + src;
+    t.first = __shfl_sync(0xffffffffu, first, src);
+    if (F == kGradW) {
+      t.a0 = at / p.b_tiles * 256;
+      t.b0 = at % p.b_tiles * 256;
+      t.count = n;
+      t.cols = p.hidden - t.b0 > 128 ? 256 : 128;
+      t.steps = ceil_div(n, kInner);
+    } else {
+      // as few tiles as hold the rows, of about equal size
+      const int tiles = ceil_div(n, kMaxCols);
+      t.cols = ceil_div(ceil_div(n, tiles), 32) * 32;
+      const int part = at % tiles;
+      t.a0 = at / tiles * (F == kGated ? 128 : 256);
+      t.b0 = 0;
+      t.first += part * t.cols;
+      t.count = min(t.cols, n - part * t.cols);
+      t.steps = ceil_div(p.inner, kInner);
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ float silu_of(float g) { return g / (1.0f + __expf(-g)); }
+
+// Barriers of two warps; the first also gives whether both say `ok`.
+__device__ __forceinline__ bool pair_agree(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
 }
 
-struct Params {
-  ProductArgs a;
-};
-struct BackwardParams {
-  ProductBackwardArgs a;
-};
+__device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
-__global__ void __launch_bounds__(kThreads) product_kernel(Params q) {
-  const ProductArgs &p = q.a;
-  __shared__ float sa[kStep][kTile], sb[kStep][kTile];
-  const int e = blockIdx.z, n0 = blockIdx.y * kTile, H = p.hidden;
+// A warp's 32 lanes hold outputs n (one a lane) of `count` <= 32 rows v[0..):
+// out[row][n] through the staging buffer, 64 bytes of a row at a time.
+template <int COUNT>
+__device__ __forceinline__ void store_transposed(const float *v, char *stage, uint16_t *out, int64_t pitch, int rows,
+                                                 int n, int limit, int lane) {
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c)
+    *reinterpret_cast<uint16_t *>(stage + c * kPitch + lane * 2) = (uint16_t)(pack_bf16x2(v[c], 0.0f) & 0xffffu);
+  __syncwarp();
+  const int part = lane & 3;
+#pragma unroll
+  for (int c = lane >> 2; c < COUNT; c += 8) {
+    if (c < rows && n + part * 8 < limit)
+      *reinterpret_cast<int4 *>(out + (int64_t)c * pitch + n + part * 8) =
+          *reinterpret_cast<const int4 *>(stage + c * kPitch + part * 16);
+  }
+  __syncwarp();
+}
+
+template <Form F>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
+  extern __shared__ char s_raw[];
+  __shared__ Barriers s_bar;
+  char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = kABytes + p.b_bytes;
+  char *staging = ring + (size_t)p.stages * stage_bytes;
+  char *exchange = staging + kResultWarps * kStagingBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s_bar.full[i], 2);  // one arrival from each CTA
+      mbar_init(&s_bar.empty[i], 1);
+      mbar_init(&s_bar.ends[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_bar.acc_full[i], 1);
+      mbar_init(&s_bar.acc_empty[i], 2 * kResultWarps);
+    }
+    fence_barrier_init();
+    prefetch_map(&p.a);
+    prefetch_map(&p.b);
+    prefetch_map(&p.b16);
+  }
+  __syncwarp();
+  if (warp == 2) tmem_alloc_pair(&s_bar.tmem, kTmemCols);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_bar.tmem;
   griddep_wait();
   griddep_launch_dependents();
-  const Segment s = segment(p.expert_offset, p.num_rows_per_expert, e, p.recv_capacity);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && s.rows != p.num_rows_per_expert[e])
-    set_error(p.error_word, EP_ERRBIT_CAPACITY);
-  const int wide = p.gated ? 2 * p.width : p.width;
-  const uint16_t *w = p.w + (int64_t)e * wide * H;
-  for (int m0 = blockIdx.x * kTile; m0 < s.rows; m0 += gridDim.x * kTile) {
-    const auto x = [&](int r, int k) {
-      return m0 + r < s.rows ? bf16_at(p.x + (int64_t)(s.first + m0 + r) * H + k) : 0.0f;
-    };
-    float c[4][4] = {}, u[4][4] = {};
-    tile_product(c, H, x, [&](int r, int k) { return n0 + r < p.width ? bf16_at(w + (int64_t)(n0 + r) * H + k) : 0.0f; },
-                 sa, sb);
-    if (p.gated)
-      tile_product(u, H, x, [&](int r, int k) {
-        return n0 + r < p.width ? bf16_at(w + (int64_t)(p.width + n0 + r) * H + k) : 0.0f;
-      }, sa, sb);
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + 4 * (threadIdx.x >> 4) + i, n = n0 + 4 * (threadIdx.x & 15) + j;
-        if (m >= s.rows || n >= p.width) continue;
-        const int64_t at = s.first + m;
-        p.out[at * p.width + n] = to_bf16(p.gated ? silu_of(c[i][j]) * u[i][j] : c[i][j]);
-        if (p.preact != nullptr) {
-          p.preact[at * wide + n] = to_bf16(c[i][j]);
-          if (p.gated) p.preact[at * wide + p.width + n] = to_bf16(u[i][j]);
+
+  bool ok = true;  // false: a wait gave up
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    Walker<F> walk(p);
+    Tile t;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      const int b_rows = t.cols / 2;
+      const bool ragged = F == kGradW && t.count % 16 != 0;  // the last step passes by the row ends
+      if (lane == 0) {
+        for (int k = 0; k < t.steps; ++k) {
+          if (!mbar_wait_cluster(&s_bar.empty[stage], phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
+          const bool last = ragged && k == t.steps - 1;
+          const uint32_t full = map_shared(smem_addr(&s_bar.full[stage]), 0);
+          uint32_t bar = full;
+          const uint32_t bytes = kABytes + b_rows * 128;
+          if (last) {
+            mbar_arrive_expect_tx(&s_bar.ends[stage], bytes);
+            bar = map_shared(smem_addr(&s_bar.ends[stage]), rank);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&s_bar.full[stage], 2 * bytes);
+          } else {
+            mbar_arrive_cluster(full);
+          }
+          const int at = k * kInner;
+          if (F == kPlain) {
+            tile_load_3d(a, &p.a, at, t.a0 + (int)rank * 128, t.e, bar);
+            tile_load_3d(a + 8192, &p.a, at, t.a0 + (int)rank * 128 + 64, t.e, bar);
+          } else if (F == kGated) {  // 64 rows of the gate and the 64 that they multiply
+            tile_load_3d(a, &p.a, at, t.a0 + (int)rank * 64, t.e, bar);
+            tile_load_3d(a + 8192, &p.a, at, p.width + t.a0 + (int)rank * 64, t.e, bar);
+          } else if (F == kGradX) {
+            tile_load_3d(a, &p.a, t.a0 + (int)rank * 128, at, t.e, bar);
+            tile_load_3d(a + 8192, &p.a, t.a0 + (int)rank * 128 + 64, at, t.e, bar);
+          } else {
+            tile_load_2d(a, &p.a, t.a0 + (int)rank * 128, t.first + at, bar);
+            tile_load_2d(a + 8192, &p.a, t.a0 + (int)rank * 128 + 64, t.first + at, bar);
+          }
+          if (F == kGradW) {
+            for (int c = 0; c < b_rows; c += 64)
+              tile_load_2d(b + c * 128, &p.b, t.b0 + (int)rank * b_rows + c, t.first + at, bar);
+          } else {
+            const int row = t.first + (int)rank * b_rows;
+            int c = 0;
+            for (; c + 64 <= b_rows; c += 64) tile_load_2d(b + c * 128, &p.b, at, row + c, bar);
+            for (; c < b_rows; c += 16) tile_load_2d(b + c * 128, &p.b16, at, row + c, bar);
+          }
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    // the products' last arrivals on this CTA's barriers come before it ends
+    for (int i = 0; ok && lane == 0 && i < p.stages; ++i) {
+      ok = mbar_wait_cluster(&s_bar.empty[stage], phase ^ 1);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------- products
+    Walker<F> walk(p);
+    Tile t;
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      if (t.steps == 0) continue;  // an expert without rows (kGradW): zeros are written
+      if (lane == 0) {
+        const uint32_t idesc = mma_desc(t.cols, F == kGradX || F == kGradW, F == kGradW);
+        const uint32_t d = tmem + acc * kMaxCols;
+        ok = mbar_wait_cluster(&s_bar.acc_empty[acc], acc_phase ^ 1);
+        tc_fence_after();
+        for (int k = 0; ok && k < t.steps; ++k) {
+          if (!mbar_wait_cluster(&s_bar.full[stage], phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
+          const int parts = F == kGradW ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j < parts) {
+              const uint64_t da = F == kGradX || F == kGradW ? outer_desc(a + j * 2048, 8192) : inner_desc(a + j * 32);
+              const uint64_t db = F == kGradW ? outer_desc(b + j * 2048, 8192) : inner_desc(b + j * 32);
+              mma_pair(d, da, db, idesc, k > 0 || j > 0);
+            }
+          }
+          commit_pair(&s_bar.empty[stage]);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) commit_pair(&s_bar.acc_full[acc]);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  } else if (warp == 2 && F == kGradW) {
+    // ---------------------------------------------------------- row ends
+    // The last step of an expert reads rows of the next one: they are zeroed
+    // in both operands (both, since what lies there may be NaN).
+    Walker<F> walk(p);
+    Tile t;
+    int stage = 0;
+    uint32_t parities = 0;
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      stage = (stage + t.steps) % p.stages;
+      if (t.count % 16 == 0) continue;
+      const int s = (stage + p.stages - 1) % p.stages;
+      ok = mbar_wait_bounded(&s_bar.ends[s], (parities >> s) & 1u);
+      if (!ok) break;
+      parities ^= 1u << s;
+      char *a = ring + (size_t)s * stage_bytes;
+      const int from = t.count % kInner, to = ceil_div(from, 16) * 16;
+      const int blocks = 2 + t.cols / 2 / 64;  // of 64 outer elements, A's two and B's
+      for (int i = lane; i < blocks * (to - from) * 8; i += 32) {
+        const int block = i / ((to - from) * 8), r = from + i / 8 % (to - from);
+        *reinterpret_cast<int4 *>(a + block * 8192 + r * 128 + (i & 7) * 16) = make_int4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.full[s]), 0));
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- results
+    // Warp w reads the tensor-memory lanes 32 (w % 4) ...; the two groups of
+    // four warps take every other 32 columns.
+    Walker<F> walk(p);
+    Tile t;
+    const int w = warp - 4, quarter = w & 3, half = w >> 2;
+    char *stage_buf = staging + w * kStagingBytes;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      if (F == kGradW && t.steps == 0) {
+        const int row = t.a0 + (int)rank * 128 + quarter * 32 + lane;
+        for (int c = half * 32; c < t.cols && row < p.wide; c += 64)
+          for (int j = 0; j < 32 && t.b0 + c + j < p.hidden; j += 8)
+            *reinterpret_cast<int4 *>(p.out + ((int64_t)t.e * p.wide + row) * p.hidden + t.b0 + c + j) =
+                make_int4(0, 0, 0, 0);
+        continue;
+      }
+      ok = mbar_wait_cluster(&s_bar.acc_full[acc], acc_phase);
+      ok = F == kGated ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      for (int c = half * 32; c < t.cols; c += 64) {
+        float v[32];
+        tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+        const int left = t.count - c;  // rows of this chunk (not kGradW)
+        if (F == kPlain || F == kGradX) {
+          const int at = t.a0 + (int)rank * 128 + quarter * 32;
+          const int64_t row = t.first + c;
+          store_transposed<32>(v, stage_buf, p.out + row * p.width, p.width, left, at, p.width, lane);
+          if (F == kPlain && p.preact != nullptr)
+            store_transposed<32>(v, stage_buf, p.preact + row * p.width, p.width, left, at, p.width, lane);
+        } else if (F == kGated) {
+          // lanes 0-63 hold the gate, lanes 64-127 what it multiplies: warps
+          // w and w + 2 exchange half of their columns and finish half each
+          const int at = t.a0 + (int)rank * 64 + (quarter & 1) * 32;
+          const int64_t row = t.first + c;
+          const bool gate = quarter < 2;
+          if (p.preact != nullptr)
+            store_transposed<32>(v, stage_buf, p.preact + row * p.wide + (gate ? 0 : p.width), p.wide, left, at,
+                                 p.width, lane);
+          float *give = reinterpret_cast<float *>(exchange + w * kExchangeBytes);
+          const float *take = reinterpret_cast<const float *>(exchange + (w ^ 2) * kExchangeBytes);
+          const int id = 1 + half * 2 + (quarter & 1);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) give[j * 32 + lane] = gate ? v[16 + j] : v[j];
+          pair_barrier(id);
+          float o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float other = take[j * 32 + lane];
+            o[j] = gate ? silu_of(v[j]) * other : silu_of(other) * v[16 + j];
+          }
+          const int skip = gate ? 0 : 16;
+          store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);
+          pair_barrier(id);  // before the next chunk overwrites what the other warp reads
+        } else {
+          // one row of the gradient a lane, 32 columns
+          uint32_t packed[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(stage_buf + lane * kPitch + j * 16) =
+                make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+          __syncwarp();
+          const int part = lane & 3, col = t.b0 + c + part * 8;
+#pragma unroll
+          for (int r = lane >> 2; r < 32; r += 8) {
+            const int row = t.a0 + (int)rank * 128 + quarter * 32 + r;
+            if (row < p.wide && col < p.hidden)
+              *reinterpret_cast<int4 *>(p.out + ((int64_t)t.e * p.wide + row) * p.hidden + col) =
+                  *reinterpret_cast<const int4 *>(stage_buf + r * kPitch + part * 16);
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.acc_empty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  }
+  if (!ok) {
+    // A wait gave up (it never should): what this CTA started lands well
+    // within the time waited here, then everything is given back.
+    set_error(p.error_word, EP_ERRBIT_TIMEOUT);
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_free_pair(tmem, kTmemCols);
   }
 }
 
-// The gradient of silu(g) * u for the rows of the layout.
-__global__ void __launch_bounds__(kThreads) gate_backward_kernel(BackwardParams q) {
-  const ProductBackwardArgs &p = q.a;
+// The gradient of silu(g) * u for the rows of the layout, kept in bf16 as the
+// preactivations are: it is an operand of two products on the tensor cores.
+struct GateParams {
+  const uint16_t *grad, *preact;
+  uint16_t *out;
+  const int32_t *rows, *offset;
+  int cap, width;
+};
+
+__global__ void __launch_bounds__(256) gate_backward_kernel(GateParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int e = blockIdx.y;
-  const Segment s = segment(p.expert_offset, p.num_rows_per_expert, e, p.recv_capacity);
-  const int64_t n = (int64_t)s.rows * p.width;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = s.first + i / p.width;
-    const int col = (int)(i % p.width);
-    const float g = bf16_at(p.preact + row * 2 * p.width + col);
-    const float u = bf16_at(p.preact + row * 2 * p.width + p.width + col);
-    const float d = bf16_at(p.grad + row * p.width + col);
-    const float sig = 1.0f / (1.0f + expf(-g));
-    p.grad_preact[row * 2 * p.width + col] = to_bf16(d * u * sig * (1.0f + g * (1.0f - sig)));
-    p.grad_preact[row * 2 * p.width + p.width + col] = to_bf16(d * g * sig);
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) product_grad_x_kernel(BackwardParams q) {
-  const ProductBackwardArgs &p = q.a;
-  __shared__ float sa[kStep][kTile], sb[kStep][kTile];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int e = blockIdx.z, h0 = blockIdx.y * kTile, H = p.hidden;
-  const Segment s = segment(p.expert_offset, p.num_rows_per_expert, e, p.recv_capacity);
-  const int wide = p.gated ? 2 * p.width : p.width;
-  const uint16_t *g = p.gated ? p.grad_preact : p.grad;
-  const uint16_t *w = p.w + (int64_t)e * wide * H;
-  for (int m0 = blockIdx.x * kTile; m0 < s.rows; m0 += gridDim.x * kTile) {
-    float c[4][4] = {};
-    tile_product(c, wide, [&](int r, int k) {
-      return m0 + r < s.rows ? bf16_at(g + (int64_t)(s.first + m0 + r) * wide + k) : 0.0f;
-    }, [&](int r, int k) { return h0 + r < H ? bf16_at(w + (int64_t)k * H + h0 + r) : 0.0f; }, sa, sb);
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + 4 * (threadIdx.x >> 4) + i, h = h0 + 4 * (threadIdx.x & 15) + j;
-        if (m < s.rows && h < H) p.grad_x[(int64_t)(s.first + m) * H + h] = to_bf16(c[i][j]);
-      }
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) product_grad_w_kernel(BackwardParams q) {
-  const ProductBackwardArgs &p = q.a;
-  __shared__ float sa[kStep][kTile], sb[kStep][kTile];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int e = blockIdx.z, n0 = blockIdx.x * kTile, h0 = blockIdx.y * kTile, H = p.hidden;
-  const Segment s = segment(p.expert_offset, p.num_rows_per_expert, e, p.recv_capacity);
-  const int wide = p.gated ? 2 * p.width : p.width;
-  const uint16_t *g = p.gated ? p.grad_preact : p.grad;
-  float c[4][4] = {};
-  tile_product(c, s.rows, [&](int r, int k) {
-    return n0 + r < wide ? bf16_at(g + (int64_t)(s.first + k) * wide + n0 + r) : 0.0f;
-  }, [&](int r, int k) { return h0 + r < H ? bf16_at(p.x + (int64_t)(s.first + k) * H + h0 + r) : 0.0f; }, sa, sb);
-  for (int i = 0; i < 4; ++i)
+  const int first = p.offset[e];
+  const int rows = first < 0 || first >= p.cap ? 0 : max(0, min(p.rows[e], p.cap - first));
+  const int groups = p.width / 8;
+  const int64_t n = (int64_t)rows * groups;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = first + i / groups;
+    const int col = (int)(i % groups) * 8;
+    const int4 g4 = ld_stream_v4(p.preact + row * 2 * p.width + col);
+    const int4 u4 = ld_stream_v4(p.preact + row * 2 * p.width + p.width + col);
+    const int4 d4 = ld_stream_v4(p.grad + row * p.width + col);
+    const uint32_t *gw = reinterpret_cast<const uint32_t *>(&g4), *uw = reinterpret_cast<const uint32_t *>(&u4);
+    const uint32_t *dw = reinterpret_cast<const uint32_t *>(&d4);
+    uint32_t og[4], ou[4];
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 4 * (threadIdx.x >> 4) + i, h = h0 + 4 * (threadIdx.x & 15) + j;
-      if (n < wide && h < H) p.grad_w[((int64_t)e * wide + n) * H + h] = to_bf16(c[i][j]);
+      float a[2], b[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float g = h ? bf16_hi(gw[j]) : bf16_lo(gw[j]);
+        const float u = h ? bf16_hi(uw[j]) : bf16_lo(uw[j]);
+        const float d = h ? bf16_hi(dw[j]) : bf16_lo(dw[j]);
+        const float sig = 1.0f / (1.0f + __expf(-g));
+        a[h] = d * u * sig * (1.0f + g * (1.0f - sig));
+        b[h] = d * g * sig;
+      }
+      og[j] = pack_bf16x2(a[0], a[1]);
+      ou[j] = pack_bf16x2(b[0], b[1]);
     }
+    *reinterpret_cast<uint4 *>(p.out + row * 2 * p.width + col) = make_uint4(og[0], og[1], og[2], og[3]);
+    *reinterpret_cast<uint4 *>(p.out + row * 2 * p.width + p.width + col) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+  }
 }
 
-int tiles(int n) { return (n + kTile - 1) / kTile; }
+// Pairs of CTAs that fit the device at once.
+template <Form F>
+ep_status_t most_pairs(const DeviceInfo *di, size_t smem, int *pairs) {
+  static std::atomic<int> known[64];  // per device; the same for every call
+  if (known[di->device] == 0) {
+    cudaError_t e = cudaFuncSetAttribute(product_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(di->num_sms / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, product_kernel<F>, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+    known[di->device] = n > 0 ? n : 1;
+  }
+  *pairs = known[di->device];
+  return EP_OK;
+}
 
-template <typename P>
-ep_status_t launch3(void (*kernel)(P), dim3 grid, const P &p, cudaStream_t stream, const char *what) {
-  if (grid.x == 0 || grid.y == 0 || grid.z == 0) return EP_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = kUsePdl ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-  return e == cudaSuccess ? EP_OK : cuda_fail(e, what);
+int up(int a, int b) { return (a + b - 1) / b; }
+
+template <Form F>
+ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream_t stream) {
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
+  // The ring takes what is left of shared memory: a stage holds 128 rows of A
+  // and half of the most columns that a tile can have.
+  const int cols = F == kGradW || most_rows > kMaxCols ? kMaxCols : up(most_rows, 32) * 32;
+  p.b_bytes = cols / 2 * 128;
+  const int fixed = 1024 + kResultWarps * kStagingBytes + (F == kGated ? kResultWarps * kExchangeBytes : 0);
+  const int limit = (int)di->max_smem_per_block_optin - (int)sizeof(Barriers) - 1024;
+  p.stages = (limit - fixed) / (kABytes + p.b_bytes);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const size_t smem = (size_t)limit;
+  int pairs = 0;
+  ep_status_t s = most_pairs<F>(di, smem, &pairs);
+  if (s != EP_OK) return s;
+  if (most_tiles < pairs) pairs = (int)most_tiles;
+  const cudaError_t e = launch_kernel(product_kernel<F>, 2 * pairs, kThreads, smem, stream, false, p);
+  return e == cudaSuccess ? EP_OK : cuda_fail(e, "product launch");
+}
+
+ep_status_t row_maps(Params &p, const void *rows, int length, int cap) {
+  ep_status_t s = encode_map(&p.b, rows, length, cap, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (s == EP_OK) s = encode_map(&p.b16, rows, length, cap, 0, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B);
+  return s;
 }
 
 }  // namespace
 
 ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
-  if (current_device_info() == nullptr) return EP_ERR_CUDA;
   const int most = a.num_tokens < a.recv_capacity ? a.num_tokens : a.recv_capacity;  // rows of one expert
-  return launch3(product_kernel, dim3(tiles(most), tiles(a.width), a.num_experts), Params{a}, stream, "product launch");
+  if (most == 0) return EP_OK;
+  Params p = {};
+  p.rows = a.num_rows_per_expert;
+  p.offset = a.expert_offset;
+  p.error_word = a.error_word;
+  p.E = a.num_experts;
+  p.cap = a.recv_capacity;
+  p.width = a.width;
+  p.wide = a.gated ? 2 * a.width : a.width;
+  p.inner = a.hidden;
+  p.a_tiles = up(a.width, a.gated ? 128 : 256);
+  p.out = a.out;
+  p.preact = a.preact;
+  ep_status_t s = encode_map(&p.a, a.w, a.hidden, p.wide, a.num_experts, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (s == EP_OK) s = row_maps(p, a.x, a.hidden, a.recv_capacity);
+  if (s != EP_OK) return s;
+  const int64_t tiles = ((int64_t)a.recv_capacity / kMaxCols + a.num_experts) * p.a_tiles;
+  return a.gated ? launch_form<kGated>(p, most, tiles, stream) : launch_form<kPlain>(p, most, tiles, stream);
 }
 
 ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t stream) {
-  const DeviceInfo *di = current_device_info();
-  if (di == nullptr) return EP_ERR_CUDA;
   const int most = a.num_tokens < a.recv_capacity ? a.num_tokens : a.recv_capacity;
   const int wide = a.gated ? 2 * a.width : a.width;
-  const BackwardParams p{a};
-  ep_status_t s = EP_OK;
-  if (a.gated) {
-    s = launch3(gate_backward_kernel, dim3(most > 0 ? 64 : 0, a.num_experts), p, stream, "gate_backward launch");
+  const uint16_t *g = a.gated ? a.grad_preact : a.grad;
+  Params p = {};
+  p.rows = a.num_rows_per_expert;
+  p.offset = a.expert_offset;
+  p.error_word = a.error_word;
+  p.E = a.num_experts;
+  p.cap = a.recv_capacity;
+  p.wide = wide;
+  p.hidden = a.hidden;
+  if (a.gated && most > 0) {
+    const GateParams q{a.grad, a.preact, a.grad_preact, p.rows, p.offset, a.recv_capacity, a.width};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(32, a.num_experts);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = kUsePdl ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gate_backward_kernel, q);
+    if (e != cudaSuccess) return cuda_fail(e, "gate_backward launch");
+  }
+  if (a.grad_x != nullptr && most > 0) {
+    p.inner = wide;
+    p.width = a.hidden;
+    p.a_tiles = up(a.hidden, 256);
+    p.out = a.grad_x;
+    ep_status_t s = encode_map(&p.a, a.w, a.hidden, wide, a.num_experts, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (s == EP_OK) s = row_maps(p, g, wide, a.recv_capacity);
+    if (s == EP_OK)
+      s = launch_form<kGradX>(p, most, ((int64_t)a.recv_capacity / kMaxCols + a.num_experts) * p.a_tiles, stream);
     if (s != EP_OK) return s;
   }
-  if (a.grad_x != nullptr) {
-    s = launch3(product_grad_x_kernel, dim3(tiles(most), tiles(a.hidden), a.num_experts), p, stream,
-                "product_grad_x launch");
+  if (a.grad_w != nullptr) {
+    p.a_tiles = up(wide, 256);
+    p.b_tiles = up(a.hidden, 256);
+    p.out = a.grad_w;
+    // without rows nothing is copied: the maps only need an address
+    const int cap = most > 0 ? a.recv_capacity : 1;
+    ep_status_t s = encode_map(&p.a, most > 0 ? g : a.grad_w, wide, cap, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (s == EP_OK) s = row_maps(p, most > 0 ? a.x : a.grad_w, a.hidden, cap);
+    if (s == EP_OK)
+      s = launch_form<kGradW>(p, most, (int64_t)a.num_experts * p.a_tiles * p.b_tiles, stream);
     if (s != EP_OK) return s;
   }
-  if (a.grad_w != nullptr)
-    s = launch3(product_grad_w_kernel, dim3(tiles(wide), tiles(a.hidden), a.num_experts), p, stream,
-                "product_grad_w launch");
-  return s;
+  return EP_OK;
 }
 
 }  // namespace ep
