@@ -58,7 +58,8 @@ struct alignas(64) Params {
 };
 
 struct Barriers {
-  uint64_t full[kMaxStages], empty[kMaxStages], ends[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t ends[kMaxStages], trimmed[kMaxStages];  // kGradW: the last step of an expert
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
 };
@@ -189,9 +190,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s_bar.full[i], 2);  // one arrival from each CTA
+      mbar_init(&s_bar.full[i], 1);
       mbar_init(&s_bar.empty[i], 1);
       mbar_init(&s_bar.ends[i], 1);
+      mbar_init(&s_bar.trimmed[i], 2);  // one arrival from each CTA
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_bar.acc_full[i], 1);
@@ -223,22 +225,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       const bool ragged = F == kGradW && t.count % 16 != 0;  // the last step passes by the row ends
       if (lane == 0) {
         for (int k = 0; k < t.steps; ++k) {
-          if (!mbar_wait_cluster(&s_bar.empty[stage], phase ^ 1)) {
+          if (!mbar_wait_pair(&s_bar.empty[stage], phase ^ 1)) {
             ok = false;
             break;
           }
           const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
           const bool last = ragged && k == t.steps - 1;
-          const uint32_t full = map_shared(smem_addr(&s_bar.full[stage]), 0);
-          uint32_t bar = full;
+          // both CTAs' copies complete on the leading CTA's barrier
+          uint32_t bar = map_shared(smem_addr(&s_bar.full[stage]), 0);
           const uint32_t bytes = kABytes + b_rows * 128;
           if (last) {
             mbar_arrive_expect_tx(&s_bar.ends[stage], bytes);
             bar = map_shared(smem_addr(&s_bar.ends[stage]), rank);
+            if (rank == 0) mbar_arrive(&s_bar.full[stage]);
           } else if (rank == 0) {
             mbar_arrive_expect_tx(&s_bar.full[stage], 2 * bytes);
-          } else {
-            mbar_arrive_cluster(full);
           }
           const int at = k * kInner;
           if (F == kPlain) {
@@ -273,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     }
     // the products' last arrivals on this CTA's barriers come before it ends
     for (int i = 0; ok && lane == 0 && i < p.stages; ++i) {
-      ok = mbar_wait_cluster(&s_bar.empty[stage], phase ^ 1);
+      ok = mbar_wait_pair(&s_bar.empty[stage], phase ^ 1);
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
@@ -284,18 +285,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     Walker<F> walk(p);
     Tile t;
     int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    uint32_t phase = 0, acc_phase = 0, trims = 0;
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       if (t.steps == 0) continue;  // an expert without rows (kGradW): zeros are written
       if (lane == 0) {
         const uint32_t idesc = mma_desc(t.cols, F == kGradX || F == kGradW, F == kGradW);
         const uint32_t d = tmem + acc * kMaxCols;
-        ok = mbar_wait_cluster(&s_bar.acc_empty[acc], acc_phase ^ 1);
+        ok = mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1);
         tc_fence_after();
         for (int k = 0; ok && k < t.steps; ++k) {
-          if (!mbar_wait_cluster(&s_bar.full[stage], phase)) {
+          if (!mbar_wait_pair(&s_bar.full[stage], phase)) {
             ok = false;
             break;
+          }
+          if (F == kGradW && k == t.steps - 1 && t.count % 16 != 0) {
+            if (!mbar_wait_cluster(&s_bar.trimmed[stage], (trims >> stage) & 1u)) {
+              ok = false;
+              break;
+            }
+            trims ^= 1u << stage;
           }
           tc_fence_after();
           const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
@@ -332,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       stage = (stage + t.steps) % p.stages;
       if (t.count % 16 == 0) continue;
       const int s = (stage + p.stages - 1) % p.stages;
-      ok = mbar_wait_bounded(&s_bar.ends[s], (parities >> s) & 1u);
+      ok = mbar_wait_pair(&s_bar.ends[s], (parities >> s) & 1u);
       if (!ok) break;
       parities ^= 1u << s;
       char *a = ring + (size_t)s * stage_bytes;
@@ -344,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.full[s]), 0));
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.trimmed[s]), 0));
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- results
@@ -366,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 make_int4(0, 0, 0, 0);
         continue;
       }
-      ok = mbar_wait_cluster(&s_bar.acc_full[acc], acc_phase);
+      ok = mbar_wait_pair(&s_bar.acc_full[acc], acc_phase);
       ok = F == kGated ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -505,6 +513,12 @@ ep_status_t most_pairs(const DeviceInfo *di, size_t smem, int *pairs) {
     cfg.gridDim = dim3(di->num_sms / 2 * 2);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, product_kernel<F>, &cfg);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");

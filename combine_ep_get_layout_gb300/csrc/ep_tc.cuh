@@ -48,14 +48,28 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
   return done != 0;
 }
 
-// As mbar_wait_bounded, for barriers that the other CTA of a pair arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_cluster(bar, parity)) {
-    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+// As mbar_wait_bounded, but the timer (slow to read, where these waits are
+// taken once a step) is looked at after every 1024th try only.  kCluster:
+// what the other CTA of a pair wrote before it arrived is visible after.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_wait_tries(uint64_t *bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++i) {
+    if (i % 1024 == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) return false;
+    }
   }
   return true;
+}
+
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t *bar, uint32_t parity) {
+  return mbar_wait_tries<false>(bar, parity);
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+  return mbar_wait_tries<true>(bar, parity);
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
