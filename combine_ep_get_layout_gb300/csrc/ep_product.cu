@@ -31,19 +31,26 @@ namespace {
 
 enum Form { kPlain, kGated, kGradX, kGradW };
 
-constexpr int kThreads = 384;        // warps: 0 copies, 1 products, 2 row ends, 4-11 results
+constexpr int kThreads = 384;        // warps: 0 and 3 copies of A and B, 1 products, 2 row ends, 4-11 results
 constexpr int kInner = 64;           // elements of an inner step
 constexpr int kABytes = 128 * 128;   // a CTA's half of A for one step
 constexpr int kMaxCols = 256;        // columns of a tile
 constexpr int kTmemCols = 512;       // two tiles: one computed, one read out
 constexpr int kMaxStages = 12;
+constexpr int kBoxes = kMaxCols / 2 / 16;  // heights of a half of B
 constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
 constexpr int kStagingBytes = 32 * kPitch;       // a result warp's 32 rows
 constexpr int kExchangeBytes = 16 * 32 * 4;      // kGated: 16 columns of a warp, fp32
 constexpr int kResultWarps = 8;
 
-struct alignas(64) Params {
-  CUtensorMap a, b, b16;  // boxes of 64 x 64; b16: 64 x 16 (rows of x or g)
+struct Params {
+  // One copy a step and operand (a copy costs its issuing thread about 200
+  // cycles, so their number bounds a step of 512): A's 128 rows (kGated: 64
+  // of the gate and the 64 that they multiply), and a half of B of any
+  // height, b[i] of 16 (i + 1) rows.  Transposed operands are blocks of 64
+  // outer elements; b[0] is kGradW's, of two.
+  CUtensorMap a, b[kBoxes];
+  bool a_blocks, b_blocks;  // both blocks in one copy (their length is a multiple of 64), else in two
   const int32_t *rows, *offset;
   uint32_t *error_word;
   int E, cap;
@@ -124,7 +131,7 @@ struct Walker {
       t.a0 = at / p.b_tiles * 256;
       t.b0 = at % p.b_tiles * 256;
       t.count = n;
-      t.cols = p.hidden - t.b0 > 128 ? 256 : 128;
+      t.cols = kMaxCols;
       t.steps = ceil_div(n, kInner);
     } else {
       // as few tiles as hold the rows, of about equal size
@@ -201,8 +208,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     }
     fence_barrier_init();
     prefetch_map(&p.a);
-    prefetch_map(&p.b);
-    prefetch_map(&p.b16);
   }
   __syncwarp();
   if (warp == 2) tmem_alloc_pair(&s_bar.tmem, kTmemCols);
@@ -214,15 +219,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
   griddep_launch_dependents();
 
   bool ok = true;  // false: a wait gave up
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ copies
+    const bool is_a = warp == 0;
     Walker<F> walk(p);
     Tile t;
     int stage = 0;
     uint32_t phase = 0;
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       const int b_rows = t.cols / 2;
-      const bool ragged = F == kGradW && t.count % 16 != 0;  // the last step passes by the row ends
+      const uint32_t bytes = kABytes + b_rows * 128;
+      const int a0 = t.a0 + (int)rank * (F == kGated ? 64 : 128);
+      const int b0 = (F == kGradW ? t.b0 : t.first) + (int)rank * b_rows;
       if (lane == 0) {
         for (int k = 0; k < t.steps; ++k) {
           if (!mbar_wait_pair(&s_bar.empty[stage], phase ^ 1)) {
@@ -230,39 +238,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             break;
           }
           const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
-          const bool last = ragged && k == t.steps - 1;
-          // both CTAs' copies complete on the leading CTA's barrier
-          uint32_t bar = map_shared(smem_addr(&s_bar.full[stage]), 0);
-          const uint32_t bytes = kABytes + b_rows * 128;
-          if (last) {
-            mbar_arrive_expect_tx(&s_bar.ends[stage], bytes);
-            bar = map_shared(smem_addr(&s_bar.ends[stage]), rank);
-            if (rank == 0) mbar_arrive(&s_bar.full[stage]);
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(&s_bar.full[stage], 2 * bytes);
+          // both CTAs' copies complete on the leading CTA's barrier, but those
+          // of a last step whose rows end raggedly go by the row ends
+          const bool last = F == kGradW && t.count % 16 != 0 && k == t.steps - 1;
+          const uint32_t bar = last ? map_shared(smem_addr(&s_bar.ends[stage]), rank)
+                                    : map_shared(smem_addr(&s_bar.full[stage]), 0);
+          if (is_a) {
+            if (last) mbar_arrive_expect_tx(&s_bar.ends[stage], bytes);
+            if (rank == 0) {
+              if (last)
+                mbar_arrive(&s_bar.full[stage]);
+              else
+                mbar_arrive_expect_tx(&s_bar.full[stage], 2 * bytes);
+            }
           }
           const int at = k * kInner;
-          if (F == kPlain) {
-            tile_load_3d(a, &p.a, at, t.a0 + (int)rank * 128, t.e, bar);
-            tile_load_3d(a + 8192, &p.a, at, t.a0 + (int)rank * 128 + 64, t.e, bar);
-          } else if (F == kGated) {  // 64 rows of the gate and the 64 that they multiply
-            tile_load_3d(a, &p.a, at, t.a0 + (int)rank * 64, t.e, bar);
-            tile_load_3d(a + 8192, &p.a, at, p.width + t.a0 + (int)rank * 64, t.e, bar);
-          } else if (F == kGradX) {
-            tile_load_3d(a, &p.a, t.a0 + (int)rank * 128, at, t.e, bar);
-            tile_load_3d(a + 8192, &p.a, t.a0 + (int)rank * 128 + 64, at, t.e, bar);
+          if (is_a) {
+            if (F == kPlain) {
+              tile_load_3d(a, &p.a, at, a0, t.e, bar);
+            } else if (F == kGated) {
+              tile_load_4d(a, &p.a, at, a0, 0, t.e, bar);
+            } else if (F == kGradX) {
+              if (p.a_blocks) {
+                tile_load_4d(a, &p.a, 0, at, a0 / 64, t.e, bar);
+              } else {
+                tile_load_3d(a, &p.a, a0, at, t.e, bar);
+                tile_load_3d(a + 8192, &p.a, a0 + 64, at, t.e, bar);
+              }
+            } else if (p.a_blocks) {
+              tile_load_3d(a, &p.a, 0, t.first + at, a0 / 64, bar);
+            } else {
+              tile_load_2d(a, &p.a, a0, t.first + at, bar);
+              tile_load_2d(a + 8192, &p.a, a0 + 64, t.first + at, bar);
+            }
+          } else if (F != kGradW) {
+            tile_load_2d(b, &p.b[b_rows / 16 - 1], at, b0, bar);
+          } else if (p.b_blocks) {
+            tile_load_3d(b, &p.b[0], 0, t.first + at, b0 / 64, bar);
           } else {
-            tile_load_2d(a, &p.a, t.a0 + (int)rank * 128, t.first + at, bar);
-            tile_load_2d(a + 8192, &p.a, t.a0 + (int)rank * 128 + 64, t.first + at, bar);
-          }
-          if (F == kGradW) {
-            for (int c = 0; c < b_rows; c += 64)
-              tile_load_2d(b + c * 128, &p.b, t.b0 + (int)rank * b_rows + c, t.first + at, bar);
-          } else {
-            const int row = t.first + (int)rank * b_rows;
-            int c = 0;
-            for (; c + 64 <= b_rows; c += 64) tile_load_2d(b + c * 128, &p.b, at, row + c, bar);
-            for (; c < b_rows; c += 16) tile_load_2d(b + c * 128, &p.b16, at, row + c, bar);
+            tile_load_2d(b, &p.b[0], b0, t.first + at, bar);
+            tile_load_2d(b + 8192, &p.b[0], b0 + 64, t.first + at, bar);
           }
           if (++stage == p.stages) {
             stage = 0;
@@ -551,10 +566,56 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "product launch");
 }
 
-ep_status_t row_maps(Params &p, const void *rows, int length, int cap) {
-  ep_status_t s = encode_map(&p.b, rows, length, cap, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (s == EP_OK) s = encode_map(&p.b16, rows, length, cap, 0, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B);
-  return s;
+constexpr uint64_t kSize = 2;  // bytes of an element
+
+// Rows [rows][length] by halves of B of every height up to `most`.
+ep_status_t row_maps(Params &p, const void *rows, int length, int cap, int most) {
+  const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {length * kSize};
+  const int cols = most > kMaxCols ? kMaxCols : up(most, 32) * 32;
+  for (int i = 0; i < cols / 32; ++i) {
+    const uint32_t box[] = {kInner, 16u * (i + 1)};
+    const ep_status_t s = encode_map(&p.b[i], rows, 2, dims, strides, box);
+    if (s != EP_OK) return s;
+  }
+  return EP_OK;
+}
+
+// Rows [rows][length] read with the outer dimension contiguous: blocks of 64
+// of a row by 64 rows, two blocks a copy where the length allows it.
+ep_status_t block_map(CUtensorMap *map, bool *blocks, const void *rows, int length, int cap) {
+  *blocks = length % 64 == 0;
+  if (*blocks) {
+    const uint64_t dims[] = {64, (uint64_t)cap, (uint64_t)length / 64}, strides[] = {length * kSize, 64 * kSize};
+    const uint32_t box[] = {64, kInner, 2};
+    return encode_map(map, rows, 3, dims, strides, box);
+  }
+  const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {length * kSize};
+  const uint32_t box[] = {64, kInner};
+  return encode_map(map, rows, 2, dims, strides, box);
+}
+
+// The weights [E][wide][hidden] as A of a form.
+ep_status_t weight_map(Params &p, Form form, const void *w, int wide, int hidden) {
+  const uint64_t E = p.E, n = wide, h = hidden;
+  if (form == kPlain) {
+    const uint64_t dims[] = {h, n, E}, strides[] = {h * kSize, n * h * kSize};
+    const uint32_t box[] = {kInner, 128, 1};
+    return encode_map(&p.a, w, 3, dims, strides, box);
+  }
+  if (form == kGated) {
+    const uint64_t dims[] = {h, n / 2, 2, E}, strides[] = {h * kSize, n / 2 * h * kSize, n * h * kSize};
+    const uint32_t box[] = {kInner, 64, 2, 1};
+    return encode_map(&p.a, w, 4, dims, strides, box);
+  }
+  p.a_blocks = hidden % 64 == 0;
+  if (p.a_blocks) {
+    const uint64_t dims[] = {64, n, h / 64, E}, strides[] = {h * kSize, 64 * kSize, n * h * kSize};
+    const uint32_t box[] = {64, kInner, 2, 1};
+    return encode_map(&p.a, w, 4, dims, strides, box);
+  }
+  const uint64_t dims[] = {h, n, E}, strides[] = {h * kSize, n * h * kSize};
+  const uint32_t box[] = {64, kInner, 1};
+  return encode_map(&p.a, w, 3, dims, strides, box);
 }
 
 }  // namespace
@@ -574,8 +635,8 @@ ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
   p.a_tiles = up(a.width, a.gated ? 128 : 256);
   p.out = a.out;
   p.preact = a.preact;
-  ep_status_t s = encode_map(&p.a, a.w, a.hidden, p.wide, a.num_experts, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (s == EP_OK) s = row_maps(p, a.x, a.hidden, a.recv_capacity);
+  ep_status_t s = weight_map(p, a.gated ? kGated : kPlain, a.w, p.wide, a.hidden);
+  if (s == EP_OK) s = row_maps(p, a.x, a.hidden, a.recv_capacity, most);
   if (s != EP_OK) return s;
   const int64_t tiles = ((int64_t)a.recv_capacity / kMaxCols + a.num_experts) * p.a_tiles;
   return a.gated ? launch_form<kGated>(p, most, tiles, stream) : launch_form<kPlain>(p, most, tiles, stream);
@@ -612,8 +673,8 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     p.width = a.hidden;
     p.a_tiles = up(a.hidden, 256);
     p.out = a.grad_x;
-    ep_status_t s = encode_map(&p.a, a.w, a.hidden, wide, a.num_experts, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (s == EP_OK) s = row_maps(p, g, wide, a.recv_capacity);
+    ep_status_t s = weight_map(p, kGradX, a.w, wide, a.hidden);
+    if (s == EP_OK) s = row_maps(p, g, wide, a.recv_capacity, most);
     if (s == EP_OK)
       s = launch_form<kGradX>(p, most, ((int64_t)a.recv_capacity / kMaxCols + a.num_experts) * p.a_tiles, stream);
     if (s != EP_OK) return s;
@@ -624,8 +685,8 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     p.out = a.grad_w;
     // without rows nothing is copied: the maps only need an address
     const int cap = most > 0 ? a.recv_capacity : 1;
-    ep_status_t s = encode_map(&p.a, most > 0 ? g : a.grad_w, wide, cap, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (s == EP_OK) s = row_maps(p, most > 0 ? a.x : a.grad_w, a.hidden, cap);
+    ep_status_t s = block_map(&p.a, &p.a_blocks, most > 0 ? g : a.grad_w, wide, cap);
+    if (s == EP_OK) s = block_map(&p.b[0], &p.b_blocks, most > 0 ? a.x : a.grad_w, a.hidden, cap);
     if (s == EP_OK)
       s = launch_form<kGradW>(p, most, (int64_t)a.num_experts * p.a_tiles * p.b_tiles, stream);
     if (s != EP_OK) return s;

@@ -24,16 +24,17 @@ EncodeFn encoder() {
 
 }  // namespace
 
-ep_status_t encode_map(CUtensorMap *map, const void *base, uint64_t x, uint64_t y, uint64_t z, uint32_t box_x,
-                       uint32_t box_y, CUtensorMapSwizzle swizzle) {
+ep_status_t encode_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                       const uint32_t *box) {
   const EncodeFn fn = encoder();
   if (fn == nullptr) return fail(EP_ERR_CUDA, "cuTensorMapEncodeTiled not found");
-  const cuuint64_t dims[3] = {x, y, z};
-  const cuuint64_t strides[2] = {x * 2, x * y * 2};
-  const cuuint32_t box[3] = {box_x, box_y, 1}, steps[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, z == 0 ? 2 : 3, const_cast<void *>(base), dims, strides,
-                        box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  cuuint64_t d[5], st[4];
+  const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) d[i] = dims[i];
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, box, steps,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(EP_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
   return EP_OK;
 }

@@ -95,6 +95,15 @@ __device__ __forceinline__ void tile_load_3d(uint32_t dst, const CUtensorMap *ma
       : "memory");
 }
 
+__device__ __forceinline__ void tile_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // ------------------------------------------------------------------ tcgen05
 
 // Tensor memory for the pair (a whole warp of each CTA calls it); the column
@@ -167,9 +176,9 @@ __host__ __device__ constexpr uint32_t mma_desc(int n, bool a_outer, bool b_oute
 
 // --------------------------------------------------------------------- host
 
-// A tensor map of bf16 [z][y][x] (z = 0: two-dimensional), boxes of
-// 64 x box_y elements, 128-byte swizzle.  x must be a multiple of 8.
-ep_status_t encode_map(CUtensorMap *map, const void *base, uint64_t x, uint64_t y, uint64_t z, uint32_t box_x,
-                       uint32_t box_y, CUtensorMapSwizzle swizzle);
+// A tensor map of bf16 elements, innermost dimension first (contiguous; the
+// others' strides in bytes, multiples of 16), with the 128-byte swizzle.
+ep_status_t encode_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                       const uint32_t *box);
 
 }  // namespace ep
