@@ -191,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
   const int stage_bytes = kABytes + p.b_bytes;
   char *staging = ring + (size_t)p.stages * stage_bytes;
   char *exchange = staging + kResultWarps * kStagingBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -231,12 +231,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       const uint32_t bytes = kABytes + b_rows * 128;
       const int a0 = t.a0 + (int)rank * (F == kGated ? 64 : 128);
       const int b0 = (F == kGradW ? t.b0 : t.first) + (int)rank * b_rows;
-      if (lane == 0) {
-        for (int k = 0; k < t.steps; ++k) {
-          if (!mbar_wait_pair(&s_bar.empty[stage], phase ^ 1)) {
-            ok = false;
-            break;
-          }
+      for (int k = 0; k < t.steps; ++k) {
+        if (!__all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1))) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
           // both CTAs' copies complete on the leading CTA's barrier, but those
           // of a last step whose rows end raggedly go by the row ends
@@ -279,17 +279,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             tile_load_2d(b, &p.b[0], b0, t.first + at, bar);
             tile_load_2d(b + 8192, &p.b[0], b0 + 64, t.first + at, bar);
           }
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     // the products' last arrivals on this CTA's barriers come before it ends
-    for (int i = 0; ok && lane == 0 && i < p.stages; ++i) {
-      ok = mbar_wait_pair(&s_bar.empty[stage], phase ^ 1);
+    for (int i = 0; ok && i < p.stages; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1));
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
@@ -301,45 +301,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     Tile t;
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0, trims = 0;
+    const uint32_t ring_addr = smem_addr(ring);
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       if (t.steps == 0) continue;  // an expert without rows (kGradW): zeros are written
-      if (lane == 0) {
-        const uint32_t idesc = mma_desc(t.cols, F == kGradX || F == kGradW, F == kGradW);
-        const uint32_t d = tmem + acc * kMaxCols;
-        ok = mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1);
-        tc_fence_after();
-        for (int k = 0; ok && k < t.steps; ++k) {
-          if (!mbar_wait_pair(&s_bar.full[stage], phase)) {
-            ok = false;
-            break;
-          }
-          if (F == kGradW && k == t.steps - 1 && t.count % 16 != 0) {
-            if (!mbar_wait_cluster(&s_bar.trimmed[stage], (trims >> stage) & 1u)) {
-              ok = false;
-              break;
-            }
-            trims ^= 1u << stage;
-          }
-          tc_fence_after();
-          const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
-          const int parts = F == kGradW ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j < parts) {
-              const uint64_t da = F == kGradX || F == kGradW ? outer_desc(a + j * 2048, 8192) : inner_desc(a + j * 32);
-              const uint64_t db = F == kGradW ? outer_desc(b + j * 2048, 8192) : inner_desc(b + j * 32);
-              mma_pair(d, da, db, idesc, k > 0 || j > 0);
-            }
-          }
-          commit_pair(&s_bar.empty[stage]);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+      const uint32_t idesc = mma_desc(t.cols, F == kGradX || F == kGradW, F == kGradW);
+      const uint32_t d = tmem + acc * kMaxCols;
+      ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1));
+      tc_fence_after();
+      for (int k = 0; ok && k < t.steps; ++k) {
+        ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
+        if (F == kGradW && ok && k == t.steps - 1 && t.count % 16 != 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&s_bar.trimmed[stage], (trims >> stage) & 1u));
+          trims ^= 1u << stage;
         }
-        if (ok) commit_pair(&s_bar.acc_full[acc]);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t addr = ring_addr + (uint32_t)(stage * stage_bytes);
+        const uint32_t a = F == kGradX || F == kGradW ? outer_desc(addr, 8192) : inner_desc(addr);
+        const uint32_t b = F == kGradW ? outer_desc(addr + kABytes, 8192) : inner_desc(addr + kABytes);
+        const int parts = F == kGradW ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < parts)
+              mma_pair(d, a + j * ((F == kGradX || F == kGradW ? 2048 : 32) >> 4), b + j * ((F == kGradW ? 2048 : 32) >> 4),
+                       idesc, k > 0 || j > 0);
+          commit_pair(&s_bar.empty[stage]);
+          if (k == t.steps - 1) commit_pair(&s_bar.acc_full[acc]);
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }

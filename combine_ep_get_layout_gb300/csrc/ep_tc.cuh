@@ -121,12 +121,26 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t columns) 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// d (+)= a b^T over 16 elements of the inner dimension, bf16 in, fp32 sums.
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One thread of a converged warp.  The loops that issue copies and products
+// run on the whole warp, so what they compute stays in uniform registers, and
+// only the instruction itself is left to this thread.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// d (+)= a b^T over 16 elements of the inner dimension, bf16 in, fp32 sums.
+// The operands' descriptors as a low word (address, block distance) and the
+// high word they share.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(0x40004040)
       : "memory");
 }
 
@@ -154,18 +168,13 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory operand in the 128-byte swizzle, inner dimension contiguous:
-// rows of 128 bytes, groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t inner_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// The same swizzle with the outer dimension contiguous: blocks of 64 outer
-// elements (128 bytes), `block` bytes apart, each one row per inner element.
-__device__ __forceinline__ uint64_t outer_desc(uint32_t addr, uint32_t block) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(block >> 4) << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
-}
+// Low words of operand descriptors, 128-byte swizzle (high word: groups of 8
+// rows 1024 bytes apart, version, swizzle).  inner_desc: inner dimension
+// contiguous, rows of 128 bytes.  outer_desc: outer dimension contiguous,
+// blocks of 64 outer elements (128 bytes), `block` bytes apart, each one row
+// per inner element.
+__device__ __forceinline__ uint32_t inner_desc(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t outer_desc(uint32_t addr, uint32_t block) { return (addr >> 4) | ((block >> 4) << 16); }
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 256 over the pair, N
 // columns; bit 15 / 16: A / B with the outer dimension contiguous.
