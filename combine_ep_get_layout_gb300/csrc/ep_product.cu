@@ -375,6 +375,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     int acc = 0;
     uint32_t acc_phase = 0;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const auto release = [&](int a) {  // this warp has read its columns of accumulator a
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.acc_empty[a]), 0));
+    };
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       if (F == kGradW && t.steps == 0) {
         const int row = t.a0 + (int)rank * 128 + quarter * 32 + lane;
@@ -391,6 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       for (int c = half * 32; c < t.cols; c += 64) {
         float v[32];
         tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+        if (c + 64 >= t.cols) release(acc);
         const int left = t.count - c;  // rows of this chunk (not kGradW)
         if (F == kPlain || F == kGradX) {
           const int at = t.a0 + (int)rank * 128 + quarter * 32;
@@ -443,9 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
           __syncwarp();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.acc_empty[acc]), 0));
+      if (t.cols <= half * 32) release(acc);  // no columns for this warp
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
