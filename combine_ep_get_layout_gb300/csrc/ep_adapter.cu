@@ -3,113 +3,380 @@
 //   y[t] = x[t] w^T + scale[a] (x[t] A_a^T) B_a^T,    a = adapter_idx[t]
 //
 // (no second term where a = -1).  bf16 in and out, sums in fp32.
-#include "ep_device.cuh"
-#include "ep_ops.h"
+//
+// Two kernels.  adapter_low_kernel computes low[t] = scale[a] x[t] A_a^T for
+// a tile of rows: the down-projections of the adapters that the tile names are
+// stacked, 128 rows of them at a time, and multiplied with all its rows on the
+// tensor cores; of every column only its own adapter's part is kept.  The
+// projection (ep_pair.cuh, kAdapter) then takes an adapter of the tile as one
+// more inner step: B_a beside low[t], zero for the rows of other adapters, so
+// the second term is summed in tensor memory with the first.
+//
+// low is kept in bf16, as the tensor cores take it: 2^-8 of the low term, the
+// size of the result's own rounding.
+#include "ep_pair.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kLowThreads = 192;  // warps 0-3 copy A and read the results, 4 copies x, 5 issues the products
+constexpr int kLowStages = 4;
+constexpr int kAhead = 2;         // steps of A in flight while one is handed over
+constexpr int kMaxSplits = 8;     // CTAs of a cluster
 
-struct Params {
-  AdapterArgs a;
+struct LowParams {
+  CUtensorMap x;  // boxes of 64 x cols
+  const uint16_t *a;
+  const int64_t *index;
+  const float *scale;
+  uint32_t *error_word;
+  int T, hidden, rank, adapters;
+  int cols;    // rows of a tile
+  int splits;  // of the inner dimension: the CTAs of a cluster
+  float *part;      // [splits][T][rank]
+  uint16_t *low;    // [T][rank]
+  int32_t *plan;    // [tiles][kPlanWords]
 };
 
-__device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+struct LowBarriers {
+  uint64_t full[kLowStages], empty[kLowStages];
+  uint64_t acc_full, acc_empty;
+  uint32_t tmem;
+};
 
-// low[t] = scale[a] x[t] A_a^T, fp32 [T, rank]: one block a row, one warp an output.
-__global__ void __launch_bounds__(kThreads) adapter_low_kernel(Params q) {
-  const AdapterArgs &p = q.a;
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_constant__ LowParams p) {
+  extern __shared__ char s_raw[];
+  __shared__ LowBarriers s_bar;
+  __shared__ int s_place[kMaxCols];  // of a row's adapter in the tile's list, or -1
+  __shared__ int s_list[kMaxCols];
+  __shared__ uint32_t s_first[kMaxCols / 32];
+  char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = kABytes + p.cols * 128;
+  int *s_table = reinterpret_cast<int *>(ring + kLowStages * stage_bytes);  // [adapters]: first row that names it
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int first = blockIdx.x * p.cols, rows = min(p.cols, p.T - first);
+  const int split = blockIdx.y;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kLowStages; ++i) {
+      mbar_init(&s_bar.full[i], 4 * 32 + 1);
+      mbar_init(&s_bar.empty[i], 1);
+    }
+    mbar_init(&s_bar.acc_full, 1);
+    mbar_init(&s_bar.acc_empty, 4);
+    fence_barrier_init();
+    prefetch_map(&p.x);
+  }
+  __syncwarp();
+  if (warp == 5) tmem_alloc_one(&s_bar.tmem, kMaxCols);
+  for (int i = threadIdx.x; i < p.adapters; i += kLowThreads) s_table[i] = kMaxCols;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_bar.tmem;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = blockIdx.x; t < p.num_rows; t += gridDim.x) {
-    const int64_t a = p.adapter_idx[t];
-    const bool none = a < 0 || a >= p.num_adapters;
-    if (none && a != -1 && threadIdx.x == 0) set_error(p.error_word, EP_ERRBIT_BAD_INDEX);
-    float *low = static_cast<float *>(p.workspace) + (int64_t)t * p.rank;
-    for (int r = warp; r < p.rank; r += kThreads / 32) {
-      float s = 0.0f;
-      if (!none) {
-        const uint16_t *row = p.lora_a + ((int64_t)a * p.rank + r) * p.hidden;
-        for (int k = lane; k < p.hidden; k += 32) s += bf16_at(p.x + (int64_t)t * p.hidden + k) * bf16_at(row + k);
+
+  // The tile's adapters in the order in which its rows name them.
+  for (int i = threadIdx.x; i < p.cols; i += kLowThreads) {
+    int a = -1;
+    if (i < rows) {
+      const int64_t v = p.index[first + i];
+      if (v >= 0 && v < p.adapters)
+        a = (int)v;
+      else if (v != -1)
+        set_error(p.error_word, EP_ERRBIT_BAD_INDEX);
+    }
+    s_place[i] = a;
+    if (a >= 0) atomicMin(&s_table[a], i);
+  }
+  __syncthreads();
+  for (int b = warp; b < kMaxCols / 32; b += kLowThreads / 32) {
+    const int i = b * 32 + lane;
+    const int a = i < p.cols ? s_place[i] : -1;
+    const uint32_t m = __ballot_sync(0xffffffffu, a >= 0 && s_table[a] == i);
+    if (lane == 0) s_first[b] = m;
+  }
+  __syncthreads();
+  int count = 0;
+  for (int b = 0; b < kMaxCols / 32; ++b) count += __popc(s_first[b]);
+  const auto place_of = [&](int i) {  // rows before i that name an adapter first
+    int n = __popc(s_first[i >> 5] & ((1u << (i & 31)) - 1u));
+    for (int b = 0; b < (i >> 5); ++b) n += __popc(s_first[b]);
+    return n;
+  };
+  for (int i = threadIdx.x; i < p.cols; i += kLowThreads) {
+    const int a = s_place[i];
+    if (a < 0) continue;
+    const int f = s_table[a], n = place_of(f);
+    if (f == i) s_list[n] = a;
+    s_place[i] = n;
+  }
+  __syncthreads();
+  if (split == 0 && blockIdx.z == 0) {
+    int32_t *plan = p.plan + (int64_t)blockIdx.x * kPlanWords;
+    if (threadIdx.x == 0) plan[0] = count;
+    for (int i = threadIdx.x; i < count; i += kLowThreads) plan[1 + i] = s_list[i];
+  }
+
+  const int per = 128 / p.rank;  // adapters of a stack
+  const int stacks = ceil_div(count, per);
+  const int all_steps = ceil_div(p.hidden, kInner);
+  const int k0 = all_steps * split / p.splits, k1 = all_steps * (split + 1) / p.splits;
+  bool ok = true;
+  int stage = 0;
+  uint32_t phase = 0, acc_phase = 0;
+  const auto advance = [&] {
+    if (++stage == kLowStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+  for (int s = blockIdx.z; s < stacks; s += gridDim.z) {
+    const int stacked = min(per, count - s * per);
+    if (warp < 4) {
+      // this warp's 32 rows of the stack, four at a time, eight lanes a row
+      const uint16_t *src[8];
+      uint32_t to[8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= p.adapter_scale == nullptr ? 1.0f : p.adapter_scale[a];
+      for (int i = 0; i < 8; ++i) {
+        const int r = warp * 32 + i * 4 + (lane >> 3), j = r / p.rank;
+        src[i] = j < stacked ? p.a + ((int64_t)s_list[s * per + j] * p.rank + (r - j * p.rank)) * p.hidden + (lane & 7) * 8
+                             : nullptr;
+        to[i] = r * 128 + (((lane & 7) ^ (r & 7)) << 4);
       }
-      if (lane == 0) low[r] = s;
+      int filled = 0;
+      int hand = stage;  // the stage handed over next
+      for (int k = k0; k < k1 + kAhead; ++k) {
+        if (k < k1) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1));
+          const uint32_t a = smem_addr(ring + stage * stage_bytes);
+          const int at = k * kInner;
+          const bool some = at + (lane & 7) * 8 < p.hidden;
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (src[i] != nullptr) copy16(a + to[i], some ? src[i] + at : src[i], some);
+          }
+          ++filled;
+          advance();
+        }
+        copy_commit();
+        if (k >= k0 + kAhead) {
+          copy_wait<kAhead>();
+          fence_proxy_async_smem();
+          mbar_arrive(&s_bar.full[hand]);
+          if (++hand == kLowStages) hand = 0;
+        }
+      }
+      copy_wait<0>();
+      // results: lane l holds row l of the stack, of adapter l / rank
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_full, acc_phase));
+      acc_phase ^= 1;
+      tc_fence_after();
+      if (ok) {
+        const int l = warp * 32 + lane, j = l / p.rank, i = l - j * p.rank;
+        const int mine = j < stacked ? s * per + j : -2;
+        for (int c = 0; c < p.cols; c += 32) {
+          float v[32];
+          tmem_load32(tmem + c + ((uint32_t)(warp * 32) << 16), v);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            if (c + q < p.cols && s_place[c + q] == mine) {
+              const int64_t at = (int64_t)(first + c + q) * p.rank + i;
+              if (p.splits == 1) {
+                const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + s_list[mine]);
+                p.low[at] = (uint16_t)(pack_bf16x2(v[q] * f, 0.0f) & 0xffffu);
+              } else {
+                p.part[(int64_t)split * p.T * p.rank + at] = v[q];
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_bar.acc_empty);
+    } else if (warp == 4) {
+      for (int k = k0; ok && k < k1; ++k) {
+        ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&s_bar.full[stage], p.cols * 128);
+          tile_load_one(smem_addr(ring + stage * stage_bytes) + kABytes, &p.x, k * kInner, first, &s_bar.full[stage]);
+        }
+        __syncwarp();
+        advance();
+      }
+    } else {
+      const uint32_t idesc = mma_desc_one(p.cols);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_empty, acc_phase ^ 1));
+      acc_phase ^= 1;
+      tc_fence_after();
+      for (int k = k0; ok && k < k1; ++k) {
+        ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = smem_addr(ring) + (uint32_t)(stage * stage_bytes);
+        const uint32_t a = inner_desc(at), b = inner_desc(at + kABytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_one(tmem, a + j * 2, b + j * 2, idesc, k > k0 || j > 0);
+          commit_one(&s_bar.empty[stage]);
+          if (k == k1 - 1) commit_one(&s_bar.acc_full);
+        }
+        __syncwarp();
+        advance();
+      }
     }
+    if (p.splits > 1) {
+      // the splits' parts are added in their order, each row by one CTA
+      cluster_sync();
+      for (int c = split; c < rows; c += p.splits) {
+        const int place = s_place[c];
+        if (place < s * per || place >= s * per + stacked) continue;
+        const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + s_list[place]);
+        for (int i = threadIdx.x; i < p.rank; i += kLowThreads) {
+          const int64_t at = (int64_t)(first + c) * p.rank + i;
+          float sum = 0.0f;
+          for (int q = 0; q < p.splits; ++q) sum += __ldcg(p.part + (int64_t)q * p.T * p.rank + at);
+          p.low[at] = (uint16_t)(pack_bf16x2(sum * f, 0.0f) & 0xffffu);
+        }
+      }
+    }
+  }
+  if (!ok) {  // a wait gave up: what was started lands well within the time waited here
+    set_error(p.error_word, EP_ERRBIT_TIMEOUT);
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_free_one(tmem, kMaxCols);
   }
 }
 
-constexpr int kTile = 64, kStep = 16;
+// How a call is cut: rows of a tile, tiles, splits of the low rows' inner
+// dimension.
+struct Cut {
+  int cols, tiles, splits;
+};
 
-__global__ void __launch_bounds__(kThreads) adapter_product_kernel(Params q) {
-  const AdapterArgs &p = q.a;
-  __shared__ float sa[kStep][kTile], sb[kStep][kTile];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int t0 = blockIdx.x * kTile, n0 = blockIdx.y * kTile;
-  float c[4][4] = {};
-  for (int k0 = 0; k0 < p.hidden; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-      const int r = i / kStep, k = k0 + i % kStep;
-      sa[i % kStep][r] = t0 + r < p.num_rows && k < p.hidden ? bf16_at(p.x + (int64_t)(t0 + r) * p.hidden + k) : 0.0f;
-      sb[i % kStep][r] = n0 + r < p.width && k < p.hidden ? bf16_at(p.w + (int64_t)(n0 + r) * p.hidden + k) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kStep; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] += sa[k][4 * ty + i] * sb[k][4 * tx + j];
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 4 * ty + i;
-    if (t >= p.num_rows) continue;
-    const int64_t a = p.adapter_idx[t];
-    const float *low = static_cast<const float *>(p.workspace) + (int64_t)t * p.rank;
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 4 * tx + j;
-      if (n >= p.width) continue;
-      float s = 0.0f;
-      if (a >= 0 && a < p.num_adapters)
-        for (int r = 0; r < p.rank; ++r) s += low[r] * bf16_at(p.lora_b + ((int64_t)a * p.width + n) * p.rank + r);
-      p.out[(int64_t)t * p.width + n] = (uint16_t)(pack_bf16x2(c[i][j] + s, 0.0f) & 0xffffu);
-    }
-  }
+Cut cut(int num_rows, int hidden) {
+  Cut c;
+  c.tiles = up(num_rows, kMaxCols);
+  c.cols = up(up(num_rows, c.tiles), 16) * 16;
+  const int steps = up(hidden, kInner);
+  c.splits = 128 / c.tiles;
+  if (c.splits > kMaxSplits) c.splits = kMaxSplits;
+  if (c.splits > steps) c.splits = steps;
+  if (c.splits < 1) c.splits = 1;
+  return c;
 }
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t adapter_workspace_bytes(int num_rows, int hidden, int rank) {
-  (void)hidden;
-  return ((size_t)num_rows * rank * 4 + 255) / 256 * 256;
+  if (num_rows == 0) return 0;
+  const Cut c = cut(num_rows, hidden);
+  return align256((size_t)c.tiles * kPlanWords * 4) + align256((size_t)num_rows * rank * 2) +
+         align256(c.splits > 1 ? (size_t)c.splits * num_rows * rank * 4 : 0);
 }
 
 ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   if (a.num_rows == 0) return EP_OK;
   const DeviceInfo *di = current_device_info();
   if (di == nullptr) return EP_ERR_CUDA;
-  const int most = di->num_sms * 8;
-  cudaError_t e = launch_kernel(adapter_low_kernel, a.num_rows < most ? a.num_rows : most, kThreads, 0, stream, false,
-                                Params{a});
-  if (e != cudaSuccess) return cuda_fail(e, "adapter_low launch");
+  const Cut c = cut(a.num_rows, a.hidden);
+  char *ws = static_cast<char *>(a.workspace);
+  LowParams q = {};
+  q.a = a.lora_a;
+  q.index = a.adapter_idx;
+  q.scale = a.adapter_scale;
+  q.error_word = a.error_word;
+  q.T = a.num_rows;
+  q.hidden = a.hidden;
+  q.rank = a.rank;
+  q.adapters = a.num_adapters;
+  q.cols = c.cols;
+  q.splits = c.splits;
+  q.plan = reinterpret_cast<int32_t *>(ws);
+  ws += align256((size_t)c.tiles * kPlanWords * 4);
+  q.low = reinterpret_cast<uint16_t *>(ws);
+  ws += align256((size_t)a.num_rows * a.rank * 2);
+  q.part = reinterpret_cast<float *>(ws);
+  const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)a.num_rows}, strides[] = {a.hidden * kSize};
+  const uint32_t box[] = {kInner, (uint32_t)c.cols};
+  ep_status_t s = encode_map(&q.x, a.x, 2, dims, strides, box);
+  if (s != EP_OK) return s;
+  // stacks of adapters side by side while there are SMs for them
+  const int named = a.num_adapters < c.cols ? a.num_adapters : c.cols;
+  const int stacks = up(named, 128 / a.rank);
+  int side = di->num_sms / (c.tiles * c.splits);
+  side = side < 1 ? 1 : side > stacks ? stacks : side;
+  const size_t smem = 1024 + kLowStages * (kABytes + (size_t)c.cols * 128) + (size_t)a.num_adapters * 4;
+  static std::atomic<bool> ready[64];
+  if (!ready[di->device]) {
+    const cudaError_t e = cudaFuncSetAttribute(adapter_low_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               1024 + kLowStages * (kABytes + kMaxCols * 128) + EP_MAX_EXPERTS * 4);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    ready[di->device] = true;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.num_rows + kTile - 1) / kTile, (a.width + kTile - 1) / kTile);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(c.tiles, c.splits, side);
+  cfg.blockDim = dim3(kLowThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = kUsePdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, adapter_product_kernel, Params{a});
-  return e == cudaSuccess ? EP_OK : cuda_fail(e, "adapter_product launch");
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
+  attr[0].val.clusterDim.y = c.splits;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kUsePdl ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_low_kernel, q);
+  if (e != cudaSuccess) return cuda_fail(e, "adapter_low launch");
+
+  Params p = {};
+  p.max_cols = c.cols;
+  p.error_word = a.error_word;
+  p.E = 1;
+  p.cap = a.num_rows;
+  p.wide = p.width = a.width;
+  p.inner = a.hidden;
+  p.a_tiles = up(a.width, 256);
+  p.out = a.out;
+  p.plan = q.plan;
+  p.low = q.low;
+  p.index = a.adapter_idx;
+  p.rank = a.rank;
+  const uint64_t wd[] = {(uint64_t)a.hidden, (uint64_t)a.width, 1};
+  const uint64_t ws_[] = {a.hidden * kSize, (uint64_t)a.hidden * a.width * kSize};
+  const uint32_t wb[] = {kInner, 128, 1};
+  s = encode_map(&p.a, a.w, 3, wd, ws_, wb);
+  if (s != EP_OK) return s;
+  const uint64_t ud[] = {(uint64_t)a.rank, (uint64_t)a.width, (uint64_t)a.num_adapters};
+  const uint64_t us[] = {a.rank * kSize, (uint64_t)a.rank * a.width * kSize};
+  s = encode_map(&p.up, a.lora_b, 3, ud, us, wb);
+  if (s == EP_OK) s = row_maps(p, a.x, a.hidden, a.num_rows, a.num_rows);
+  if (s != EP_OK) return s;
+  return launch_form<kAdapter>(p, a.num_rows, (int64_t)c.tiles * p.a_tiles, stream);
 }
 
 }  // namespace ep

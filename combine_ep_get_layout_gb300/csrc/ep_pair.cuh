@@ -1,0 +1,663 @@
+// Products of ragged groups of rows on the tensor cores, for pairs of CTAs:
+// the kernel behind the experts' products, their gradients and the adapters'
+// projection (each includes the forms it launches).
+//
+// A pair of CTAs computes a tile of 256 x up to 256: A, the operand with 256
+// rows, is the weights (so the ragged number of an expert's rows meets the
+// dimension that comes in steps of 16, not of 256), B the rows:
+//   kPlain, kGated   A = w[e] (inner dimension hidden),  B = rows of x
+//   kGradX           A = w[e]^T (inner dimension wide),  B = rows of g
+//   kGradW           A = g^T, B = x^T (inner dimension the expert's rows)
+//   kAdapter         kPlain with one expert, and more inner steps: A = the
+//                    up-projections of the adapters that the tile's rows name,
+//                    B = the rows' low-rank factors, zero for other adapters
+// An inner step is 64 elements, a 128-byte row of shared memory in the
+// 128-byte swizzle; the transposed operands are read with their outer
+// dimension contiguous, so nothing is ever transposed in memory.
+#pragma once
+
+#include <atomic>
+
+#include "ep_ops.h"
+#include "ep_tc.cuh"
+
+namespace ep {
+
+namespace {
+
+enum Form { kPlain, kGated, kGradX, kGradW, kAdapter };
+
+constexpr int kThreads = 384;        // warps: 0 and 3 copies of A and B, 1 products, 2 row ends (kGradW) and low rows (kAdapter), 4-11 results
+constexpr int kInner = 64;           // elements of an inner step
+constexpr int kABytes = 128 * 128;   // a CTA's half of A for one step
+constexpr int kMaxCols = 256;        // columns of a tile
+constexpr int kTmemCols = 512;       // two tiles: one computed, one read out
+constexpr int kMaxStages = 12;
+constexpr int kSideStages = 4;
+constexpr int kBoxes = kMaxCols / 2 / 8;  // heights of a half of B
+constexpr int kPlanWords = kMaxCols + 1;  // kAdapter: a tile's number of adapters, then their indices
+constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
+constexpr int kStagingBytes = 32 * kPitch;       // a result warp's 32 rows
+constexpr int kExchangeBytes = 16 * 32 * 4;      // kGated: 16 columns of a warp, fp32
+constexpr int kResultWarps = 8;
+
+struct Params {
+  // One copy a step and operand (a copy costs its issuing thread about 200
+  // cycles, so their number bounds a step of 512): A's 128 rows (kGated: 64
+  // of the gate and the 64 that they multiply), and a half of B of any
+  // height, b[i] of 8 (i + 1) rows.  Transposed operands are blocks of 64
+  // outer elements; b[0] is kGradW's, of two.
+  CUtensorMap a, b[kBoxes];
+  bool a_blocks, b_blocks;  // both blocks in one copy (their length is a multiple of 64), else in two
+  const int32_t *rows, *offset;
+  uint32_t *error_word;
+  int E, cap;
+  int wide;      // outputs of an expert: rows of A (kPlain, kGated, kGradW), inner (kGradX)
+  int width;     // kGated: wide / 2; else the outputs of a row
+  int inner;     // length of the inner dimension (not kGradW)
+  int a_tiles;   // tiles along A
+  int b_tiles;   // kGradW: tiles along B (hidden)
+  int hidden;    // kGradW
+  uint16_t *out, *preact;
+  int max_cols;         // rows of a tile, at most
+  int stages, b_bytes;  // ring; bytes of a CTA's half of B in a stage
+  // kAdapter
+  CUtensorMap up;        // the up-projections [adapters][width][rank]
+  const int32_t *plan;   // kPlanWords a tile of rows
+  const uint16_t *low;   // [rows][rank], scaled
+  const int64_t *index;  // [rows]
+  int rank;
+  int side_stages;  // a ring of its own for the adapters' steps, so that the main one waits for nothing
+};
+
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t ends[kMaxStages];   // kGradW: the last step of an expert has landed
+  uint64_t fixed[kMaxStages];  // and was trimmed
+  uint64_t side_full[kSideStages], side_empty[kSideStages], side_low[kSideStages];  // kAdapter's further steps
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem;
+};
+
+struct Tile {
+  int e, first, count;  // rows of the tile (kGradW: all rows of the expert)
+  int cols;             // columns of the product (multiple of 16)
+  int part;             // which of the expert's tiles of rows
+  int a0, b0;           // first row of A; kGradW: first column
+  int steps;
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Walks the tiles of a pair, 32 experts at a time (a whole warp calls it).
+// Tiles are ordered by expert, then along A, then along the expert's rows, so
+// pairs that run at the same time read the same weights.
+template <Form F>
+struct Walker {
+  const Params &p;
+  int lane, chunk = -1, base = 0, total = 0;
+  int rows = 0, first = 0, prefix = 0, mine = 0;
+
+  __device__ Walker(const Params &p_) : p(p_), lane(threadIdx.x & 31) {}
+
+  __device__ void load(int c) {
+    chunk = c;
+    const int e = c * 32 + lane;
+    rows = first = mine = 0;
+    if (F == kAdapter) {
+      rows = e == 0 ? p.cap : 0;
+      mine = p.a_tiles * ceil_div(rows, p.max_cols);
+    } else if (e < p.E) {
+      first = p.offset[e];
+      const int n = p.rows[e];
+      rows = first < 0 || first >= p.cap ? 0 : max(0, min(n, p.cap - first));
+      if (rows != n && blockIdx.x == 0 && threadIdx.x < 32) set_error(p.error_word, EP_ERRBIT_CAPACITY);
+      mine = F == kGradW ? p.a_tiles * p.b_tiles : p.a_tiles * ceil_div(rows, p.max_cols);
+    }
+    prefix = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, prefix, o);
+      if (lane >= o) prefix += v;
+    }
+    total = __shfl_sync(0xffffffffu, prefix, 31);
+  }
+
+  // The tile with this number (numbers only grow); false past the last.
+  __device__ bool find(int number, Tile &t) {
+    while (chunk < 0 || number >= base + total) {
+      base += total;
+      if ((chunk + 1) * 32 >= p.E) {
+        total = 0;
+        return false;
+      }
+      load(chunk + 1);
+    }
+    const int local = number - base;
+    const int src = __ffs(__ballot_sync(0xffffffffu, prefix > local)) - 1;
+    const int at = local - __shfl_sync(0xffffffffu, prefix - mine, src);
+    const int n = __shfl_sync(0xffffffffu, rows, src);
+    t.e = chunk * 32 + src;
+    t.first = __shfl_sync(0xffffffffu, first, src);
+    if (F == kGradW) {
+      t.a0 = at / p.b_tiles * 256;
+      t.b0 = at % p.b_tiles * 256;
+      t.count = n;
+      t.cols = kMaxCols;
+      t.steps = ceil_div(n, kInner);
+    } else {
+      // as few tiles as hold the rows, of about equal size
+      const int tiles = ceil_div(n, p.max_cols);
+      t.cols = ceil_div(ceil_div(n, tiles), 16) * 16;
+      if (F == kAdapter) {
+        // eight tiles of rows go along A together, so the pairs running at
+        // once share rows as well as weights
+        const int band = at / (8 * p.a_tiles), in = at - band * 8 * p.a_tiles, high = min(8, tiles - band * 8);
+        t.part = band * 8 + in % high;
+        t.a0 = in / high * 256;
+      } else {
+        t.part = at % tiles;
+        t.a0 = at / tiles * (F == kGated ? 128 : 256);
+      }
+      t.b0 = 0;
+      t.first += t.part * t.cols;
+      t.count = min(t.cols, n - t.part * t.cols);
+      t.steps = ceil_div(p.inner, kInner);
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ float silu_of(float g) { return g / (1.0f + __expf(-g)); }
+
+// Barriers of two warps; the first also gives whether both say `ok`.
+__device__ __forceinline__ bool pair_agree(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// A warp's 32 lanes hold outputs n (one a lane) of `count` <= 32 rows v[0..):
+// out[row][n] through the staging buffer, 64 bytes of a row at a time.
+template <int COUNT>
+__device__ __forceinline__ void store_transposed(const float *v, char *stage, uint16_t *out, int64_t pitch, int rows,
+                                                 int n, int limit, int lane) {
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c)
+    *reinterpret_cast<uint16_t *>(stage + c * kPitch + lane * 2) = (uint16_t)(pack_bf16x2(v[c], 0.0f) & 0xffffu);
+  __syncwarp();
+  const int part = lane & 3;
+#pragma unroll
+  for (int c = lane >> 2; c < COUNT; c += 8) {
+    if (c < rows && n + part * 8 < limit)
+      *reinterpret_cast<int4 *>(out + (int64_t)c * pitch + n + part * 8) =
+          *reinterpret_cast<const int4 *>(stage + c * kPitch + part * 16);
+  }
+  __syncwarp();
+}
+
+// What the kernel ahead made, after the wait for it: kept in its place by the
+// compiler, read from L2.
+__device__ __forceinline__ int load_made(const int32_t *p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ int4 load_made(const int4 *p) {
+  int4 v;
+  asm volatile("ld.global.cg.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+template <Form F>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
+  extern __shared__ char s_raw[];
+  __shared__ Barriers s_bar;
+  char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = kABytes + p.b_bytes;
+  char *side = ring + (size_t)p.stages * stage_bytes;
+  char *staging = side + (F == kAdapter ? (size_t)p.side_stages * stage_bytes : 0);
+  char *exchange = staging + kResultWarps * kStagingBytes;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s_bar.full[i], 1);
+      mbar_init(&s_bar.empty[i], 1);
+      mbar_init(&s_bar.ends[i], 1);
+      mbar_init(&s_bar.fixed[i], 2);  // one arrival from each CTA
+    }
+    for (int i = 0; i < kSideStages; ++i) {
+      mbar_init(&s_bar.side_full[i], 1);
+      mbar_init(&s_bar.side_empty[i], 1);
+      mbar_init(&s_bar.side_low[i], 2);  // one arrival from each CTA
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_bar.acc_full[i], 1);
+      mbar_init(&s_bar.acc_empty[i], 2 * kResultWarps);
+    }
+    fence_barrier_init();
+    prefetch_map(&p.a);
+  }
+  __syncwarp();
+  if (warp == 2) tmem_alloc_pair(&s_bar.tmem, kTmemCols);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_bar.tmem;
+  // kAdapter: only the low rows and the plan come from the kernel ahead, which
+  // started after all that was before it had ended; who reads them waits.
+  if (F != kAdapter || warp == 2) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
+  // inner steps of a tile that its adapters take
+  const int chunks = F == kAdapter ? ceil_div(p.rank, kInner) : 1;
+  const auto adapter_steps = [&](const Tile &t) { return chunks * load_made(p.plan + t.part * kPlanWords); };
+
+  bool ok = true;  // false: a wait gave up
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ copies
+    const bool is_a = warp == 0;
+    Walker<F> walk(p);
+    Tile t;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      const int b_rows = t.cols / 2;
+      const uint32_t bytes = kABytes + b_rows * 128;
+      const int a0 = t.a0 + (int)rank * (F == kGated ? 64 : 128);
+      const int b0 = (F == kGradW ? t.b0 : t.first) + (int)rank * b_rows;
+      for (int k = 0; k < t.steps; ++k) {
+        if (!__all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1))) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
+          // both CTAs' copies complete on the leading CTA's barrier, but those
+          // of a last step whose rows end raggedly go by the row ends
+          const bool last = F == kGradW && t.count % 16 != 0 && k == t.steps - 1;
+          const uint32_t bar = last ? map_shared(smem_addr(&s_bar.ends[stage]), rank)
+                                    : map_shared(smem_addr(&s_bar.full[stage]), 0);
+          if (is_a) {
+            if (last) mbar_arrive_expect_tx(&s_bar.ends[stage], bytes);
+            if (rank == 0) {
+              if (last)
+                mbar_arrive(&s_bar.full[stage]);
+              else
+                mbar_arrive_expect_tx(&s_bar.full[stage], 2 * bytes);
+            }
+          }
+          const int at = k * kInner;
+          if (is_a) {
+            if (F == kPlain || F == kAdapter) {
+              tile_load_3d(a, &p.a, at, a0, t.e, bar);
+            } else if (F == kGated) {
+              tile_load_4d(a, &p.a, at, a0, 0, t.e, bar);
+            } else if (F == kGradX) {
+              if (p.a_blocks) {
+                tile_load_4d(a, &p.a, 0, at, a0 / 64, t.e, bar);
+              } else {
+                tile_load_3d(a, &p.a, a0, at, t.e, bar);
+                tile_load_3d(a + 8192, &p.a, a0 + 64, at, t.e, bar);
+              }
+            } else if (p.a_blocks) {
+              tile_load_3d(a, &p.a, 0, t.first + at, a0 / 64, bar);
+            } else {
+              tile_load_2d(a, &p.a, a0, t.first + at, bar);
+              tile_load_2d(a + 8192, &p.a, a0 + 64, t.first + at, bar);
+            }
+          } else if (F != kGradW) {
+            tile_load_2d(b, &p.b[b_rows / 8 - 1], at, b0, bar);
+          } else if (p.b_blocks) {
+            tile_load_3d(b, &p.b[0], 0, t.first + at, b0 / 64, bar);
+          } else {
+            tile_load_2d(b, &p.b[0], b0, t.first + at, bar);
+            tile_load_2d(b + 8192, &p.b[0], b0 + 64, t.first + at, bar);
+          }
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // the products' last arrivals on this CTA's barriers come before it ends
+    for (int i = 0; ok && i < p.stages; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1));
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------- products
+    Walker<F> walk(p);
+    Tile t;
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0, trims = 0;
+    int side_stage = 0;
+    uint32_t side_phase = 0;
+    const uint32_t ring_addr = smem_addr(ring);
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      if (t.steps == 0) continue;  // an expert without rows (kGradW): zeros are written
+      const uint32_t idesc = mma_desc(t.cols, F == kGradX || F == kGradW, F == kGradW);
+      const uint32_t d = tmem + acc * kMaxCols;
+      ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1));
+      tc_fence_after();
+      for (int k = 0; ok && k < t.steps; ++k) {
+        ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
+        if (F == kGradW && ok && k == t.steps - 1 && t.count % 16 != 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&s_bar.fixed[stage], (trims >> stage) & 1u));
+          trims ^= 1u << stage;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t addr = ring_addr + (uint32_t)(stage * stage_bytes);
+        const uint32_t a = F == kGradX || F == kGradW ? outer_desc(addr, 8192) : inner_desc(addr);
+        const uint32_t b = F == kGradW ? outer_desc(addr + kABytes, 8192) : inner_desc(addr + kABytes);
+        const int parts = F == kGradW ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < parts)
+              mma_pair(d, a + j * ((F == kGradX || F == kGradW ? 2048 : 32) >> 4), b + j * ((F == kGradW ? 2048 : 32) >> 4),
+                       idesc, k > 0 || j > 0);
+          commit_pair(&s_bar.empty[stage]);
+          if (F != kAdapter && k == t.steps - 1) commit_pair(&s_bar.acc_full[acc]);
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (F == kAdapter && ok) {
+        if (n == pair) griddep_wait();
+        const int steps = adapter_steps(t);
+        for (int k = 0; ok && k < steps; ++k) {
+          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_full[side_stage], side_phase) &&
+                                           mbar_wait_cluster(&s_bar.side_low[side_stage], side_phase));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t addr = smem_addr(side) + (uint32_t)(side_stage * stage_bytes);
+          const uint32_t a = inner_desc(addr), b = inner_desc(addr + kABytes);
+          const int parts = min(4, ceil_div(p.rank - k % chunks * kInner, 16));
+          if (elect_one()) {
+            for (int j = 0; j < parts; ++j) mma_pair(d, a + j * 2, b + j * 2, idesc, true);
+            commit_pair(&s_bar.side_empty[side_stage]);
+          }
+          __syncwarp();
+          if (++side_stage == p.side_stages) {
+            side_stage = 0;
+            side_phase ^= 1;
+          }
+        }
+        if (ok && elect_one()) commit_pair(&s_bar.acc_full[acc]);
+        __syncwarp();
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  } else if (warp == 2 && F == kGradW) {
+    // ---------------------------------------------------------- row ends
+    // The last step of an expert reads rows of the next one: they are zeroed
+    // in both operands (both, since what lies there may be NaN).
+    Walker<F> walk(p);
+    Tile t;
+    int stage = 0;
+    uint32_t parities = 0;
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      stage = (stage + t.steps) % p.stages;
+      if (t.count % 16 == 0) continue;
+      const int s = (stage + p.stages - 1) % p.stages;
+      ok = mbar_wait_pair(&s_bar.ends[s], (parities >> s) & 1u);
+      if (!ok) break;
+      parities ^= 1u << s;
+      char *a = ring + (size_t)s * stage_bytes;
+      const int from = t.count % kInner, to = ceil_div(from, 16) * 16;
+      const int blocks = 2 + t.cols / 2 / 64;  // of 64 outer elements, A's two and B's
+      for (int i = lane; i < blocks * (to - from) * 8; i += 32) {
+        const int block = i / ((to - from) * 8), r = from + i / 8 % (to - from);
+        *reinterpret_cast<int4 *>(a + block * 8192 + r * 128 + (i & 7) * 16) = make_int4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.fixed[s]), 0));
+    }
+  } else if (warp == 2 && F == kAdapter) {
+    // ---------------------------------------------------------- adapters
+    // A is copied; B, the low rows of the adapter's own rows and zeros for the
+    // others, is written in the swizzled order that a copy would give it.
+    Walker<F> walk(p);
+    Tile t;
+    int stage = 0;
+    uint32_t phase = 0;
+    const auto advance = [&] {
+      if (++stage == p.side_stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    };
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      const int steps = adapter_steps(t), b_rows = t.cols / 2;
+      for (int k = 0; k < steps; ++k) {
+        const int adapter = load_made(p.plan + t.part * kPlanWords + 1 + k / chunks), from = k % chunks * kInner;
+        const int pieces = min(4, ceil_div(p.rank - from, 16)) * 2;  // of 8 elements a row
+        ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
+        if (!ok) break;
+        char *b = side + (size_t)stage * stage_bytes + kABytes;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&s_bar.side_full[stage], 2 * kABytes);
+          tile_load_3d(smem_addr(b) - kABytes, &p.up, from, t.a0 + (int)rank * 128, adapter,
+                       map_shared(smem_addr(&s_bar.side_full[stage]), 0));
+        }
+        __syncwarp();
+        for (int i = lane; i < b_rows * pieces; i += 32) {
+          const int r = i / pieces, c = i - r * pieces, in = (int)rank * b_rows + r;
+          int4 v = make_int4(0, 0, 0, 0);
+          if (in < t.count && from + c * 8 < p.rank && __ldg(p.index + t.first + in) == adapter)
+            v = load_made(reinterpret_cast<const int4 *>(p.low + (int64_t)(t.first + in) * p.rank + from + c * 8));
+          *reinterpret_cast<int4 *>(b + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.side_low[stage]), 0));
+        advance();
+      }
+    }
+    for (int i = 0; ok && i < p.side_stages; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
+      advance();
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- results
+    // Warp w reads the tensor-memory lanes 32 (w % 4) ...; the two groups of
+    // four warps take every other 32 columns.
+    Walker<F> walk(p);
+    Tile t;
+    const int w = warp - 4, quarter = w & 3, half = w >> 2;
+    char *stage_buf = staging + w * kStagingBytes;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const auto release = [&](int a) {  // this warp has read its columns of accumulator a
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.acc_empty[a]), 0));
+    };
+    for (int n = pair; ok && walk.find(n, t); n += pairs) {
+      if (F == kGradW && t.steps == 0) {
+        const int row = t.a0 + (int)rank * 128 + quarter * 32 + lane;
+        for (int c = half * 32; c < t.cols && row < p.wide; c += 64)
+          for (int j = 0; j < 32 && t.b0 + c + j < p.hidden; j += 8)
+            *reinterpret_cast<int4 *>(p.out + ((int64_t)t.e * p.wide + row) * p.hidden + t.b0 + c + j) =
+                make_int4(0, 0, 0, 0);
+        continue;
+      }
+      ok = mbar_wait_pair(&s_bar.acc_full[acc], acc_phase);
+      ok = F == kGated ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      for (int c = half * 32; c < t.cols; c += 64) {
+        float v[32];
+        tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+        if (c + 64 >= t.cols) release(acc);
+        const int left = t.count - c;  // rows of this chunk (not kGradW)
+        if (F == kPlain || F == kGradX || F == kAdapter) {
+          const int at = t.a0 + (int)rank * 128 + quarter * 32;
+          const int64_t row = t.first + c;
+          store_transposed<32>(v, stage_buf, p.out + row * p.width, p.width, left, at, p.width, lane);
+          if (F == kPlain && p.preact != nullptr)
+            store_transposed<32>(v, stage_buf, p.preact + row * p.width, p.width, left, at, p.width, lane);
+        } else if (F == kGated) {
+          // lanes 0-63 hold the gate, lanes 64-127 what it multiplies: warps
+          // w and w + 2 exchange half of their columns and finish half each
+          const int at = t.a0 + (int)rank * 64 + (quarter & 1) * 32;
+          const int64_t row = t.first + c;
+          const bool gate = quarter < 2;
+          if (p.preact != nullptr)
+            store_transposed<32>(v, stage_buf, p.preact + row * p.wide + (gate ? 0 : p.width), p.wide, left, at,
+                                 p.width, lane);
+          float *give = reinterpret_cast<float *>(exchange + w * kExchangeBytes);
+          const float *take = reinterpret_cast<const float *>(exchange + (w ^ 2) * kExchangeBytes);
+          const int id = 1 + half * 2 + (quarter & 1);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) give[j * 32 + lane] = gate ? v[16 + j] : v[j];
+          pair_barrier(id);
+          float o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float other = take[j * 32 + lane];
+            o[j] = gate ? silu_of(v[j]) * other : silu_of(other) * v[16 + j];
+          }
+          const int skip = gate ? 0 : 16;
+          store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);
+          pair_barrier(id);  // before the next chunk overwrites what the other warp reads
+        } else {
+          // one row of the gradient a lane, 32 columns
+          uint32_t packed[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(stage_buf + lane * kPitch + j * 16) =
+                make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+          __syncwarp();
+          const int part = lane & 3, col = t.b0 + c + part * 8;
+#pragma unroll
+          for (int r = lane >> 2; r < 32; r += 8) {
+            const int row = t.a0 + (int)rank * 128 + quarter * 32 + r;
+            if (row < p.wide && col < p.hidden)
+              *reinterpret_cast<int4 *>(p.out + ((int64_t)t.e * p.wide + row) * p.hidden + col) =
+                  *reinterpret_cast<const int4 *>(stage_buf + r * kPitch + part * 16);
+          }
+          __syncwarp();
+        }
+      }
+      if (t.cols <= half * 32) release(acc);  // no columns for this warp
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  }
+  if (!ok) {
+    // A wait gave up (it never should): what this CTA started lands well
+    // within the time waited here, then everything is given back.
+    set_error(p.error_word, EP_ERRBIT_TIMEOUT);
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_free_pair(tmem, kTmemCols);
+  }
+}
+
+// Pairs of CTAs that fit the device at once.
+template <Form F>
+ep_status_t most_pairs(const DeviceInfo *di, size_t smem, int *pairs) {
+  static std::atomic<int> known[64];  // per device; the same for every call
+  if (known[di->device] == 0) {
+    cudaError_t e = cudaFuncSetAttribute(product_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(di->num_sms / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, product_kernel<F>, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+    known[di->device] = n > 0 ? n : 1;
+  }
+  *pairs = known[di->device];
+  return EP_OK;
+}
+
+constexpr uint64_t kSize = 2;  // bytes of an element
+
+int up(int a, int b) { return (a + b - 1) / b; }
+
+template <Form F>
+ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream_t stream) {
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
+  // The ring takes what is left of shared memory: a stage holds 128 rows of A
+  // and half of the most columns that a tile can have.
+  const int cols = F == kGradW || most_rows > p.max_cols ? p.max_cols : up(most_rows, 16) * 16;
+  p.b_bytes = cols / 2 * 128;  // a multiple of 1024, as the swizzle needs
+  const int fixed = 1024 + kResultWarps * kStagingBytes + (F == kGated ? kResultWarps * kExchangeBytes : 0);
+  const int limit = (int)di->max_smem_per_block_optin - (int)sizeof(Barriers) - 1024;
+  p.stages = (limit - fixed) / (kABytes + p.b_bytes);
+  if (F == kAdapter) {
+    p.side_stages = p.stages >= 8 ? kSideStages : 2;
+    p.stages -= p.side_stages;
+  }
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const size_t smem = (size_t)limit;
+  int pairs = 0;
+  ep_status_t s = most_pairs<F>(di, smem, &pairs);
+  if (s != EP_OK) return s;
+  if (most_tiles < pairs) pairs = (int)most_tiles;
+  const cudaError_t e = launch_kernel(product_kernel<F>, 2 * pairs, kThreads, smem, stream, false, p);
+  return e == cudaSuccess ? EP_OK : cuda_fail(e, "product launch");
+}
+
+// Rows [rows][length] by halves of B of every height up to `most`.
+ep_status_t row_maps(Params &p, const void *rows, int length, int cap, int most) {
+  const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {length * kSize};
+  const int cols = most > p.max_cols ? p.max_cols : up(most, 16) * 16;
+  for (int i = 0; i < cols / 16; ++i) {
+    const uint32_t box[] = {kInner, 8u * (i + 1)};
+    const ep_status_t s = encode_map(&p.b[i], rows, 2, dims, strides, box);
+    if (s != EP_OK) return s;
+  }
+  return EP_OK;
+}
+
+
+}  // namespace
+
+}  // namespace ep

@@ -160,6 +160,40 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
       : "memory");
 }
 
+// The same for a CTA by itself (128 rows of A).
+
+__device__ __forceinline__ void tile_load_one(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_one(uint32_t *dst, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free_one(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+
+__device__ __forceinline__ void mma_one(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(0x40004040)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_one(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
 // 32 columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   uint32_t *r = reinterpret_cast<uint32_t *>(v);
@@ -187,6 +221,11 @@ __device__ __forceinline__ uint32_t outer_desc(uint32_t addr, uint32_t block) { 
 __host__ __device__ constexpr uint32_t mma_desc(int n, bool a_outer, bool b_outer) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_outer ? 1u : 0u) << 15) | ((b_outer ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | (16u << 24);
+}
+
+// The same for M = 128 on one CTA, inner dimensions contiguous.
+__host__ __device__ constexpr uint32_t mma_desc_one(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
 // --------------------------------------------------------------------- host
