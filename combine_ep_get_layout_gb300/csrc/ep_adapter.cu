@@ -7,10 +7,11 @@
 // Two kernels.  adapter_low_kernel computes low[t] = scale[a] x[t] A_a^T for
 // a tile of rows: the down-projections of the adapters that the tile names are
 // stacked, 128 rows of them at a time, and multiplied with all its rows on the
-// tensor cores; of every column only its own adapter's part is kept.  The
-// projection (ep_pair.cuh, kAdapter) then takes an adapter of the tile as one
-// more inner step: B_a beside low[t], zero for the rows of other adapters, so
-// the second term is summed in tensor memory with the first.
+// tensor cores; of every column only its own adapter's part is kept.  For the
+// projection (ep_pair.cuh, kAdapter) the adapters of a tile, side by side, are
+// a longer inner dimension: 64 / rank of them a step, their B_a against low[t]
+// in its adapter's columns and zeros in the others, so the second term is
+// summed in tensor memory with the first.
 //
 // low is kept in bf16, as the tensor cores take it: 2^-8 of the low term, the
 // size of the result's own rounding.
@@ -44,15 +45,6 @@ struct LowBarriers {
   uint64_t acc_full, acc_empty;
   uint32_t tmem;
 };
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_constant__ LowParams p) {
   extern __shared__ char s_raw[];
@@ -127,6 +119,7 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
     int32_t *plan = p.plan + (int64_t)blockIdx.x * kPlanWords;
     if (threadIdx.x == 0) plan[0] = count;
     for (int i = threadIdx.x; i < count; i += kLowThreads) plan[1 + i] = s_list[i];
+    for (int i = threadIdx.x; i < p.cols; i += kLowThreads) plan[1 + kMaxCols + i] = s_place[i];
   }
 
   const int per = 128 / p.rank;  // adapters of a stack
@@ -364,17 +357,14 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   p.out = a.out;
   p.plan = q.plan;
   p.low = q.low;
-  p.index = a.adapter_idx;
+  p.up = a.lora_b;
   p.rank = a.rank;
   const uint64_t wd[] = {(uint64_t)a.hidden, (uint64_t)a.width, 1};
   const uint64_t ws_[] = {a.hidden * kSize, (uint64_t)a.hidden * a.width * kSize};
   const uint32_t wb[] = {kInner, 128, 1};
   s = encode_map(&p.a, a.w, 3, wd, ws_, wb);
   if (s != EP_OK) return s;
-  const uint64_t ud[] = {(uint64_t)a.rank, (uint64_t)a.width, (uint64_t)a.num_adapters};
-  const uint64_t us[] = {a.rank * kSize, (uint64_t)a.rank * a.width * kSize};
-  s = encode_map(&p.up, a.lora_b, 3, ud, us, wb);
-  if (s == EP_OK) s = row_maps(p, a.x, a.hidden, a.num_rows, a.num_rows);
+  s = row_maps(p, a.x, a.hidden, a.num_rows, a.num_rows);
   if (s != EP_OK) return s;
   return launch_form<kAdapter>(p, a.num_rows, (int64_t)c.tiles * p.a_tiles, stream);
 }

@@ -10,7 +10,8 @@
 //   kGradW           A = g^T, B = x^T (inner dimension the expert's rows)
 //   kAdapter         kPlain with one expert, and more inner steps: A = the
 //                    up-projections of the adapters that the tile's rows name,
-//                    B = the rows' low-rank factors, zero for other adapters
+//                    side by side, B = the rows' low-rank factors in their
+//                    adapter's columns, zero in the others
 // An inner step is 64 elements, a 128-byte row of shared memory in the
 // 128-byte swizzle; the transposed operands are read with their outer
 // dimension contiguous, so nothing is ever transposed in memory.
@@ -35,7 +36,8 @@ constexpr int kTmemCols = 512;       // two tiles: one computed, one read out
 constexpr int kMaxStages = 12;
 constexpr int kSideStages = 4;
 constexpr int kBoxes = kMaxCols / 2 / 8;  // heights of a half of B
-constexpr int kPlanWords = kMaxCols + 1;  // kAdapter: a tile's number of adapters, then their indices
+// kAdapter, a tile: its number of adapters, their indices, each row's place among them or -1
+constexpr int kPlanWords = 1 + 2 * kMaxCols;
 constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
 constexpr int kStagingBytes = 32 * kPitch;       // a result warp's 32 rows
 constexpr int kExchangeBytes = 16 * 32 * 4;      // kGated: 16 columns of a warp, fp32
@@ -62,10 +64,9 @@ struct Params {
   int max_cols;         // rows of a tile, at most
   int stages, b_bytes;  // ring; bytes of a CTA's half of B in a stage
   // kAdapter
-  CUtensorMap up;        // the up-projections [adapters][width][rank]
+  const uint16_t *up;    // the up-projections [adapters][width][rank]
   const int32_t *plan;   // kPlanWords a tile of rows
   const uint16_t *low;   // [rows][rank], scaled
-  const int64_t *index;  // [rows]
   int rank;
   int side_stages;  // a ring of its own for the adapters' steps, so that the main one waits for nothing
 };
@@ -74,7 +75,7 @@ struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t ends[kMaxStages];   // kGradW: the last step of an expert has landed
   uint64_t fixed[kMaxStages];  // and was trimmed
-  uint64_t side_full[kSideStages], side_empty[kSideStages], side_low[kSideStages];  // kAdapter's further steps
+  uint64_t side_full[kSideStages], side_empty[kSideStages];  // kAdapter's further steps
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
 };
@@ -240,9 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       mbar_init(&s_bar.fixed[i], 2);  // one arrival from each CTA
     }
     for (int i = 0; i < kSideStages; ++i) {
-      mbar_init(&s_bar.side_full[i], 1);
+      mbar_init(&s_bar.side_full[i], 2);  // one arrival from each CTA
       mbar_init(&s_bar.side_empty[i], 1);
-      mbar_init(&s_bar.side_low[i], 2);  // one arrival from each CTA
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_bar.acc_full[i], 1);
@@ -263,9 +263,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     griddep_wait();
     griddep_launch_dependents();
   }
-  // inner steps of a tile that its adapters take
-  const int chunks = F == kAdapter ? ceil_div(p.rank, kInner) : 1;
-  const auto adapter_steps = [&](const Tile &t) { return chunks * load_made(p.plan + t.part * kPlanWords); };
 
   bool ok = true;  // false: a wait gave up
   if (warp == 0 || warp == 3) {
@@ -388,15 +385,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       }
       if (F == kAdapter && ok) {
         if (n == pair) griddep_wait();
-        const int steps = adapter_steps(t);
-        for (int k = 0; ok && k < steps; ++k) {
-          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_full[side_stage], side_phase) &&
-                                           mbar_wait_cluster(&s_bar.side_low[side_stage], side_phase));
+        const int length = p.rank * load_made(p.plan + t.part * kPlanWords);  // of the adapters side by side
+        for (int k = 0; ok && k * kInner < length; ++k) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&s_bar.side_full[side_stage], side_phase));
           if (!ok) break;
           tc_fence_after();
           const uint32_t addr = smem_addr(side) + (uint32_t)(side_stage * stage_bytes);
           const uint32_t a = inner_desc(addr), b = inner_desc(addr + kABytes);
-          const int parts = min(4, ceil_div(p.rank - k % chunks * kInner, 16));
+          const int parts = min(4, ceil_div(length - k * kInner, 16));
           if (elect_one()) {
             for (int j = 0; j < parts; ++j) mma_pair(d, a + j * 2, b + j * 2, idesc, true);
             commit_pair(&s_bar.side_empty[side_stage]);
@@ -441,48 +437,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     }
   } else if (warp == 2 && F == kAdapter) {
     // ---------------------------------------------------------- adapters
-    // A is copied; B, the low rows of the adapter's own rows and zeros for the
-    // others, is written in the swizzled order that a copy would give it.
+    // Both operands of a further step are gathered 16 bytes at a time, in the
+    // swizzled order that a tile's copy would give them: eight lanes take the
+    // eight pieces of a row, so a lane stays with one adapter in a step.
     Walker<F> walk(p);
     Tile t;
-    int stage = 0;
+    int stage = 0, hand = 0;  // hand: the stage handed over next
     uint32_t phase = 0;
-    const auto advance = [&] {
-      if (++stage == p.side_stages) {
-        stage = 0;
-        phase ^= 1;
-      }
+    int flying = 0;
+    const int piece = lane & 7;
+    const auto hand_over = [&] {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.side_full[hand]), 0));
+      if (++hand == p.side_stages) hand = 0;
+      --flying;
     };
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
-      const int steps = adapter_steps(t), b_rows = t.cols / 2;
-      for (int k = 0; k < steps; ++k) {
-        const int adapter = load_made(p.plan + t.part * kPlanWords + 1 + k / chunks), from = k % chunks * kInner;
-        const int pieces = min(4, ceil_div(p.rank - from, 16)) * 2;  // of 8 elements a row
+      const int32_t *plan = p.plan + t.part * kPlanWords;
+      const int count = load_made(plan), length = count * p.rank, b_rows = t.cols / 2;
+      int place[4];  // of the rows lane, lane + 32, ... of this CTA's half
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        place[i] = lane + 32 * i < b_rows ? load_made(plan + 1 + kMaxCols + (int)rank * b_rows + lane + 32 * i) : -1;
+      const int a0 = t.a0 + (int)rank * 128;
+      const uint16_t *low = p.low + (int64_t)(t.first + (int)rank * b_rows) * p.rank;
+      for (int k = 0; k * kInner < length; ++k) {
         ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
         if (!ok) break;
-        char *b = side + (size_t)stage * stage_bytes + kABytes;
-        if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&s_bar.side_full[stage], 2 * kABytes);
-          tile_load_3d(smem_addr(b) - kABytes, &p.up, from, t.a0 + (int)rank * 128, adapter,
-                       map_shared(smem_addr(&s_bar.side_full[stage]), 0));
+        const uint32_t a = smem_addr(side + (size_t)stage * stage_bytes), b = a + kABytes;
+        const int col = k * kInner + piece * 8, mine = col / p.rank, in = col - mine * p.rank;
+        const bool there = col < length;
+        if (piece * 8 < ceil_div(min(length - k * kInner, kInner), 16) * 16) {
+          const int adapter = there ? load_made(plan + 1 + mine) : 0;
+          const uint16_t *up = p.up + ((int64_t)adapter * p.width + a0) * p.rank + in;
+#pragma unroll 8
+          for (int r = lane >> 3; r < 128; r += 4) {
+            const bool some = there && a0 + r < p.width;
+            copy16(a + r * 128 + ((piece ^ (r & 7)) << 4), some ? up + (int64_t)r * p.rank : p.up, some);
+          }
         }
         __syncwarp();
-        for (int i = lane; i < b_rows * pieces; i += 32) {
-          const int r = i / pieces, c = i - r * pieces, in = (int)rank * b_rows + r;
-          int4 v = make_int4(0, 0, 0, 0);
-          if (in < t.count && from + c * 8 < p.rank && __ldg(p.index + t.first + in) == adapter)
-            v = load_made(reinterpret_cast<const int4 *>(p.low + (int64_t)(t.first + in) * p.rank + from + c * 8));
-          *reinterpret_cast<int4 *>(b + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = i * 32 + j * 4 + (lane >> 3);
+            const int at = __shfl_sync(0xffffffffu, place[i], j * 4 + (lane >> 3));
+            const bool some = there && at == mine;
+            if (r < b_rows)
+              copy16(b + r * 128 + ((piece ^ (r & 7)) << 4), some ? low + (int64_t)r * p.rank + in : p.low, some);
+          }
+        copy_commit();
+        ++flying;
+        if (flying == 2) {
+          copy_wait<1>();
+          hand_over();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.side_low[stage]), 0));
-        advance();
+        if (++stage == p.side_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (flying > 0) {
+        copy_wait<0>();
+        hand_over();
       }
     }
     for (int i = 0; ok && i < p.side_stages; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
-      advance();
+      if (++stage == p.side_stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- results

@@ -110,6 +110,16 @@ __device__ __forceinline__ void tile_load_4d(uint32_t dst, const CUtensorMap *ma
       : "memory");
 }
 
+// 16 bytes to shared memory, zeros unless `some` (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ------------------------------------------------------------------ tcgen05
 
 // Tensor memory for the pair (a whole warp of each CTA calls it); the column
