@@ -526,11 +526,33 @@ _ACTIVATIONS = {None: N.EP_ACT_NONE, "swiglu": N.EP_ACT_SWIGLU}
 
 
 def _want_shape(t: torch.Tensor, name: str, shape: tuple):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _want_logits(logits: torch.Tensor, device=None) -> int:
+def _launch(dev: torch.device, fn: str, args, stream):
+    """``_call`` for functions of one argument block and a stream, with the
+    fewest steps in Python: these calls can be shorter than their set-up."""
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    else:
+        handle = stream.cuda_stream
+    f = getattr(N.load(), fn)
+    if torch.cuda.current_device() == dev.index:
+        status = f(C.byref(args), handle)
+    else:
+        with torch.cuda.device(dev):
+            status = f(C.byref(args), handle)
+    if status != N.EP_OK:
+        _check(status, fn)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _want_logits(logits: torch.Tensor) -> int:
     """Checks the logits (rows may be apart, a row's entries may not) and
     returns the row stride."""
     if not isinstance(logits, torch.Tensor):
@@ -539,9 +561,13 @@ def _want_logits(logits: torch.Tensor, device=None) -> int:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     if logits.dim() != 2:
         raise ValueError("logits must be [num_tokens, num_experts]")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
     T, E = logits.shape
-    _want(logits[:1].reshape(-1) if E == 1 or logits.stride(1) == 1 else logits, "logits", logits.dtype, device)
-    return logits.stride(0) if T > 1 else max(E, 1)
+    stride = logits.stride()
+    if (E > 1 and stride[1] != 1) or (T > 1 and stride[0] < E):
+        raise ValueError("a row of logits must be contiguous, and rows must not overlap")
+    return stride[0] if T > 1 else max(E, 1)
 
 
 def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
@@ -577,7 +603,7 @@ def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
         logits.data_ptr(), _LOGITS[logits.dtype], stride, T, E, num_topk, _SCORES[score],
         None if bias is None else bias.data_ptr(), num_groups, topk_groups, group_top,
         1 if renormalize else 0, weight_scale, out.topk_idx.data_ptr(), out.topk_weights.data_ptr())
-    _call(dev, "ep_route", C.byref(args), _stream(stream, dev))
+    _launch(dev, "ep_route", args, stream)
     return out
 
 
@@ -604,7 +630,7 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
         grad_weights.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], stride,
         topk_idx.data_ptr(), T, E, K, _SCORES[score], 1 if renormalize else 0, weight_scale,
         out.data_ptr())
-    _call(dev, "ep_route_backward", C.byref(args), _stream(stream, dev))
+    _launch(dev, "ep_route_backward", args, stream)
     return out
 
 
@@ -649,7 +675,7 @@ def ep_expert_product(x: torch.Tensor, w: torch.Tensor, layout: ExpandedLayout,
     args = N.ep_expert_product_args_t(
         x.data_ptr(), cap, layout.num_tokens, H, layout.num_experts, C.pointer(st), w.data_ptr(),
         width, act, out.data_ptr(), None if preact is None else preact.data_ptr())
-    _call(dev, "ep_expert_product", C.byref(args), _stream(stream, dev))
+    _launch(dev, "ep_expert_product", args, stream)
     return out
 
 
@@ -697,7 +723,7 @@ def ep_expert_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Ten
         C.pointer(st), width, act, None if preact is None else preact.data_ptr(),
         None if grad_preact is None else grad_preact.data_ptr(),
         None if grad_x is None else grad_x.data_ptr(), None if grad_w is None else grad_w.data_ptr())
-    _call(dev, "ep_expert_product_backward", C.byref(args), _stream(stream, dev))
+    _launch(dev, "ep_expert_product_backward", args, stream)
     return grad_x, grad_w
 
 
@@ -748,7 +774,7 @@ def ep_adapter_product(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, l
         adapter_idx.data_ptr(), None if adapter_scale is None else adapter_scale.data_ptr(),
         out.data_ptr(), workspace.data_ptr(), workspace.numel(),
         None if error_word is None else error_word.data_ptr())
-    _call(dev, "ep_adapter_product", C.byref(args), _stream(stream, dev))
+    _launch(dev, "ep_adapter_product", args, stream)
     return out
 
 
