@@ -22,8 +22,8 @@ namespace ep {
 namespace {
 
 constexpr int kLowThreads = 192;  // warps 0-3 copy A and read the results, 4 copies x, 5 issues the products
-constexpr int kLowStages = 4;
-constexpr int kAhead = 2;         // steps of A in flight while one is handed over
+constexpr int kLowMaxStages = 8;
+constexpr int kLowChunk = 32 * 128 * 4;  // 32 columns of the results, fp32
 constexpr int kMaxSplits = 8;     // CTAs of a cluster
 
 struct LowParams {
@@ -41,11 +41,25 @@ struct LowParams {
 };
 
 struct LowBarriers {
-  uint64_t full[kLowStages], empty[kLowStages];
+  uint64_t full[kLowMaxStages], empty[kLowMaxStages];
   uint64_t acc_full, acc_empty;
   uint32_t tmem;
 };
 
+// A barrier of the first four warps; whether all of them say `ok`.
+__device__ __forceinline__ bool four_agree(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+// STAGES: of the ring; STAGES - 1 steps of A are in flight.
+template <int STAGES>
 __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_constant__ LowParams p) {
   extern __shared__ char s_raw[];
   __shared__ LowBarriers s_bar;
@@ -54,13 +68,15 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
   __shared__ uint32_t s_first[kMaxCols / 32];
   char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   const int stage_bytes = kABytes + p.cols * 128;
-  int *s_table = reinterpret_cast<int *>(ring + kLowStages * stage_bytes);  // [adapters]: first row that names it
+  // [adapters]: first row that names it; later 32 columns of the results
+  int *s_table = reinterpret_cast<int *>(ring + STAGES * stage_bytes);
+  float *s_chunk = reinterpret_cast<float *>(s_table);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int first = blockIdx.x * p.cols, rows = min(p.cols, p.T - first);
   const int split = blockIdx.y;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kLowStages; ++i) {
+    for (int i = 0; i < STAGES; ++i) {
       mbar_init(&s_bar.full[i], 4 * 32 + 1);
       mbar_init(&s_bar.empty[i], 1);
     }
@@ -130,7 +146,7 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
   int stage = 0;
   uint32_t phase = 0, acc_phase = 0;
   const auto advance = [&] {
-    if (++stage == kLowStages) {
+    if (++stage == STAGES) {
       stage = 0;
       phase ^= 1;
     }
@@ -150,7 +166,7 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
       }
       int filled = 0;
       int hand = stage;  // the stage handed over next
-      for (int k = k0; k < k1 + kAhead; ++k) {
+      for (int k = k0; k < k1 + (STAGES - 1); ++k) {
         if (k < k1) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1));
           const uint32_t a = smem_addr(ring + stage * stage_bytes);
@@ -165,11 +181,11 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
           advance();
         }
         copy_commit();
-        if (k >= k0 + kAhead) {
-          copy_wait<kAhead>();
+        if (k >= k0 + (STAGES - 1)) {
+          copy_wait<(STAGES - 1)>();
           fence_proxy_async_smem();
           mbar_arrive(&s_bar.full[hand]);
-          if (++hand == kLowStages) hand = 0;
+          if (++hand == STAGES) hand = 0;
         }
       }
       copy_wait<0>();
@@ -177,24 +193,30 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_full, acc_phase));
       acc_phase ^= 1;
       tc_fence_after();
-      if (ok) {
-        const int l = warp * 32 + lane, j = l / p.rank, i = l - j * p.rank;
-        const int mine = j < stacked ? s * per + j : -2;
+      if (four_agree(ok)) {
+        const int fours = p.rank / 4;
         for (int c = 0; c < p.cols; c += 32) {
           float v[32];
           tmem_load32(tmem + c + ((uint32_t)(warp * 32) << 16), v);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            if (c + q < p.cols && s_place[c + q] == mine) {
-              const int64_t at = (int64_t)(first + c + q) * p.rank + i;
-              if (p.splits == 1) {
-                const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + s_list[mine]);
-                p.low[at] = (uint16_t)(pack_bf16x2(v[q] * f, 0.0f) & 0xffffu);
-              } else {
-                p.part[(int64_t)split * p.T * p.rank + at] = v[q];
-              }
+          for (int q = 0; q < 32; ++q) s_chunk[q * 128 + warp * 32 + lane] = v[q];
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          // of every row its own adapter's part, four values at a time
+          for (int item = threadIdx.x; item < 32 * fours; item += 128) {
+            const int q = item / fours, i = item - q * fours;
+            const int place = c + q < p.cols ? s_place[c + q] : -1;
+            if (place < s * per || place >= s * per + stacked) continue;
+            const float4 f = *reinterpret_cast<const float4 *>(s_chunk + q * 128 + (place - s * per) * p.rank + i * 4);
+            const int64_t at = (int64_t)(first + c + q) * p.rank + i * 4;
+            if (p.splits == 1) {
+              const float g = p.scale == nullptr ? 1.0f : __ldg(p.scale + s_list[place]);
+              *reinterpret_cast<uint2 *>(p.low + at) =
+                  make_uint2(pack_bf16x2(f.x * g, f.y * g), pack_bf16x2(f.z * g, f.w * g));
+            } else {
+              *reinterpret_cast<float4 *>(p.part + (int64_t)split * p.T * p.rank + at) = f;
             }
           }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
         }
       }
       tc_fence_before();
@@ -235,16 +257,26 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
     if (p.splits > 1) {
       // the splits' parts are added in their order, each row by one CTA
       cluster_sync();
-      for (int c = split; c < rows; c += p.splits) {
+      const int fours = p.rank / 4, mine = ceil_div(rows - split, p.splits);
+      for (int item = threadIdx.x; item < mine * fours; item += kLowThreads) {
+        const int c = split + item / fours * p.splits, i = item % fours * 4;
         const int place = s_place[c];
         if (place < s * per || place >= s * per + stacked) continue;
         const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + s_list[place]);
-        for (int i = threadIdx.x; i < p.rank; i += kLowThreads) {
-          const int64_t at = (int64_t)(first + c) * p.rank + i;
-          float sum = 0.0f;
-          for (int q = 0; q < p.splits; ++q) sum += __ldcg(p.part + (int64_t)q * p.T * p.rank + at);
-          p.low[at] = (uint16_t)(pack_bf16x2(sum * f, 0.0f) & 0xffffu);
+        const int64_t at = (int64_t)(first + c) * p.rank + i, pitch = (int64_t)p.T * p.rank;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int q = 0; q < kMaxSplits; ++q) {
+          if (q < p.splits) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + q * pitch + at));
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+          }
         }
+        *reinterpret_cast<uint2 *>(p.low + at) =
+            make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
       }
     }
   }
@@ -322,13 +354,18 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   const int stacks = up(named, 128 / a.rank);
   int side = di->num_sms / (c.tiles * c.splits);
   side = side < 1 ? 1 : side > stacks ? stacks : side;
-  const size_t smem = 1024 + kLowStages * (kABytes + (size_t)c.cols * 128) + (size_t)a.num_adapters * 4;
-  static std::atomic<bool> ready[64];
-  if (!ready[di->device]) {
-    const cudaError_t e = cudaFuncSetAttribute(adapter_low_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               1024 + kLowStages * (kABytes + kMaxCols * 128) + EP_MAX_EXPERTS * 4);
+  const bool shallow = c.cols > 64;  // a stage of x and A: up to 48 KB, or up to 24
+  const auto kernel = shallow ? adapter_low_kernel<4> : adapter_low_kernel<kLowMaxStages>;
+  const size_t table = (size_t)a.num_adapters * 4;
+  const size_t smem = 1024 + (shallow ? 4 : kLowMaxStages) * (kABytes + (size_t)c.cols * 128) +
+                      (table > kLowChunk ? table : kLowChunk);
+  static std::atomic<bool> ready[64][2];
+  if (!ready[di->device][shallow]) {
+    const int most = 1024 + (shallow ? 4 * (kABytes + kMaxCols * 128) : kLowMaxStages * (kABytes + 64 * 128)) +
+                     EP_MAX_EXPERTS * 4;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    ready[di->device] = true;
+    ready[di->device][shallow] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.tiles, c.splits, side);
@@ -343,7 +380,7 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kUsePdl ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_low_kernel, q);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q);
   if (e != cudaSuccess) return cuda_fail(e, "adapter_low launch");
 
   Params p = {};
