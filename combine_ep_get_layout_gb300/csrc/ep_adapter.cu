@@ -294,22 +294,49 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
   }
 }
 
-// How a call is cut: rows of a tile, tiles, splits of the low rows' inner
-// dimension.
+// How a call is cut: rows of a tile, tiles, pairs that share a tile's inner
+// dimension, splits of the low rows' inner dimension.
 struct Cut {
-  int cols, tiles, splits;
+  int cols, tiles, parts, splits;
 };
 
-Cut cut(int num_rows, int hidden) {
-  Cut c;
-  c.tiles = up(num_rows, kMaxCols);
-  c.cols = up(up(num_rows, c.tiles), 16) * 16;
+int low_splits(int tiles, int hidden) {
   const int steps = up(hidden, kInner);
-  c.splits = 128 / c.tiles;
-  if (c.splits > kMaxSplits) c.splits = kMaxSplits;
-  if (c.splits > steps) c.splits = steps;
-  if (c.splits < 1) c.splits = 1;
-  return c;
+  int n = 128 / tiles;
+  if (n > kMaxSplits) n = kMaxSplits;
+  if (n > steps) n = steps;
+  return n < 1 ? 1 : n;
+}
+
+// The cheapest of a few cuts by the cycles of the projection: a step costs
+// its products (two cycles a column) or its copies (58 bytes a cycle of A's
+// half and B's half), a tile its results, a shared tile its joining.
+ep_status_t choose(const DeviceInfo *di, int num_rows, int hidden, int width, Cut *best) {
+  int64_t least = -1;
+  for (int most = kMaxCols; most >= 32; most /= 2) {
+    Cut c;
+    c.tiles = up(num_rows, most);
+    c.cols = up(up(num_rows, c.tiles), 32) * 32;
+    c.tiles = up(num_rows, c.cols);
+    for (c.parts = 1; c.parts <= parts_for(c.cols); c.parts *= 2) {
+      int clusters = 0;
+      const ep_status_t s = most_clusters<kAdapter>(di, c.parts, &clusters);
+      if (s != EP_OK) return s;
+      const int64_t tiles = (int64_t)c.tiles * up(width, 256);
+      if (c.parts > 1 && (tiles > clusters || up(hidden, kInner) < 2 * c.parts)) break;
+      const int64_t copies = (kABytes + c.cols / 2 * 128) / 58, products = 2 * c.cols;
+      const int64_t step = copies > products ? copies : products;
+      const int64_t cost = (tiles + clusters - 1) / clusters *
+                           (up(up(hidden, kInner), c.parts) * step + 2000 + 10 * c.cols) +
+                           (c.parts > 1 ? 1000 + c.parts * 10 * c.cols : 0);
+      if (least < 0 || cost < least) {
+        least = cost;
+        *best = c;
+      }
+    }
+  }
+  best->splits = low_splits(best->tiles, hidden);
+  return EP_OK;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -318,16 +345,19 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t adapter_workspace_bytes(int num_rows, int hidden, int rank) {
   if (num_rows == 0) return 0;
-  const Cut c = cut(num_rows, hidden);
-  return align256((size_t)c.tiles * kPlanWords * 4) + align256((size_t)num_rows * rank * 2) +
-         align256(c.splits > 1 ? (size_t)c.splits * num_rows * rank * 4 : 0);
+  // whatever the cut: tiles of 32 columns or more, splits as for the fewest tiles
+  const int splits = low_splits(up(num_rows, kMaxCols), hidden);
+  return align256((size_t)up(num_rows, 32) * kPlanWords * 4) + align256((size_t)num_rows * rank * 2) +
+         align256(splits > 1 ? (size_t)splits * num_rows * rank * 4 : 0);
 }
 
 ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   if (a.num_rows == 0) return EP_OK;
   const DeviceInfo *di = current_device_info();
   if (di == nullptr) return EP_ERR_CUDA;
-  const Cut c = cut(a.num_rows, a.hidden);
+  Cut c;
+  ep_status_t s = choose(di, a.num_rows, a.hidden, a.width, &c);
+  if (s != EP_OK) return s;
   char *ws = static_cast<char *>(a.workspace);
   LowParams q = {};
   q.a = a.lora_a;
@@ -341,13 +371,13 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   q.cols = c.cols;
   q.splits = c.splits;
   q.plan = reinterpret_cast<int32_t *>(ws);
-  ws += align256((size_t)c.tiles * kPlanWords * 4);
+  ws += align256((size_t)up(a.num_rows, 32) * kPlanWords * 4);
   q.low = reinterpret_cast<uint16_t *>(ws);
   ws += align256((size_t)a.num_rows * a.rank * 2);
   q.part = reinterpret_cast<float *>(ws);
   const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)a.num_rows}, strides[] = {a.hidden * kSize};
   const uint32_t box[] = {kInner, (uint32_t)c.cols};
-  ep_status_t s = encode_map(&q.x, a.x, 2, dims, strides, box);
+  s = encode_map(&q.x, a.x, 2, dims, strides, box);
   if (s != EP_OK) return s;
   // stacks of adapters side by side while there are SMs for them
   const int named = a.num_adapters < c.cols ? a.num_adapters : c.cols;
@@ -385,6 +415,7 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
 
   Params p = {};
   p.max_cols = c.cols;
+  p.parts = c.parts;
   p.error_word = a.error_word;
   p.E = 1;
   p.cap = a.num_rows;

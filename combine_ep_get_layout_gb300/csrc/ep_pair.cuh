@@ -4,7 +4,7 @@
 //
 // A pair of CTAs computes a tile of 256 x up to 256: A, the operand with 256
 // rows, is the weights (so the ragged number of an expert's rows meets the
-// dimension that comes in steps of 16, not of 256), B the rows:
+// dimension that comes in steps of 32, not of 256), B the rows:
 //   kPlain, kGated   A = w[e] (inner dimension hidden),  B = rows of x
 //   kGradX           A = w[e]^T (inner dimension wide),  B = rows of g
 //   kGradW           A = g^T, B = x^T (inner dimension the expert's rows)
@@ -35,19 +35,20 @@ constexpr int kMaxCols = 256;        // columns of a tile
 constexpr int kTmemCols = 512;       // two tiles: one computed, one read out
 constexpr int kMaxStages = 12;
 constexpr int kSideStages = 4;
-constexpr int kBoxes = kMaxCols / 2 / 8;  // heights of a half of B
+constexpr int kBoxes = kMaxCols / 2 / 16;  // heights of a half of B
 // kAdapter, a tile: its number of adapters, their indices, each row's place among them or -1
 constexpr int kPlanWords = 1 + 2 * kMaxCols;
 constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
 constexpr int kStagingBytes = 32 * kPitch;       // a result warp's 32 rows
 constexpr int kExchangeBytes = 16 * 32 * 4;      // kGated: 16 columns of a warp, fp32
 constexpr int kResultWarps = 8;
+constexpr int kMaxParts = 4;         // pairs of a cluster, which share the inner dimension of one tile
 
 struct Params {
   // One copy a step and operand (a copy costs its issuing thread about 200
   // cycles, so their number bounds a step of 512): A's 128 rows (kGated: 64
   // of the gate and the 64 that they multiply), and a half of B of any
-  // height, b[i] of 8 (i + 1) rows.  Transposed operands are blocks of 64
+  // height, b[i] of 16 (i + 1) rows.  Transposed operands are blocks of 64
   // outer elements; b[0] is kGradW's, of two.
   CUtensorMap a, b[kBoxes];
   bool a_blocks, b_blocks;  // both blocks in one copy (their length is a multiple of 64), else in two
@@ -62,6 +63,8 @@ struct Params {
   int hidden;    // kGradW
   uint16_t *out, *preact;
   int max_cols;         // rows of a tile, at most
+  int parts;            // pairs that share a tile's inner dimension
+  int part_cols;        // columns of their results
   int stages, b_bytes;  // ring; bytes of a CTA's half of B in a stage
   // kAdapter
   const uint16_t *up;    // the up-projections [adapters][width][rank]
@@ -77,12 +80,13 @@ struct Barriers {
   uint64_t fixed[kMaxStages];  // and was trimmed
   uint64_t side_full[kSideStages], side_empty[kSideStages];  // kAdapter's further steps
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t part_full, part_empty;  // the other pairs' results in the first one's shared memory
   uint32_t tmem;
 };
 
 struct Tile {
   int e, first, count;  // rows of the tile (kGradW: all rows of the expert)
-  int cols;             // columns of the product (multiple of 16)
+  int cols;             // columns of the product (multiple of 32: what a pair's product takes)
   int part;             // which of the expert's tiles of rows
   int a0, b0;           // first row of A; kGradW: first column
   int steps;
@@ -149,7 +153,7 @@ struct Walker {
     } else {
       // as few tiles as hold the rows, of about equal size
       const int tiles = ceil_div(n, p.max_cols);
-      t.cols = ceil_div(ceil_div(n, tiles), 16) * 16;
+      t.cols = ceil_div(ceil_div(n, tiles), 32) * 32;
       if (F == kAdapter) {
         // eight tiles of rows go along A together, so the pairs running at
         // once share rows as well as weights
@@ -221,7 +225,7 @@ __device__ __forceinline__ int4 load_made(const int4 *p) {
 }
 
 template <Form F>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
   extern __shared__ char s_raw[];
   __shared__ Barriers s_bar;
   char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
@@ -229,9 +233,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
   char *side = ring + (size_t)p.stages * stage_bytes;
   char *staging = side + (F == kAdapter ? (size_t)p.side_stages * stage_bytes : 0);
   char *exchange = staging + kResultWarps * kStagingBytes;
+  // [parts - 1][columns][128]: the other pairs' results
+  float *joined = reinterpret_cast<float *>(exchange + (F == kGated ? kResultWarps * kExchangeBytes : 0));
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // A cluster is one pair, or the pairs that share a tile (`part`: which of them).
+  const uint32_t rank = cluster_rank() & 1u, lead = cluster_rank() & ~1u, both = 3u << lead;
+  const int part = (int)(cluster_rank() >> 1);
+  const int pair = blockIdx.x / (2 * p.parts), pairs = gridDim.x / (2 * p.parts);
+  const auto first_step = [&](const Tile &t) { return t.steps * part / p.parts; };
+  const auto last_step = [&](const Tile &t) { return t.steps * (part + 1) / p.parts; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -248,6 +258,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       mbar_init(&s_bar.acc_full[i], 1);
       mbar_init(&s_bar.acc_empty[i], 2 * kResultWarps);
     }
+    mbar_init(&s_bar.part_full, kResultWarps * (p.parts > 1 ? p.parts - 1 : 1));
+    mbar_init(&s_bar.part_empty, kResultWarps);
     fence_barrier_init();
     prefetch_map(&p.a);
   }
@@ -277,7 +289,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       const uint32_t bytes = kABytes + b_rows * 128;
       const int a0 = t.a0 + (int)rank * (F == kGated ? 64 : 128);
       const int b0 = (F == kGradW ? t.b0 : t.first) + (int)rank * b_rows;
-      for (int k = 0; k < t.steps; ++k) {
+      const int k1 = last_step(t);
+      for (int k = first_step(t); k < k1; ++k) {
         if (!__all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1))) {
           ok = false;
           break;
@@ -287,8 +300,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
           // both CTAs' copies complete on the leading CTA's barrier, but those
           // of a last step whose rows end raggedly go by the row ends
           const bool last = F == kGradW && t.count % 16 != 0 && k == t.steps - 1;
-          const uint32_t bar = last ? map_shared(smem_addr(&s_bar.ends[stage]), rank)
-                                    : map_shared(smem_addr(&s_bar.full[stage]), 0);
+          const uint32_t bar = last ? map_shared(smem_addr(&s_bar.ends[stage]), lead | rank)
+                                    : map_shared(smem_addr(&s_bar.full[stage]), lead);
           if (is_a) {
             if (last) mbar_arrive_expect_tx(&s_bar.ends[stage], bytes);
             if (rank == 0) {
@@ -318,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
               tile_load_2d(a + 8192, &p.a, a0 + 64, t.first + at, bar);
             }
           } else if (F != kGradW) {
-            tile_load_2d(b, &p.b[b_rows / 8 - 1], at, b0, bar);
+            tile_load_2d(b, &p.b[b_rows / 16 - 1], at, b0, bar);
           } else if (p.b_blocks) {
             tile_load_3d(b, &p.b[0], 0, t.first + at, b0 / 64, bar);
           } else {
@@ -356,7 +369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       const uint32_t d = tmem + acc * kMaxCols;
       ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1));
       tc_fence_after();
-      for (int k = 0; ok && k < t.steps; ++k) {
+      const int k0 = first_step(t), k1 = last_step(t);
+      for (int k = k0; ok && k < k1; ++k) {
         ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
         if (F == kGradW && ok && k == t.steps - 1 && t.count % 16 != 0) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster(&s_bar.fixed[stage], (trims >> stage) & 1u));
@@ -373,9 +387,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
           for (int j = 0; j < 4; ++j)
             if (j < parts)
               mma_pair(d, a + j * ((F == kGradX || F == kGradW ? 2048 : 32) >> 4), b + j * ((F == kGradW ? 2048 : 32) >> 4),
-                       idesc, k > 0 || j > 0);
-          commit_pair(&s_bar.empty[stage]);
-          if (F != kAdapter && k == t.steps - 1) commit_pair(&s_bar.acc_full[acc]);
+                       idesc, k > k0 || j > 0);
+          commit_pair(&s_bar.empty[stage], both);
+          if (F != kAdapter && k == k1 - 1) commit_pair(&s_bar.acc_full[acc], both);
         }
         __syncwarp();
         if (++stage == p.stages) {
@@ -386,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       if (F == kAdapter && ok) {
         if (n == pair) griddep_wait();
         const int length = p.rank * load_made(p.plan + t.part * kPlanWords);  // of the adapters side by side
-        for (int k = 0; ok && k * kInner < length; ++k) {
+        for (int k = part; ok && k * kInner < length; k += p.parts) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster(&s_bar.side_full[side_stage], side_phase));
           if (!ok) break;
           tc_fence_after();
@@ -395,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
           const int parts = min(4, ceil_div(length - k * kInner, 16));
           if (elect_one()) {
             for (int j = 0; j < parts; ++j) mma_pair(d, a + j * 2, b + j * 2, idesc, true);
-            commit_pair(&s_bar.side_empty[side_stage]);
+            commit_pair(&s_bar.side_empty[side_stage], both);
           }
           __syncwarp();
           if (++side_stage == p.side_stages) {
@@ -403,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             side_phase ^= 1;
           }
         }
-        if (ok && elect_one()) commit_pair(&s_bar.acc_full[acc]);
+        if (ok && elect_one()) commit_pair(&s_bar.acc_full[acc], both);
         __syncwarp();
       }
       acc ^= 1;
@@ -433,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.fixed[s]), 0));
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.fixed[s]), lead));
     }
   } else if (warp == 2 && F == kAdapter) {
     // ---------------------------------------------------------- adapters
@@ -449,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     const auto hand_over = [&] {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.side_full[hand]), 0));
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.side_full[hand]), lead));
       if (++hand == p.side_stages) hand = 0;
       --flying;
     };
@@ -462,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         place[i] = lane + 32 * i < b_rows ? load_made(plan + 1 + kMaxCols + (int)rank * b_rows + lane + 32 * i) : -1;
       const int a0 = t.a0 + (int)rank * 128;
       const uint16_t *low = p.low + (int64_t)(t.first + (int)rank * b_rows) * p.rank;
-      for (int k = 0; k * kInner < length; ++k) {
+      for (int k = part; k * kInner < length; k += p.parts) {
         ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
         if (!ok) break;
         const uint32_t a = smem_addr(side + (size_t)stage * stage_bytes), b = a + kABytes;
@@ -520,12 +534,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     const int w = warp - 4, quarter = w & 3, half = w >> 2;
     char *stage_buf = staging + w * kStagingBytes;
     int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t acc_phase = 0, part_phase = 0;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const auto release = [&](int a) {  // this warp has read its columns of accumulator a
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.acc_empty[a]), 0));
+      if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.acc_empty[a]), lead));
     };
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       if (F == kGradW && t.steps == 0) {
@@ -537,6 +551,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         continue;
       }
       ok = mbar_wait_pair(&s_bar.acc_full[acc], acc_phase);
+      if (F != kGradW && p.parts > 1) {
+        if (part > 0) {
+          // this pair's sums go to the first pair's CTA with the same rows
+          ok = ok && mbar_wait_cluster(&s_bar.part_empty, part_phase ^ 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          const uint32_t to = map_shared(smem_addr(joined + (part - 1) * p.part_cols * 128 + quarter * 32 + lane), rank);
+          for (int c = half * 32; c < t.cols; c += 64) {
+            float v[32];
+            tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < p.part_cols) store_cluster(to + (uint32_t)(c + j) * 512, v[j]);
+          }
+          release(acc);
+          fence_cluster();  // every lane's own stores, before one arrives for all
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.part_full), rank));
+          part_phase ^= 1;
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+          continue;
+        }
+        ok = ok && mbar_wait_cluster(&s_bar.part_full, part_phase);
+      }
       ok = F == kGated ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -544,6 +583,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         float v[32];
         tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
         if (c + 64 >= t.cols) release(acc);
+        if (F != kGradW && p.parts > 1) {
+          // the parts are added in their order
+          for (int q = 0; q + 1 < p.parts; ++q) {
+            const float *more = joined + (q * p.part_cols + c) * 128 + quarter * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < p.part_cols) v[j] += more[j * 128];
+          }
+        }
         const int left = t.count - c;  // rows of this chunk (not kGradW)
         if (F == kPlain || F == kGradX || F == kAdapter) {
           const int at = t.a0 + (int)rank * 128 + quarter * 32;
@@ -597,6 +645,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         }
       }
       if (t.cols <= half * 32) release(acc);  // no columns for this warp
+      if (F != kGradW && p.parts > 1) {
+        __syncwarp();
+        if (lane == 0)
+          for (int q = 1; q < p.parts; ++q) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.part_empty), 2 * q + rank));
+        part_phase ^= 1;
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
@@ -617,29 +671,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
   }
 }
 
-// Pairs of CTAs that fit the device at once.
+// Dynamic shared memory of the kernel: all that a block may have.
+int shared_limit(const DeviceInfo *di) { return (int)di->max_smem_per_block_optin - (int)sizeof(Barriers) - 1024; }
+
+// Clusters of `parts` pairs that fit the device at once.
 template <Form F>
-ep_status_t most_pairs(const DeviceInfo *di, size_t smem, int *pairs) {
-  static std::atomic<int> known[64];  // per device; the same for every call
-  if (known[di->device] == 0) {
+ep_status_t most_clusters(const DeviceInfo *di, int parts, int *clusters) {
+  const size_t smem = shared_limit(di);
+  static std::atomic<int> known[64][kMaxParts + 1];  // per device; the same for every call
+  if (known[di->device][parts] == 0) {
     cudaError_t e = cudaFuncSetAttribute(product_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(di->num_sms / 2 * 2);
+    cfg.gridDim = dim3(di->num_sms / (2 * parts) * (2 * parts));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.x = 2 * parts;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, product_kernel<F>, &cfg);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
-    known[di->device] = n > 0 ? n : 1;
+    known[di->device][parts] = n > 0 ? n : 1;
   }
-  *pairs = known[di->device];
+  *clusters = known[di->device][parts];
   return EP_OK;
 }
 
@@ -647,16 +705,33 @@ constexpr uint64_t kSize = 2;  // bytes of an element
 
 int up(int a, int b) { return (a + b - 1) / b; }
 
+// Pairs that may share a tile of so many columns: their sums wait in the
+// first pair's shared memory, beside its ring.
+int parts_for(int cols) { return cols <= 64 ? kMaxParts : cols <= 128 ? 2 : 1; }
+
+// p.parts: 0, chosen here, or the caller's choice.
 template <Form F>
 ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream_t stream) {
   const DeviceInfo *di = current_device_info();
   if (di == nullptr) return EP_ERR_CUDA;
+  const int cols = F == kGradW || most_rows > p.max_cols ? p.max_cols : up(most_rows, 32) * 32;
+  if (p.parts == 0) {
+    // Few tiles leave SMs idle: two or four pairs share one while there is a
+    // pair for each.  The number of tiles is known on the device only, so its
+    // bound decides.
+    p.parts = 1;
+    if (F != kGradW)
+      while (p.parts * 2 <= parts_for(cols) && most_tiles * p.parts * 2 <= di->num_sms / 2 &&
+             up(p.inner, kInner) >= 4 * p.parts)
+        p.parts *= 2;
+  }
+  p.part_cols = cols;
   // The ring takes what is left of shared memory: a stage holds 128 rows of A
   // and half of the most columns that a tile can have.
-  const int cols = F == kGradW || most_rows > p.max_cols ? p.max_cols : up(most_rows, 16) * 16;
   p.b_bytes = cols / 2 * 128;  // a multiple of 1024, as the swizzle needs
-  const int fixed = 1024 + kResultWarps * kStagingBytes + (F == kGated ? kResultWarps * kExchangeBytes : 0);
-  const int limit = (int)di->max_smem_per_block_optin - (int)sizeof(Barriers) - 1024;
+  const int fixed = 1024 + kResultWarps * kStagingBytes + (F == kGated ? kResultWarps * kExchangeBytes : 0) +
+                    (p.parts - 1) * cols * 128 * 4;
+  const int limit = shared_limit(di);
   p.stages = (limit - fixed) / (kABytes + p.b_bytes);
   if (F == kAdapter) {
     p.side_stages = p.stages >= 8 ? kSideStages : 2;
@@ -664,20 +739,33 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
   }
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = (size_t)limit;
-  int pairs = 0;
-  ep_status_t s = most_pairs<F>(di, smem, &pairs);
+  int clusters = 0;
+  const ep_status_t s = most_clusters<F>(di, p.parts, &clusters);
   if (s != EP_OK) return s;
-  if (most_tiles < pairs) pairs = (int)most_tiles;
-  const cudaError_t e = launch_kernel(product_kernel<F>, 2 * pairs, kThreads, smem, stream, false, p);
+  if (most_tiles < clusters) clusters = (int)most_tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.parts * clusters);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * p.parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kUsePdl ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, product_kernel<F>, p);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "product launch");
 }
 
 // Rows [rows][length] by halves of B of every height up to `most`.
 ep_status_t row_maps(Params &p, const void *rows, int length, int cap, int most) {
   const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {length * kSize};
-  const int cols = most > p.max_cols ? p.max_cols : up(most, 16) * 16;
-  for (int i = 0; i < cols / 16; ++i) {
-    const uint32_t box[] = {kInner, 8u * (i + 1)};
+  const int cols = most > p.max_cols ? p.max_cols : up(most, 32) * 32;
+  for (int i = 0; i < cols / 32; ++i) {
+    const uint32_t box[] = {kInner, 16u * (i + 1)};
     const ep_status_t s = encode_map(&p.b[i], rows, 2, dims, strides, box);
     if (s != EP_OK) return s;
   }

@@ -100,6 +100,9 @@ ep_status_t weight_map(Params &p, Form form, const void *w, int wide, int hidden
   return encode_map(&p.a, w, 3, dims, strides, box);
 }
 
+// Tiles of rows, at most: an expert with n rows has n / 256 rounded up.
+int64_t most_tiles(int cap, int experts) { return cap / kMaxCols + (cap < experts ? cap : experts); }
+
 }  // namespace
 
 ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
@@ -121,7 +124,7 @@ ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
   ep_status_t s = weight_map(p, a.gated ? kGated : kPlain, a.w, p.wide, a.hidden);
   if (s == EP_OK) s = row_maps(p, a.x, a.hidden, a.recv_capacity, most);
   if (s != EP_OK) return s;
-  const int64_t tiles = ((int64_t)a.recv_capacity / kMaxCols + a.num_experts) * p.a_tiles;
+  const int64_t tiles = most_tiles(a.recv_capacity, a.num_experts) * p.a_tiles;
   return a.gated ? launch_form<kGated>(p, most, tiles, stream) : launch_form<kPlain>(p, most, tiles, stream);
 }
 
@@ -160,10 +163,11 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     ep_status_t s = weight_map(p, kGradX, a.w, wide, a.hidden);
     if (s == EP_OK) s = row_maps(p, g, wide, a.recv_capacity, most);
     if (s == EP_OK)
-      s = launch_form<kGradX>(p, most, ((int64_t)a.recv_capacity / kMaxCols + a.num_experts) * p.a_tiles, stream);
+      s = launch_form<kGradX>(p, most, most_tiles(a.recv_capacity, a.num_experts) * p.a_tiles, stream);
     if (s != EP_OK) return s;
   }
   if (a.grad_w != nullptr) {
+    p.parts = 0;
     p.a_tiles = up(wide, 256);
     p.b_tiles = up(a.hidden, 256);
     p.out = a.grad_w;

@@ -42,6 +42,12 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+__device__ __forceinline__ void store_cluster(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -160,13 +166,13 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uin
       : "memory");
 }
 
-// Arrives on the barrier at this offset in both CTAs once the products issued
-// so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+// Arrives on the barrier at this offset in the CTAs of `mask` (both of the
+// pair) once the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t *bar, uint32_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_addr(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)mask)
       : "memory");
 }
 
@@ -222,9 +228,12 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
 // rows 1024 bytes apart, version, swizzle).  inner_desc: inner dimension
 // contiguous, rows of 128 bytes.  outer_desc: outer dimension contiguous,
 // blocks of 64 outer elements (128 bytes), `block` bytes apart, each one row
-// per inner element.
-__device__ __forceinline__ uint32_t inner_desc(uint32_t addr) { return (addr >> 4) | (1u << 16); }
-__device__ __forceinline__ uint32_t outer_desc(uint32_t addr, uint32_t block) { return (addr >> 4) | ((block >> 4) << 16); }
+// per inner element.  A shared address carries the CTA's rank in the cluster
+// above its low 18 bits, which must not reach the block distance.
+__device__ __forceinline__ uint32_t inner_desc(uint32_t addr) { return ((addr & 0x3ffffu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t outer_desc(uint32_t addr, uint32_t block) {
+  return ((addr & 0x3ffffu) >> 4) | ((block >> 4) << 16);
+}
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 256 over the pair, N
 // columns; bit 15 / 16: A / B with the outer dimension contiguous.
