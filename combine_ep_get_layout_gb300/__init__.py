@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -727,6 +728,7 @@ def ep_expert_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Ten
     return grad_x, grad_w
 
 
+@lru_cache(maxsize=256)
 def ep_adapter_workspace_bytes(num_rows: int, hidden: int, rank: int) -> int:
     return int(N.load().ep_adapter_workspace_bytes(num_rows, hidden, rank))
 

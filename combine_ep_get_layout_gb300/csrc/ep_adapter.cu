@@ -28,7 +28,7 @@ constexpr int kMaxSplits = 8;     // CTAs of a cluster
 
 struct LowParams {
   CUtensorMap x;  // boxes of 64 x cols
-  const uint16_t *a;
+  const uint16_t *a, *rows_x;
   const int64_t *index;
   const float *scale;
   uint32_t *error_word;
@@ -45,6 +45,109 @@ struct LowBarriers {
   uint64_t acc_full, acc_empty;
   uint32_t tmem;
 };
+
+// The adapters of a tile in the order in which its rows name them (*list),
+// each row's place among them or -1 (*place), their number; written to the
+// plan if `write`.  table[adapters] holds kMaxCols in every entry.  The whole
+// block calls it.
+__device__ __forceinline__ int list_adapters(const LowParams &p, int tile, int *table, int *place, int *list,
+                                             uint32_t *first_of, bool write) {
+  const int first = tile * p.cols, rows = min(p.cols, p.T - first);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < p.cols; i += blockDim.x) {
+    int a = -1;
+    if (i < rows) {
+      const int64_t v = p.index[first + i];
+      if (v >= 0 && v < p.adapters)
+        a = (int)v;
+      else if (v != -1)
+        set_error(p.error_word, EP_ERRBIT_BAD_INDEX);
+    }
+    place[i] = a;
+    if (a >= 0) atomicMin(&table[a], i);
+  }
+  __syncthreads();
+  for (int b = warp; b < kMaxCols / 32; b += blockDim.x / 32) {
+    const int i = b * 32 + lane;
+    const int a = i < p.cols ? place[i] : -1;
+    const uint32_t m = __ballot_sync(0xffffffffu, a >= 0 && table[a] == i);
+    if (lane == 0) first_of[b] = m;
+  }
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int b = 0; b < kMaxCols / 32; ++b) count += __popc(first_of[b]);
+  for (int i = threadIdx.x; i < p.cols; i += blockDim.x) {
+    const int a = place[i];
+    if (a < 0) continue;
+    const int f = table[a];
+    int n = 0;  // rows before f that name an adapter first
+#pragma unroll
+    for (int b = 0; b < kMaxCols / 32; ++b)
+      n += __popc(first_of[b] & (b < f >> 5 ? ~0u : b == f >> 5 ? (1u << (f & 31)) - 1u : 0u));
+    if (f == i) list[n] = a;
+    place[i] = n;
+  }
+  __syncthreads();
+  if (write) {
+    int32_t *plan = p.plan + (int64_t)tile * kPlanWords;
+    if (threadIdx.x == 0) plan[0] = count;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) plan[1 + i] = list[i];
+    for (int i = threadIdx.x; i < p.cols; i += blockDim.x) plan[1 + kMaxCols + i] = place[i];
+  }
+  return count;
+}
+
+// The low rows of few rows: a block a row, which reads its adapter's
+// down-projection by itself (rows of one adapter meet it in L2), a warp two
+// of its vectors at a time; the first blocks make the tiles' plans.
+constexpr int kRowThreads = 256;
+constexpr int64_t kRowBytes = 64 << 20;
+
+__global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_constant__ LowParams p, int tiles) {
+  extern __shared__ int s_dyn[];  // [adapters]
+  __shared__ int s_place[kMaxCols], s_list[kMaxCols];
+  __shared__ uint32_t s_first[kMaxCols / 32];
+  if ((int)blockIdx.x < tiles)
+    for (int i = threadIdx.x; i < p.adapters; i += kRowThreads) s_dyn[i] = kMaxCols;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  if ((int)blockIdx.x < tiles) {
+    list_adapters(p, blockIdx.x, s_dyn, s_place, s_list, s_first, true);
+    return;
+  }
+  const int t = blockIdx.x - tiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t a = p.index[t];
+  if (a < 0 || a >= p.adapters) return;
+  const uint16_t *x = p.rows_x + (int64_t)t * p.hidden;
+  const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + a);
+  for (int i = warp * 2; i < p.rank; i += kRowThreads / 32 * 2) {
+    const uint16_t *v = p.a + (a * p.rank + i) * p.hidden;
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll 4
+    for (int k = lane * 8; k < p.hidden; k += 256) {
+      const int4 xv = __ldg(reinterpret_cast<const int4 *>(x + k));
+      const int4 a0 = __ldg(reinterpret_cast<const int4 *>(v + k));
+      const int4 a1 = __ldg(reinterpret_cast<const int4 *>(v + p.hidden + k));
+      const uint32_t *xw = reinterpret_cast<const uint32_t *>(&xv);
+      const uint32_t *w0 = reinterpret_cast<const uint32_t *>(&a0), *w1 = reinterpret_cast<const uint32_t *>(&a1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[0] += bf16_lo(xw[j]) * bf16_lo(w0[j]);
+        sum[0] += bf16_hi(xw[j]) * bf16_hi(w0[j]);
+        sum[1] += bf16_lo(xw[j]) * bf16_lo(w1[j]);
+        sum[1] += bf16_hi(xw[j]) * bf16_hi(w1[j]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+    }
+    if (lane == 0) *reinterpret_cast<uint32_t *>(p.low + (int64_t)t * p.rank + i) = pack_bf16x2(sum[0] * f, sum[1] * f);
+  }
+}
 
 // A barrier of the first four warps; whether all of them say `ok`.
 __device__ __forceinline__ bool four_agree(bool ok) {
@@ -95,48 +198,7 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
   griddep_wait();
   griddep_launch_dependents();
 
-  // The tile's adapters in the order in which its rows name them.
-  for (int i = threadIdx.x; i < p.cols; i += kLowThreads) {
-    int a = -1;
-    if (i < rows) {
-      const int64_t v = p.index[first + i];
-      if (v >= 0 && v < p.adapters)
-        a = (int)v;
-      else if (v != -1)
-        set_error(p.error_word, EP_ERRBIT_BAD_INDEX);
-    }
-    s_place[i] = a;
-    if (a >= 0) atomicMin(&s_table[a], i);
-  }
-  __syncthreads();
-  for (int b = warp; b < kMaxCols / 32; b += kLowThreads / 32) {
-    const int i = b * 32 + lane;
-    const int a = i < p.cols ? s_place[i] : -1;
-    const uint32_t m = __ballot_sync(0xffffffffu, a >= 0 && s_table[a] == i);
-    if (lane == 0) s_first[b] = m;
-  }
-  __syncthreads();
-  int count = 0;
-  for (int b = 0; b < kMaxCols / 32; ++b) count += __popc(s_first[b]);
-  const auto place_of = [&](int i) {  // rows before i that name an adapter first
-    int n = __popc(s_first[i >> 5] & ((1u << (i & 31)) - 1u));
-    for (int b = 0; b < (i >> 5); ++b) n += __popc(s_first[b]);
-    return n;
-  };
-  for (int i = threadIdx.x; i < p.cols; i += kLowThreads) {
-    const int a = s_place[i];
-    if (a < 0) continue;
-    const int f = s_table[a], n = place_of(f);
-    if (f == i) s_list[n] = a;
-    s_place[i] = n;
-  }
-  __syncthreads();
-  if (split == 0 && blockIdx.z == 0) {
-    int32_t *plan = p.plan + (int64_t)blockIdx.x * kPlanWords;
-    if (threadIdx.x == 0) plan[0] = count;
-    for (int i = threadIdx.x; i < count; i += kLowThreads) plan[1 + i] = s_list[i];
-    for (int i = threadIdx.x; i < p.cols; i += kLowThreads) plan[1 + kMaxCols + i] = s_place[i];
-  }
+  const int count = list_adapters(p, blockIdx.x, s_table, s_place, s_list, s_first, split == 0 && blockIdx.z == 0);
 
   const int per = 128 / p.rank;  // adapters of a stack
   const int stacks = ceil_div(count, per);
@@ -318,7 +380,7 @@ ep_status_t choose(const DeviceInfo *di, int num_rows, int hidden, int width, Cu
     c.tiles = up(num_rows, most);
     c.cols = up(up(num_rows, c.tiles), 32) * 32;
     c.tiles = up(num_rows, c.cols);
-    for (c.parts = 1; c.parts <= parts_for(c.cols); c.parts *= 2) {
+    for (c.parts = 1; c.parts <= parts_for(c.cols); ++c.parts) {
       int clusters = 0;
       const ep_status_t s = most_clusters<kAdapter>(di, c.parts, &clusters);
       if (s != EP_OK) return s;
@@ -341,43 +403,19 @@ ep_status_t choose(const DeviceInfo *di, int num_rows, int hidden, int width, Cu
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-}  // namespace
+// Where every row may read its adapter by itself: up to 64 MB from L2.
+bool row_kernel(const AdapterArgs &a) { return (int64_t)a.num_rows * a.rank * a.hidden * 2 <= kRowBytes; }
 
-size_t adapter_workspace_bytes(int num_rows, int hidden, int rank) {
-  if (num_rows == 0) return 0;
-  // whatever the cut: tiles of 32 columns or more, splits as for the fewest tiles
-  const int splits = low_splits(up(num_rows, kMaxCols), hidden);
-  return align256((size_t)up(num_rows, 32) * kPlanWords * 4) + align256((size_t)num_rows * rank * 2) +
-         align256(splits > 1 ? (size_t)splits * num_rows * rank * 4 : 0);
+ep_status_t launch_rows(const LowParams &q, const Cut &c, cudaStream_t stream) {
+  const cudaError_t e = launch_kernel(adapter_row_kernel, q.T + c.tiles, kRowThreads, (size_t)q.adapters * 4, stream,
+                                      false, q, c.tiles);
+  return e == cudaSuccess ? EP_OK : cuda_fail(e, "adapter_row launch");
 }
 
-ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
-  if (a.num_rows == 0) return EP_OK;
-  const DeviceInfo *di = current_device_info();
-  if (di == nullptr) return EP_ERR_CUDA;
-  Cut c;
-  ep_status_t s = choose(di, a.num_rows, a.hidden, a.width, &c);
-  if (s != EP_OK) return s;
-  char *ws = static_cast<char *>(a.workspace);
-  LowParams q = {};
-  q.a = a.lora_a;
-  q.index = a.adapter_idx;
-  q.scale = a.adapter_scale;
-  q.error_word = a.error_word;
-  q.T = a.num_rows;
-  q.hidden = a.hidden;
-  q.rank = a.rank;
-  q.adapters = a.num_adapters;
-  q.cols = c.cols;
-  q.splits = c.splits;
-  q.plan = reinterpret_cast<int32_t *>(ws);
-  ws += align256((size_t)up(a.num_rows, 32) * kPlanWords * 4);
-  q.low = reinterpret_cast<uint16_t *>(ws);
-  ws += align256((size_t)a.num_rows * a.rank * 2);
-  q.part = reinterpret_cast<float *>(ws);
+ep_status_t launch_low(LowParams &q, const AdapterArgs &a, const Cut &c, const DeviceInfo *di, cudaStream_t stream) {
   const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)a.num_rows}, strides[] = {a.hidden * kSize};
   const uint32_t box[] = {kInner, (uint32_t)c.cols};
-  s = encode_map(&q.x, a.x, 2, dims, strides, box);
+  const ep_status_t s = encode_map(&q.x, a.x, 2, dims, strides, box);
   if (s != EP_OK) return s;
   // stacks of adapters side by side while there are SMs for them
   const int named = a.num_adapters < c.cols ? a.num_adapters : c.cols;
@@ -411,7 +449,46 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = kUsePdl ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q);
-  if (e != cudaSuccess) return cuda_fail(e, "adapter_low launch");
+  return e == cudaSuccess ? EP_OK : cuda_fail(e, "adapter_low launch");
+}
+
+}  // namespace
+
+size_t adapter_workspace_bytes(int num_rows, int hidden, int rank) {
+  if (num_rows == 0) return 0;
+  // whatever the cut: tiles of 32 columns or more, splits as for the fewest tiles
+  const int splits = low_splits(up(num_rows, kMaxCols), hidden);
+  return align256((size_t)up(num_rows, 32) * kPlanWords * 4) + align256((size_t)num_rows * rank * 2) +
+         align256(splits > 1 ? (size_t)splits * num_rows * rank * 4 : 0);
+}
+
+ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
+  if (a.num_rows == 0) return EP_OK;
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
+  Cut c;
+  ep_status_t s = choose(di, a.num_rows, a.hidden, a.width, &c);
+  if (s != EP_OK) return s;
+  char *ws = static_cast<char *>(a.workspace);
+  LowParams q = {};
+  q.a = a.lora_a;
+  q.rows_x = a.x;
+  q.index = a.adapter_idx;
+  q.scale = a.adapter_scale;
+  q.error_word = a.error_word;
+  q.T = a.num_rows;
+  q.hidden = a.hidden;
+  q.rank = a.rank;
+  q.adapters = a.num_adapters;
+  q.cols = c.cols;
+  q.splits = c.splits;
+  q.plan = reinterpret_cast<int32_t *>(ws);
+  ws += align256((size_t)up(a.num_rows, 32) * kPlanWords * 4);
+  q.low = reinterpret_cast<uint16_t *>(ws);
+  ws += align256((size_t)a.num_rows * a.rank * 2);
+  q.part = reinterpret_cast<float *>(ws);
+  s = row_kernel(a) ? launch_rows(q, c, stream) : launch_low(q, a, c, di, stream);
+  if (s != EP_OK) return s;
 
   Params p = {};
   p.max_cols = c.cols;

@@ -716,14 +716,16 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
   if (di == nullptr) return EP_ERR_CUDA;
   const int cols = F == kGradW || most_rows > p.max_cols ? p.max_cols : up(most_rows, 32) * 32;
   if (p.parts == 0) {
-    // Few tiles leave SMs idle: two or four pairs share one while there is a
-    // pair for each.  The number of tiles is known on the device only, so its
-    // bound decides.
+    // Few tiles leave SMs idle: up to four pairs share one while there is a
+    // pair for each and each has four steps.  The number of tiles is known on
+    // the device only, so its bound decides.
     p.parts = 1;
-    if (F != kGradW)
-      while (p.parts * 2 <= parts_for(cols) && most_tiles * p.parts * 2 <= di->num_sms / 2 &&
-             up(p.inner, kInner) >= 4 * p.parts)
-        p.parts *= 2;
+    for (int n = 2; F != kGradW && n <= parts_for(cols) && up(p.inner, kInner) >= 4 * n; ++n) {
+      int clusters = 0;
+      const ep_status_t s = most_clusters<F>(di, n, &clusters);
+      if (s != EP_OK) return s;
+      if (most_tiles <= clusters) p.parts = n;
+    }
   }
   p.part_cols = cols;
   // The ring takes what is left of shared memory: a stage holds 128 rows of A
