@@ -102,7 +102,7 @@ __device__ __forceinline__ int list_adapters(const LowParams &p, int tile, int *
 // down-projection by itself (rows of one adapter meet it in L2), a warp two
 // of its vectors at a time; the first blocks make the tiles' plans.
 constexpr int kRowThreads = 256;
-constexpr int64_t kRowBytes = 64 << 20;
+constexpr int64_t kRowBytes = 128 << 20;
 
 __global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_constant__ LowParams p, int tiles) {
   extern __shared__ int s_dyn[];  // [adapters]
@@ -403,7 +403,7 @@ ep_status_t choose(const DeviceInfo *di, int num_rows, int hidden, int width, Cu
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Where every row may read its adapter by itself: up to 64 MB from L2.
+// Where every row may read its adapter by itself: up to 128 MB from L2.
 bool row_kernel(const AdapterArgs &a) { return (int64_t)a.num_rows * a.rank * a.hidden * 2 <= kRowBytes; }
 
 ep_status_t launch_rows(const LowParams &q, const Cut &c, cudaStream_t stream) {

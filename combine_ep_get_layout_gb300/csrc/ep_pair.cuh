@@ -28,7 +28,10 @@ namespace {
 
 enum Form { kPlain, kGated, kGradX, kGradW, kAdapter };
 
-constexpr int kThreads = 384;        // warps: 0 and 3 copies of A and B, 1 products, 2 row ends (kGradW) and low rows (kAdapter), 4-11 results
+// Warps: 0 and 3 copies of A and B, 1 products, 2 row ends (kGradW), 4-11
+// results; kAdapter: 12-15 gather the adapters.
+constexpr int kGatherWarps = 4;
+__host__ __device__ constexpr int threads_of(Form f) { return f == kAdapter ? 384 + 32 * kGatherWarps : 384; }
 constexpr int kInner = 64;           // elements of an inner step
 constexpr int kABytes = 128 * 128;   // a CTA's half of A for one step
 constexpr int kMaxCols = 256;        // columns of a tile
@@ -225,7 +228,7 @@ __device__ __forceinline__ int4 load_made(const int4 *p) {
 }
 
 template <Form F>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_constant__ Params p) {
   extern __shared__ char s_raw[];
   __shared__ Barriers s_bar;
   char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       mbar_init(&s_bar.fixed[i], 2);  // one arrival from each CTA
     }
     for (int i = 0; i < kSideStages; ++i) {
-      mbar_init(&s_bar.side_full[i], 2);  // one arrival from each CTA
+      mbar_init(&s_bar.side_full[i], 2 * kGatherWarps);
       mbar_init(&s_bar.side_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -449,13 +452,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.fixed[s]), lead));
     }
-  } else if (warp == 2 && F == kAdapter) {
+  } else if (F == kAdapter && warp >= 12) {
     // ---------------------------------------------------------- adapters
     // Both operands of a further step are gathered 16 bytes at a time, in the
     // swizzled order that a tile's copy would give them: eight lanes take the
     // eight pieces of a row, so a lane stays with one adapter in a step.
+    griddep_wait();
     Walker<F> walk(p);
     Tile t;
+    const int rows = (warp - 12) * 32;  // this warp's of A, and of B
     int stage = 0, hand = 0;  // hand: the stage handed over next
     uint32_t phase = 0;
     int flying = 0;
@@ -470,10 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       const int32_t *plan = p.plan + t.part * kPlanWords;
       const int count = load_made(plan), length = count * p.rank, b_rows = t.cols / 2;
-      int place[4];  // of the rows lane, lane + 32, ... of this CTA's half
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        place[i] = lane + 32 * i < b_rows ? load_made(plan + 1 + kMaxCols + (int)rank * b_rows + lane + 32 * i) : -1;
+      const int place = rows + lane < b_rows ? load_made(plan + 1 + kMaxCols + (int)rank * b_rows + rows + lane) : -1;
       const int a0 = t.a0 + (int)rank * 128;
       const uint16_t *low = p.low + (int64_t)(t.first + (int)rank * b_rows) * p.rank;
       for (int k = part; k * kInner < length; k += p.parts) {
@@ -485,23 +487,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (piece * 8 < ceil_div(min(length - k * kInner, kInner), 16) * 16) {
           const int adapter = there ? load_made(plan + 1 + mine) : 0;
           const uint16_t *up = p.up + ((int64_t)adapter * p.width + a0) * p.rank + in;
-#pragma unroll 8
-          for (int r = lane >> 3; r < 128; r += 4) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = rows + j * 4 + (lane >> 3);
             const bool some = there && a0 + r < p.width;
             copy16(a + r * 128 + ((piece ^ (r & 7)) << 4), some ? up + (int64_t)r * p.rank : p.up, some);
           }
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = i * 32 + j * 4 + (lane >> 3);
-            const int at = __shfl_sync(0xffffffffu, place[i], j * 4 + (lane >> 3));
-            const bool some = there && at == mine;
-            if (r < b_rows)
-              copy16(b + r * 128 + ((piece ^ (r & 7)) << 4), some ? low + (int64_t)r * p.rank + in : p.low, some);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const int r = rows + j * 4 + (lane >> 3);
+          const bool some = __shfl_sync(0xffffffffu, place, j * 4 + (lane >> 3)) == mine && there;
+          if (r < b_rows)
+            copy16(b + r * 128 + ((piece ^ (r & 7)) << 4), some ? low + (int64_t)r * p.rank + in : p.low, some);
+        }
         copy_commit();
         ++flying;
         if (flying == 2) {
@@ -684,7 +684,7 @@ ep_status_t most_clusters(const DeviceInfo *di, int parts, int *clusters) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(di->num_sms / (2 * parts) * (2 * parts));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(F));
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -747,7 +747,7 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
   if (most_tiles < clusters) clusters = (int)most_tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.parts * clusters);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(F));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
