@@ -298,3 +298,69 @@ def test_gradient_of_masked_and_bad_choices():
         (weights64(x, idx[:1], score, False, 1.0) * grad[:1].double()).sum().backward()
         np.testing.assert_allclose(got[:1].numpy(), x.grad.numpy(), rtol=2e-5, atol=1e-6)
         assert got[2, 3] == 0 and got[2, 4] != 0
+
+
+# ---------------------------------------- enough tokens for a lane a token
+
+MANY = 2051
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(1, 1), (8, 8), (7, 3), (64, 6), (33, 16), (256, 8), (257, 5), (384, 10), (1000, 12),
+                                 (1024, 1), (100, 17)])
+def test_many_sizes_and_types(E, K, score, dtype):
+    b = torch.randn(E, generator=torch.Generator().manual_seed(5)) * 0.1
+    x = make_logits(MANY, E, dtype, E)
+    x[5] = -math.inf
+    x[6, E // 2:] = -math.inf
+    for renorm, bias in ((True, None), (False, None), (True, b), (False, b)):
+        check(x, K, score, bias, renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,Gk,K", [(64, 8, 4, 6), (256, 8, 3, 8), (256, 64, 2, 8), (96, 3, 2, 16), (40, 40, 5, 4),
+                                      (1024, 16, 16, 8), (72, 2, 1, 16), (72, 6, 3, 7)])
+@pytest.mark.parametrize("top", [1, 2])
+def test_many_groups(E, G, Gk, K, top, score):
+    bias = torch.randn(E, generator=torch.Generator().manual_seed(7)) * 0.1
+    for b in (None, bias):
+        x = make_logits(MANY, E, torch.float32, E + G)
+        x[3] = -math.inf
+        x[4, E // 4:] = -math.inf
+        check(x, K, score, b, G, Gk, top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("G,Gk,top", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
+def test_many_ties_and_extremes(G, Gk, top, score):
+    """Ties; logits that differ by less than a key's upper bits; masks, the
+    type's lowest value, infinities and NaN."""
+    E, K = 64, 8
+    x = make_logits(MANY, E, torch.float32, 1, lattice=True)
+    x[100:200] = 0.0
+    x[200:] = torch.where(torch.rand((MANY - 200, 1), generator=torch.Generator().manual_seed(1)) < 0.5, x[200:],
+                          1.0 + torch.randint(0, 40, (MANY - 200, E), generator=torch.Generator().manual_seed(2)) * 2.0 ** -22)
+    low = torch.finfo(torch.float32).min
+    x[0], x[1], x[2, :60], x[3, ::2], x[4] = -math.inf, low, -math.inf, math.nan, math.nan
+    x[5, 7] = x[6, 7] = x[6, 9] = math.inf
+    x[7] = 1e30 * torch.sign(x[7])
+    x[8, 5:] = low
+    x[9] = -200.0
+    if G == 1 or top == 1:
+        check(x, K, score, None, G, Gk, top)  # compared as logits: exact
+    check(x[:200].repeat(11, 1), K, score, None, G, Gk, top)
+    check(x[:200].repeat(11, 1), K, score, torch.zeros(E), G, Gk, top)
+
+
+def test_the_two_forms_agree():
+    """The same rows by a warp a token and by a lane a token: bit for bit the
+    choice, where keys are logits, and the weights within their bound."""
+    x = make_logits(MANY, 128, torch.float32, 13).to(DEV)
+    many = ep.ep_route(x, 7)
+    few = [ep.ep_route(x[i:i + 500], 7) for i in range(0, MANY, 500)]
+    assert torch.equal(many.topk_idx, torch.cat([r.topk_idx for r in few]))
+    torch.testing.assert_close(many.topk_weights, torch.cat([r.topk_weights for r in few]), rtol=4e-6, atol=0)
+    part = make_logits(MANY, 160, torch.bfloat16, 14).to(DEV)[:, 5:133]  # rows that start at odd places
+    a, b = ep.ep_route(part, 7), ep.ep_route(part.contiguous(), 7)
+    assert torch.equal(a.topk_idx, b.topk_idx) and torch.equal(a.topk_weights, b.topk_weights)
