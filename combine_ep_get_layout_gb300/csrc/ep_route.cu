@@ -24,7 +24,8 @@ namespace {
 constexpr int kRouteWarps = 4;
 constexpr int kLanesTokens = 2048;
 constexpr int kLaneWarps = 4;
-constexpr int kLoads = 8;  // of 16 bytes in flight a lane
+constexpr float kMost = 3.402823466e38f;
+constexpr uint32_t kLeast = 0x00800000u;  // order_of the lowest number, its low bits cleared
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct RouteParams {
@@ -55,6 +56,16 @@ __device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + exp
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);  // -0 counts as +0
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// The same for a float that is not -0.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const int b = __float_as_int(v);
+  return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -190,8 +201,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
 // ------------------------------------------------------------- many tokens
 // A lane a token: no exchange between lanes, and a selection by sorting
 // networks, whose steps are one minimum and one maximum.  32 rows lie in
-// shared memory, pieces of 16 bytes at (piece ^ (row & 7)), so that the lanes
-// read the same place of their rows without conflicts.  The networks sort
+// shared memory an odd number of 16-byte pieces apart, so that the lanes read
+// the same place of their rows without conflicts.  The networks sort
 // words of a key's upper bits over the complement of its index (ties go to
 // the lowest); the few words found are then ordered by their keys, and where
 // the upper bits alone cannot tell the last choice from what was left out, the
@@ -199,42 +210,60 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Scores for keys, a few units in the last place from the weights' own.
-__device__ __forceinline__ float sigmoid_key(float l) { return rcp_approx(1.0f + exp2_approx(-l * kLog2e)); }
+__device__ __forceinline__ float sigmoid_key(float l) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_approx(-l * kLog2e)));
+  return r;
+}
 
-template <int N>
-__device__ __forceinline__ void merge_words(uint32_t (&w)[N]) {  // a bitonic sequence, to descending order
+enum KeyKind { kLogitKey, kSigmoidKey, kSoftmaxKey };
+
+__device__ __forceinline__ void order_words(uint32_t &a, uint32_t &b) {
+  const uint32_t x = max(a, b);
+  b = min(a, b);
+  a = x;
+}
+
+// Words L ... L + N - 1, a bitonic sequence, to descending order.
+template <int L, int N, int M>
+__device__ __forceinline__ void merge_words(uint32_t (&w)[M]) {
+  if constexpr (N > 1) {
 #pragma unroll
-  for (int d = N / 2; d > 0; d >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if ((i & d) == 0) {
-        const uint32_t a = w[i], b = w[i + d];
-        w[i] = max(a, b);
-        w[i + d] = min(a, b);
-      }
+    for (int i = 0; i < N / 2; ++i) order_words(w[L + i], w[L + N / 2 + i]);
+    merge_words<L, N / 2>(w);
+    merge_words<L + N / 2, N / 2>(w);
+  }
+}
+
+// Words L ... L + 7 to descending order, Batcher's odd-even merge sort.
+template <int L, int M>
+__device__ __forceinline__ void sort_eight(uint32_t (&w)[M]) {
+  order_words(w[L + 0], w[L + 1]); order_words(w[L + 2], w[L + 3]); order_words(w[L + 4], w[L + 5]);
+  order_words(w[L + 6], w[L + 7]); order_words(w[L + 0], w[L + 2]); order_words(w[L + 1], w[L + 3]);
+  order_words(w[L + 4], w[L + 6]); order_words(w[L + 5], w[L + 7]); order_words(w[L + 1], w[L + 2]);
+  order_words(w[L + 5], w[L + 6]); order_words(w[L + 0], w[L + 4]); order_words(w[L + 1], w[L + 5]);
+  order_words(w[L + 2], w[L + 6]); order_words(w[L + 3], w[L + 7]); order_words(w[L + 2], w[L + 4]);
+  order_words(w[L + 3], w[L + 5]); order_words(w[L + 1], w[L + 2]); order_words(w[L + 3], w[L + 4]);
+  order_words(w[L + 5], w[L + 6]);
 }
 
 template <int N>
-__device__ __forceinline__ void sort_words(uint32_t (&w)[N]) {  // to descending order
+__device__ __forceinline__ void sort_words(uint32_t (&w)[N]) {
+  sort_eight<0>(w);
+  if constexpr (N == 16) {
+    sort_eight<8>(w);
 #pragma unroll
-  for (int size = 2; size <= N; size <<= 1)
-#pragma unroll
-    for (int d = size / 2; d > 0; d >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if ((i & d) == 0) {
-          const bool down = (i & size) == 0 || size == N;
-          const uint32_t a = w[i], b = w[i + d];
-          w[i] = down ? max(a, b) : min(a, b);
-          w[i + d] = down ? min(a, b) : max(a, b);
-        }
+    for (int i = 0; i < 8; ++i) order_words(w[i], w[15 - i]);
+    merge_words<0, 8>(w);
+    merge_words<8, 8>(w);
+  }
 }
 
 // top: the N largest of top and w (both descending); out: the largest of the others.
@@ -247,54 +276,47 @@ __device__ __forceinline__ void join_words(uint32_t (&top)[N], uint32_t (&w)[N],
     top[i] = max(top[i], a);
     top[N - 1 - i] = max(top[N - 1 - i], b);
   }
-  merge_words(top);
+  merge_words<0, N>(top);
 }
 
 // kLaneWarps warps take 32 tokens together: each looks through a share of
 // every row, the first joins what they found.  p.logits' rows are `aligned`
 // where all of them are made of whole 16-byte pieces.
-template <bool BF16, int N>
-__global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParams p, int pitch, int bits, bool aligned) {
+template <bool BF16, int N, KeyKind KIND>
+__global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParams p, int pitch, int tail, int bits,
+                                                                       bool aligned) {
   extern __shared__ float4 s_rows4[];
   float *rows = reinterpret_cast<float *>(s_rows4);
-  uint32_t *words = reinterpret_cast<uint32_t *>(rows + 32 * pitch);  // [kLaneWarps][N + 1][32]
-  float *bias = reinterpret_cast<float *>(words + kLaneWarps * (N + 1) * 32);  // [pitch]
-  float *scores = bias + pitch;                                                // [groups][32]
+  float *raw = rows + 32 * pitch;                          // bf16 rows before they are fp32
+  uint32_t *words = reinterpret_cast<uint32_t *>(raw);     // [kLaneWarps][N + 1][32]
+  float *scores = raw + kLaneWarps * (N + 1) * 32;         // [groups][32]
+  float *bias = raw + tail;                                // [pitch]
   __shared__ float s_part[2][kLaneWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quads = (p.E + 3) / 4;
   const int t0 = blockIdx.x * 32, count = min(32, p.T - t0);
-  const auto quad_at = [&](int row, int q) { return row * pitch + ((q ^ (row & 7)) << 2); };
+  const auto quad_at = [&](int row, int q) { return row * pitch + q * 4; };
   griddep_wait();
   griddep_launch_dependents();
 
-  // the rows, as fp32; NaN counts as masked, +infinity as the largest number
-  const auto clean = [](float v) { return fminf(v != v ? kNegInf : v, 3.402823466e38f); };
+  // the rows, as fp32 (NaN and +infinity as they are); rows of whole pieces
+  // are copied, bf16 ones first to where the scores and words come later
   const int64_t step = p.row_stride * (BF16 ? 2 : 4);
   const char *base = static_cast<const char *>(p.logits) + (int64_t)t0 * step;
   if (aligned) {
-    const int pieces = BF16 ? p.E / 8 : quads;
-    for (int i = threadIdx.x; i < count * pieces; i += kLaneWarps * 32 * kLoads) {
-      int4 v[kLoads];
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int at = i + kLaneWarps * 32 * j, r = at / pieces, c = at - r * pieces;
-        if (at < count * pieces) v[j] = __ldcs(reinterpret_cast<const int4 *>(base + r * step + c * 16));
-      }
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int at = i + kLaneWarps * 32 * j, r = at / pieces, c = at - r * pieces;
-        if (at >= count * pieces) break;
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(&v[j]);
-        if (BF16) {
-          *reinterpret_cast<float4 *>(rows + quad_at(r, 2 * c)) =
-              make_float4(clean(bf16_lo(w[0])), clean(bf16_hi(w[0])), clean(bf16_lo(w[1])), clean(bf16_hi(w[1])));
-          *reinterpret_cast<float4 *>(rows + quad_at(r, 2 * c + 1)) =
-              make_float4(clean(bf16_lo(w[2])), clean(bf16_hi(w[2])), clean(bf16_lo(w[3])), clean(bf16_hi(w[3])));
-        } else {
-          *reinterpret_cast<float4 *>(rows + quad_at(r, c)) =
-              make_float4(clean(__uint_as_float(w[0])), clean(__uint_as_float(w[1])), clean(__uint_as_float(w[2])),
-                          clean(__uint_as_float(w[3])));
-        }
+    const int pieces = BF16 ? p.E / 8 : quads, apart = BF16 ? pieces | 1 : pitch / 4;
+    char *to = reinterpret_cast<char *>(BF16 ? raw : rows);
+    for (int r = warp; r < count; r += kLaneWarps)
+#pragma unroll 2
+      for (int c = lane; c < pieces; c += 32) copy16(smem_addr(to + (r * apart + c) * 16), base + r * step + c * 16);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (BF16) {
+      __syncthreads();
+      const int c0 = pieces * warp / kLaneWarps, c1 = pieces * (warp + 1) / kLaneWarps;
+      for (int c = c0; c < c1; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(to + (lane * apart + c) * 16);
+        float4 *f = reinterpret_cast<float4 *>(rows + quad_at(lane, 2 * c));
+        f[0] = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+        f[1] = make_float4(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w));
       }
     }
   } else {
@@ -304,7 +326,10 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
       rows[quad_at(r, e >> 2) + (e & 3)] = e < p.E ? load_logit<BF16>(base + r * step, e) : kNegInf;
     }
   }
-  for (int i = threadIdx.x; i < pitch; i += kLaneWarps * 32) bias[i] = p.bias != nullptr && i < p.E ? p.bias[i] : 0.0f;
+  for (int i = threadIdx.x; i < pitch; i += kLaneWarps * 32) {
+    const float v = p.bias != nullptr && i < p.E ? p.bias[i] : 0.0f;
+    bias[i] = v != v ? kNegInf : v;
+  }
   __syncthreads();
 
   const bool here = lane < count;
@@ -317,15 +342,16 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
     v[3] = f.w;
   };
   float m = 0.0f, sum = 1.0f;
-  if (!p.sigmoid && !(p.by_logit && p.renorm)) {
+  if (!p.sigmoid && !(KIND == kLogitKey && p.renorm)) {
     m = kNegInf;
     if (here)
 #pragma unroll 4
       for (int q = q0; q < q1; ++q) {
         float v[4];
         read4(q, v);
-        m = fmaxf(fmaxf(m, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+        m = fmaxf(fmaxf(m, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));  // NaN gives way to a number
       }
+    m = fminf(m, kMost);
     s_part[0][warp][lane] = m;
     __syncthreads();
 #pragma unroll
@@ -337,7 +363,7 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
         float v[4];
         read4(q, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum += exp2_approx((v[j] - m) * kLog2e);
+        for (int j = 0; j < 4; ++j) sum += v[j] > kNegInf ? exp2_approx((fminf(v[j], kMost) - m) * kLog2e) : 0.0f;
       }
     s_part[1][warp][lane] = sum;
     __syncthreads();
@@ -345,45 +371,62 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
 #pragma unroll
     for (int w = 0; w < kLaneWarps; ++w) sum += s_part[1][w][lane];
   }
-  // keys in place of logits, and the groups' scores: a warp some groups, or
-  // of a single group its share of the row
+  // Keys in place of logits (a logit that is its own key is only cleaned), and
+  // the groups' scores: a warp some groups, or of a single group its share.
   const int per = p.E / p.G / 4;  // quads of a group
-  if (!p.by_logit || p.G > 1) {
-    const float inv = 1.0f / sum;
-    for (int g = p.G == 1 ? 0 : warp; here && g < p.G; g += kLaneWarps) {
+  const float inv = 1.0f / sum;
+  if (here)
+    for (int g = p.G == 1 ? 0 : warp; g < p.G; g += kLaneWarps) {
       float a = kNegInf, b = kNegInf;
       const int from = p.G == 1 ? q0 : g * per, to = p.G == 1 ? q1 : (g + 1) * per;
 #pragma unroll 4
       for (int q = from; q < to; ++q) {
         float v[4];
         read4(q, v);
-        if (!p.by_logit) {
-          const float4 c = *reinterpret_cast<const float4 *>(bias + q * 4);
-          const float more[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float key = (p.sigmoid ? sigmoid_key(v[j]) : exp2_approx((v[j] - m) * kLog2e) * inv) + more[j];
-            v[j] = v[j] == kNegInf || key != key ? kNegInf : key;
-          }
-          *reinterpret_cast<float4 *>(rows + quad_at(lane, q)) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+        const float4 c = KIND == kLogitKey ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                           : *reinterpret_cast<const float4 *>(bias + q * 4);
+        const float more[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          b = fmaxf(b, fminf(a, v[j]));
-          a = fmaxf(a, v[j]);
+          float key;
+          if (KIND == kLogitKey)
+            key = fminf(v[j], kMost) + 0.0f;  // -0 counts as +0
+          else if (KIND == kSigmoidKey)
+            key = sigmoid_key(v[j]) + more[j];
+          else
+            key = exp2_approx((fminf(v[j], kMost) - m) * kLog2e) * inv + more[j];
+          v[j] = v[j] > kNegInf ? key : kNegInf;
         }
+        *reinterpret_cast<float4 *>(rows + quad_at(lane, q)) = make_float4(v[0], v[1], v[2], v[3]);
+        if (p.G > 1)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            b = fmaxf(b, fminf(a, v[j]));
+            a = fmaxf(a, v[j]);
+          }
       }
       if (p.G == 1) break;
       scores[g * 32 + lane] = p.group_top == 2 && b != kNegInf ? a + b : a;
     }
-    __syncthreads();
-  }
+  __syncthreads();
   uint64_t offered = p.G == 1 && here ? 1ull : 0ull;
-  if (p.G > 1 && here)
+  if (p.G > 1 && p.G <= 8 && here) {
+    // a group's rank among the few: how many come before it
+    float s[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) s[g] = g < p.G ? scores[g * 32 + lane] : kNegInf;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      int rank = 0;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) rank += h < g ? s[h] >= s[g] : h > g ? s[h] > s[g] : 0;
+      if (s[g] != kNegInf && rank < p.Gk) offered |= 1ull << g;
+    }
+  } else if (p.G > 8 && here) {
     for (int k = 0; k < p.Gk; ++k) {
       float best = kNegInf;
       int at = -1;
-#pragma unroll 4
+#pragma unroll 8
       for (int g = 0; g < p.G; ++g) {
         const float v = scores[g * 32 + lane];
         if (v > best && !((offered >> g) & 1ull)) {
@@ -394,6 +437,7 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
       if (at < 0) break;
       offered |= 1ull << at;
     }
+  }
 
   // this warp's share of the offered groups, one after the other: the N
   // largest words, and the largest of the others
@@ -404,29 +448,29 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
   int i = all * warp / kLaneWarps, in = i % length;
   uint64_t left = offered;
   for (int k = i / length; k > 0; --k) left &= left - 1ull;
-  while (i < i1) {
-    uint32_t w[N];
+  while (i < i1) {  // words of masked experts (below kLeast) lie under all others
+    // a run of quads of one group (a lane may have none left)
+    const int run = min(i1 - i, length - in);
+    const bool some = left != 0ull;
+    const int from = (some ? __ffsll((long long)left) - 1 : 0) * length + in;
+    for (int q = 0; q < run; q += N / 4) {
+      uint32_t w[N];
 #pragma unroll
-    for (int n = 0; n < N / 4; ++n) {
-      float v[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-      int at = 0;
-      if (i < i1) {
-        if (left != 0ull) {
-          at = (__ffsll((long long)left) - 1) * length + in;
-          read4(at, v);
-        }
-        ++i;
-        if (++in == length) {
-          in = 0;
-          left &= left - 1ull;
-        }
+      for (int n = 0; n < N / 4; ++n) {
+        float v[4];
+        const int at = from + min(q + n, run - 1);
+        read4(at, v);
+        const uint32_t index = low - (uint32_t)(at * 4);
+        const bool use = some && q + n < run;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[n * 4 + j] = use ? (order_of(v[j]) & ~low) | (index - j) : 0u;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[n * 4 + j] = v[j] == kNegInf ? 0u : (ordered(v[j]) & ~low) | (low - (uint32_t)(at * 4 + j));
+      sort_words(w);
+      join_words(top, w, out);
     }
-    sort_words(w);
-    join_words(top, w, out);
+    i += run;
+    in = 0;
+    left &= left - 1ull;
   }
   uint32_t *mine = words + warp * (N + 1) * 32 + lane;
   if (warp > 0) {
@@ -451,9 +495,9 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
     uint32_t last = 0u;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      idx[n] = top[n] == 0u ? -1 : (int)(low - (top[n] & low));
-      if (n > 0) alike = alike || (top[n] != 0u && (top[n] & ~low) == (top[n - 1] & ~low));
-      if (n == p.K - 1) last = top[n];
+      idx[n] = top[n] < kLeast ? -1 : (int)(low - (top[n] & low));
+      if (n > 0) alike = alike || (top[n] >= kLeast && (top[n] & ~low) == (top[n - 1] & ~low));
+      last = n < p.K ? top[n] : last;
     }
     if (alike) {
       // by whole keys: descending, ties to the lowest index
@@ -472,70 +516,83 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
             idx[n + 1] = x;
           }
     }
-    if (out != 0u && (out & ~low) == (last & ~low) && !(BF16 && p.by_logit)) {
+    if (out >= kLeast && (out & ~low) == (last & ~low) && !(BF16 && KIND == kLogitKey)) {
+      // the last places go by whole keys among all words of those upper bits
+      const uint32_t bits_of = last & ~low;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        key[n] = kNegInf;
-        idx[n] = -1;
+        if ((top[n] & ~low) == bits_of) idx[n] = -1;
+        key[n] = idx[n] < 0 ? kNegInf : rows[quad_at(lane, idx[n] >> 2) + (idx[n] & 3)];
       }
       for (left = offered; left != 0ull; left &= left - 1ull) {
         const int g = __ffsll((long long)left) - 1;
-        for (int e = g * length * 4; e < (g + 1) * length * 4; ++e) {
-          const float v = rows[quad_at(lane, e >> 2) + (e & 3)];
-          if (!(v > key[N - 1])) continue;
+#pragma unroll 2
+        for (int q = g * length; q < (g + 1) * length; ++q) {
+          float v[4];
+          read4(q, v);
 #pragma unroll
-          for (int n = N - 1; n > 0; --n) {
-            const bool up = v > key[n - 1], here_in = v > key[n];
-            idx[n] = up ? idx[n - 1] : here_in ? e : idx[n];
-            key[n] = up ? key[n - 1] : here_in ? v : key[n];
-          }
-          if (v > key[0]) {
-            key[0] = v;
-            idx[0] = e;
+          for (int j = 0; j < 4; ++j) {
+            if ((order_of(v[j]) & ~low) != bits_of || !(v[j] > key[N - 1])) continue;
+            const float x = v[j];
+            const int e = q * 4 + j;
+#pragma unroll
+            for (int n = N - 1; n > 0; --n) {
+              const bool up = x > key[n - 1], at = x > key[n];
+              idx[n] = up ? idx[n - 1] : at ? e : idx[n];
+              key[n] = up ? key[n - 1] : at ? x : key[n];
+            }
+            if (x > key[0]) {
+              key[0] = x;
+              idx[0] = e;
+            }
           }
         }
       }
     }
 
-    // weights, as in choice_weight
-    float l[N], w[N], most = kNegInf;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const bool some = here && n < p.K && idx[n] >= 0;
-      l[n] = !some          ? kNegInf
-             : p.by_logit ? rows[quad_at(lane, idx[n] >> 2) + (idx[n] & 3)]
-                          : load_logit<BF16>(base + lane * step, idx[n]);
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) most = fmaxf(most, p.sigmoid ? fminf(l[n], 0.0f) : l[n]);
-    if (!p.renorm) most = p.sigmoid ? 0.0f : m;
-    float total = 0.0f;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const bool some = l[n] != kNegInf;
-      if (p.sigmoid)
-        w[n] = some ? expf(fminf(l[n], 0.0f) - most) / (1.0f + expf(-fabsf(l[n]))) : 0.0f;
-      else
-        w[n] = some ? expf(l[n] - most) : 0.0f;
-      total += w[n];
-    }
-    if (!p.renorm) total = p.sigmoid ? 1.0f : sum;
-    __syncwarp();
-    // through shared memory: the rows' choices are one run of memory
-    int64_t *s_idx = reinterpret_cast<int64_t *>(rows);
-    float *s_w = reinterpret_cast<float *>(s_idx + 32 * N);
+    __syncwarp();  // the other warps' words have been read
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (n < p.K) {
-        s_idx[lane * p.K + n] = here ? idx[n] : -1;
-        s_w[lane * p.K + n] = total > 0.0f ? w[n] / total * p.scale : 0.0f;
-      }
-    __syncwarp();
-    for (int n = lane; n < count * p.K; n += 32) {
-      p.idx[(int64_t)t0 * p.K + n] = s_idx[n];
-      p.w[(int64_t)t0 * p.K + n] = s_w[n];
-    }
+      if (n < p.K) reinterpret_cast<int *>(words)[lane * p.K + n] = here ? idx[n] : -1;
+    s_part[0][0][lane] = m;
+    s_part[1][0][lane] = sum;
   }
+  __syncthreads();
+
+  // weights, as in choice_weight: four threads a token
+  const int *choice = reinterpret_cast<const int *>(words);
+  const int t = threadIdx.x >> 2;
+  m = s_part[0][0][t];
+  sum = s_part[1][0][t];
+  float l[N / 4], w[N / 4], most = kNegInf, total = 0.0f;
+#pragma unroll
+  for (int n = 0; n < N / 4; ++n) {
+    const int k = n * 4 + (threadIdx.x & 3), e = t < count && k < p.K ? choice[t * p.K + k] : -1;
+    l[n] = e < 0               ? kNegInf
+           : KIND == kLogitKey ? rows[quad_at(t, e >> 2) + (e & 3)]
+                               : load_logit<BF16>(base + t * step, e);
+    most = fmaxf(most, p.sigmoid ? fminf(l[n], 0.0f) : l[n]);
+  }
+  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  if (!p.renorm) most = p.sigmoid ? 0.0f : m;
+#pragma unroll
+  for (int n = 0; n < N / 4; ++n) {
+    if (p.sigmoid)
+      w[n] = l[n] == kNegInf ? 0.0f : expf(fminf(l[n], 0.0f) - most) / (1.0f + expf(-fabsf(l[n])));
+    else
+      w[n] = l[n] == kNegInf ? 0.0f : expf(l[n] - most);
+    total += w[n];
+  }
+  total += __shfl_xor_sync(0xffffffffu, total, 1);
+  total += __shfl_xor_sync(0xffffffffu, total, 2);
+  if (!p.renorm) total = p.sigmoid ? 1.0f : sum;
+#pragma unroll
+  for (int n = 0; n < N / 4; ++n) {
+    const int k = n * 4 + (threadIdx.x & 3);
+    if (t < count && k < p.K) p.w[(int64_t)(t0 + t) * p.K + k] = total > 0.0f ? w[n] / total * p.scale : 0.0f;
+  }
+  for (int i = threadIdx.x; i < count * p.K; i += kLaneWarps * 32) p.idx[(int64_t)t0 * p.K + i] = choice[i];
 }
 
 // Where a lane a token is used: enough tokens that their warps fill the SMs
@@ -546,27 +603,35 @@ bool lanes_fit(const RouteArgs &a) {
          (a.num_groups == 1 || a.num_experts / a.num_groups % 4 == 0);
 }
 
-template <bool BF16, int N>
-ep_status_t launch_lanes(const RouteParams &p, cudaStream_t stream) {
-  const int pitch = (p.E + 31) / 32 * 32;
+template <bool BF16, int N, KeyKind KIND>
+ep_status_t launch_lanes_as(const RouteParams &p, cudaStream_t stream) {
+  const int pitch = (((p.E + 3) / 4) | 1) * 4;
   int bits = 1;
-  while ((1 << bits) < pitch) ++bits;
-  size_t smem = ((size_t)33 * pitch + kLaneWarps * (N + 1) * 32 + (p.G > 1 ? p.G * 32 : 0)) * 4;
-  if (smem < 32 * N * 12) smem = 32 * N * 12;
+  while ((1 << bits) < (p.E + 3) / 4 * 4) ++bits;
+  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
+                       p.row_stride % (BF16 ? 8 : 4) == 0 && p.E % (BF16 ? 8 : 4) == 0;
+  int tail = kLaneWarps * (N + 1) * 32 + (p.G > 1 ? p.G * 32 : 0);
+  const int raw = BF16 && aligned ? 32 * (p.E / 8 | 1) * 4 : 0;
+  if (tail < raw) tail = raw;
+  const size_t smem = ((size_t)32 * pitch + tail + pitch) * 4;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && !ready[dev]) {
-    e = cudaFuncSetAttribute(route_lanes_kernel<BF16, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (33 * 1024 + kLaneWarps * (N + 1) * 32 + EP_MAX_RANKS * 32) * 4);
+    e = cudaFuncSetAttribute(route_lanes_kernel<BF16, N, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (33 * 1028 + 32 * 129 * 4) * 4);
     if (e == cudaSuccess) ready[dev] = true;
   }
-  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
-                       p.row_stride % (BF16 ? 8 : 4) == 0 && p.E % (BF16 ? 8 : 4) == 0;
   if (e == cudaSuccess)
-    e = launch_kernel(route_lanes_kernel<BF16, N>, (p.T + 31) / 32, kLaneWarps * 32, smem, stream, false, p, pitch,
-                      bits, aligned);
+    e = launch_kernel(route_lanes_kernel<BF16, N, KIND>, (p.T + 31) / 32, kLaneWarps * 32, smem, stream, false, p, pitch,
+                      tail, bits, aligned);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "route launch");
+}
+
+template <bool BF16, int N>
+ep_status_t launch_lanes(const RouteParams &p, cudaStream_t stream) {
+  if (p.by_logit) return launch_lanes_as<BF16, N, kLogitKey>(p, stream);
+  return p.sigmoid ? launch_lanes_as<BF16, N, kSigmoidKey>(p, stream) : launch_lanes_as<BF16, N, kSoftmaxKey>(p, stream);
 }
 
 struct RouteBackwardParams {
