@@ -653,60 +653,114 @@ __device__ __forceinline__ void store_grad(void *row, int j, float v) {
     static_cast<float *>(row)[j] = v;
 }
 
-// One warp a token; the row of gradients in shared memory.
+constexpr int kBackwardWarps = 8;
+
+// One warp a token, lane k its k-th choice.  Only a softmax over all experts
+// (not renormalised) gives every logit a gradient, -p (sum d p), and needs
+// the whole row of logits; otherwise the row is zeros but for the choices,
+// and only their logits are read.  Either is written 16 bytes at a time
+// (`wide`: rows of whole pieces) and the choices' values after it: writes to
+// L2, which are one to memory.
 template <bool BF16>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteBackwardParams p) {
-  extern __shared__ float s_rows[];
+__global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(RouteBackwardParams p, bool wide) {
+  constexpr int kPiece = BF16 ? 8 : 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float *dense = s_rows + (size_t)warp * p.E;
+  const bool dense = !p.sigmoid && !p.renorm;
   griddep_wait();
   griddep_launch_dependents();
-  for (int t = blockIdx.x * kRouteWarps + warp; t < p.T; t += gridDim.x * kRouteWarps) {
+  for (int t = blockIdx.x * kBackwardWarps + warp; t < p.T; t += gridDim.x * kBackwardWarps) {
     const void *row = static_cast<const char *>(p.logits) + (int64_t)t * p.row_stride * (BF16 ? 2 : 4);
     void *out = static_cast<char *>(p.out) + (int64_t)t * p.E * (BF16 ? 2 : 4);
-    for (int j = lane; j < p.E; j += 32) dense[j] = 0.0f;
-    float m = kNegInf, sum = 0.0f;
-    if (!p.sigmoid && !p.renorm) {
-      for (int j = lane; j < p.E; j += 32) m = fmaxf(m, load_logit<BF16>(row, j));
-      m = warp_max(m);
-      for (int j = lane; j < p.E; j += 32) {
-        const float l = load_logit<BF16>(row, j);
-        sum += l == kNegInf ? 0.0f : expf(l - m);
-      }
-      sum = warp_sum(sum);
-    }
     const int64_t at64 = lane < p.K ? p.idx[(int64_t)t * p.K + lane] : -1;
+    const float g = lane < p.K ? p.grad[(int64_t)t * p.K + lane] * p.scale : 0.0f;
     const int at = at64 >= 0 && at64 < p.E ? (int)at64 : -1;
     const float l = at < 0 ? kNegInf : load_logit<BF16>(row, at);
     const bool none = l == kNegInf;
-    float d = none ? 0.0f : p.grad[(int64_t)t * p.K + lane] * p.scale;
-    float dot = 0.0f;
-    if (p.renorm) {
+    float d = none ? 0.0f : g, dot = 0.0f, m = kNegInf, inv = 0.0f;
+    const auto piece = [&](int c, float (&v)[kPiece]) {
+      const int4 f = __ldg(static_cast<const int4 *>(row) + c);
+      const uint32_t *w = reinterpret_cast<const uint32_t *>(&f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (BF16) {
+          v[2 * j] = bf16_lo(w[j]);
+          v[(2 * j + 1) % kPiece] = bf16_hi(w[j]);
+        } else {
+          v[j] = __uint_as_float(w[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) v[j] = fminf(v[j] != v[j] ? kNegInf : v[j], 3.402823466e38f);
+    };
+    if (dense) {
+      float sum = 0.0f;
+      if (wide) {
+        for (int c = lane; c < p.E / kPiece; c += 32) {
+          float v[kPiece];
+          piece(c, v);
+#pragma unroll
+          for (int j = 0; j < kPiece; ++j) m = fmaxf(m, v[j]);
+        }
+        m = warp_max(m);
+        if (m != kNegInf)
+          for (int c = lane; c < p.E / kPiece; c += 32) {
+            float v[kPiece];
+            piece(c, v);
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) sum += exp2_approx((v[j] - m) * kLog2e);
+          }
+      } else {
+        for (int j = lane; j < p.E; j += 32) m = fmaxf(m, load_logit<BF16>(row, j));
+        m = warp_max(m);
+        if (m != kNegInf)
+          for (int j = lane; j < p.E; j += 32) sum += exp2_approx((load_logit<BF16>(row, j) - m) * kLog2e);
+      }
+      sum = warp_sum(sum);
+      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      dot = warp_sum(none ? 0.0f : d * (exp2_approx((l - m) * kLog2e) * inv));
+    } else if (p.renorm) {
       // u = p / sum p; du_k/dl_k' carries p' / sum = u (1 - p) for a sigmoid,
       // and u for a softmax (its share of the chosen alone)
       const float u = choice_weight(none, l, p.sigmoid, true, 0.0f, 1.0f);
       d = u * (d - warp_sum(d * u));
       if (p.sigmoid) d *= none ? 0.0f : 1.0f / (1.0f + expf(l));
-    } else if (p.sigmoid) {
+    } else {
       const float e = expf(-fabsf(l));  // p (1 - p) = e / (1 + e)^2
       d = none ? 0.0f : d * (e / ((1.0f + e) * (1.0f + e)));
-    } else {
-      dot = warp_sum(none ? 0.0f : d * (expf(l - m) / sum));
     }
-    __syncwarp();
-    for (int k = 0; k < p.K; ++k) {  // one lane after the other: an index named twice adds up
-      if (lane == k && !none) dense[at] += d;
-      __syncwarp();
-    }
-    for (int j = lane; j < p.E; j += 32) {
-      float v = dense[j];
-      if (!p.sigmoid && !p.renorm) {
-        const float lj = load_logit<BF16>(row, j);
-        v = lj == kNegInf ? 0.0f : (expf(lj - m) / sum) * (v - dot);
+    // an expert named twice receives both: every one of its lanes adds all
+    const uint32_t same = __match_any_sync(0xffffffffu, none ? -1 - lane : at);
+    if (__any_sync(0xffffffffu, !none && (same & (same - 1u)) != 0u)) {
+      float all = 0.0f;
+      for (int k = 0; k < p.K; ++k) {
+        const float v = __shfl_sync(0xffffffffu, d, k);
+        if ((same >> k) & 1u) all += v;
       }
-      store_grad<BF16>(out, j, v);
+      d = all;
+    }
+    if (wide) {
+      for (int c = lane; c < p.E / kPiece; c += 32) {
+        int4 f = make_int4(0, 0, 0, 0);
+        if (dense && m != kNegInf) {
+          float v[kPiece];
+          piece(c, v);
+#pragma unroll
+          for (int j = 0; j < kPiece; ++j) v[j] = -(exp2_approx((v[j] - m) * kLog2e) * inv) * dot;
+          int *w = reinterpret_cast<int *>(&f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = BF16 ? (int)pack_bf16x2(v[2 * j % kPiece], v[(2 * j + 1) % kPiece]) : __float_as_int(v[j]);
+        }
+        static_cast<int4 *>(out)[c] = f;
+      }
+    } else {
+      for (int j = lane; j < p.E; j += 32) {
+        const float v = dense && m != kNegInf ? -(exp2_approx((load_logit<BF16>(row, j) - m) * kLog2e) * inv) * dot : 0.0f;
+        store_grad<BF16>(out, j, v);
+      }
     }
     __syncwarp();
+    if (!none) store_grad<BF16>(out, at, dense ? (exp2_approx((l - m) * kLog2e) * inv) * (d - dot) : d);
   }
 }
 
@@ -768,11 +822,12 @@ ep_status_t launch_route_backward(const RouteBackwardArgs &a, cudaStream_t strea
   RouteBackwardParams p{a.grad_weights, a.logits, a.row_stride,   a.topk_idx, a.num_tokens, a.num_experts,
                         a.num_topk,     a.weight_scale, a.grad_logits, a.sigmoid,  a.renormalize};
   auto kernel = a.bf16 ? route_backward_kernel<true> : route_backward_kernel<false>;
-  int grid;
-  size_t smem;
-  const ep_status_t s = route_grid(kernel, a.num_tokens, a.num_experts, di, &grid, &smem);
-  if (s != EP_OK) return s;
-  const cudaError_t e = launch_kernel(kernel, grid, kRouteWarps * 32, smem, stream, false, p);
+  const int piece = a.bf16 ? 8 : 4;
+  const bool wide = a.num_experts % piece == 0 && a.row_stride % piece == 0 &&
+                    reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && reinterpret_cast<uintptr_t>(a.grad_logits) % 16 == 0;
+  const int64_t need = ((int64_t)a.num_tokens + kBackwardWarps - 1) / kBackwardWarps, most = (int64_t)di->num_sms * 32;
+  const cudaError_t e =
+      launch_kernel(kernel, (int)(need < most ? need : most), kBackwardWarps * 32, 0, stream, false, p, wide);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "route_backward launch");
 }
 
