@@ -68,15 +68,18 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Over L neighbouring lanes; the whole warp calls them.
+template <int L = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
+template <int L = 32>
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -95,19 +98,20 @@ __device__ __forceinline__ int warp_argmax(float v, int i) {
 // is not renormalised.  Renormalised weights are shares, so the largest
 // exponential of the chosen is taken out and none of them can underflow
 // together: sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)).
+template <int L = 32>
 __device__ __forceinline__ float choice_weight(bool none, float l, bool sigmoid, bool renorm, float m, float sum) {
   float p;
   if (sigmoid) {
     const float low = fminf(l, 0.0f);
-    const float top = renorm ? warp_max(none ? kNegInf : low) : 0.0f;
+    const float top = renorm ? warp_max<L>(none ? kNegInf : low) : 0.0f;
     p = none ? 0.0f : expf(low - top) / (1.0f + expf(-fabsf(l)));
   } else {
-    const float top = renorm ? warp_max(none ? kNegInf : l) : m;
+    const float top = renorm ? warp_max<L>(none ? kNegInf : l) : m;
     p = none ? 0.0f : expf(l - top);
     if (!renorm) p = none ? 0.0f : p / sum;
   }
   if (renorm) {
-    const float total = warp_sum(p);
+    const float total = warp_sum<L>(p);
     p = total > 0.0f ? p / total : 0.0f;
   }
   return p;
@@ -655,24 +659,28 @@ __device__ __forceinline__ void store_grad(void *row, int j, float v) {
 
 constexpr int kBackwardWarps = 8;
 
-// One warp a token, lane k its k-th choice.  Only a softmax over all experts
+// L lanes a token (8, 16 or 32, as its choices need), lane k its k-th choice.  Only a softmax over all experts
 // (not renormalised) gives every logit a gradient, -p (sum d p), and needs
 // the whole row of logits; otherwise the row is zeros but for the choices,
 // and only their logits are read.  Either is written 16 bytes at a time
 // (`wide`: rows of whole pieces) and the choices' values after it: writes to
 // L2, which are one to memory.
-template <bool BF16>
+template <bool BF16, int L>
 __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(RouteBackwardParams p, bool wide) {
   constexpr int kPiece = BF16 ? 8 : 4;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kTokens = kBackwardWarps * 32 / L;  // of a block
+  const int lane = threadIdx.x % L;
   const bool dense = !p.sigmoid && !p.renorm;
   griddep_wait();
   griddep_launch_dependents();
-  for (int t = blockIdx.x * kBackwardWarps + warp; t < p.T; t += gridDim.x * kBackwardWarps) {
-    const void *row = static_cast<const char *>(p.logits) + (int64_t)t * p.row_stride * (BF16 ? 2 : 4);
-    void *out = static_cast<char *>(p.out) + (int64_t)t * p.E * (BF16 ? 2 : 4);
-    const int64_t at64 = lane < p.K ? p.idx[(int64_t)t * p.K + lane] : -1;
-    const float g = lane < p.K ? p.grad[(int64_t)t * p.K + lane] * p.scale : 0.0f;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.T; t0 += (int64_t)gridDim.x * kTokens) {
+    const int64_t own = t0 + threadIdx.x / L;
+    const bool here = own < p.T;
+    const int64_t t = here ? own : p.T - 1;  // all lanes take part in the exchanges
+    const void *row = static_cast<const char *>(p.logits) + t * p.row_stride * (BF16 ? 2 : 4);
+    void *out = static_cast<char *>(p.out) + t * p.E * (BF16 ? 2 : 4);
+    const int64_t at64 = here && lane < p.K ? p.idx[t * p.K + lane] : -1;
+    const float g = here && lane < p.K ? p.grad[t * p.K + lane] * p.scale : 0.0f;
     const int at = at64 >= 0 && at64 < p.E ? (int)at64 : -1;
     const float l = at < 0 ? kNegInf : load_logit<BF16>(row, at);
     const bool none = l == kNegInf;
@@ -695,51 +703,52 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(Rou
     if (dense) {
       float sum = 0.0f;
       if (wide) {
-        for (int c = lane; c < p.E / kPiece; c += 32) {
+        for (int c = lane; c < p.E / kPiece; c += L) {
           float v[kPiece];
           piece(c, v);
 #pragma unroll
           for (int j = 0; j < kPiece; ++j) m = fmaxf(m, v[j]);
         }
-        m = warp_max(m);
+        m = warp_max<L>(m);
         if (m != kNegInf)
-          for (int c = lane; c < p.E / kPiece; c += 32) {
+          for (int c = lane; c < p.E / kPiece; c += L) {
             float v[kPiece];
             piece(c, v);
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) sum += exp2_approx((v[j] - m) * kLog2e);
           }
       } else {
-        for (int j = lane; j < p.E; j += 32) m = fmaxf(m, load_logit<BF16>(row, j));
-        m = warp_max(m);
+        for (int j = lane; j < p.E; j += L) m = fmaxf(m, load_logit<BF16>(row, j));
+        m = warp_max<L>(m);
         if (m != kNegInf)
-          for (int j = lane; j < p.E; j += 32) sum += exp2_approx((load_logit<BF16>(row, j) - m) * kLog2e);
+          for (int j = lane; j < p.E; j += L) sum += exp2_approx((load_logit<BF16>(row, j) - m) * kLog2e);
       }
-      sum = warp_sum(sum);
+      sum = warp_sum<L>(sum);
       inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-      dot = warp_sum(none ? 0.0f : d * (exp2_approx((l - m) * kLog2e) * inv));
+      dot = warp_sum<L>(none ? 0.0f : d * (exp2_approx((l - m) * kLog2e) * inv));
     } else if (p.renorm) {
       // u = p / sum p; du_k/dl_k' carries p' / sum = u (1 - p) for a sigmoid,
       // and u for a softmax (its share of the chosen alone)
-      const float u = choice_weight(none, l, p.sigmoid, true, 0.0f, 1.0f);
-      d = u * (d - warp_sum(d * u));
+      const float u = choice_weight<L>(none, l, p.sigmoid, true, 0.0f, 1.0f);
+      d = u * (d - warp_sum<L>(d * u));
       if (p.sigmoid) d *= none ? 0.0f : 1.0f / (1.0f + expf(l));
     } else {
       const float e = expf(-fabsf(l));  // p (1 - p) = e / (1 + e)^2
       d = none ? 0.0f : d * (e / ((1.0f + e) * (1.0f + e)));
     }
     // an expert named twice receives both: every one of its lanes adds all
-    const uint32_t same = __match_any_sync(0xffffffffu, none ? -1 - lane : at);
+    const uint32_t same = __match_any_sync(0xffffffffu, none ? -1 - (int)(threadIdx.x & 31) : at | (int)(threadIdx.x & 31) / L << 16);
     if (__any_sync(0xffffffffu, !none && (same & (same - 1u)) != 0u)) {
       float all = 0.0f;
       for (int k = 0; k < p.K; ++k) {
-        const float v = __shfl_sync(0xffffffffu, d, k);
-        if ((same >> k) & 1u) all += v;
+        const int from = (int)(threadIdx.x & 31) / L * L + k;
+        const float v = __shfl_sync(0xffffffffu, d, from);
+        if ((same >> from) & 1u) all += v;
       }
       d = all;
     }
-    if (wide) {
-      for (int c = lane; c < p.E / kPiece; c += 32) {
+    if (here && wide) {
+      for (int c = lane; c < p.E / kPiece; c += L) {
         int4 f = make_int4(0, 0, 0, 0);
         if (dense && m != kNegInf) {
           float v[kPiece];
@@ -753,8 +762,8 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(Rou
         }
         static_cast<int4 *>(out)[c] = f;
       }
-    } else {
-      for (int j = lane; j < p.E; j += 32) {
+    } else if (here) {
+      for (int j = lane; j < p.E; j += L) {
         const float v = dense && m != kNegInf ? -(exp2_approx((load_logit<BF16>(row, j) - m) * kLog2e) * inv) * dot : 0.0f;
         store_grad<BF16>(out, j, v);
       }
@@ -821,11 +830,15 @@ ep_status_t launch_route_backward(const RouteBackwardArgs &a, cudaStream_t strea
   if (di == nullptr) return EP_ERR_CUDA;
   RouteBackwardParams p{a.grad_weights, a.logits, a.row_stride,   a.topk_idx, a.num_tokens, a.num_experts,
                         a.num_topk,     a.weight_scale, a.grad_logits, a.sigmoid,  a.renormalize};
-  auto kernel = a.bf16 ? route_backward_kernel<true> : route_backward_kernel<false>;
+  const int lanes = a.num_topk <= 8 ? 8 : a.num_topk <= 16 ? 16 : 32;
+  const auto kernel = lanes == 8    ? (a.bf16 ? route_backward_kernel<true, 8> : route_backward_kernel<false, 8>)
+                      : lanes == 16 ? (a.bf16 ? route_backward_kernel<true, 16> : route_backward_kernel<false, 16>)
+                                    : (a.bf16 ? route_backward_kernel<true, 32> : route_backward_kernel<false, 32>);
   const int piece = a.bf16 ? 8 : 4;
   const bool wide = a.num_experts % piece == 0 && a.row_stride % piece == 0 &&
                     reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && reinterpret_cast<uintptr_t>(a.grad_logits) % 16 == 0;
-  const int64_t need = ((int64_t)a.num_tokens + kBackwardWarps - 1) / kBackwardWarps, most = (int64_t)di->num_sms * 32;
+  const int tokens = kBackwardWarps * 32 / lanes;  // of a block
+  const int64_t need = ((int64_t)a.num_tokens + tokens - 1) / tokens, most = (int64_t)di->num_sms * 32;
   const cudaError_t e =
       launch_kernel(kernel, (int)(need < most ? need : most), kBackwardWarps * 32, 0, stream, false, p, wide);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "route_backward launch");
