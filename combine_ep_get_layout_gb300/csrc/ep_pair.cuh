@@ -43,6 +43,7 @@ constexpr int kBoxes = kMaxCols / 2 / 16;  // heights of a half of B
 constexpr int kPlanWords = 1 + 2 * kMaxCols;
 constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
 constexpr int kStagingBytes = 32 * kPitch;       // a result warp's 32 rows
+__host__ __device__ constexpr int staging_of(Form f) { return f == kGradW ? 32 * 128 : kStagingBytes; }
 constexpr int kExchangeBytes = 16 * 32 * 4;      // kGated: 16 columns of a warp, fp32
 constexpr int kResultWarps = 8;
 constexpr int kMaxParts = 4;         // pairs of a cluster, which share the inner dimension of one tile
@@ -64,6 +65,7 @@ struct Params {
   int a_tiles;   // tiles along A
   int b_tiles;   // kGradW: tiles along B (hidden)
   int hidden;    // kGradW
+  CUtensorMap grad;  // kGradW: the gradient [E][wide][hidden], boxes of 64 x 32
   uint16_t *out, *preact;
   int max_cols;         // rows of a tile, at most
   int parts;            // pairs that share a tile's inner dimension
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
   const int stage_bytes = kABytes + p.b_bytes;
   char *side = ring + (size_t)p.stages * stage_bytes;
   char *staging = side + (F == kAdapter ? (size_t)p.side_stages * stage_bytes : 0);
-  char *exchange = staging + kResultWarps * kStagingBytes;
+  char *exchange = staging + kResultWarps * staging_of(F);
   // [parts - 1][columns][128]: the other pairs' results
   float *joined = reinterpret_cast<float *>(exchange + (F == kGated ? kResultWarps * kExchangeBytes : 0));
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -532,22 +534,32 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     Walker<F> walk(p);
     Tile t;
     const int w = warp - 4, quarter = w & 3, half = w >> 2;
-    char *stage_buf = staging + w * kStagingBytes;
+    char *stage_buf = staging + w * staging_of(F);
     int acc = 0;
     uint32_t acc_phase = 0, part_phase = 0;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const auto store_block = [&](char *from, const Tile &t, int c) {  // kGradW: 32 rows of 64 columns
+      const int col = t.b0 + c, row = t.a0 + (int)rank * 128 + quarter * 32;
+      if (col < p.hidden && row < p.wide) tile_store_3d(&p.grad, smem_addr(from), col, row, t.e);
+      bulk_commit();
+    };
     const auto release = [&](int a) {  // this warp has read its columns of accumulator a
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.acc_empty[a]), lead));
     };
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
-      if (F == kGradW && t.steps == 0) {
-        const int row = t.a0 + (int)rank * 128 + quarter * 32 + lane;
-        for (int c = half * 32; c < t.cols && row < p.wide; c += 64)
-          for (int j = 0; j < 32 && t.b0 + c + j < p.hidden; j += 8)
-            *reinterpret_cast<int4 *>(p.out + ((int64_t)t.e * p.wide + row) * p.hidden + t.b0 + c + j) =
-                make_int4(0, 0, 0, 0);
+      if (F == kGradW && t.steps == 0) {  // an expert without rows
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<int4 *>(stage_buf + (j * 32 + lane) * 16) = make_int4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (int c = half * 64; c < t.cols; c += 128)
+            store_block(stage_buf, t, c);
         continue;
       }
       ok = mbar_wait_pair(&s_bar.acc_full[acc], acc_phase);
@@ -579,6 +591,29 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       ok = F == kGated ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      if (F == kGradW) {
+        // a row of the gradient a lane; 64 columns are staged in the swizzled
+        // order and stored as a tile
+        for (int c = half * 64; c < t.cols; c += 128) {
+          float v[64];
+          tmem_load32(tmem + acc * kMaxCols + c + lane_base, reinterpret_cast<float (&)[32]>(v[0]));
+          tmem_load32(tmem + acc * kMaxCols + c + 32 + lane_base, reinterpret_cast<float (&)[32]>(v[32]));
+          if (c + 128 >= t.cols) release(acc);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4 *>(stage_buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) store_block(stage_buf, t, c);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+        continue;
+      }
       for (int c = half * 32; c < t.cols; c += 64) {
         float v[32];
         tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
@@ -623,25 +658,6 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           const int skip = gate ? 0 : 16;
           store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);
           pair_barrier(id);  // before the next chunk overwrites what the other warp reads
-        } else {
-          // one row of the gradient a lane, 32 columns
-          uint32_t packed[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(stage_buf + lane * kPitch + j * 16) =
-                make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-          __syncwarp();
-          const int part = lane & 3, col = t.b0 + c + part * 8;
-#pragma unroll
-          for (int r = lane >> 2; r < 32; r += 8) {
-            const int row = t.a0 + (int)rank * 128 + quarter * 32 + r;
-            if (row < p.wide && col < p.hidden)
-              *reinterpret_cast<int4 *>(p.out + ((int64_t)t.e * p.wide + row) * p.hidden + col) =
-                  *reinterpret_cast<const int4 *>(stage_buf + r * kPitch + part * 16);
-          }
-          __syncwarp();
         }
       }
       if (t.cols <= half * 32) release(acc);  // no columns for this warp
@@ -655,6 +671,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       if (acc == 0) acc_phase ^= 1;
     }
   }
+  if (F == kGradW && warp >= 4 && lane == 0) bulk_wait<0>();
   if (!ok) {
     // A wait gave up (it never should): what this CTA started lands well
     // within the time waited here, then everything is given back.
@@ -731,7 +748,7 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
   // The ring takes what is left of shared memory: a stage holds 128 rows of A
   // and half of the most columns that a tile can have.
   p.b_bytes = cols / 2 * 128;  // a multiple of 1024, as the swizzle needs
-  const int fixed = 1024 + kResultWarps * kStagingBytes + (F == kGated ? kResultWarps * kExchangeBytes : 0) +
+  const int fixed = 1024 + kResultWarps * staging_of(F) + (F == kGated ? kResultWarps * kExchangeBytes : 0) +
                     (p.parts - 1) * cols * 128 * 4;
   const int limit = shared_limit(di);
   p.stages = (limit - fixed) / (kABytes + p.b_bytes);

@@ -21,24 +21,22 @@ namespace {
 struct GateParams {
   const uint16_t *grad, *preact;
   uint16_t *out;
-  const int32_t *rows, *offset;
-  int cap, width;
+  const int32_t *offset;
+  int E, cap, width;
 };
 
 __global__ void __launch_bounds__(256) gate_backward_kernel(GateParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int e = blockIdx.y;
-  const int first = p.offset[e];
-  const int rows = first < 0 || first >= p.cap ? 0 : max(0, min(p.rows[e], p.cap - first));
-  const int groups = p.width / 8;
+  // every row up to the layout's last, padding rows too (nobody reads them)
+  const int rows = min(max(p.offset[p.E], 0), p.cap), groups = p.width / 8;
   const int64_t n = (int64_t)rows * groups;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = first + i / groups;
-    const int col = (int)(i % groups) * 8;
-    const int4 g4 = ld_stream_v4(p.preact + row * 2 * p.width + col);
-    const int4 u4 = ld_stream_v4(p.preact + row * 2 * p.width + p.width + col);
-    const int4 d4 = ld_stream_v4(p.grad + row * p.width + col);
+    const int64_t row = i / groups;
+    const int col = (int)(i - row * groups) * 8;
+    const int4 g4 = __ldcs(reinterpret_cast<const int4 *>(p.preact + row * 2 * p.width + col));
+    const int4 u4 = __ldcs(reinterpret_cast<const int4 *>(p.preact + row * 2 * p.width + p.width + col));
+    const int4 d4 = __ldcs(reinterpret_cast<const int4 *>(p.grad + row * p.width + col));
     const uint32_t *gw = reinterpret_cast<const uint32_t *>(&g4), *uw = reinterpret_cast<const uint32_t *>(&u4);
     const uint32_t *dw = reinterpret_cast<const uint32_t *>(&d4);
     uint32_t og[4], ou[4];
@@ -142,17 +140,12 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
   p.wide = wide;
   p.hidden = a.hidden;
   if (a.gated && most > 0) {
-    const GateParams q{a.grad, a.preact, a.grad_preact, p.rows, p.offset, a.recv_capacity, a.width};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(32, a.num_experts);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = kUsePdl ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gate_backward_kernel, q);
+    const GateParams q{a.grad, a.preact, a.grad_preact, p.offset, a.num_experts, a.recv_capacity, a.width};
+    const DeviceInfo *di = current_device_info();
+    if (di == nullptr) return EP_ERR_CUDA;
+    const int64_t need = ((int64_t)a.recv_capacity * (a.width / 8) + 255) / 256, fill = (int64_t)di->num_sms * 32;
+    const cudaError_t e =
+        launch_kernel(gate_backward_kernel, (int)(need < fill ? need : fill), 256, 0, stream, false, q);
     if (e != cudaSuccess) return cuda_fail(e, "gate_backward launch");
   }
   if (a.grad_x != nullptr && most > 0) {
@@ -174,6 +167,10 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     // without rows nothing is copied: the maps only need an address
     const int cap = most > 0 ? a.recv_capacity : 1;
     ep_status_t s = block_map(&p.a, &p.a_blocks, most > 0 ? g : a.grad_w, wide, cap);
+    const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)wide, (uint64_t)a.num_experts};
+    const uint64_t strides[] = {a.hidden * kSize, (uint64_t)wide * a.hidden * kSize};
+    const uint32_t box[] = {64, 32, 1};
+    if (s == EP_OK) s = encode_map(&p.grad, a.grad_w, 3, dims, strides, box);
     if (s == EP_OK) s = block_map(&p.b[0], &p.b_blocks, most > 0 ? a.x : a.grad_w, a.hidden, cap);
     if (s == EP_OK)
       s = launch_form<kGradW>(p, most, (int64_t)a.num_experts * p.a_tiles * p.b_tiles, stream);

@@ -116,6 +116,14 @@ __device__ __forceinline__ void tile_load_4d(uint32_t dst, const CUtensorMap *ma
       : "memory");
 }
 
+// A tile from shared memory (in the map's swizzle); what lies past an end is
+// not written.  Coordinates must not be negative.
+__device__ __forceinline__ void tile_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
 // 16 bytes to shared memory, zeros unless `some` (src is then not read).
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
