@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       for (int k = k0; ok && k < k1; ++k) {
         ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
         if (F == kGradW && ok && k == t.steps - 1 && t.count % 16 != 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&s_bar.fixed[stage], (trims >> stage) & 1u));
+          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.fixed[stage], (trims >> stage) & 1u));
           trims ^= 1u << stage;
         }
         if (!ok) break;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         if (n == pair) griddep_wait();
         const int length = p.rank * load_made(p.plan + t.part * kPlanWords);  // of the adapters side by side
         for (int k = part; ok && k * kInner < length; k += p.parts) {
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&s_bar.side_full[side_stage], side_phase));
+          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_full[side_stage], side_phase));
           if (!ok) break;
           tc_fence_after();
           const uint32_t addr = smem_addr(side) + (uint32_t)(side_stage * stage_bytes);
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.fixed[s]), lead));
+      if (lane == 0) mbar_arrive_cluster_local(map_shared(smem_addr(&s_bar.fixed[s]), lead));
     }
   } else if (F == kAdapter && warp >= 12) {
     // ---------------------------------------------------------- adapters
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     const auto hand_over = [&] {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.side_full[hand]), lead));
+      if (lane == 0) mbar_arrive_cluster_local(map_shared(smem_addr(&s_bar.side_full[hand]), lead));
       if (++hand == p.side_stages) hand = 0;
       --flying;
     };
