@@ -42,9 +42,9 @@ constexpr int kBoxes = kMaxCols / 2 / 16;  // heights of a half of B
 // kAdapter, a tile: its number of adapters, their indices, each row's place among them or -1
 constexpr int kPlanWords = 1 + 2 * kMaxCols;
 constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
-constexpr int kStagingBytes = 32 * kPitch;       // a result warp's 32 rows
-__host__ __device__ constexpr int staging_of(Form f) { return f == kGradW ? 32 * 128 : kStagingBytes; }
-constexpr int kExchangeBytes = 16 * 32 * 4;      // kGated: 16 columns of a warp, fp32
+constexpr int kStagedRows = 16;                  // of a result warp at a time
+constexpr int kExchangeBytes = 8 * 32 * 4;       // kGated: 8 columns of a warp, fp32
+__host__ __device__ constexpr int staging_of(Form f) { return f == kGradW ? 32 * 128 : kStagedRows * kPitch; }
 constexpr int kResultWarps = 8;
 constexpr int kMaxParts = 4;         // pairs of a cluster, which share the inner dimension of one tile
 
@@ -68,15 +68,15 @@ struct Params {
   CUtensorMap grad;  // kGradW: the gradient [E][wide][hidden], boxes of 64 x 32
   uint16_t *out, *preact;
   int max_cols;         // rows of a tile, at most
+  int most_rows;        // of an expert, at most
   int parts;            // pairs that share a tile's inner dimension
   int part_cols;        // columns of their results
-  int stages, b_bytes;  // ring; bytes of a CTA's half of B in a stage
+  int ring_bytes;       // of the ring (kAdapter: both rings)
   // kAdapter
   const uint16_t *up;    // the up-projections [adapters][width][rank]
   const int32_t *plan;   // kPlanWords a tile of rows
   const uint16_t *low;   // [rows][rank], scaled
   int rank;
-  int side_stages;  // a ring of its own for the adapters' steps, so that the main one waits for nothing
 };
 
 struct Barriers {
@@ -109,6 +109,22 @@ struct Walker {
   int rows = 0, first = 0, prefix = 0, mine = 0;
 
   __device__ Walker(const Params &p_) : p(p_), lane(threadIdx.x & 31) {}
+
+  // The most columns that a tile has (the whole warp calls it).
+  __device__ static int most_cols(const Params &p) {
+    if (F == kGradW) return kMaxCols;
+    int n = p.most_rows;  // with so few the counts need not be read
+    if (F != kAdapter && n > 64) {
+      n = 0;
+#pragma unroll 8
+      for (int e = threadIdx.x & 31; e < p.E; e += 32) {
+        const int rows = max(0, min(p.rows[e], p.cap)), tiles = ceil_div(rows, p.max_cols);
+        n = max(n, tiles > 0 ? ceil_div(rows, tiles) : 0);
+      }
+      n = __reduce_max_sync(0xffffffffu, n);
+    }
+    return n >= p.max_cols ? p.max_cols : max(32, ceil_div(n, 32) * 32);
+  }
 
   __device__ void load(int c) {
     chunk = c;
@@ -172,6 +188,7 @@ struct Walker {
       t.b0 = 0;
       t.first += t.part * t.cols;
       t.count = min(t.cols, n - t.part * t.cols);
+      t.cols = ceil_div(t.count, 32) * 32;  // the last tile takes no more than it needs
       t.steps = ceil_div(p.inner, kInner);
     }
     return true;
@@ -194,23 +211,29 @@ __device__ __forceinline__ bool pair_agree(int id, bool ok) {
 
 __device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
-// A warp's 32 lanes hold outputs n (one a lane) of `count` <= 32 rows v[0..):
-// out[row][n] through the staging buffer, 64 bytes of a row at a time.
+// A warp's 32 lanes hold outputs n (one a lane) of COUNT rows v[0..), `rows`
+// of them real: out[row][n] through the staging buffer, 64 bytes of a row at
+// a time.
 template <int COUNT>
 __device__ __forceinline__ void store_transposed(const float *v, char *stage, uint16_t *out, int64_t pitch, int rows,
                                                  int n, int limit, int lane) {
-#pragma unroll
-  for (int c = 0; c < COUNT; ++c)
-    *reinterpret_cast<uint16_t *>(stage + c * kPitch + lane * 2) = (uint16_t)(pack_bf16x2(v[c], 0.0f) & 0xffffu);
-  __syncwarp();
+  constexpr int kRows = COUNT < kStagedRows ? COUNT : kStagedRows;
   const int part = lane & 3;
 #pragma unroll
-  for (int c = lane >> 2; c < COUNT; c += 8) {
-    if (c < rows && n + part * 8 < limit)
-      *reinterpret_cast<int4 *>(out + (int64_t)c * pitch + n + part * 8) =
-          *reinterpret_cast<const int4 *>(stage + c * kPitch + part * 16);
+  for (int r = 0; r < COUNT; r += kRows) {
+    if (r >= rows) return;
+#pragma unroll
+    for (int c = 0; c < kRows; ++c)
+      *reinterpret_cast<uint16_t *>(stage + c * kPitch + lane * 2) = (uint16_t)(pack_bf16x2(v[r + c], 0.0f) & 0xffffu);
+    __syncwarp();
+#pragma unroll
+    for (int c = lane >> 2; c < kRows; c += 8) {
+      if (r + c < rows && n + part * 8 < limit)
+        *reinterpret_cast<int4 *>(out + (int64_t)(r + c) * pitch + n + part * 8) =
+            *reinterpret_cast<const int4 *>(stage + c * kPitch + part * 16);
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // What the kernel ahead made, after the wait for it: kept in its place by the
@@ -234,9 +257,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
   extern __shared__ char s_raw[];
   __shared__ Barriers s_bar;
   char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
-  const int stage_bytes = kABytes + p.b_bytes;
-  char *side = ring + (size_t)p.stages * stage_bytes;
-  char *staging = side + (F == kAdapter ? (size_t)p.side_stages * stage_bytes : 0);
+  char *staging = ring + p.ring_bytes / 1024 * 1024;
   char *exchange = staging + kResultWarps * staging_of(F);
   // [parts - 1][columns][128]: the other pairs' results
   float *joined = reinterpret_cast<float *>(exchange + (F == kGated ? kResultWarps * kExchangeBytes : 0));
@@ -249,7 +270,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
   const auto last_step = [&](const Tile &t) { return t.steps * (part + 1) / p.parts; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&s_bar.full[i], 1);
       mbar_init(&s_bar.empty[i], 1);
       mbar_init(&s_bar.ends[i], 1);
@@ -280,6 +301,18 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     griddep_wait();
     griddep_launch_dependents();
   }
+
+  // A stage holds 128 rows of A and half of the most columns that a tile of
+  // this call has (every CTA finds the same): the fewer, the deeper the ring,
+  // which has to cover the latency of memory (gated product of 384 rows an
+  // expert: 499, 442, 385 us with 3, 4, 5 stages).  kAdapter: a second ring
+  // for the adapters' steps, so that the first waits for nothing.
+  const int b_bytes = Walker<F>::most_cols(p) / 2 * 128, stage_bytes = kABytes + b_bytes;
+  int stages = p.ring_bytes / 1024 * 1024 / stage_bytes;
+  const int side_stages = stages >= 8 ? kSideStages : 2;
+  if (F == kAdapter) stages -= side_stages;
+  stages = min(stages, kMaxStages);
+  char *side = ring + stages * stage_bytes;
 
   bool ok = true;  // false: a wait gave up
   if (warp == 0 || warp == 3) {
@@ -345,16 +378,16 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           }
         }
         __syncwarp();
-        if (++stage == p.stages) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
     // the products' last arrivals on this CTA's barriers come before it ends
-    for (int i = 0; ok && i < p.stages; ++i) {
+    for (int i = 0; ok && i < stages; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1));
-      if (++stage == p.stages) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1;
       }
@@ -397,7 +430,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           if (F != kAdapter && k == k1 - 1) commit_pair(&s_bar.acc_full[acc], both);
         }
         __syncwarp();
-        if (++stage == p.stages) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
@@ -417,7 +450,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
             commit_pair(&s_bar.side_empty[side_stage], both);
           }
           __syncwarp();
-          if (++side_stage == p.side_stages) {
+          if (++side_stage == side_stages) {
             side_stage = 0;
             side_phase ^= 1;
           }
@@ -437,9 +470,9 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     int stage = 0;
     uint32_t parities = 0;
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
-      stage = (stage + t.steps) % p.stages;
+      stage = (stage + t.steps) % stages;
       if (t.count % 16 == 0) continue;
-      const int s = (stage + p.stages - 1) % p.stages;
+      const int s = (stage + stages - 1) % stages;
       ok = mbar_wait_pair(&s_bar.ends[s], (parities >> s) & 1u);
       if (!ok) break;
       parities ^= 1u << s;
@@ -471,7 +504,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_local(map_shared(smem_addr(&s_bar.side_full[hand]), lead));
-      if (++hand == p.side_stages) hand = 0;
+      if (++hand == side_stages) hand = 0;
       --flying;
     };
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
@@ -510,7 +543,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           copy_wait<1>();
           hand_over();
         }
-        if (++stage == p.side_stages) {
+        if (++stage == side_stages) {
           stage = 0;
           phase ^= 1;
         }
@@ -520,9 +553,9 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         hand_over();
       }
     }
-    for (int i = 0; ok && i < p.side_stages; ++i) {
+    for (int i = 0; ok && i < side_stages; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
-      if (++stage == p.side_stages) {
+      if (++stage == side_stages) {
         stage = 0;
         phase ^= 1;
       }
@@ -646,18 +679,21 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           float *give = reinterpret_cast<float *>(exchange + w * kExchangeBytes);
           const float *take = reinterpret_cast<const float *>(exchange + (w ^ 2) * kExchangeBytes);
           const int id = 1 + half * 2 + (quarter & 1);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) give[j * 32 + lane] = gate ? v[16 + j] : v[j];
-          pair_barrier(id);
           float o[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float other = take[j * 32 + lane];
-            o[j] = gate ? silu_of(v[j]) * other : silu_of(other) * v[16 + j];
+          for (int r = 0; r < 16; r += 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) give[j * 32 + lane] = gate ? v[16 + r + j] : v[r + j];
+            pair_barrier(id);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float other = take[j * 32 + lane];
+              o[r + j] = gate ? silu_of(v[r + j]) * other : silu_of(other) * v[16 + r + j];
+            }
+            pair_barrier(id);  // before the next columns overwrite what the other warp reads
           }
           const int skip = gate ? 0 : 16;
           store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);
-          pair_barrier(id);  // before the next chunk overwrites what the other warp reads
         }
       }
       if (t.cols <= half * 32) release(acc);  // no columns for this warp
@@ -745,18 +781,12 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
     }
   }
   p.part_cols = cols;
-  // The ring takes what is left of shared memory: a stage holds 128 rows of A
-  // and half of the most columns that a tile can have.
-  p.b_bytes = cols / 2 * 128;  // a multiple of 1024, as the swizzle needs
+  p.most_rows = most_rows;
+  // The ring takes what is left of shared memory.
+  const int limit = shared_limit(di);
   const int fixed = 1024 + kResultWarps * staging_of(F) + (F == kGated ? kResultWarps * kExchangeBytes : 0) +
                     (p.parts - 1) * cols * 128 * 4;
-  const int limit = shared_limit(di);
-  p.stages = (limit - fixed) / (kABytes + p.b_bytes);
-  if (F == kAdapter) {
-    p.side_stages = p.stages >= 8 ? kSideStages : 2;
-    p.stages -= p.side_stages;
-  }
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.ring_bytes = limit - fixed;
   const size_t smem = (size_t)limit;
   int clusters = 0;
   const ep_status_t s = most_clusters<F>(di, p.parts, &clusters);
