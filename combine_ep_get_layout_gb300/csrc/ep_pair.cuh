@@ -118,7 +118,7 @@ struct Walker {
       n = 0;
 #pragma unroll 8
       for (int e = threadIdx.x & 31; e < p.E; e += 32) {
-        const int rows = max(0, min(p.rows[e], p.cap)), tiles = ceil_div(rows, p.max_cols);
+        const int rows = max(0, min(p.rows[e], p.most_rows)), tiles = ceil_div(rows, p.max_cols);
         n = max(n, tiles > 0 ? ceil_div(rows, tiles) : 0);
       }
       n = __reduce_max_sync(0xffffffffu, n);
@@ -136,7 +136,7 @@ struct Walker {
     } else if (e < p.E) {
       first = p.offset[e];
       const int n = p.rows[e];
-      rows = first < 0 || first >= p.cap ? 0 : max(0, min(n, p.cap - first));
+      rows = first < 0 || first >= p.cap ? 0 : max(0, min(n, min(p.cap - first, p.most_rows)));
       if (rows != n && blockIdx.x == 0 && threadIdx.x < 32) set_error(p.error_word, EP_ERRBIT_CAPACITY);
       mine = F == kGradW ? p.a_tiles * p.b_tiles : p.a_tiles * ceil_div(rows, p.max_cols);
     }
@@ -309,7 +309,9 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
   // for the adapters' steps, so that the first waits for nothing.
   const int b_bytes = Walker<F>::most_cols(p) / 2 * 128, stage_bytes = kABytes + b_bytes;
   int stages = p.ring_bytes / 1024 * 1024 / stage_bytes;
-  const int side_stages = stages >= 8 ? kSideStages : 2;
+  // (a stage less in the first costs 10% with six in all, so one is enough
+  // for the second then: long runs of rows need a step or two a tile)
+  const int side_stages = stages >= 8 ? kSideStages : 1;
   if (F == kAdapter) stages -= side_stages;
   stages = min(stages, kMaxStages);
   char *side = ring + stages * stage_bytes;
@@ -539,7 +541,10 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         }
         copy_commit();
         ++flying;
-        if (flying == 2) {
+        if (side_stages == 1) {
+          copy_wait<0>();
+          hand_over();
+        } else if (flying == 2) {
           copy_wait<1>();
           hand_over();
         }
