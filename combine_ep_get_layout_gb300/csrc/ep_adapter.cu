@@ -98,23 +98,24 @@ __device__ __forceinline__ int list_adapters(const LowParams &p, int tile, int *
   return count;
 }
 
-// The low rows of few rows: a block a row, which reads its adapter's
-// down-projection by itself (rows of one adapter meet it in L2), a warp two
-// of its vectors at a time; the first blocks make the tiles' plans.
+// The low rows of few rows: a block for 16 low values of a row, which reads
+// its part of the adapter's down-projection by itself (rows of one adapter
+// meet it in L2), a warp two vectors; the first blocks make the tiles' plans.
 constexpr int kRowThreads = 256;
-constexpr int64_t kRowBytes = 128 << 20;
+constexpr int kRowRanks = kRowThreads / 32 * 2;
+constexpr int64_t kRowBytes = 256 << 20;
 
 __global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_constant__ LowParams p, int tiles) {
   extern __shared__ int s_dyn[];  // [adapters]
   __shared__ int s_place[kMaxCols], s_list[kMaxCols];
   __shared__ uint32_t s_first[kMaxCols / 32];
-  if ((int)blockIdx.x < tiles)
+  if ((int)blockIdx.x < tiles && blockIdx.y == 0)
     for (int i = threadIdx.x; i < p.adapters; i += kRowThreads) s_dyn[i] = kMaxCols;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   if ((int)blockIdx.x < tiles) {
-    list_adapters(p, blockIdx.x, s_dyn, s_place, s_list, s_first, true);
+    if (blockIdx.y == 0) list_adapters(p, blockIdx.x, s_dyn, s_place, s_list, s_first, true);
     return;
   }
   const int t = blockIdx.x - tiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -122,31 +123,31 @@ __global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_c
   if (a < 0 || a >= p.adapters) return;
   const uint16_t *x = p.rows_x + (int64_t)t * p.hidden;
   const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + a);
-  for (int i = warp * 2; i < p.rank; i += kRowThreads / 32 * 2) {
-    const uint16_t *v = p.a + (a * p.rank + i) * p.hidden;
-    float sum[2] = {0.0f, 0.0f};
+  const int i = (int)blockIdx.y * kRowRanks + warp * 2;
+  if (i >= p.rank) return;
+  const uint16_t *v = p.a + (a * p.rank + i) * p.hidden;
+  float sum[2] = {0.0f, 0.0f};
 #pragma unroll 4
-    for (int k = lane * 8; k < p.hidden; k += 256) {
-      const int4 xv = __ldg(reinterpret_cast<const int4 *>(x + k));
-      const int4 a0 = __ldg(reinterpret_cast<const int4 *>(v + k));
-      const int4 a1 = __ldg(reinterpret_cast<const int4 *>(v + p.hidden + k));
-      const uint32_t *xw = reinterpret_cast<const uint32_t *>(&xv);
-      const uint32_t *w0 = reinterpret_cast<const uint32_t *>(&a0), *w1 = reinterpret_cast<const uint32_t *>(&a1);
+  for (int k = lane * 8; k < p.hidden; k += 256) {
+    const int4 xv = __ldg(reinterpret_cast<const int4 *>(x + k));
+    const int4 a0 = __ldg(reinterpret_cast<const int4 *>(v + k));
+    const int4 a1 = __ldg(reinterpret_cast<const int4 *>(v + p.hidden + k));
+    const uint32_t *xw = reinterpret_cast<const uint32_t *>(&xv);
+    const uint32_t *w0 = reinterpret_cast<const uint32_t *>(&a0), *w1 = reinterpret_cast<const uint32_t *>(&a1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum[0] += bf16_lo(xw[j]) * bf16_lo(w0[j]);
-        sum[0] += bf16_hi(xw[j]) * bf16_hi(w0[j]);
-        sum[1] += bf16_lo(xw[j]) * bf16_lo(w1[j]);
-        sum[1] += bf16_hi(xw[j]) * bf16_hi(w1[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      sum[0] += bf16_lo(xw[j]) * bf16_lo(w0[j]);
+      sum[0] += bf16_hi(xw[j]) * bf16_hi(w0[j]);
+      sum[1] += bf16_lo(xw[j]) * bf16_lo(w1[j]);
+      sum[1] += bf16_hi(xw[j]) * bf16_hi(w1[j]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
-    }
-    if (lane == 0) *reinterpret_cast<uint32_t *>(p.low + (int64_t)t * p.rank + i) = pack_bf16x2(sum[0] * f, sum[1] * f);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+    sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+  }
+  if (lane == 0) *reinterpret_cast<uint32_t *>(p.low + (int64_t)t * p.rank + i) = pack_bf16x2(sum[0] * f, sum[1] * f);
 }
 
 // A barrier of the first four warps; whether all of them say `ok`.
@@ -403,12 +404,23 @@ ep_status_t choose(const DeviceInfo *di, int num_rows, int hidden, int width, Cu
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Where every row may read its adapter by itself: up to 128 MB from L2.
+// Where every row may read its adapter by itself: up to 256 MB from L2
+// (2048 rows of rank 16, 4096 -> 1024, 40 adapters: interleaved 42 us against 101
+// by stacks, in runs 34 against 28).
 bool row_kernel(const AdapterArgs &a) { return (int64_t)a.num_rows * a.rank * a.hidden * 2 <= kRowBytes; }
 
 ep_status_t launch_rows(const LowParams &q, const Cut &c, cudaStream_t stream) {
-  const cudaError_t e = launch_kernel(adapter_row_kernel, q.T + c.tiles, kRowThreads, (size_t)q.adapters * 4, stream,
-                                      false, q, c.tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(q.T + c.tiles, up(q.rank, kRowRanks));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = (size_t)q.adapters * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = kUsePdl ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_row_kernel, q, c.tiles);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "adapter_row launch");
 }
 

@@ -69,6 +69,20 @@ def test_adapters(T, H, N, A, r, spread):
     check(x, w, a, b, idx, None, ep.ep_adapter_product(x, w, a, b, idx))
 
 
+@pytest.mark.parametrize("T,H,N,A,r", [(1100, 4096, 128, 5, 32), (2100, 1024, 72, 40, 64), (1500, 2048, 2048, 300, 48),
+                                       (4200, 4096, 1032, 3, 8), (2600, 4096, 264, 20, 16)])
+@pytest.mark.parametrize("spread", ["rows", "runs", "one"])
+def test_many_rows(T, H, N, A, r, spread):
+    """Sizes at which the low rows come from stacked adapters."""
+    x, w, a, b, idx, s = make(T, H, N, A, r, T + A, spread)
+    idx[7], idx[T - 1] = -1, A
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = ep.ep_adapter_product(x, w, a, b, idx, s, error_word=word)
+    assert int(word) == ep.EP_ERRBIT_BAD_INDEX
+    check(x, w, a, b, idx, s, out)
+    assert torch.equal(out, ep.ep_adapter_product(x, w, a, b, idx, s))
+
+
 def test_bad_indices_count_as_none_and_are_flagged():
     x, w, a, b, idx, s = make(40, 128, 64, 4, 16, 3, "rows")
     word = torch.zeros(1, dtype=torch.int32, device=DEV)

@@ -185,6 +185,22 @@ def test_experts_without_rows(act):
     assert bool((grad_w[empty] == 0).all()) and bool((grad_w[3] != 0).any())
 
 
+def test_counts_beyond_num_tokens_are_cut_and_flagged():
+    """A layout whose counts belong to more tokens than it says: rows past
+    num_tokens an expert are skipped and flagged, the others computed."""
+    lay, x, used, g = rows_and_layout(100, 1, 2, 64, 1, 12)
+    w = weights(g, 2, 64, 64)
+    want = ep.ep_expert_product(x, w, lay)
+    assert lay.errors() == 0
+    lay.num_tokens = 20
+    out = torch.full((x.shape[0], 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product(x, w, lay, out=out)
+    assert lay.errors() == ep.EP_ERRBIT_CAPACITY
+    for a, n in segments(lay):
+        keep = min(n, 20)
+        assert torch.equal(out[a:a + keep], want[a:a + keep]) and bool((out[a + keep:a + n] == 7.0).all())
+
+
 def test_no_tokens():
     idx = torch.empty((0, 2), dtype=torch.int64, device=DEV)
     lay = ep.ep_get_layout_expanded(idx, 4, 1)
