@@ -531,31 +531,39 @@ def _want_shape(t: torch.Tensor, name: str, shape: tuple):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _launch(dev: torch.device, fn: str, args, stream):
-    """``_call`` for functions of one argument block and a stream, with the
-    fewest steps in Python: these calls can be shorter than their set-up."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_functions = {}
+
+# These calls can be shorter than their set-up in Python, so each wrapper
+# looks at its tensors in one expression and lets a second function say what
+# is wrong.  Tensors are on device `i` (get_device() is -1 off the GPU).
+
+
+def _launch(index: int, fn: str, args, stream):
+    """``_call`` for functions of one argument block and a stream."""
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev.index)
-    elif stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        handle = _raw_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     else:
         handle = stream.cuda_stream
-    f = getattr(N.load(), fn)
-    if torch.cuda.current_device() == dev.index:
+    f = _functions.get(fn)
+    if f is None:
+        f = _functions[fn] = getattr(N.load(), fn)
+    if _current() == index:
         status = f(C.byref(args), handle)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             status = f(C.byref(args), handle)
-    if status != N.EP_OK:
+    if status:
         _check(status, fn)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _want_logits(logits: torch.Tensor) -> int:
-    """Checks the logits (rows may be apart, a row's entries may not) and
-    returns the row stride."""
+def _logits_stride(logits: torch.Tensor) -> int:
+    """The row stride of logits [T, E] (rows may be apart, a row's entries may
+    not)."""
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")
     if logits.dtype not in _LOGITS:
@@ -565,10 +573,10 @@ def _want_logits(logits: torch.Tensor) -> int:
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
     T, E = logits.shape
-    stride = logits.stride()
-    if (E > 1 and stride[1] != 1) or (T > 1 and stride[0] < E):
+    apart, step = logits.stride()
+    if (E > 1 and step != 1) or (T > 1 and apart < E):
         raise ValueError("a row of logits must be contiguous, and rows must not overlap")
-    return stride[0] if T > 1 else max(E, 1)
+    return apart if T > 1 else max(E, 1)
 
 
 def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
@@ -586,25 +594,26 @@ def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
     with a logit of -infinity or NaN are never chosen; missing choices are -1
     with weight 0.  Ties go to the lowest index.
     """
-    stride = _want_logits(logits)
-    dev = logits.device
+    apart = _logits_stride(logits)
     T, E = logits.shape
-    if bias is not None:
+    dev = logits.device
+    if bias is not None and not (bias.dtype is torch.float32 and bias.device == dev
+                                 and bias.is_contiguous() and bias.shape == (E,)):
         _want(bias, "bias", torch.float32, dev)
         _want_shape(bias, "bias", (E,))
     if out is None:
-        out = Routing(torch.empty((T, num_topk), dtype=torch.int64, device=dev),
-                      torch.empty((T, num_topk), dtype=torch.float32, device=dev))
+        idx = torch.empty((T, num_topk), dtype=torch.int64, device=dev)
+        out = Routing(idx, torch.empty((T, num_topk), dtype=torch.float32, device=dev))
     else:
-        _want(out.topk_idx, "topk_idx", torch.int64, dev)
-        _want(out.topk_weights, "topk_weights", torch.float32, dev)
-        _want_shape(out.topk_idx, "topk_idx", (T, num_topk))
-        _want_shape(out.topk_weights, "topk_weights", (T, num_topk))
-    args = N.ep_route_args_t(
-        logits.data_ptr(), _LOGITS[logits.dtype], stride, T, E, num_topk, _SCORES[score],
+        for name, t, dtype in (("topk_idx", out.topk_idx, torch.int64),
+                               ("topk_weights", out.topk_weights, torch.float32)):
+            _want(t, name, dtype, dev)
+            _want_shape(t, name, (T, num_topk))
+    _launch(dev.index, "ep_route", N.ep_route_args_t(
+        logits.data_ptr(), _LOGITS[logits.dtype], apart, T, E, num_topk, _SCORES[score],
         None if bias is None else bias.data_ptr(), num_groups, topk_groups, group_top,
-        1 if renormalize else 0, weight_scale, out.topk_idx.data_ptr(), out.topk_weights.data_ptr())
-    _launch(dev, "ep_route", args, stream)
+        1 if renormalize else 0, weight_scale, out.topk_idx.data_ptr(), out.topk_weights.data_ptr()),
+        stream)
     return out
 
 
@@ -614,9 +623,9 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
     """The gradient of ``ep_route``'s weights for the logits ([T, E], the
     logits' dtype), given the weights' gradient (fp32 [T, K]) and the choice.
     The choice itself, and so the bias, has no gradient."""
-    stride = _want_logits(logits)
-    dev = logits.device
+    apart = _logits_stride(logits)
     T, E = logits.shape
+    dev = logits.device
     _want(topk_idx, "topk_idx", torch.int64, dev)
     _want(grad_weights, "grad_weights", torch.float32, dev)
     K = topk_idx.shape[-1]
@@ -627,26 +636,43 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
     else:
         _want(out, "out", logits.dtype, dev)
         _want_shape(out, "out", (T, E))
-    args = N.ep_route_backward_args_t(
-        grad_weights.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], stride,
+    _launch(dev.index, "ep_route_backward", N.ep_route_backward_args_t(
+        grad_weights.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], apart,
         topk_idx.data_ptr(), T, E, K, _SCORES[score], 1 if renormalize else 0, weight_scale,
-        out.data_ptr())
-    _launch(dev, "ep_route_backward", args, stream)
+        out.data_ptr()), stream)
     return out
 
 
+def _refuse_tensors(*wanted):
+    """Raises for the first of (tensor, name, dtype, device, shape) that is
+    not so (None tensors pass)."""
+    for t, name, dtype, dev, shape in wanted:
+        if t is not None:
+            _want(t, name, dtype, dev)
+            _want_shape(t, name, shape)
+
+
 def _product_sizes(x, w, layout, activation):
-    """Checks rows and weights; (capacity, hidden, width, wide)."""
-    _want(x, "x", torch.bfloat16)
-    _want(w, "w", torch.bfloat16, x.device)
+    """(capacity, hidden, width, wide) of rows and weights, checked."""
+    bf = torch.bfloat16
+    if not (x.dtype is bf and w.dtype is bf and x.is_cuda and x.get_device() == w.get_device()
+            and x.is_contiguous() and w.is_contiguous()):
+        _want(x, "x", bf)
+        _want(w, "w", bf, x.device)
     if x.dim() != 2 or w.dim() != 3:
         raise ValueError("x must be [recv_capacity, hidden] and w [num_experts, outputs, hidden]")
     cap, H = x.shape
-    wide = w.shape[1]
-    _want_shape(w, "w", (layout.num_experts, wide, H))
-    if activation == "swiglu" and wide % 2:
-        raise ValueError("w must have an even number of outputs with swiglu")
-    return cap, H, wide // 2 if activation == "swiglu" else wide, wide
+    experts, wide, inner = w.shape
+    if experts != layout.num_experts or inner != H:
+        _want_shape(w, "w", (layout.num_experts, wide, H))
+    if activation == "swiglu":
+        if wide % 2:
+            raise ValueError("w must have an even number of outputs with swiglu")
+        return cap, H, wide // 2, wide
+    return cap, H, wide, wide
+
+
+_LAYOUT_POINTER = C.POINTER(N.ep_expanded_layout_t)
 
 
 def ep_expert_product(x: torch.Tensor, w: torch.Tensor, layout: ExpandedLayout,
@@ -663,20 +689,16 @@ def ep_expert_product(x: torch.Tensor, w: torch.Tensor, layout: ExpandedLayout,
     """
     act = _ACTIVATIONS[activation]
     cap, H, width, wide = _product_sizes(x, w, layout, activation)
-    dev = x.device
+    bf, dev = torch.bfloat16, x.device
     if out is None:
-        out = torch.empty((cap, width), dtype=torch.bfloat16, device=dev)
-    else:
-        _want(out, "out", torch.bfloat16, dev)
-        _want_shape(out, "out", (cap, width))
+        out = torch.empty((cap, width), dtype=bf, device=dev)
+    elif not (out.dtype is bf and out.device == dev and out.is_contiguous() and out.shape == (cap, width)):
+        _refuse_tensors((out, "out", bf, dev, (cap, width)))
     if preact is not None:
-        _want(preact, "preact", torch.bfloat16, dev)
-        _want_shape(preact, "preact", (cap, wide))
-    st = layout.c_struct()
-    args = N.ep_expert_product_args_t(
-        x.data_ptr(), cap, layout.num_tokens, H, layout.num_experts, C.pointer(st), w.data_ptr(),
-        width, act, out.data_ptr(), None if preact is None else preact.data_ptr())
-    _launch(dev, "ep_expert_product", args, stream)
+        _refuse_tensors((preact, "preact", bf, dev, (cap, wide)))
+    _launch(dev.index, "ep_expert_product", N.ep_expert_product_args_t(
+        x.data_ptr(), cap, layout.num_tokens, H, layout.num_experts, _LAYOUT_POINTER(layout.c_struct()),
+        w.data_ptr(), width, act, out.data_ptr(), None if preact is None else preact.data_ptr()), stream)
     return out
 
 
@@ -695,36 +717,30 @@ def ep_expert_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Ten
     is zero."""
     act = _ACTIVATIONS[activation]
     cap, H, width, wide = _product_sizes(x, w, layout, activation)
-    dev = x.device
-    _want(grad, "grad", torch.bfloat16, dev)
-    _want_shape(grad, "grad", (cap, width))
+    bf, dev = torch.bfloat16, x.device
     if act == N.EP_ACT_SWIGLU:
         if preact is None:
             raise ValueError("swiglu needs preact")
         if grad_preact is None:
-            grad_preact = torch.empty((cap, wide), dtype=torch.bfloat16, device=dev)
-        for name, t in (("preact", preact), ("grad_preact", grad_preact)):
-            _want(t, name, torch.bfloat16, dev)
-            _want_shape(t, name, (cap, wide))
+            grad_preact = torch.empty((cap, wide), dtype=bf, device=dev)
+    else:
+        preact = grad_preact = None
     if not need_x:
         grad_x = None
     elif grad_x is None:
-        grad_x = torch.empty((cap, H), dtype=torch.bfloat16, device=dev)
+        grad_x = torch.empty((cap, H), dtype=bf, device=dev)
     if not need_w:
         grad_w = None
     elif grad_w is None:
-        grad_w = torch.empty(w.shape, dtype=torch.bfloat16, device=dev)
-    for name, t, shape in (("grad_x", grad_x, (cap, H)), ("grad_w", grad_w, tuple(w.shape))):
-        if t is not None:
-            _want(t, name, torch.bfloat16, dev)
-            _want_shape(t, name, shape)
-    st = layout.c_struct()
-    args = N.ep_expert_product_backward_args_t(
+        grad_w = torch.empty(w.shape, dtype=bf, device=dev)
+    _refuse_tensors((grad, "grad", bf, dev, (cap, width)), (preact, "preact", bf, dev, (cap, wide)),
+                    (grad_preact, "grad_preact", bf, dev, (cap, wide)), (grad_x, "grad_x", bf, dev, (cap, H)),
+                    (grad_w, "grad_w", bf, dev, w.shape))
+    _launch(dev.index, "ep_expert_product_backward", N.ep_expert_product_backward_args_t(
         grad.data_ptr(), x.data_ptr(), w.data_ptr(), cap, layout.num_tokens, H, layout.num_experts,
-        C.pointer(st), width, act, None if preact is None else preact.data_ptr(),
+        _LAYOUT_POINTER(layout.c_struct()), width, act, None if preact is None else preact.data_ptr(),
         None if grad_preact is None else grad_preact.data_ptr(),
-        None if grad_x is None else grad_x.data_ptr(), None if grad_w is None else grad_w.data_ptr())
-    _launch(dev, "ep_expert_product_backward", args, stream)
+        None if grad_x is None else grad_x.data_ptr(), None if grad_w is None else grad_w.data_ptr()), stream)
     return grad_x, grad_w
 
 
@@ -743,40 +759,43 @@ def ep_adapter_product(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, l
     ``lora_b`` bf16 [A, N, r], ``adapter_scale`` fp32 [A] (1 when not given).
     An index outside [-1, A) counts as -1 and sets EP_ERRBIT_BAD_INDEX in
     ``error_word`` (int32 [1], if given).  Returns bf16 [T, N]."""
-    _want(x, "x", torch.bfloat16)
-    dev = x.device
-    for name, t in (("w", w), ("lora_a", lora_a), ("lora_b", lora_b)):
-        _want(t, name, torch.bfloat16, dev)
-    _want(adapter_idx, "adapter_idx", torch.int64, dev)
+    bf = torch.bfloat16
+    _want(x, "x", bf)
     if x.dim() != 2 or w.dim() != 2 or lora_a.dim() != 3:
         raise ValueError("x must be [rows, hidden], w [outputs, hidden], lora_a [adapters, rank, hidden]")
     T, H = x.shape
+    A, r, _ = lora_a.shape
     width = w.shape[0]
-    A, r = lora_a.shape[:2]
-    _want_shape(w, "w", (width, H))
-    _want_shape(lora_a, "lora_a", (A, r, H))
-    _want_shape(lora_b, "lora_b", (A, width, r))
-    _want_shape(adapter_idx, "adapter_idx", (T,))
-    if adapter_scale is not None:
-        _want(adapter_scale, "adapter_scale", torch.float32, dev)
-        _want_shape(adapter_scale, "adapter_scale", (A,))
+    dev, i = x.device, x.get_device()
+    if not (w.dtype is bf and lora_a.dtype is bf and lora_b.dtype is bf and adapter_idx.dtype is torch.int64
+            and w.get_device() == i and lora_a.get_device() == i and lora_b.get_device() == i
+            and adapter_idx.get_device() == i and w.is_contiguous() and lora_a.is_contiguous()
+            and lora_b.is_contiguous() and adapter_idx.is_contiguous() and w.shape == (width, H)
+            and lora_a.shape == (A, r, H) and lora_b.shape == (A, width, r) and adapter_idx.shape == (T,)):
+        _refuse_tensors((w, "w", bf, dev, (width, H)), (lora_a, "lora_a", bf, dev, (A, r, H)),
+                        (lora_b, "lora_b", bf, dev, (A, width, r)),
+                        (adapter_idx, "adapter_idx", torch.int64, dev, (T,)))
+    if adapter_scale is not None and not (
+            adapter_scale.dtype is torch.float32 and adapter_scale.get_device() == i
+            and adapter_scale.is_contiguous() and adapter_scale.shape == (A,)):
+        _refuse_tensors((adapter_scale, "adapter_scale", torch.float32, dev, (A,)))
     if error_word is not None:
         _want(error_word, "error_word", torch.int32, dev)
     if out is None:
-        out = torch.empty((T, width), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, width), dtype=bf, device=dev)
     else:
-        _want(out, "out", torch.bfloat16, dev)
-        _want_shape(out, "out", (T, width))
+        _refuse_tensors((out, "out", bf, dev, (T, width)))
     if workspace is None:
-        workspace = torch.empty(max(ep_adapter_workspace_bytes(T, H, r), 16), dtype=torch.uint8, device=dev)
+        nbytes = ep_adapter_workspace_bytes(T, H, r) or 16
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
         _want(workspace, "workspace", torch.uint8, dev)
-    args = N.ep_adapter_product_args_t(
+        nbytes = workspace.numel()
+    _launch(i, "ep_adapter_product", N.ep_adapter_product_args_t(
         x.data_ptr(), T, H, w.data_ptr(), width, lora_a.data_ptr(), lora_b.data_ptr(), A, r,
         adapter_idx.data_ptr(), None if adapter_scale is None else adapter_scale.data_ptr(),
-        out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        None if error_word is None else error_word.data_ptr())
-    _launch(dev, "ep_adapter_product", args, stream)
+        out.data_ptr(), workspace.data_ptr(), nbytes, None if error_word is None else error_word.data_ptr()),
+        stream)
     return out
 
 
