@@ -205,11 +205,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
 // A lane a token: no exchange between lanes, and a selection by sorting
 // networks, whose steps are one minimum and one maximum.  32 rows lie in
 // shared memory an odd number of 16-byte pieces apart, so that the lanes read
-// the same place of their rows without conflicts.  The networks sort
-// words of a key's upper bits over the complement of its index (ties go to
-// the lowest); the few words found are then ordered by their keys, and where
-// the upper bits alone cannot tell the last choice from what was left out, the
-// row is searched again by whole keys.
+// the same place of their rows without conflicts.  The networks sort words:
+// a key's place below the row's largest, in fixed point (23 bits of a window
+// of kWindow; bf16 logits: their own 16 bits), over the complement of its
+// index, so that ties go to the lowest.  Words of the same place are then
+// ordered by their keys, and where the places alone cannot tell the last
+// choice from what was left out (some 1e-4 of the tokens), or the window does
+// not reach it, the row is searched again by whole keys.
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
   uint32_t *words = reinterpret_cast<uint32_t *>(raw);     // [kLaneWarps][N + 1][32]
   float *scores = raw + kLaneWarps * (N + 1) * 32;         // [groups][32]
   float *bias = raw + tail;                                // [pitch]
-  __shared__ float s_part[2][kLaneWarps][32];
+  __shared__ float s_part[3][kLaneWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quads = (p.E + 3) / 4;
   const int t0 = blockIdx.x * 32, count = min(32, p.T - t0);
   const auto quad_at = [&](int row, int q) { return row * pitch + q * 4; };
@@ -378,6 +380,7 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
   // the groups' scores: a warp some groups, or of a single group its share.
   const int per = p.E / p.G / 4;  // quads of a group
   const float inv = 1.0f / sum;
+  float most_key = kNegInf;
   if (here)
     for (int g = p.G == 1 ? 0 : warp; g < p.G; g += kLaneWarps) {
       float a = kNegInf, b = kNegInf;
@@ -401,17 +404,24 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
           v[j] = v[j] > kNegInf ? key : kNegInf;
         }
         *reinterpret_cast<float4 *>(rows + quad_at(lane, q)) = make_float4(v[0], v[1], v[2], v[3]);
-        if (p.G > 1)
+        if (p.G > 1) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             b = fmaxf(b, fminf(a, v[j]));
             a = fmaxf(a, v[j]);
           }
+        } else {
+          a = fmaxf(fmaxf(a, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+        }
       }
+      most_key = fmaxf(most_key, a);
       if (p.G == 1) break;
       scores[g * 32 + lane] = p.group_top == 2 && b != kNegInf ? a + b : a;
     }
+  s_part[2][warp][lane] = most_key;
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kLaneWarps; ++w) most_key = fmaxf(most_key, s_part[2][w][lane]);
   uint64_t offered = p.G == 1 && here ? 1ull : 0ull;
   if (p.G > 1 && p.G <= 8 && here) {
     // a group's rank among the few: how many come before it
@@ -444,14 +454,23 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
 
   // this warp's share of the offered groups, one after the other: the N
   // largest words, and the largest of the others
+  constexpr bool kExact = BF16 && KIND == kLogitKey;
+  constexpr float kWindow = KIND == kLogitKey ? 32.0f : 4.0f;
   const uint32_t low = (1u << bits) - 1u;
+  const float steps = (float)((1u << (32 - bits)) - 1u), scale = steps * (1.0f / kWindow);
+  // A key's place in a word's upper bits.  8388608 + the place, as a float,
+  // has it in its low bits, and the shift drops the others.
+  const auto place_of = [&](float v, float from) {
+    return kExact ? order_of(v) & ~low : __float_as_uint(fmaxf(fmaf(v - from, scale, 8388608.0f + steps), 8388608.0f)) << bits;
+  };
+  const uint32_t least = kExact ? kLeast : 1u << bits;  // smaller words: none, or below the window
   uint32_t top[N] = {}, out = 0u;
   const int length = p.G == 1 ? quads : per, all = length * p.Gk;
   const int i1 = all * (warp + 1) / kLaneWarps;
   int i = all * warp / kLaneWarps, in = i % length;
   uint64_t left = offered;
   for (int k = i / length; k > 0; --k) left &= left - 1ull;
-  while (i < i1) {  // words of masked experts (below kLeast) lie under all others
+  while (i < i1) {
     // a run of quads of one group (a lane may have none left)
     const int run = min(i1 - i, length - in);
     const bool some = left != 0ull;
@@ -466,7 +485,7 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
         const uint32_t index = low - (uint32_t)(at * 4);
         const bool use = some && q + n < run;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[n * 4 + j] = use ? (order_of(v[j]) & ~low) | (index - j) : 0u;
+        for (int j = 0; j < 4; ++j) w[n * 4 + j] = use ? place_of(v[j], most_key) + (index - j) : 0u;
       }
       sort_words(w);
       join_words(top, w, out);
@@ -498,8 +517,8 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
     uint32_t last = 0u;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      idx[n] = top[n] < kLeast ? -1 : (int)(low - (top[n] & low));
-      if (n > 0) alike = alike || (top[n] >= kLeast && (top[n] & ~low) == (top[n - 1] & ~low));
+      idx[n] = top[n] < least ? -1 : (int)(low - (top[n] & low));
+      if (n > 0) alike = alike || (!kExact && top[n] >= least && (top[n] & ~low) == (top[n - 1] & ~low));
       last = n < p.K ? top[n] : last;
     }
     if (alike) {
@@ -519,8 +538,8 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
             idx[n + 1] = x;
           }
     }
-    if (out >= kLeast && (out & ~low) == (last & ~low) && !(BF16 && KIND == kLogitKey)) {
-      // the last places go by whole keys among all words of those upper bits
+    if (!kExact && (last < least || (out & ~low) == (last & ~low))) {
+      // the last choices go by whole keys among all of that place
       const uint32_t bits_of = last & ~low;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
@@ -535,7 +554,7 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
           read4(q, v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if ((order_of(v[j]) & ~low) != bits_of || !(v[j] > key[N - 1])) continue;
+            if (place_of(v[j], most_key) != bits_of || !(v[j] > key[N - 1])) continue;
             const float x = v[j];
             const int e = q * 4 + j;
 #pragma unroll
@@ -562,37 +581,35 @@ __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParam
   }
   __syncthreads();
 
-  // weights, as in choice_weight: four threads a token
+  // weights, as in choice_weight: kLaneWarps threads a token
   const int *choice = reinterpret_cast<const int *>(words);
-  const int t = threadIdx.x >> 2;
+  const int t = threadIdx.x / kLaneWarps, own = threadIdx.x % kLaneWarps;
   m = s_part[0][0][t];
   sum = s_part[1][0][t];
-  float l[N / 4], w[N / 4], most = kNegInf, total = 0.0f;
+  float l[N / kLaneWarps], w[N / kLaneWarps], most = kNegInf, total = 0.0f;
 #pragma unroll
-  for (int n = 0; n < N / 4; ++n) {
-    const int k = n * 4 + (threadIdx.x & 3), e = t < count && k < p.K ? choice[t * p.K + k] : -1;
+  for (int n = 0; n < N / kLaneWarps; ++n) {
+    const int k = n * kLaneWarps + own, e = t < count && k < p.K ? choice[t * p.K + k] : -1;
     l[n] = e < 0               ? kNegInf
            : KIND == kLogitKey ? rows[quad_at(t, e >> 2) + (e & 3)]
                                : load_logit<BF16>(base + t * step, e);
     most = fmaxf(most, p.sigmoid ? fminf(l[n], 0.0f) : l[n]);
   }
-  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  most = warp_max<kLaneWarps>(most);
   if (!p.renorm) most = p.sigmoid ? 0.0f : m;
 #pragma unroll
-  for (int n = 0; n < N / 4; ++n) {
+  for (int n = 0; n < N / kLaneWarps; ++n) {
     if (p.sigmoid)
       w[n] = l[n] == kNegInf ? 0.0f : expf(fminf(l[n], 0.0f) - most) / (1.0f + expf(-fabsf(l[n])));
     else
       w[n] = l[n] == kNegInf ? 0.0f : expf(l[n] - most);
     total += w[n];
   }
-  total += __shfl_xor_sync(0xffffffffu, total, 1);
-  total += __shfl_xor_sync(0xffffffffu, total, 2);
+  total = warp_sum<kLaneWarps>(total);
   if (!p.renorm) total = p.sigmoid ? 1.0f : sum;
 #pragma unroll
-  for (int n = 0; n < N / 4; ++n) {
-    const int k = n * 4 + (threadIdx.x & 3);
+  for (int n = 0; n < N / kLaneWarps; ++n) {
+    const int k = n * kLaneWarps + own;
     if (t < count && k < p.K) p.w[(int64_t)(t0 + t) * p.K + k] = total > 0.0f ? w[n] / total * p.scale : 0.0f;
   }
   for (int i = threadIdx.x; i < count * p.K; i += kLaneWarps * 32) p.idx[(int64_t)t0 * p.K + i] = choice[i];
@@ -610,7 +627,7 @@ bool lanes_fit(const RouteArgs &a) {
 template <bool BF16, int N, KeyKind KIND>
 ep_status_t launch_lanes_as(const RouteParams &p, cudaStream_t stream) {
   const int pitch = (((p.E + 3) / 4) | 1) * 4;
-  int bits = 1;
+  int bits = 9;  // of a word, for the index
   while ((1 << bits) < (p.E + 3) / 4 * 4) ++bits;
   const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
                        p.row_stride % (BF16 ? 8 : 4) == 0 && p.E % (BF16 ? 8 : 4) == 0;
