@@ -478,13 +478,11 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       ok = mbar_wait_pair(&s_bar.ends[s], (parities >> s) & 1u);
       if (!ok) break;
       parities ^= 1u << s;
-      char *a = ring + (size_t)s * stage_bytes;
+      // four blocks of 64 outer elements (A's two and B's), 128 bytes of each
+      // a row: one store of the warp
+      char *row = ring + (size_t)s * stage_bytes + (lane >> 3) * 8192 + (lane & 7) * 16;
       const int from = t.count % kInner, to = ceil_div(from, 16) * 16;
-      const int blocks = 2 + t.cols / 2 / 64;  // of 64 outer elements, A's two and B's
-      for (int i = lane; i < blocks * (to - from) * 8; i += 32) {
-        const int block = i / ((to - from) * 8), r = from + i / 8 % (to - from);
-        *reinterpret_cast<int4 *>(a + block * 8192 + r * 128 + (i & 7) * 16) = make_int4(0, 0, 0, 0);
-      }
+      for (int r = from; r < to; ++r) *reinterpret_cast<int4 *>(row + r * 128) = make_int4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_local(map_shared(smem_addr(&s_bar.fixed[s]), lead));
