@@ -8,8 +8,11 @@
 //   grad_x[s] = g[s] w[e],   grad_w[e] = sum over e's rows of g[s]^T x[s]
 //
 // with g the gradient of x w^T.  bf16 in and out, sums in fp32 in tensor
-// memory, rounded once.
-// The kernel is in ep_pair.cuh.
+// memory, rounded once.  The kernel is in ep_pair.cuh.
+//
+// Gradients through the gate of 4096 tokens top-6 of 64 experts, 4096 -> 2 x
+// 1408: 856 to 887 us sustained (814 us the first time, before the power limit
+// is met), of which the gate 43, the rows about 340, the weights about 400.
 #include "ep_pair.cuh"
 
 namespace ep {
@@ -18,6 +21,8 @@ namespace {
 
 // The gradient of silu(g) * u for the rows of the layout, kept in bf16 as the
 // preactivations are: it is an operand of two products on the tensor cores.
+// One pass over flat rows: 22 000 rows of 1408, 311 MB, 43 us (rows by expert
+// and block: 73 us, since experts differ in their rows).
 struct GateParams {
   const uint16_t *grad, *preact;
   uint16_t *out;

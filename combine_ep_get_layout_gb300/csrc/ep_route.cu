@@ -116,7 +116,8 @@ __device__ __forceinline__ float choice_weight(bool none, float l, bool sigmoid,
   return p;
 }
 
-// One warp a token; the keys of its row in shared memory.
+// One warp a token; the keys of its row in shared memory, a round of argmax a
+// choice.  8 experts, top-2: 2.7 us up to 2048 tokens, latency.
 template <bool BF16>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) {
   extern __shared__ float s_keys[];
@@ -285,7 +286,11 @@ __device__ __forceinline__ void join_words(uint32_t (&top)[N], uint32_t (&w)[N],
 }
 
 // kLaneWarps warps take 32 tokens together: each looks through a share of
-// every row, the first joins what they found.  p.logits' rows are `aligned`
+// every row, the first joins what they found.  65536 tokens, 256 experts in 8
+// groups, top-8: 33 us (rounds of argmax, a warp a token: 276; one warp for
+// the 32 tokens: 114; eight warps: 37).  The reads would take 11 us; it is
+// bound by the integer pipe, which makes the networks' comparisons.  Few
+// tokens: 7 us, mostly latency.  p.logits' rows are `aligned`
 // where all of them are made of whole 16-byte pieces.
 template <bool BF16, int N, KeyKind KIND>
 __global__ void __launch_bounds__(kLaneWarps * 32) route_lanes_kernel(RouteParams p, int pitch, int tail, int bits,
@@ -681,7 +686,9 @@ constexpr int kBackwardWarps = 8;
 // the whole row of logits; otherwise the row is zeros but for the choices,
 // and only their logits are read.  Either is written 16 bytes at a time
 // (`wide`: rows of whole pieces) and the choices' values after it: writes to
-// L2, which are one to memory.
+// L2, which are one to memory.  65536 tokens, 256 experts, top-8, not a full
+// softmax: 19 us, 7.3 TB/s of the bytes that would also read the logits
+// (rows in shared memory, a warp a token: 41 us; 16-byte zeros: 31 us).
 template <bool BF16, int L>
 __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(RouteBackwardParams p, bool wide) {
   constexpr int kPiece = BF16 ? 8 : 4;

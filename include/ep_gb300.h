@@ -501,7 +501,9 @@ ep_status_t ep_combine_expanded(const ep_combine_expanded_args_t *args, ep_strea
  * pointers, nothing allocated or synchronised, host-detectable problems
  * returned before anything is enqueued.  No counterpart in the pages, whose
  * dispatch takes the routing as given and whose combine takes the experts'
- * outputs as given.
+ * outputs as given.  A device wait that gives up sets EP_ERRBIT_TIMEOUT in
+ * the layout's error word (ep_adapter_product: in error_word, if given), and
+ * the outputs are then not complete.
  */
 
 typedef enum {
@@ -597,7 +599,8 @@ typedef enum {
  * EP_ERRBIT_CAPACITY.
  *   x       [recv_capacity * hidden] bf16
  *   layout  num_rows_per_expert, expert_offset and error_word are used; an
- *           expert has at most num_tokens rows (a token names it once)
+ *           expert has at most num_tokens rows (a token names it once), more
+ *           are skipped and set EP_ERRBIT_CAPACITY
  *   w       [E * wide * hidden] bf16, wide = width, or 2 * width with
  *           EP_ACT_SWIGLU (the gate's rows, then the others)
  *   out     [recv_capacity * width] bf16
@@ -629,7 +632,8 @@ ep_status_t ep_expert_product(const ep_expert_product_args_t *args, ep_stream_t 
  *   grad_w[e] = bf16(sum over e's rows s of g[s]^T x[s])   0 without rows
  *   grad         [recv_capacity * width] bf16
  *   preact       [recv_capacity * 2 * width] bf16 (EP_ACT_SWIGLU)
- *   grad_preact  [recv_capacity * 2 * width] bf16 (EP_ACT_SWIGLU): written
+ *   grad_preact  [recv_capacity * 2 * width] bf16 (EP_ACT_SWIGLU): written,
+ *                padding rows included
  *   grad_x       [recv_capacity * hidden] bf16 or NULL (not computed)
  *   grad_w       [E * wide * hidden] bf16 or NULL (not computed)
  * Sizes, alignment and the rest as for ep_expert_product.  The sums run in a
