@@ -101,6 +101,7 @@ struct Barriers {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t part_full, part_empty;  // the other pairs' results in the first one's shared memory
   uint32_t tmem;
+  int odd;  // kAdapter, the first pair's: the last tile with an up-projection that is not finite
 };
 
 struct Tile {
@@ -266,6 +267,45 @@ __device__ __forceinline__ int4 load_made(const int4 *p) {
   return v;
 }
 
+// The halves of a word of two bf16 that are not finite: their top bits.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t not_finite(const uint4 &w) {
+  return not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
+}
+
+// kAdapter: the infinities and NaN of the up-projections, which the gathering
+// warps left out, added to 32 rows c ... of output `at` that this warp wrote
+// (a sum with one of them is that one, whatever the rest was rounded to).
+__device__ __forceinline__ void add_odd(const Params &p, const Tile &t, int c, int at) {
+  const int32_t *plan = p.plan + (int64_t)t.part * kPlanWords;
+  for (int j = c; j < c + 32 && j < t.count; ++j) {
+    const int place = load_made(plan + 1 + kMaxCols + j);
+    if (place < 0 || at >= p.width) continue;
+    const uint16_t *up = p.up + ((int64_t)load_made(plan + 1 + place) * p.width + at) * p.rank;
+    const uint16_t *low = p.low + (int64_t)(t.first + j) * p.rank;
+    float more = 0.0f;
+    bool some = false;
+    for (int i = 0; i < p.rank; i += 8) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(up + i));
+      if (not_finite(u) == 0u) continue;
+      const int4 l = load_made(reinterpret_cast<const int4 *>(low + i));
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+      const uint32_t lw[4] = {(uint32_t)l.x, (uint32_t)l.y, (uint32_t)l.z, (uint32_t)l.w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint32_t odd = not_finite(uw[h]);
+        if (odd & 0x8000u) more += bf16_lo(uw[h]) * bf16_lo(lw[h]);
+        if (odd & 0x80000000u) more += bf16_hi(uw[h]) * bf16_hi(lw[h]);
+      }
+      some = true;
+    }
+    if (some) {
+      uint16_t *o = p.out + (int64_t)(t.first + j) * p.width + at;
+      *o = (uint16_t)(pack_bf16x2(bf16_lo(*o) + more, 0.0f) & 0xffffu);
+    }
+  }
+}
+
 template <Form F>
 __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_constant__ Params p) {
   extern __shared__ char s_raw[];
@@ -300,6 +340,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     }
     mbar_init(&s_bar.part_full, kResultWarps * (p.parts > 1 ? p.parts - 1 : 1));
     mbar_init(&s_bar.part_empty, kResultWarps);
+    s_bar.odd = -1;
     fence_barrier_init();
     prefetch_map(&p.a);
   }
@@ -453,7 +494,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       }
       if (F == kAdapter && ok) {
         if (n == pair) griddep_wait();
-        const int length = p.rank * load_made(p.plan + t.part * kPlanWords);  // of the adapters side by side
+        const int length = p.rank * load_made(p.plan + (int64_t)t.part * kPlanWords);  // of the adapters side by side
         for (int k = part; ok && k * kInner < length; k += p.parts) {
           ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_full[side_stage], side_phase));
           if (!ok) break;
@@ -505,7 +546,10 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     // ---------------------------------------------------------- adapters
     // Both operands of a further step are gathered 16 bytes at a time, in the
     // swizzled order that a tile's copy would give them: eight lanes take the
-    // eight pieces of a row, so a lane stays with one adapter in a step.
+    // eight pieces of a row, so a lane stays with one adapter in a step.  An
+    // up-projection meets every row of the tile, and in other adapters' rows
+    // zeros, which would make NaN of what is not finite: that is put to zero
+    // here, the tile is noted, and the results' warps add it to its own rows.
     griddep_wait();
     Walker<F> walk(p);
     Tile t;
@@ -514,7 +558,24 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     uint32_t phase = 0;
     int flying = 0;
     const int piece = lane & 7;
-    const auto hand_over = [&] {
+    const auto hand_over = [&](int n, int left) {  // left: of the inner dimension from this step on
+      if (piece * 8 < left) {
+        char *a = side + (size_t)hand * stage_bytes;
+        const auto at = [&](int j) {
+          const int r = rows + j * 4 + (lane >> 3);
+          return reinterpret_cast<uint4 *>(a + r * 128 + ((piece ^ (r & 7)) << 4));
+        };
+        uint32_t odd = 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) odd |= not_finite(*at(j));
+        if (odd != 0u) {
+          for (int j = 0; j < 8; ++j) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(at(j));
+            for (int i = 0; i < 4; ++i) w[i] &= ~((not_finite(w[i]) >> 15) * 0xffffu);
+          }
+          atom_max_cluster(map_shared(smem_addr(&s_bar.odd), rank), n);  // where the results are finished
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_local(map_shared(smem_addr(&s_bar.side_full[hand]), lead));
@@ -522,11 +583,12 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       --flying;
     };
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
-      const int32_t *plan = p.plan + t.part * kPlanWords;
+      const int32_t *plan = p.plan + (int64_t)t.part * kPlanWords;
       const int count = load_made(plan), length = count * p.rank, b_rows = t.cols / 2;
       const int place = rows + lane < b_rows ? load_made(plan + 1 + kMaxCols + (int)rank * b_rows + rows + lane) : -1;
       const int a0 = t.a0 + (int)rank * 128;
       const uint16_t *low = p.low + (int64_t)(t.first + (int)rank * b_rows) * p.rank;
+      int last = part;
       for (int k = part; k * kInner < length; k += p.parts) {
         ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
         if (!ok) break;
@@ -555,11 +617,12 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         ++flying;
         if (side_stages == 1) {
           copy_wait<0>();
-          hand_over();
+          hand_over(n, length - k * kInner);
         } else if (flying == 2) {
           copy_wait<1>();
-          hand_over();
+          hand_over(n, length - (k - p.parts) * kInner);
         }
+        last = k;
         if (++stage == side_stages) {
           stage = 0;
           phase ^= 1;
@@ -567,7 +630,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       }
       if (flying > 0) {
         copy_wait<0>();
-        hand_over();
+        hand_over(n, length - last * kInner);
       }
     }
     for (int i = 0; ok && i < side_stages; ++i) {
@@ -714,6 +777,10 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         }
       }
       if (t.cols <= half * 32) release(acc);  // no columns for this warp
+      if (F == kAdapter && *static_cast<volatile int *>(&s_bar.odd) >= n) {
+        __syncwarp();  // what other lanes wrote
+        for (int c = half * 32; c < t.cols; c += 64) add_odd(p, t, c, t.a0 + (int)rank * 128 + quarter * 32 + lane);
+      }
       if (F != kGradW && p.parts > 1) {
         __syncwarp();
         if (lane == 0)
@@ -773,7 +840,7 @@ ep_status_t most_clusters(const DeviceInfo *di, int parts, int *clusters) {
 
 constexpr uint64_t kSize = 2;  // bytes of an element
 
-int up(int a, int b) { return (a + b - 1) / b; }
+int up(int a, int b) { return a / b + (a % b != 0); }
 
 // Pairs that may share a tile of so many columns: their sums wait in the
 // first pair's shared memory, beside its ring.

@@ -55,6 +55,12 @@ __device__ __forceinline__ void store_cluster(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
+// Done when it returns: whoever is told of it afterwards sees the new value.
+__device__ __forceinline__ void atom_max_cluster(uint32_t cluster_addr, int v) {
+  int old;
+  asm volatile("atom.acq_rel.cluster.shared::cluster.max.s32 %0, [%1], %2;" : "=r"(old) : "r"(cluster_addr), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
   uint32_t done;
   asm volatile(

@@ -111,6 +111,32 @@ def test_unused_adapters_and_other_rows_do_not_leak():
     assert torch.equal(got[rest], want[rest]) and torch.isnan(got[11]).all()
 
 
+@pytest.mark.parametrize("T,H,N,A,r", [(3, 512, 136, 3, 8), (32, 4096, 520, 24, 16), (70, 128, 264, 6, 128),
+                                       (300, 256, 512, 40, 24), (1100, 4096, 128, 5, 32)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_an_up_projection_that_is_not_finite_stays_with_its_rows(T, H, N, A, r, value):
+    """Rows of other adapters, and outputs that it does not reach, keep their
+    bits; its own get what the formula gives (the sign too, where the low
+    value's sign is certain)."""
+    x, w, a, b, idx, s = make(T, H, N, A, r, T, "rows")
+    idx[0], idx[1], idx[2] = 1, 0, 1
+    clean = ep.ep_adapter_product(x, w, a, b, idx, s)
+    b[1, 5, r - 1], b[1, N - 1, 0], b[A - 1, N // 2] = value, value, -value
+    got = ep.ep_adapter_product(x, w, a, b, idx, s)
+    reached = torch.zeros((T, N), dtype=torch.bool, device=DEV)
+    for k, n in ((1, 5), (1, N - 1), (A - 1, N // 2)):
+        reached[(idx == k).nonzero()[:, 0], n] = True
+    assert torch.equal(got[~reached], clean[~reached])
+    assert reached.any() and not torch.isfinite(got[reached]).any()
+    if math.isinf(value):
+        for n, i in ((5, r - 1), (N - 1, 0)):
+            at = (idx == 1).nonzero()[:, 0]
+            low = x[at].double() @ a[1, i].double()
+            sure = low.abs() > H * 2.0 ** -23 * (x[at].double().abs() @ a[1, i].double().abs())
+            assert torch.equal(got[at[sure], n].double(), low[sure].sign() * value)
+    assert torch.equal(got.nan_to_num(nan=7.0), ep.ep_adapter_product(x, w, a, b, idx, s).nan_to_num(nan=7.0))
+
+
 def test_no_rows_and_another_stream():
     x, w, a, b, idx, s = make(0, 64, 32, 2, 8, 5, "rows")
     assert ep.ep_adapter_product(x, w, a, b, idx, s).shape == (0, 32)
