@@ -541,6 +541,16 @@ _functions = {}
 # is wrong.  Tensors are on device `i` (get_device() is -1 off the GPU).
 
 
+def _empty(shape, dtype, dev, stream):
+    """A new tensor for work on ``stream``: its memory comes from that
+    stream's, so neither what held it before nor what holds it next overlaps
+    the work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _launch(index: int, fn: str, args, stream):
     """``_call`` for functions of one argument block and a stream."""
     if stream is None:
@@ -602,8 +612,8 @@ def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
         _want(bias, "bias", torch.float32, dev)
         _want_shape(bias, "bias", (E,))
     if out is None:
-        idx = torch.empty((T, num_topk), dtype=torch.int64, device=dev)
-        out = Routing(idx, torch.empty((T, num_topk), dtype=torch.float32, device=dev))
+        idx = _empty((T, num_topk), torch.int64, dev, stream)
+        out = Routing(idx, _empty((T, num_topk), torch.float32, dev, stream))
     else:
         for name, t, dtype in (("topk_idx", out.topk_idx, torch.int64),
                                ("topk_weights", out.topk_weights, torch.float32)):
@@ -632,7 +642,7 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
     _want_shape(topk_idx, "topk_idx", (T, K))
     _want_shape(grad_weights, "grad_weights", (T, K))
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        out = _empty((T, E), logits.dtype, dev, stream)
     else:
         _want(out, "out", logits.dtype, dev)
         _want_shape(out, "out", (T, E))
@@ -691,7 +701,7 @@ def ep_expert_product(x: torch.Tensor, w: torch.Tensor, layout: ExpandedLayout,
     cap, H, width, wide = _product_sizes(x, w, layout, activation)
     bf, dev = torch.bfloat16, x.device
     if out is None:
-        out = torch.empty((cap, width), dtype=bf, device=dev)
+        out = _empty((cap, width), bf, dev, stream)
     elif not (out.dtype is bf and out.device == dev and out.is_contiguous() and out.shape == (cap, width)):
         _refuse_tensors((out, "out", bf, dev, (cap, width)))
     if preact is not None:
@@ -722,17 +732,17 @@ def ep_expert_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Ten
         if preact is None:
             raise ValueError("swiglu needs preact")
         if grad_preact is None:
-            grad_preact = torch.empty((cap, wide), dtype=bf, device=dev)
+            grad_preact = _empty((cap, wide), bf, dev, stream)
     else:
         preact = grad_preact = None
     if not need_x:
         grad_x = None
     elif grad_x is None:
-        grad_x = torch.empty((cap, H), dtype=bf, device=dev)
+        grad_x = _empty((cap, H), bf, dev, stream)
     if not need_w:
         grad_w = None
     elif grad_w is None:
-        grad_w = torch.empty(w.shape, dtype=bf, device=dev)
+        grad_w = _empty(w.shape, bf, dev, stream)
     _refuse_tensors((grad, "grad", bf, dev, (cap, width)), (preact, "preact", bf, dev, (cap, wide)),
                     (grad_preact, "grad_preact", bf, dev, (cap, wide)), (grad_x, "grad_x", bf, dev, (cap, H)),
                     (grad_w, "grad_w", bf, dev, w.shape))
@@ -782,12 +792,12 @@ def ep_adapter_product(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, l
     if error_word is not None:
         _want(error_word, "error_word", torch.int32, dev)
     if out is None:
-        out = torch.empty((T, width), dtype=bf, device=dev)
+        out = _empty((T, width), bf, dev, stream)
     else:
         _refuse_tensors((out, "out", bf, dev, (T, width)))
     if workspace is None:
         nbytes = ep_adapter_workspace_bytes(T, H, r) or 16
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(nbytes, torch.uint8, dev, stream)
     else:
         _want(workspace, "workspace", torch.uint8, dev)
         nbytes = workspace.numel()

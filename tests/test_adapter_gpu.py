@@ -151,3 +151,22 @@ def test_no_rows_and_another_stream():
         ep.ep_adapter_product(y, w, a, b, idx, s, out=out, workspace=ws)
     st.synchronize()
     assert torch.equal(out, want)
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """The workspace that a call takes for itself is not handed to the current
+    stream while the call's own stream still uses it."""
+    x, w, a, b, idx, s = make(300, 512, 512, 8, 16, 6, "rows")
+    want = ep.ep_adapter_product(x, w, a, b, idx, s)
+    out = torch.zeros_like(want)
+    nbytes = ep.ep_adapter_workspace_bytes(300, 512, 16)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        m = torch.ones((4096, 4096), device=DEV)
+        for _ in range(8):
+            m = m @ m * 1e-4
+    ep.ep_adapter_product(x, w, a, b, idx, s, out=out, stream=st)
+    held = [torch.zeros(nbytes, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and not any(t.any() for t in held)

@@ -259,6 +259,35 @@ def test_another_stream():
     assert torch.equal(out[used], want[used])
 
 
+def delay(stream):
+    """Some 10 ms of work on a stream."""
+    with torch.cuda.stream(stream):
+        m = torch.ones((4096, 4096), device=DEV)
+        for _ in range(8):
+            m = m @ m * 1e-4
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """Memory that a call takes and gives back for itself is not handed to
+    the current stream while the call's own stream still uses it."""
+    lay, x, used, g = rows_and_layout(512, 4, 8, 512, 1, 8)
+    w = weights(g, 8, 1024, 512)
+    grad = torch.randn((x.shape[0], 512), generator=g, device=DEV).to(torch.bfloat16)
+    pre = torch.empty((x.shape[0], 1024), dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product(x, w, lay, activation="swiglu", preact=pre)
+    want = ep.ep_expert_product_backward(grad, x, w, lay, activation="swiglu", preact=pre)
+    out = [torch.empty_like(t) for t in want]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    delay(s)
+    ep.ep_expert_product_backward(grad, x, w, lay, activation="swiglu", preact=pre, grad_x=out[0], grad_w=out[1],
+                                  stream=s)
+    held = [torch.zeros_like(pre) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out[0][used], want[0][used]) and torch.equal(out[1], want[1])
+    assert not any(t.any() for t in held)
+
+
 def test_a_layer_end_to_end():
     """Router, expanded layout, dispatch, both products, combine: the whole
     layer against 64 bits.  The hidden rows are rounded to bf16 once, as the
