@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteParams p) 
   float *key = s_keys + (size_t)warp * p.E;
   griddep_wait();
   griddep_launch_dependents();
-  for (int t = blockIdx.x * kRouteWarps + warp; t < p.T; t += gridDim.x * kRouteWarps) {
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < p.T; t += (int64_t)gridDim.x * kRouteWarps) {
     const void *row = static_cast<const char *>(p.logits) + (int64_t)t * p.row_stride * (BF16 ? 2 : 4);
     float m = kNegInf, sum = 0.0f;
     for (int j = lane; j < p.E; j += 32) {
@@ -649,7 +649,7 @@ ep_status_t launch_lanes_as(const RouteParams &p, cudaStream_t stream) {
     if (e == cudaSuccess) ready[dev] = true;
   }
   if (e == cudaSuccess)
-    e = launch_kernel(route_lanes_kernel<BF16, N, KIND>, (p.T + 31) / 32, kLaneWarps * 32, smem, stream, false, p, pitch,
+    e = launch_kernel(route_lanes_kernel<BF16, N, KIND>, (p.T - 1) / 32 + 1, kLaneWarps * 32, smem, stream, false, p, pitch,
                       tail, bits, aligned);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "route launch");
 }

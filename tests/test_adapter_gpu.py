@@ -170,3 +170,33 @@ def test_what_a_call_allocates_belongs_to_its_stream():
     held = [torch.zeros(nbytes, dtype=torch.uint8, device=DEV) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(out, want) and not any(t.any() for t in held)
+
+
+def test_offsets_past_32_bits():
+    """Rows and results of more than 2^31 elements, then adapters of as many."""
+    T, H, r = 132000, 16384, 16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    bf = torch.bfloat16
+    x = torch.randn((T, H), generator=g, device=DEV, dtype=bf)
+    w = torch.randn((H, H), generator=g, device=DEV, dtype=bf) / 128
+    a = torch.randn((5, r, H), generator=g, device=DEV, dtype=bf) / 128
+    b = torch.randn((5, H, r), generator=g, device=DEV, dtype=bf) / 4
+    idx = torch.randint(-1, 5, (T,), generator=g, device=DEV)
+    out = ep.ep_adapter_product(x, w, a, b, idx)
+    assert x.numel() > 2 ** 31
+    last = slice(T - 24, T)
+    check(x[last], w, a, b, idx[last], None, out[last])
+    del a, b, out
+    # 4096 adapters of rank 128: only those that are named are filled
+    x, A, r = x[last].clone(), 4096, 128
+    a = torch.empty((A, r, H), dtype=bf, device=DEV)
+    b = torch.empty((A, H, r), dtype=bf, device=DEV)
+    assert a.numel() > 2 ** 32
+    idx = torch.tensor([-1, 0, 1023, 1024, 2047, 4094, 4095, 4095], device=DEV).repeat(3)
+    for k in idx.unique().tolist():
+        if k >= 0:
+            a[k] = torch.randn((r, H), generator=g, device=DEV, dtype=bf) / 128
+            b[k] = torch.randn((H, r), generator=g, device=DEV, dtype=bf) / 8
+    check(x, w, a, b, idx, None, ep.ep_adapter_product(x, w, a, b, idx))
+    del x, w, a, b
+    torch.cuda.empty_cache()

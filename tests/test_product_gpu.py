@@ -288,6 +288,40 @@ def test_what_a_call_allocates_belongs_to_its_stream():
     assert not any(t.any() for t in held)
 
 
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_offsets_past_32_bits(act):
+    """Rows, weights and their gradients of more than 2^31 elements each; the
+    last of them are checked."""
+    E, H, wide = 9, 16384, 16384
+    width = wide // 2 if act else wide
+    lay, x, used, g = rows_and_layout(70000, 2, E, H, 1, 1)
+    w = torch.randn((E, wide, H), generator=g, device=DEV, dtype=torch.bfloat16) / 128
+    pre = torch.empty((x.shape[0], wide), dtype=torch.bfloat16, device=DEV) if act else None
+    out = ep.ep_expert_product(x, w, lay, activation=act, preact=pre)
+    assert lay.errors() == 0 and x.numel() > 2 ** 31 and w.numel() > 2 ** 31
+    first, n = segments(lay)[-1]
+    end = first + n
+    last = slice(end - 16, end)
+    h, tol = fp32_sum(x[last], w[-1])
+    if act is None:
+        close(out[last], h, tol)
+    else:
+        close(pre[last], h, tol)
+        gate, up, tg, tu = h[:, :width], h[:, width:], tol[:, :width], tol[:, width:]
+        s = gate * torch.sigmoid(gate)
+        close(out[last], s * up, 1.1 * tg * (up.abs() + tu) + s.abs() * tu + 1e-6 * (s * up).abs())
+    grad = out.normal_(generator=g)
+    gp = torch.empty_like(pre) if act else None
+    grad_x, grad_w = ep.ep_expert_product_backward(grad, x, w, lay, activation=act, preact=pre, grad_preact=gp)
+    d = gp if act else grad
+    want, tol = fp32_sum(d[last], w[-1].T)
+    close(grad_x[last], want, tol)
+    want, tol = fp32_sum(d[first:end, -16:].T, x[first:end].T)
+    close(grad_w[-1, -16:], want, tol)
+    del x, w, pre, out, grad, gp, grad_x, grad_w, d, want, tol, h
+    torch.cuda.empty_cache()
+
+
 def test_a_layer_end_to_end():
     """Router, expanded layout, dispatch, both products, combine: the whole
     layer against 64 bits.  The hidden rows are rounded to bf16 once, as the

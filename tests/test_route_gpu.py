@@ -364,3 +364,29 @@ def test_the_two_forms_agree():
     part = make_logits(MANY, 160, torch.bfloat16, 14).to(DEV)[:, 5:133]  # rows that start at odd places
     a, b = ep.ep_route(part, 7), ep.ep_route(part.contiguous(), 7)
     assert torch.equal(a.topk_idx, b.topk_idx) and torch.equal(a.topk_weights, b.topk_weights)
+
+
+@pytest.mark.parametrize("T,E,apart,K", [(70000, 64, 32768, 6), (540000, 4000, 4000, 3)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_offsets_past_32_bits(T, E, apart, K, renorm):
+    """Logits of more than 2^31 elements: the last rows are copies of the
+    first and give the same."""
+    wide = torch.zeros((T, apart), dtype=torch.float32, device=DEV)
+    assert wide.numel() > 2 ** 31
+    n = 5000
+    some = make_logits(n, E, torch.float32, 3).to(DEV)
+    wide[:n, :E] = some
+    wide[-n:, :E] = some
+    r = ep.ep_route(wide[:, :E], K, renormalize=renorm)
+    few = ep.ep_route(some, K, renormalize=renorm)
+    for rows in (slice(0, n), slice(T - n, T)):
+        assert torch.equal(r.topk_idx[rows], few.topk_idx) and torch.equal(r.topk_weights[rows], few.topk_weights)
+    d = torch.randn((n, K), generator=torch.Generator(device=DEV).manual_seed(4), device=DEV)
+    all_d = torch.zeros((T, K), device=DEV)
+    all_d[:n] = d
+    all_d[-n:] = d
+    want = ep.ep_route_backward(d, some, few.topk_idx, renormalize=renorm)
+    got = ep.ep_route_backward(all_d, wide[:, :E], r.topk_idx, renormalize=renorm)
+    assert torch.equal(got[:n], want) and torch.equal(got[-n:], want)
+    del wide, got, r
+    torch.cuda.empty_cache()
