@@ -104,33 +104,33 @@ __device__ __forceinline__ int list_adapters(const LowParams &p, int tile, int *
   return count;
 }
 
-// The low rows of few rows: a block for 16 low values of a row, which reads
+// The low rows of few rows: a warp for two low values of a row, which reads
 // its part of the adapter's down-projection by itself (rows of one adapter
-// meet it in L2), a warp two vectors; the first blocks make the tiles' plans.
+// meet it in L2); the first blocks make the tiles' plans.
 constexpr int kRowThreads = 256;
-constexpr int kRowRanks = kRowThreads / 32 * 2;
+constexpr int kRowWarps = kRowThreads / 32;
 constexpr int64_t kRowBytes = 256 << 20;
 
 __global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_constant__ LowParams p, int tiles) {
   extern __shared__ int s_dyn[];  // [adapters]
   __shared__ int s_place[kMaxCols], s_list[kMaxCols];
   __shared__ uint32_t s_first[kMaxCols / 32];
-  if ((int)blockIdx.x < tiles && blockIdx.y == 0)
+  if ((int)blockIdx.x < tiles)
     for (int i = threadIdx.x; i < p.adapters; i += kRowThreads) s_dyn[i] = kMaxCols;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   if ((int)blockIdx.x < tiles) {
-    if (blockIdx.y == 0) list_adapters(p, blockIdx.x, s_dyn, s_place, s_list, s_first, true);
+    list_adapters(p, blockIdx.x, s_dyn, s_place, s_list, s_first, true);
     return;
   }
-  const int t = blockIdx.x - tiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = ((int)blockIdx.x - tiles) * kRowWarps + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int t = item / (p.rank / 2), i = item % (p.rank / 2) * 2;
+  if (t >= p.T) return;
   const int64_t a = p.index[t];
   if (a < 0 || a >= p.adapters) return;
   const uint16_t *x = p.rows_x + (int64_t)t * p.hidden;
   const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + a);
-  const int i = (int)blockIdx.y * kRowRanks + warp * 2;
-  if (i >= p.rank) return;
   const uint16_t *v = p.a + (a * p.rank + i) * p.hidden;
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll 4
@@ -417,7 +417,7 @@ bool row_kernel(const AdapterArgs &a) { return (int64_t)a.num_rows * a.rank * a.
 
 ep_status_t launch_rows(const LowParams &q, const Cut &c, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(q.T + c.tiles, up(q.rank, kRowRanks));
+  cfg.gridDim = dim3(up(q.T * (q.rank / 2), kRowWarps) + c.tiles);
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = (size_t)q.adapters * 4;
   cfg.stream = stream;
