@@ -535,6 +535,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _functions = {}
+_route_args = N.packer(N.ep_route_args_t)
+_route_backward_args = N.packer(N.ep_route_backward_args_t)
+_product_args = N.packer(N.ep_expert_product_args_t)
+_product_backward_args = N.packer(N.ep_expert_product_backward_args_t)
+_adapter_args = N.packer(N.ep_adapter_product_args_t)
 
 # These calls can be shorter than their set-up in Python, so each wrapper
 # looks at its tensors in one expression and lets a second function say what
@@ -551,8 +556,8 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _launch(index: int, fn: str, args, stream):
-    """``_call`` for functions of one argument block and a stream."""
+def _launch(index: int, fn: str, args: bytes, stream):
+    """``_call`` for functions of one argument block, packed, and a stream."""
     if stream is None:
         handle = _raw_stream(index)
     elif stream.device.index != index:
@@ -561,19 +566,21 @@ def _launch(index: int, fn: str, args, stream):
         handle = stream.cuda_stream
     f = _functions.get(fn)
     if f is None:
-        f = _functions[fn] = getattr(N.load(), fn)
+        f = N.load()[fn]
+        f.restype, f.argtypes = C.c_int, [C.c_char_p, C.c_void_p]
+        _functions[fn] = f
     if _current() == index:
-        status = f(C.byref(args), handle)
+        status = f(args, handle)
     else:
         with torch.cuda.device(index):
-            status = f(C.byref(args), handle)
+            status = f(args, handle)
     if status:
         _check(status, fn)
 
 
-def _logits_stride(logits: torch.Tensor) -> int:
-    """The row stride of logits [T, E] (rows may be apart, a row's entries may
-    not)."""
+def _logits_sizes(logits: torch.Tensor) -> tuple:
+    """T, E and the row stride of logits [T, E] (rows may be apart, a row's
+    entries may not)."""
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")
     if logits.dtype not in _LOGITS:
@@ -586,7 +593,7 @@ def _logits_stride(logits: torch.Tensor) -> int:
     apart, step = logits.stride()
     if (E > 1 and step != 1) or (T > 1 and apart < E):
         raise ValueError("a row of logits must be contiguous, and rows must not overlap")
-    return apart if T > 1 else max(E, 1)
+    return T, E, apart if T > 1 else max(E, 1)
 
 
 def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
@@ -604,8 +611,7 @@ def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
     with a logit of -infinity or NaN are never chosen; missing choices are -1
     with weight 0.  Ties go to the lowest index.
     """
-    apart = _logits_stride(logits)
-    T, E = logits.shape
+    T, E, apart = _logits_sizes(logits)
     dev = logits.device
     if bias is not None and not (bias.dtype is torch.float32 and bias.device == dev
                                  and bias.is_contiguous() and bias.shape == (E,)):
@@ -619,9 +625,9 @@ def ep_route(logits: torch.Tensor, num_topk: int, score: str = "softmax",
                                ("topk_weights", out.topk_weights, torch.float32)):
             _want(t, name, dtype, dev)
             _want_shape(t, name, (T, num_topk))
-    _launch(dev.index, "ep_route", N.ep_route_args_t(
+    _launch(dev.index, "ep_route", _route_args(
         logits.data_ptr(), _LOGITS[logits.dtype], apart, T, E, num_topk, _SCORES[score],
-        None if bias is None else bias.data_ptr(), num_groups, topk_groups, group_top,
+        0 if bias is None else bias.data_ptr(), num_groups, topk_groups, group_top,
         1 if renormalize else 0, weight_scale, out.topk_idx.data_ptr(), out.topk_weights.data_ptr()),
         stream)
     return out
@@ -633,8 +639,7 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
     """The gradient of ``ep_route``'s weights for the logits ([T, E], the
     logits' dtype), given the weights' gradient (fp32 [T, K]) and the choice.
     The choice itself, and so the bias, has no gradient."""
-    apart = _logits_stride(logits)
-    T, E = logits.shape
+    T, E, apart = _logits_sizes(logits)
     dev = logits.device
     _want(topk_idx, "topk_idx", torch.int64, dev)
     _want(grad_weights, "grad_weights", torch.float32, dev)
@@ -646,7 +651,7 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
     else:
         _want(out, "out", logits.dtype, dev)
         _want_shape(out, "out", (T, E))
-    _launch(dev.index, "ep_route_backward", N.ep_route_backward_args_t(
+    _launch(dev.index, "ep_route_backward", _route_backward_args(
         grad_weights.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], apart,
         topk_idx.data_ptr(), T, E, K, _SCORES[score], 1 if renormalize else 0, weight_scale,
         out.data_ptr()), stream)
@@ -682,9 +687,6 @@ def _product_sizes(x, w, layout, activation):
     return cap, H, wide, wide
 
 
-_LAYOUT_POINTER = C.POINTER(N.ep_expanded_layout_t)
-
-
 def ep_expert_product(x: torch.Tensor, w: torch.Tensor, layout: ExpandedLayout,
                       activation: Optional[str] = None, out: Optional[torch.Tensor] = None,
                       preact: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -706,9 +708,10 @@ def ep_expert_product(x: torch.Tensor, w: torch.Tensor, layout: ExpandedLayout,
         _refuse_tensors((out, "out", bf, dev, (cap, width)))
     if preact is not None:
         _refuse_tensors((preact, "preact", bf, dev, (cap, wide)))
-    _launch(dev.index, "ep_expert_product", N.ep_expert_product_args_t(
-        x.data_ptr(), cap, layout.num_tokens, H, layout.num_experts, _LAYOUT_POINTER(layout.c_struct()),
-        w.data_ptr(), width, act, out.data_ptr(), None if preact is None else preact.data_ptr()), stream)
+    lay = layout.c_struct()
+    _launch(dev.index, "ep_expert_product", _product_args(
+        x.data_ptr(), cap, layout.num_tokens, H, layout.num_experts, C.addressof(lay),
+        w.data_ptr(), width, act, out.data_ptr(), 0 if preact is None else preact.data_ptr()), stream)
     return out
 
 
@@ -746,11 +749,12 @@ def ep_expert_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Ten
     _refuse_tensors((grad, "grad", bf, dev, (cap, width)), (preact, "preact", bf, dev, (cap, wide)),
                     (grad_preact, "grad_preact", bf, dev, (cap, wide)), (grad_x, "grad_x", bf, dev, (cap, H)),
                     (grad_w, "grad_w", bf, dev, w.shape))
-    _launch(dev.index, "ep_expert_product_backward", N.ep_expert_product_backward_args_t(
+    lay = layout.c_struct()
+    _launch(dev.index, "ep_expert_product_backward", _product_backward_args(
         grad.data_ptr(), x.data_ptr(), w.data_ptr(), cap, layout.num_tokens, H, layout.num_experts,
-        _LAYOUT_POINTER(layout.c_struct()), width, act, None if preact is None else preact.data_ptr(),
-        None if grad_preact is None else grad_preact.data_ptr(),
-        None if grad_x is None else grad_x.data_ptr(), None if grad_w is None else grad_w.data_ptr()), stream)
+        C.addressof(lay), width, act, 0 if preact is None else preact.data_ptr(),
+        0 if grad_preact is None else grad_preact.data_ptr(),
+        0 if grad_x is None else grad_x.data_ptr(), 0 if grad_w is None else grad_w.data_ptr()), stream)
     return grad_x, grad_w
 
 
@@ -801,10 +805,10 @@ def ep_adapter_product(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, l
     else:
         _want(workspace, "workspace", torch.uint8, dev)
         nbytes = workspace.numel()
-    _launch(i, "ep_adapter_product", N.ep_adapter_product_args_t(
+    _launch(i, "ep_adapter_product", _adapter_args(
         x.data_ptr(), T, H, w.data_ptr(), width, lora_a.data_ptr(), lora_b.data_ptr(), A, r,
-        adapter_idx.data_ptr(), None if adapter_scale is None else adapter_scale.data_ptr(),
-        out.data_ptr(), workspace.data_ptr(), nbytes, None if error_word is None else error_word.data_ptr()),
+        adapter_idx.data_ptr(), 0 if adapter_scale is None else adapter_scale.data_ptr(),
+        out.data_ptr(), workspace.data_ptr(), nbytes, 0 if error_word is None else error_word.data_ptr()),
         stream)
     return out
 

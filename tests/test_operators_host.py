@@ -140,3 +140,14 @@ def test_the_binding_checks_tensors():
         ep.ep_expert_product(bf, bf, None, activation="relu")
     with pytest.raises(TypeError, match="x must be"):
         ep.ep_adapter_product(torch.zeros((4, 64)), bf, bf, bf, torch.zeros(4, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("cls", [N.ep_route_args_t, N.ep_route_backward_args_t, N.ep_expert_product_args_t,
+                                 N.ep_expert_product_backward_args_t, N.ep_adapter_product_args_t])
+def test_packed_arguments_are_the_structures_bytes(cls):
+    """Every field at its place: the structure read back from the bytes."""
+    values = [0.5 + i if t is C.c_float else 1000 + 7 * i for i, (_, t) in enumerate(cls._fields_)]
+    got = cls.from_buffer_copy(N.packer(cls)(*values))
+    for (name, t), want in zip(cls._fields_, values):
+        v = getattr(got, name)
+        assert (C.cast(v, C.c_void_p).value if issubclass(t, C._Pointer) else v) == want, name
