@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
   char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   char *staging = ring + p.ring_bytes / 1024 * 1024;
   char *exchange = staging + kResultWarps * staging_of(F);
-  // [parts - 1][columns][128]: the other pairs' results
-  float *joined = reinterpret_cast<float *>(exchange + (F == kGated ? kResultWarps * kExchangeBytes : 0));
+  // [parts - 1][columns / 4][128][4]: the other pairs' results
+  float4 *joined = reinterpret_cast<float4 *>(exchange + (F == kGated ? kResultWarps * kExchangeBytes : 0));
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // A cluster is one pair, or the pairs that share a tile (`part`: which of them).
   const uint32_t rank = cluster_rank() & 1u, lead = cluster_rank() & ~1u, both = 3u << lead;
@@ -365,8 +365,10 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
   const int b_bytes = Walker<F>::most_cols(p) / 2 * 128, stage_bytes = kABytes + b_bytes;
   int stages = p.ring_bytes / 1024 * 1024 / stage_bytes;
   // (a stage less in the first costs 10% with six in all, so one is enough
-  // for the second then: long runs of rows need a step or two a tile)
-  const int side_stages = stages >= 8 ? kSideStages : 1;
+  // for the second then: long runs of rows need a step or two a tile.  A tile
+  // that pairs share is their only one, and its adapters' steps come last:
+  // two, 1021 rows of 40 adapters 21.3 us against 22.3)
+  const int side_stages = stages >= 8 ? kSideStages : p.parts > 1 ? 2 : 1;
   if (F == kAdapter) stages -= side_stages;
   stages = min(stages, kMaxStages);
   char *side = ring + stages * stage_bytes;
@@ -588,15 +590,21 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       const int place = rows + lane < b_rows ? load_made(plan + 1 + kMaxCols + (int)rank * b_rows + rows + lane) : -1;
       const int a0 = t.a0 + (int)rank * 128;
       const uint16_t *low = p.low + (int64_t)(t.first + (int)rank * b_rows) * p.rank;
-      int last = part;
+      // the adapter of this lane's columns, read a step ahead
+      const auto adapter_of = [&](int k) {
+        const int col = k * kInner + piece * 8;
+        return col < length ? load_made(plan + 1 + col / p.rank) : 0;
+      };
+      int last = part, next = adapter_of(part);
       for (int k = part; k * kInner < length; k += p.parts) {
+        const int adapter = next;
+        next = adapter_of(k + p.parts);
         ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_empty[stage], phase ^ 1));
         if (!ok) break;
         const uint32_t a = smem_addr(side + (size_t)stage * stage_bytes), b = a + kABytes;
         const int col = k * kInner + piece * 8, mine = col / p.rank, in = col - mine * p.rank;
         const bool there = col < length;
         if (piece * 8 < ceil_div(min(length - k * kInner, kInner), 16) * 16) {
-          const int adapter = there ? load_made(plan + 1 + mine) : 0;
           const uint16_t *up = p.up + ((int64_t)adapter * p.width + a0) * p.rank + in;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -682,18 +690,18 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           ok = ok && mbar_wait_cluster(&s_bar.part_empty, part_phase ^ 1);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
-          const uint32_t to = map_shared(smem_addr(joined + (part - 1) * p.part_cols * 128 + quarter * 32 + lane), rank);
+          const uint32_t to = map_shared(smem_addr(joined + (part - 1) * p.part_cols * 32 + quarter * 32 + lane), rank);
           for (int c = half * 32; c < t.cols; c += 64) {
             float v[32];
             tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < p.part_cols) store_cluster(to + (uint32_t)(c + j) * 512, v[j]);
+            for (int j = 0; j < 32; j += 4)
+              store_cluster(to + (uint32_t)(c + j) * 512, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
           }
           release(acc);
           fence_cluster();  // every lane's own stores, before one arrives for all
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.part_full), rank));
+          if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.part_full), rank));
           part_phase ^= 1;
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
@@ -734,10 +742,15 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         if (F != kGradW && p.parts > 1) {
           // the parts are added in their order
           for (int q = 0; q + 1 < p.parts; ++q) {
-            const float *more = joined + (q * p.part_cols + c) * 128 + quarter * 32 + lane;
+            const float4 *more = joined + (q * p.part_cols + c) * 32 + quarter * 32 + lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < p.part_cols) v[j] += more[j * 128];
+            for (int j = 0; j < 32; j += 4) {
+              const float4 m = more[j * 32];
+              v[j] += m.x;
+              v[j + 1] += m.y;
+              v[j + 2] += m.z;
+              v[j + 3] += m.w;
+            }
           }
         }
         const int left = t.count - c;  // rows of this chunk (not kGradW)
@@ -784,7 +797,8 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       if (F != kGradW && p.parts > 1) {
         __syncwarp();
         if (lane == 0)
-          for (int q = 1; q < p.parts; ++q) mbar_arrive_cluster(map_shared(smem_addr(&s_bar.part_empty), 2 * q + rank));
+          for (int q = 1; q < p.parts; ++q)
+            mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.part_empty), 2 * q + rank));
         part_phase ^= 1;
       }
       acc ^= 1;
