@@ -640,18 +640,20 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
     logits' dtype), given the weights' gradient (fp32 [T, K]) and the choice.
     The choice itself, and so the bias, has no gradient."""
     T, E, apart = _logits_sizes(logits)
-    dev = logits.device
-    _want(topk_idx, "topk_idx", torch.int64, dev)
-    _want(grad_weights, "grad_weights", torch.float32, dev)
+    dev, i = logits.device, logits.get_device()
     K = topk_idx.shape[-1]
-    _want_shape(topk_idx, "topk_idx", (T, K))
-    _want_shape(grad_weights, "grad_weights", (T, K))
+    if not (topk_idx.dtype is torch.int64 and grad_weights.dtype is torch.float32
+            and topk_idx.get_device() == i and grad_weights.get_device() == i
+            and topk_idx.is_contiguous() and grad_weights.is_contiguous()
+            and topk_idx.shape == (T, K) and grad_weights.shape == (T, K)):
+        _refuse_tensors((topk_idx, "topk_idx", torch.int64, dev, (T, K)),
+                        (grad_weights, "grad_weights", torch.float32, dev, (T, K)))
     if out is None:
         out = _empty((T, E), logits.dtype, dev, stream)
     else:
         _want(out, "out", logits.dtype, dev)
         _want_shape(out, "out", (T, E))
-    _launch(dev.index, "ep_route_backward", _route_backward_args(
+    _launch(i, "ep_route_backward", _route_backward_args(
         grad_weights.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], apart,
         topk_idx.data_ptr(), T, E, K, _SCORES[score], 1 if renormalize else 0, weight_scale,
         out.data_ptr()), stream)
@@ -730,27 +732,35 @@ def ep_expert_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Ten
     is zero."""
     act = _ACTIVATIONS[activation]
     cap, H, width, wide = _product_sizes(x, w, layout, activation)
-    bf, dev = torch.bfloat16, x.device
+    bf, dev, i = torch.bfloat16, x.device, x.get_device()
+    if not (grad.dtype is bf and grad.get_device() == i and grad.is_contiguous() and grad.shape == (cap, width)):
+        _refuse_tensors((grad, "grad", bf, dev, (cap, width)))
     if act == N.EP_ACT_SWIGLU:
         if preact is None:
             raise ValueError("swiglu needs preact")
+        if not (preact.dtype is bf and preact.get_device() == i and preact.is_contiguous()
+                and preact.shape == (cap, wide)):
+            _refuse_tensors((preact, "preact", bf, dev, (cap, wide)))
         if grad_preact is None:
             grad_preact = _empty((cap, wide), bf, dev, stream)
+        else:
+            _refuse_tensors((grad_preact, "grad_preact", bf, dev, (cap, wide)))
     else:
         preact = grad_preact = None
     if not need_x:
         grad_x = None
     elif grad_x is None:
         grad_x = _empty((cap, H), bf, dev, stream)
+    else:
+        _refuse_tensors((grad_x, "grad_x", bf, dev, (cap, H)))
     if not need_w:
         grad_w = None
     elif grad_w is None:
         grad_w = _empty(w.shape, bf, dev, stream)
-    _refuse_tensors((grad, "grad", bf, dev, (cap, width)), (preact, "preact", bf, dev, (cap, wide)),
-                    (grad_preact, "grad_preact", bf, dev, (cap, wide)), (grad_x, "grad_x", bf, dev, (cap, H)),
-                    (grad_w, "grad_w", bf, dev, w.shape))
+    else:
+        _refuse_tensors((grad_w, "grad_w", bf, dev, w.shape))
     lay = layout.c_struct()
-    _launch(dev.index, "ep_expert_product_backward", _product_backward_args(
+    _launch(i, "ep_expert_product_backward", _product_backward_args(
         grad.data_ptr(), x.data_ptr(), w.data_ptr(), cap, layout.num_tokens, H, layout.num_experts,
         C.addressof(lay), width, act, 0 if preact is None else preact.data_ptr(),
         0 if grad_preact is None else grad_preact.data_ptr(),
