@@ -104,15 +104,17 @@ __device__ __forceinline__ int list_adapters(const LowParams &p, int tile, int *
   return count;
 }
 
-// The low rows of few rows: a warp for two low values of a row, which reads
-// its part of the adapter's down-projection by itself (rows of one adapter
-// meet it in L2); the first blocks make the tiles' plans.
+// The low rows of few rows: SHARE warps for two low values of a row, which
+// read their part of the adapter's down-projection by themselves (rows of one
+// adapter meet it in L2); the first blocks make the tiles' plans.
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int64_t kRowBytes = 256 << 20;
 
+template <int SHARE>
 __global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_constant__ LowParams p, int tiles) {
   extern __shared__ int s_dyn[];  // [adapters]
+  __shared__ float2 s_sum[kRowWarps];
   __shared__ int s_place[kMaxCols], s_list[kMaxCols];
   __shared__ uint32_t s_first[kMaxCols / 32];
   if ((int)blockIdx.x < tiles)
@@ -124,17 +126,18 @@ __global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_c
     list_adapters(p, blockIdx.x, s_dyn, s_place, s_list, s_first, true);
     return;
   }
-  const int item = ((int)blockIdx.x - tiles) * kRowWarps + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % SHARE;
+  const int item = ((int)blockIdx.x - tiles) * (kRowWarps / SHARE) + warp / SHARE;
   const int t = item / (p.rank / 2), i = item % (p.rank / 2) * 2;
-  if (t >= p.T) return;
-  const int64_t a = p.index[t];
-  if (a < 0 || a >= p.adapters) return;
+  const int64_t a = t < p.T ? p.index[t] : -1;
+  const bool some = a >= 0 && a < p.adapters;
+  if (SHARE == 1 && !some) return;
+  const float f = p.scale == nullptr || !some ? 1.0f : __ldg(p.scale + a);
   const uint16_t *x = p.rows_x + (int64_t)t * p.hidden;
-  const float f = p.scale == nullptr ? 1.0f : __ldg(p.scale + a);
   const uint16_t *v = p.a + (a * p.rank + i) * p.hidden;
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll 4
-  for (int k = lane * 8; k < p.hidden; k += 256) {
+  for (int k = some ? (part * 32 + lane) * 8 : p.hidden; k < p.hidden; k += SHARE * 256) {
     const int4 xv = __ldg(reinterpret_cast<const int4 *>(x + k));
     const int4 a0 = __ldg(reinterpret_cast<const int4 *>(v + k));
     const int4 a1 = __ldg(reinterpret_cast<const int4 *>(v + p.hidden + k));
@@ -153,7 +156,18 @@ __global__ void __launch_bounds__(kRowThreads) adapter_row_kernel(const __grid_c
     sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
     sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
   }
-  if (lane == 0) *reinterpret_cast<uint32_t *>(p.low + (int64_t)t * p.rank + i) = pack_bf16x2(sum[0] * f, sum[1] * f);
+  if constexpr (SHARE > 1) {  // the parts in their order
+    if (lane == 0) s_sum[warp] = make_float2(sum[0], sum[1]);
+    __syncthreads();
+#pragma unroll
+    for (int q = 1; q < SHARE; ++q) {
+      if (part > 0) break;
+      sum[0] += s_sum[warp + q].x;
+      sum[1] += s_sum[warp + q].y;
+    }
+  }
+  if (some && part == 0 && lane == 0)
+    *reinterpret_cast<uint32_t *>(p.low + (int64_t)t * p.rank + i) = pack_bf16x2(sum[0] * f, sum[1] * f);
 }
 
 // A barrier of the first four warps; whether all of them say `ok`.
@@ -415,9 +429,17 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // by stacks, in runs 34 against 28).
 bool row_kernel(const AdapterArgs &a) { return (int64_t)a.num_rows * a.rank * a.hidden * 2 <= kRowBytes; }
 
-ep_status_t launch_rows(const LowParams &q, const Cut &c, cudaStream_t stream) {
+// Warps share a row's values while two blocks an SM hold them all, since a
+// warp's rounds of loads come one after the other.  The whole call with inputs
+// in memory: 32 rows of rank 16, 4096 -> 4096 25 us alone, 21 shared by eight;
+// 300 of rank 8, 4096 -> 1000 27, 23 shared by two.  With inputs in L2: 11.2
+// and 10.6; 12.4 to 15.0 and 14.6 to 15.3.
+ep_status_t launch_rows(const LowParams &q, const Cut &c, const DeviceInfo *di, cudaStream_t stream) {
+  const int items = q.T * (q.rank / 2);
+  int share = 1;
+  while (share < kRowWarps && items * share <= di->num_sms * kRowWarps && q.hidden > 512 * share) share *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(up(q.T * (q.rank / 2), kRowWarps) + c.tiles);
+  cfg.gridDim = dim3(up(items, kRowWarps / share) + c.tiles);
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = (size_t)q.adapters * 4;
   cfg.stream = stream;
@@ -426,7 +448,11 @@ ep_status_t launch_rows(const LowParams &q, const Cut &c, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = kUsePdl ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_row_kernel, q, c.tiles);
+  const auto kernel = share == 1   ? adapter_row_kernel<1>
+                      : share == 2 ? adapter_row_kernel<2>
+                      : share == 4 ? adapter_row_kernel<4>
+                                   : adapter_row_kernel<8>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q, c.tiles);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "adapter_row launch");
 }
 
@@ -505,7 +531,7 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   q.low = reinterpret_cast<uint16_t *>(ws);
   ws += align256((size_t)a.num_rows * a.rank * 2);
   q.part = reinterpret_cast<float *>(ws);
-  s = row_kernel(a) ? launch_rows(q, c, stream) : launch_low(q, a, c, di, stream);
+  s = row_kernel(a) ? launch_rows(q, c, di, stream) : launch_low(q, a, c, di, stream);
   if (s != EP_OK) return s;
 
   Params p = {};
