@@ -18,8 +18,8 @@
 //
 // Measured: 8192 rows 7168 -> 4096, rank 32: 314 to 325 us, of which the low
 // rows 32 (the projection's power limit bounds it); 1021 rows 4096 -> 1000, 40
-// adapters of rank 8: 21 to 23 us in a graph; 32 rows 4096 -> 4096, 24 adapters
-// of rank 16: 12 us in a graph, where reading the weights takes 6 (the low
+// adapters of rank 8: 20 to 21 us in a graph; 32 rows 4096 -> 4096, 24 adapters
+// of rank 16: 10.5 us in a graph, where reading the weights takes 6 (the low
 // rows and the gather come one after the other).
 #include "ep_pair.cuh"
 
@@ -377,49 +377,12 @@ __global__ void __launch_bounds__(kLowThreads) adapter_low_kernel(const __grid_c
   }
 }
 
-// How a call is cut: rows of a tile, tiles, pairs that share a tile's inner
-// dimension, splits of the low rows' inner dimension.
-struct Cut {
-  int cols, tiles, parts, splits;
-};
-
 int low_splits(int tiles, int hidden) {
   const int steps = up(hidden, kInner);
   int n = 128 / tiles;
   if (n > kMaxSplits) n = kMaxSplits;
   if (n > steps) n = steps;
   return n < 1 ? 1 : n;
-}
-
-// The cheapest of a few cuts by the cycles of the projection: a step costs
-// its products (two cycles a column) or its copies (58 bytes a cycle of A's
-// half and B's half), a tile its results, a shared tile its joining.
-ep_status_t choose(const DeviceInfo *di, int num_rows, int hidden, int width, Cut *best) {
-  int64_t least = -1;
-  for (int most = kMaxCols; most >= 32; most /= 2) {
-    Cut c;
-    c.tiles = up(num_rows, most);
-    c.cols = up(up(num_rows, c.tiles), 32) * 32;
-    c.tiles = up(num_rows, c.cols);
-    for (c.parts = 1; c.parts <= parts_for(c.cols); ++c.parts) {
-      int clusters = 0;
-      const ep_status_t s = most_clusters<kAdapter>(di, c.parts, &clusters);
-      if (s != EP_OK) return s;
-      const int64_t tiles = (int64_t)c.tiles * up(width, 256);
-      if (c.parts > 1 && (tiles > clusters || up(hidden, kInner) < 2 * c.parts)) break;
-      const int64_t copies = (kABytes + c.cols / 2 * 128) / 58, products = 2 * c.cols;
-      const int64_t step = copies > products ? copies : products;
-      const int64_t cost = (tiles + clusters - 1) / clusters *
-                           (up(up(hidden, kInner), c.parts) * step + 2000 + 10 * c.cols) +
-                           (c.parts > 1 ? 1000 + c.parts * 10 * c.cols : 0);
-      if (least < 0 || cost < least) {
-        least = cost;
-        *best = c;
-      }
-    }
-  }
-  best->splits = low_splits(best->tiles, hidden);
-  return EP_OK;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -429,17 +392,18 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // by stacks, in runs 34 against 28).
 bool row_kernel(const AdapterArgs &a) { return (int64_t)a.num_rows * a.rank * a.hidden * 2 <= kRowBytes; }
 
-// Warps share a row's values while two blocks an SM hold them all, since a
+// Warps share a row's values while four blocks an SM hold them all, since a
 // warp's rounds of loads come one after the other.  The whole call with inputs
 // in memory: 32 rows of rank 16, 4096 -> 4096 25 us alone, 21 shared by eight;
-// 300 of rank 8, 4096 -> 1000 27, 23 shared by two.  With inputs in L2: 11.2
-// and 10.6; 12.4 to 15.0 and 14.6 to 15.3.
-ep_status_t launch_rows(const LowParams &q, const Cut &c, const DeviceInfo *di, cudaStream_t stream) {
+// 300 of rank 8, 4096 -> 1000 27, 21 shared by four; 64 of rank 64, 7168 ->
+// 2048 37, 33 shared by two.  With inputs in L2: 11.2 and 10.6; 12.4 to 15.0
+// and 13.5 to 14.1; 16.8 and 17.8.
+ep_status_t launch_rows(const LowParams &q, int tiles, const DeviceInfo *di, cudaStream_t stream) {
   const int items = q.T * (q.rank / 2);
   int share = 1;
-  while (share < kRowWarps && items * share <= di->num_sms * kRowWarps && q.hidden > 512 * share) share *= 2;
+  while (share < kRowWarps && 2 * items * share <= 4 * di->num_sms * kRowWarps && q.hidden > 512 * share) share *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(up(items, kRowWarps / share) + c.tiles);
+  cfg.gridDim = dim3(up(items, kRowWarps / share) + tiles);
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = (size_t)q.adapters * 4;
   cfg.stream = stream;
@@ -452,24 +416,24 @@ ep_status_t launch_rows(const LowParams &q, const Cut &c, const DeviceInfo *di, 
                       : share == 2 ? adapter_row_kernel<2>
                       : share == 4 ? adapter_row_kernel<4>
                                    : adapter_row_kernel<8>;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q, c.tiles);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q, tiles);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "adapter_row launch");
 }
 
-ep_status_t launch_low(LowParams &q, const AdapterArgs &a, const Cut &c, const DeviceInfo *di, cudaStream_t stream) {
+ep_status_t launch_low(LowParams &q, const AdapterArgs &a, int tiles, const DeviceInfo *di, cudaStream_t stream) {
   const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)a.num_rows}, strides[] = {a.hidden * kSize};
-  const uint32_t box[] = {kInner, (uint32_t)c.cols};
+  const uint32_t box[] = {kInner, (uint32_t)q.cols};
   const ep_status_t s = encode_map(&q.x, a.x, 2, dims, strides, box);
   if (s != EP_OK) return s;
   // stacks of adapters side by side while there are SMs for them
-  const int named = a.num_adapters < c.cols ? a.num_adapters : c.cols;
+  const int named = a.num_adapters < q.cols ? a.num_adapters : q.cols;
   const int stacks = up(named, 128 / a.rank);
-  int side = di->num_sms / (c.tiles * c.splits);
+  int side = di->num_sms / (tiles * q.splits);
   side = side < 1 ? 1 : side > stacks ? stacks : side;
-  const bool shallow = c.cols > 64;  // a stage of x and A: up to 48 KB, or up to 24
+  const bool shallow = q.cols > 64;  // a stage of x and A: up to 48 KB, or up to 24
   const auto kernel = shallow ? adapter_low_kernel<4> : adapter_low_kernel<kLowMaxStages>;
   const size_t table = (size_t)a.num_adapters * 4;
-  const size_t smem = 1024 + (shallow ? 4 : kLowMaxStages) * (kABytes + (size_t)c.cols * 128) +
+  const size_t smem = 1024 + (shallow ? 4 : kLowMaxStages) * (kABytes + (size_t)q.cols * 128) +
                       (table > kLowChunk ? table : kLowChunk);
   static std::atomic<bool> ready[64][2];
   if (!ready[di->device][shallow]) {
@@ -480,14 +444,14 @@ ep_status_t launch_low(LowParams &q, const AdapterArgs &a, const Cut &c, const D
     ready[di->device][shallow] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(c.tiles, c.splits, side);
+  cfg.gridDim = dim3(tiles, q.splits, side);
   cfg.blockDim = dim3(kLowThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
-  attr[0].val.clusterDim.y = c.splits;
+  attr[0].val.clusterDim.y = q.splits;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
@@ -511,8 +475,9 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   const DeviceInfo *di = current_device_info();
   if (di == nullptr) return EP_ERR_CUDA;
   Cut c;
-  ep_status_t s = choose(di, a.num_rows, a.hidden, a.width, &c);
+  ep_status_t s = choose<kAdapter>(di, a.num_rows, 1, a.num_rows, up(a.width, 256), a.hidden, &c);
   if (s != EP_OK) return s;
+  const int tiles = up(a.num_rows, c.cols);
   char *ws = static_cast<char *>(a.workspace);
   LowParams q = {};
   q.a = a.lora_a;
@@ -525,18 +490,19 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   q.rank = a.rank;
   q.adapters = a.num_adapters;
   q.cols = c.cols;
-  q.splits = c.splits;
+  q.splits = low_splits(tiles, a.hidden);
   q.plan = reinterpret_cast<int32_t *>(ws);
   ws += align256((size_t)up(a.num_rows, 32) * kPlanWords * 4);
   q.low = reinterpret_cast<uint16_t *>(ws);
   ws += align256((size_t)a.num_rows * a.rank * 2);
   q.part = reinterpret_cast<float *>(ws);
-  s = row_kernel(a) ? launch_rows(q, c, di, stream) : launch_low(q, a, c, di, stream);
+  s = row_kernel(a) ? launch_rows(q, tiles, di, stream) : launch_low(q, a, tiles, di, stream);
   if (s != EP_OK) return s;
 
   Params p = {};
   p.max_cols = c.cols;
   p.parts = c.parts;
+  p.most_rows = a.num_rows;
   p.error_word = a.error_word;
   p.E = 1;
   p.cap = a.num_rows;
@@ -553,9 +519,9 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   const uint32_t wb[] = {kInner, 128, 1};
   s = encode_map(&p.a, a.w, 3, wd, ws_, wb);
   if (s != EP_OK) return s;
-  s = row_maps(p, a.x, a.hidden, a.num_rows, a.num_rows);
+  s = row_maps(p, a.x, a.hidden, a.num_rows);
   if (s != EP_OK) return s;
-  return launch_form<kAdapter>(p, a.num_rows, (int64_t)c.tiles * p.a_tiles, stream);
+  return launch_form<kAdapter>(p, (int64_t)tiles * p.a_tiles, stream);
 }
 
 }  // namespace ep

@@ -32,6 +32,7 @@
 #pragma once
 
 #include <atomic>
+#include <cmath>
 
 #include "ep_ops.h"
 #include "ep_tc.cuh"
@@ -860,26 +861,62 @@ int up(int a, int b) { return a / b + (a % b != 0); }
 // first pair's shared memory, beside its ring.
 int parts_for(int cols) { return cols <= 64 ? kMaxParts : cols <= 128 ? 2 : 1; }
 
-// p.parts: 0, chosen here, or the caller's choice.
+// How a call is cut: the most columns of a tile, the pairs that share its
+// inner dimension.
+struct Cut {
+  int cols, parts;
+};
+
+// Tiles of rows, at most: an expert with n rows has n / cols rounded up.
+int64_t most_tiles(int rows, int experts, int cols) { return (rows - 1) / cols + (rows < experts ? rows : experts); }
+
+// The cheapest of a few cuts by its cycles: a step costs its products (two
+// cycles a column) or its copies (58 bytes a cycle of A's half and B's half), a
+// tile its results, a shared tile its joining.  Few tiles leave SMs idle, so
+// they are narrower, or shared by up to four pairs where there is a pair for
+// each even if every expert wastes most of a tile.  The rows of an expert are
+// known on the device only; what is reckoned with is their mean and twice its
+// root more.  Gated products: 1024 tokens top-2 of 4 experts 4096 -> 2 x 512
+// tiles of 256 29.2 us, cut here 20.2; 1021 rows of one expert 4096 -> 2 x 1000
+// 34.7, 20.5.  `most`: rows of an expert, at most.
 template <Form F>
-ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream_t stream) {
-  const DeviceInfo *di = current_device_info();
-  if (di == nullptr) return EP_ERR_CUDA;
-  const int cols = F == kGradW || most_rows > p.max_cols ? p.max_cols : up(most_rows, 32) * 32;
-  if (p.parts == 0) {
-    // Few tiles leave SMs idle: up to four pairs share one while there is a
-    // pair for each and each has four steps.  The number of tiles is known on
-    // the device only, so its bound decides.
-    p.parts = 1;
-    for (int n = 2; F != kGradW && n <= parts_for(cols) && up(p.inner, kInner) >= 4 * n; ++n) {
+ep_status_t choose(const DeviceInfo *di, int rows, int experts, int most, int a_tiles, int inner, Cut *best) {
+  const int steps = up(inner, kInner);
+  const int used = rows < experts ? rows : experts, mean = up(rows, used);
+  const int64_t likely = experts == 1 ? most : mean + (int64_t)(2.0f * sqrtf((float)mean));
+  int64_t least = -1;
+  for (int cut = kMaxCols; cut >= 32; cut -= 32) {
+    // the rows of a single expert go to tiles of about equal size
+    const int need = experts == 1 ? up(most, up(most, cut)) : most < cut ? most : cut;
+    const int cols = up(need, 32) * 32;
+    const int64_t tiles = most_tiles(rows, experts, cols) * a_tiles;
+    for (int parts = 1; parts <= parts_for(cols); ++parts) {
       int clusters = 0;
-      const ep_status_t s = most_clusters<F>(di, n, &clusters);
+      const ep_status_t s = most_clusters<F>(di, parts, &clusters);
       if (s != EP_OK) return s;
-      if (most_tiles <= clusters) p.parts = n;
+      if (parts > 1 && (tiles > clusters || steps < 2 * parts)) break;
+      const int64_t copies = (kABytes + cols / 2 * 128) / 58, products = 2 * cols;
+      const int64_t count = used * ((likely + cols - 1) / cols) * a_tiles, waves = (count + clusters - 1) / clusters;
+      if (experts > 1 && waves > 1 && cut < kMaxCols) continue;  // too uncertain to leave the widest for
+      const int64_t cost =
+          waves * (up(steps, parts) * (copies > products ? copies : products) + 2000 + 10 * cols) +
+          (parts > 1 ? 1000 + parts * 10 * cols : 0);
+      if (least < 0 || cost < least) {
+        least = cost;
+        *best = Cut{cols, parts};
+      }
     }
   }
+  return EP_OK;
+}
+
+// With p.max_cols, p.parts and p.most_rows set.
+template <Form F>
+ep_status_t launch_form(Params &p, int64_t tiles, cudaStream_t stream) {
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
+  const int cols = p.max_cols;
   p.part_cols = cols;
-  p.most_rows = most_rows;
   // The ring takes what is left of shared memory.
   const int limit = shared_limit(di);
   const int fixed = 1024 + kResultWarps * staging_of(F) + (F == kGated ? kResultWarps * kExchangeBytes : 0) +
@@ -889,7 +926,7 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
   int clusters = 0;
   const ep_status_t s = most_clusters<F>(di, p.parts, &clusters);
   if (s != EP_OK) return s;
-  if (most_tiles < clusters) clusters = (int)most_tiles;
+  if (tiles < clusters) clusters = (int)tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.parts * clusters);
   cfg.blockDim = dim3(threads_of(F));
@@ -907,11 +944,10 @@ ep_status_t launch_form(Params &p, int most_rows, int64_t most_tiles, cudaStream
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "product launch");
 }
 
-// Rows [rows][length] by halves of B of every height up to `most`.
-ep_status_t row_maps(Params &p, const void *rows, int length, int cap, int most) {
+// Rows [rows][length] by halves of B of every height that a tile may have.
+ep_status_t row_maps(Params &p, const void *rows, int length, int cap) {
   const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {length * kSize};
-  const int cols = most > p.max_cols ? p.max_cols : up(most, 32) * 32;
-  for (int i = 0; i < cols / 32; ++i) {
+  for (int i = 0; i < p.max_cols / 32; ++i) {
     const uint32_t box[] = {kInner, 16u * (i + 1)};
     const ep_status_t s = encode_map(&p.b[i], rows, 2, dims, strides, box);
     if (s != EP_OK) return s;

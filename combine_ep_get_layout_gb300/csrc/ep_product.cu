@@ -103,8 +103,20 @@ ep_status_t weight_map(Params &p, Form form, const void *w, int wide, int hidden
   return encode_map(&p.a, w, 3, dims, strides, box);
 }
 
-// Tiles of rows, at most: an expert with n rows has n / 256 rounded up.
-int64_t most_tiles(int cap, int experts) { return cap / kMaxCols + (cap < experts ? cap : experts); }
+// A product whose columns are the experts' rows, cut and launched.
+template <Form F>
+ep_status_t launch_rows_form(Params &p, const void *rows, cudaStream_t stream) {
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
+  Cut c;
+  ep_status_t s = choose<F>(di, p.cap, p.E, p.most_rows, p.a_tiles, p.inner, &c);
+  if (s != EP_OK) return s;
+  p.max_cols = c.cols;
+  p.parts = c.parts;
+  s = row_maps(p, rows, p.inner, p.cap);
+  if (s != EP_OK) return s;
+  return launch_form<F>(p, most_tiles(p.cap, p.E, c.cols) * p.a_tiles, stream);
+}
 
 }  // namespace
 
@@ -112,7 +124,7 @@ ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
   const int most = a.num_tokens < a.recv_capacity ? a.num_tokens : a.recv_capacity;  // rows of one expert
   if (most == 0) return EP_OK;
   Params p = {};
-  p.max_cols = kMaxCols;
+  p.most_rows = most;
   p.rows = a.num_rows_per_expert;
   p.offset = a.expert_offset;
   p.error_word = a.error_word;
@@ -124,11 +136,9 @@ ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
   p.a_tiles = up(a.width, a.gated ? 128 : 256);
   p.out = a.out;
   p.preact = a.preact;
-  ep_status_t s = weight_map(p, a.gated ? kGated : kPlain, a.w, p.wide, a.hidden);
-  if (s == EP_OK) s = row_maps(p, a.x, a.hidden, a.recv_capacity, most);
+  const ep_status_t s = weight_map(p, a.gated ? kGated : kPlain, a.w, p.wide, a.hidden);
   if (s != EP_OK) return s;
-  const int64_t tiles = most_tiles(a.recv_capacity, a.num_experts) * p.a_tiles;
-  return a.gated ? launch_form<kGated>(p, most, tiles, stream) : launch_form<kPlain>(p, most, tiles, stream);
+  return a.gated ? launch_rows_form<kGated>(p, a.x, stream) : launch_rows_form<kPlain>(p, a.x, stream);
 }
 
 ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t stream) {
@@ -136,7 +146,7 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
   const int wide = a.gated ? 2 * a.width : a.width;
   const uint16_t *g = a.gated ? a.grad_preact : a.grad;
   Params p = {};
-  p.max_cols = kMaxCols;
+  p.most_rows = most;
   p.rows = a.num_rows_per_expert;
   p.offset = a.expert_offset;
   p.error_word = a.error_word;
@@ -159,13 +169,12 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     p.a_tiles = up(a.hidden, 256);
     p.out = a.grad_x;
     ep_status_t s = weight_map(p, kGradX, a.w, wide, a.hidden);
-    if (s == EP_OK) s = row_maps(p, g, wide, a.recv_capacity, most);
-    if (s == EP_OK)
-      s = launch_form<kGradX>(p, most, most_tiles(a.recv_capacity, a.num_experts) * p.a_tiles, stream);
+    if (s == EP_OK) s = launch_rows_form<kGradX>(p, g, stream);
     if (s != EP_OK) return s;
   }
   if (a.grad_w != nullptr) {
-    p.parts = 0;
+    p.parts = 1;
+    p.max_cols = kMaxCols;
     p.a_tiles = up(wide, 256);
     p.b_tiles = up(a.hidden, 256);
     p.out = a.grad_w;
@@ -178,7 +187,7 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     if (s == EP_OK) s = encode_map(&p.grad, a.grad_w, 3, dims, strides, box);
     if (s == EP_OK) s = block_map(&p.b[0], &p.b_blocks, most > 0 ? a.x : a.grad_w, a.hidden, cap);
     if (s == EP_OK)
-      s = launch_form<kGradW>(p, most, (int64_t)a.num_experts * p.a_tiles * p.b_tiles, stream);
+      s = launch_form<kGradW>(p, (int64_t)a.num_experts * p.a_tiles * p.b_tiles, stream);
     if (s != EP_OK) return s;
   }
   return EP_OK;

@@ -169,6 +169,39 @@ def test_gradients_against_differences():
         assert abs(float(terms.sum()) - want) <= 2.0 ** -8 * float(terms.norm()) * 4
 
 
+@pytest.mark.parametrize("T,K,E,H,width,only", [(1021, 1, 1, 2048, 1000, None), (1024, 2, 4, 1024, 512, None),
+                                                (600, 1, 2, 1024, 264, [1]), (2100, 1, 3, 512, 72, [0, 2]),
+                                                (70, 1, 1, 4096, 8, None), (330, 1, 2, 4096, 136, [0])])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_few_experts(T, K, E, H, width, only, act):
+    """Few tiles, which are cut narrower or shared by pairs, also where some
+    experts get nothing and the others more than was reckoned with."""
+    lay, x, used, g = rows_and_layout(T, K, E, H, 1, T, only=only)
+    wide = 2 * width if act else width
+    w = weights(g, E, wide, H)
+    pre = torch.empty((x.shape[0], wide), dtype=torch.bfloat16, device=DEV)
+    out = ep.ep_expert_product(x, w, lay, activation=act, preact=pre)
+    assert torch.equal(out[used], ep.ep_expert_product(x, w, lay, activation=act)[used])
+    grad = torch.randn((x.shape[0], width), generator=g, device=DEV).to(torch.bfloat16)
+    gp = torch.zeros_like(pre)
+    grad_x, grad_w = ep.ep_expert_product_backward(grad, x, w, lay, activation=act, preact=pre, grad_preact=gp)
+    assert lay.errors() == 0
+    for e, (a, n) in enumerate(segments(lay)):
+        h, tol = fp32_sum(x[a:a + n], w[e])
+        close(pre[a:a + n], h, tol)
+        if act is None:
+            close(out[a:a + n], h, tol)
+        else:
+            gate, up, tg, tu = h[:, :width], h[:, width:], tol[:, :width], tol[:, width:]
+            s = gate * torch.sigmoid(gate)
+            close(out[a:a + n], s * up, 1.1 * tg * (up.abs() + tu) + s.abs() * tu + 1e-6 * (s * up).abs())
+        d = (gp if act else grad)[a:a + n]
+        want, tol = fp32_sum(d, w[e].T)
+        close(grad_x[a:a + n], want, tol)
+        want, tol = fp32_sum(d.T, x[a:a + n].T)
+        close(grad_w[e], want, tol)
+
+
 @pytest.mark.parametrize("act", [None, "swiglu"])
 def test_experts_without_rows(act):
     lay, x, used, g = rows_and_layout(50, 2, 16, 128, 1, 4, only=[3, 9, 10])
