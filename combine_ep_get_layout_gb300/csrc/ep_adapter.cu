@@ -16,7 +16,7 @@
 // low is kept in bf16, as the tensor cores take it: 2^-8 of the low term, the
 // size of the result's own rounding.
 //
-// Measured: 8192 rows 7168 -> 4096, rank 32: 314 to 325 us, of which the low
+// Measured: 8192 rows 7168 -> 4096, rank 32: 313 to 325 us, of which the low
 // rows 32 (the projection's power limit bounds it); 1021 rows 4096 -> 1000, 40
 // adapters of rank 8: 20 to 21 us in a graph; 32 rows 4096 -> 4096, 24 adapters
 // of rank 16: 10.5 us in a graph, where reading the weights takes 6 (the low

@@ -26,8 +26,8 @@
 // cycles; the copies, the issue and the results have to stay below that.
 // Dense 8192 x 4096 x 4096: 148 us, 1859 TFLOP/s (burst).  Few rows: reading
 // the weights, 24 tokens top-6 of 64 experts, 4096 -> 2 x 1408, 191 us, 6.9
-// TB/s.  Many: the power limit (1370 W), 4096 tokens 421 to 450 us sustained
-// at 1.3 GHz, 371 us in a burst.  8192 tokens top-8 of 256 experts, 512 ->
+// TB/s.  Many: the power limit (1370 W), 4096 tokens 421 to 457 us sustained
+// at 1.3 GHz, 358 to 371 us in a burst.  8192 tokens top-8 of 256 experts, 512 ->
 // 7168: 477 to 505 us, 6 TB/s.
 #pragma once
 
@@ -85,7 +85,6 @@ struct Params {
   int max_cols;         // rows of a tile, at most
   int most_rows;        // of an expert, at most
   int parts;            // pairs that share a tile's inner dimension
-  int part_cols;        // columns of their results
   int ring_bytes;       // of the ring (kAdapter: both rings)
   // kAdapter
   const uint16_t *up;    // the up-projections [adapters][width][rank]
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           ok = ok && mbar_wait_cluster(&s_bar.part_empty, part_phase ^ 1);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
-          const uint32_t to = map_shared(smem_addr(joined + (part - 1) * p.part_cols * 32 + quarter * 32 + lane), rank);
+          const uint32_t to = map_shared(smem_addr(joined + (part - 1) * p.max_cols * 32 + quarter * 32 + lane), rank);
           for (int c = half * 32; c < t.cols; c += 64) {
             float v[32];
             tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
@@ -743,7 +742,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         if (F != kGradW && p.parts > 1) {
           // the parts are added in their order
           for (int q = 0; q + 1 < p.parts; ++q) {
-            const float4 *more = joined + (q * p.part_cols + c) * 32 + quarter * 32 + lane;
+            const float4 *more = joined + (q * p.max_cols + c) * 32 + quarter * 32 + lane;
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const float4 m = more[j * 32];
@@ -916,7 +915,6 @@ ep_status_t launch_form(Params &p, int64_t tiles, cudaStream_t stream) {
   const DeviceInfo *di = current_device_info();
   if (di == nullptr) return EP_ERR_CUDA;
   const int cols = p.max_cols;
-  p.part_cols = cols;
   // The ring takes what is left of shared memory.
   const int limit = shared_limit(di);
   const int fixed = 1024 + kResultWarps * staging_of(F) + (F == kGated ? kResultWarps * kExchangeBytes : 0) +
@@ -954,7 +952,6 @@ ep_status_t row_maps(Params &p, const void *rows, int length, int cap) {
   }
   return EP_OK;
 }
-
 
 }  // namespace
 

@@ -11,7 +11,7 @@
 // memory, rounded once.  The kernel is in ep_pair.cuh.
 //
 // Gradients through the gate of 4096 tokens top-6 of 64 experts, 4096 -> 2 x
-// 1408: 856 to 887 us sustained (814 us the first time, before the power limit
+// 1408: 846 to 890 us sustained (789 to 814 the first time, before the power limit
 // is met), of which the gate 43, the rows about 340, the weights about 400.
 #include "ep_pair.cuh"
 

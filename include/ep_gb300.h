@@ -670,7 +670,8 @@ size_t ep_adapter_workspace_bytes(int num_rows, int hidden, int rank);
  * without the second term where a = -1; any other a outside [0, num_adapters)
  * counts as -1 and sets EP_ERRBIT_BAD_INDEX in error_word (if given).  Sums
  * in fp32.  Rows may come in any order; rows of one request next to
- * each other are faster than interleaved ones.
+ * each other are faster than interleaved ones.  What is not finite in an
+ * adapter reaches only the rows that name it.
  *   x [num_rows * hidden], w [width * hidden], lora_a [num_adapters * rank *
  *   hidden], lora_b [num_adapters * width * rank], out [num_rows * width]:
  *   bf16, 16-byte aligned; adapter_idx [num_rows] int64; adapter_scale
