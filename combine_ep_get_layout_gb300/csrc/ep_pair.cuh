@@ -699,8 +699,8 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
               store_cluster(to + (uint32_t)(c + j) * 512, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
           }
           release(acc);
-          fence_cluster();  // every lane's own stores, before one arrives for all
           __syncwarp();
+          fence_cluster();  // every lane's stores, before one arrives for all
           if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.part_full), rank));
           part_phase ^= 1;
           acc ^= 1;

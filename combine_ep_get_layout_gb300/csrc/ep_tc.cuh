@@ -32,12 +32,9 @@ __device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// The same without ordering this thread's memory operations (a release to the
-// cluster first waits for all its stores to global memory).
+// An arrival at another CTA's barrier that does not order this thread's memory
+// operations (a release to the cluster first waits for all its stores to
+// global memory).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
