@@ -29,7 +29,7 @@ LIB = os.path.join(HERE, "libep_gb300.so")
 SOURCES = ["ep_api.cu", "ep_layout.cu", "ep_layout_expanded.cu", "ep_dispatch.cu", "ep_combine.cu",
            "ep_noalloc.cu", "ep_selftest.cu", "ep_ops_api.cu", "ep_route.cu", "ep_product.cu",
            "ep_adapter.cu", "ep_tc.cu"]
-HEADERS = ["ep_device.cuh", "ep_internal.h", "ep_ops.h", "ep_pair.cuh", "ep_tc.cuh", "ep_trace.cuh"]
+HEADERS = ["ep_cut.h", "ep_device.cuh", "ep_internal.h", "ep_ops.h", "ep_pair.cuh", "ep_tc.cuh", "ep_trace.cuh"]
 TRACE_LIB = os.path.join(HERE, "libep_gb300_trace.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",

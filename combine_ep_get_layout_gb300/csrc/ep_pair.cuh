@@ -34,6 +34,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "ep_cut.h"
 #include "ep_ops.h"
 #include "ep_tc.cuh"
 
@@ -128,18 +129,13 @@ struct Walker {
   // The most columns that a tile has (the whole warp calls it).
   __device__ static int most_cols(const Params &p) {
     if (F == kGradW) return kMaxCols;
-    int n = p.most_rows;  // with so few the counts need not be read
-    if (F != kAdapter && n > 64) {
-      n = 0;
-#pragma unroll 8
-      for (int e = threadIdx.x & 31; e < p.E; e += 32) {
-        const int rows = max(0, min(p.rows[e], p.most_rows)), tiles = ceil_div(rows, p.max_cols);
-        n = max(n, tiles > 0 ? ceil_div(rows, tiles) : 0);
-      }
-      n = __reduce_max_sync(0xffffffffu, n);
-    }
-    return n >= p.max_cols ? p.max_cols : max(32, ceil_div(n, 32) * 32);
+    // with so few rows the counts need not be read
+    if (F == kAdapter || p.most_rows <= 64) return most_cols_of(limits(p));
+    const int n = widest_tile(limits(p), p.offset, p.rows, p.E, threadIdx.x & 31, 32);
+    return max(kColumnStep, __reduce_max_sync(0xffffffffu, n));
   }
+
+  __device__ static RowLimits limits(const Params &p) { return RowLimits{p.cap, p.most_rows, p.max_cols}; }
 
   __device__ void load(int c) {
     chunk = c;
@@ -147,13 +143,13 @@ struct Walker {
     rows = first = mine = 0;
     if (F == kAdapter) {
       rows = e == 0 ? p.cap : 0;
-      mine = p.a_tiles * ceil_div(rows, p.max_cols);
+      mine = p.a_tiles * tiles_of(limits(p), rows);
     } else if (e < p.E) {
       first = p.offset[e];
       const int n = p.rows[e];
-      rows = first < 0 || first >= p.cap ? 0 : max(0, min(n, min(p.cap - first, p.most_rows)));
+      rows = rows_within(limits(p), first, n);
       if (rows != n && blockIdx.x == 0 && threadIdx.x < 32) set_error(p.error_word, EP_ERRBIT_CAPACITY);
-      mine = F == kGradW ? p.a_tiles * p.b_tiles : p.a_tiles * ceil_div(rows, p.max_cols);
+      mine = F == kGradW ? p.a_tiles * p.b_tiles : p.a_tiles * tiles_of(limits(p), rows);
     }
     prefix = mine;
 #pragma unroll
@@ -187,9 +183,7 @@ struct Walker {
       t.cols = kMaxCols;
       t.steps = ceil_div(n, kInner);
     } else {
-      // as few tiles as hold the rows, of about equal size
-      const int tiles = ceil_div(n, p.max_cols);
-      t.cols = ceil_div(ceil_div(n, tiles), 32) * 32;
+      const int tiles = tiles_of(limits(p), n);
       if (F == kAdapter) {
         // eight tiles of rows go along A together, so the pairs running at
         // once share rows as well as weights
@@ -201,9 +195,10 @@ struct Walker {
         t.a0 = at / tiles * (F == kGated ? 128 : 256);
       }
       t.b0 = 0;
-      t.first += t.part * t.cols;
-      t.count = min(t.cols, n - t.part * t.cols);
-      t.cols = ceil_div(t.count, 32) * 32;  // the last tile takes no more than it needs
+      int from;
+      t.count = tile_rows(limits(p), n, t.part, &from);
+      t.first += from;
+      t.cols = ceil_div(t.count, kColumnStep) * kColumnStep;
       t.steps = ceil_div(p.inner, kInner);
     }
     return true;

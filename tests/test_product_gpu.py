@@ -278,6 +278,65 @@ def test_rows_past_the_capacity_are_flagged_and_skipped():
     assert torch.equal(out[:cap], want[:cap]) and bool((out[cap:] == 7.0).all())
 
 
+CUT = [
+    # rows of each expert, capacity, H, width
+    ((300, 300, 300, 300), 1080, 1024, 4096),      # tiles of 160 columns, the cut one of 192
+    ((260, 260), 516, 256, 8192),                  # 160, 256
+    ((300, 1, 300), 481, 6144, 4104),              # the rows' gradient too
+    ((390,) * 16, 390 * 15 + 230, 1032, 704),      # 224, 256
+    ((65, 400, 260, 500), 700, 328, 264),          # one cut, one without a row
+    ((300, 300, 300, 300), 1080, 1024, 512),       # tiles cut narrower
+]
+
+
+def counted_layout(counts):
+    """The layout of one choice a token: the first tokens the first expert's, and so on."""
+    idx = torch.cat([torch.full((n,), e) for e, n in enumerate(counts)])[:, None].to(DEV).contiguous()
+    lay = ep.ep_get_layout_expanded(idx, len(counts))
+    assert lay.num_rows_per_expert.tolist() == list(counts)
+    return lay
+
+
+@pytest.mark.parametrize("counts,cap,H,width", CUT)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_a_capacity_that_cuts_an_expert(counts, cap, H, width, act):
+    """Hundreds of rows an expert, and a capacity inside one's segment, whose
+    tiles may then be wider than the whole ones': every row below the capacity
+    is right, in the outputs and in the rows' and the weights' gradients, and
+    no row past it is touched."""
+    g = torch.Generator(device=DEV).manual_seed(sum(counts) + cap)
+    x = torch.randn((sum(counts), H), generator=g, device=DEV).to(torch.bfloat16)
+    lay = counted_layout(counts)
+    wide = 2 * width if act else width
+    w = weights(g, len(counts), wide, H)
+    out = torch.full((len(x), width), 7.0, dtype=torch.bfloat16, device=DEV)
+    pre = torch.full((len(x), wide), 7.0, dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product(x[:cap], w, lay, activation=act, out=out[:cap], preact=pre[:cap])
+    assert lay.errors() == ep.EP_ERRBIT_CAPACITY
+    assert bool((out[cap:] == 7.0).all()) and bool((pre[cap:] == 7.0).all())
+    grad = torch.randn((len(x), width), generator=g, device=DEV).to(torch.bfloat16)
+    grad_x = torch.full((len(x), H), 7.0, dtype=torch.bfloat16, device=DEV)
+    gp = torch.zeros_like(pre)
+    _, grad_w = ep.ep_expert_product_backward(grad[:cap], x[:cap], w, lay, activation=act, preact=pre[:cap] if act else None,
+                                              grad_x=grad_x[:cap], grad_preact=gp[:cap] if act else None)
+    assert lay.errors() == ep.EP_ERRBIT_CAPACITY and bool((grad_x[cap:] == 7.0).all())
+    for e, (a, n) in enumerate(segments(lay)):
+        here = slice(a, max(a, min(a + n, cap)))
+        h, tol = fp32_sum(x[here], w[e])
+        close(pre[here], h, tol)
+        if act is None:
+            close(out[here], h, tol)
+        else:
+            gate, up, tg, tu = h[:, :width], h[:, width:], tol[:, :width], tol[:, width:]
+            s = gate * torch.sigmoid(gate)
+            close(out[here], s * up, 1.1 * tg * (up.abs() + tu) + s.abs() * tu + 1e-6 * (s * up).abs())
+        d = (gp if act else grad)[here]
+        want, tol = fp32_sum(d, w[e].T)
+        close(grad_x[here], want, tol)
+        want, tol = fp32_sum(d.T, x[here].T)
+        close(grad_w[e], want, tol)
+
+
 def test_another_stream():
     lay, x, used, g = rows_and_layout(512, 4, 8, 512, 1, 8)
     w = weights(g, 8, 512, 512)
