@@ -797,17 +797,23 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(Rou
   }
 }
 
-template <typename K>
-ep_status_t route_grid(K kernel, int T, int E, const DeviceInfo *di, int *grid, size_t *smem) {
-  *smem = (size_t)kRouteWarps * E * sizeof(float);
-  if (*smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*smem);
+// The limit of dynamic shared memory belongs to the kernel, not to a launch:
+// it is set to the most that any call needs, so a call in another thread with
+// fewer experts cannot lower it between this one's check and its launch.
+template <bool BF16>
+ep_status_t launch_warps(const RouteParams &p, const DeviceInfo *di, cudaStream_t stream) {
+  const size_t smem = (size_t)kRouteWarps * p.E * sizeof(float);
+  static std::atomic<bool> ready[64];
+  if (smem > 48 * 1024 && !ready[di->device]) {
+    const cudaError_t e = cudaFuncSetAttribute(route_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kRouteWarps * EP_MAX_EXPERTS * (int)sizeof(float));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    ready[di->device] = true;
   }
-  const int64_t need = ((int64_t)T + kRouteWarps - 1) / kRouteWarps;
-  const int64_t most = (int64_t)di->num_sms * 16;
-  *grid = (int)(need < most ? need : most);
-  return EP_OK;
+  const int64_t need = ((int64_t)p.T + kRouteWarps - 1) / kRouteWarps, most = (int64_t)di->num_sms * 16;
+  const cudaError_t e = launch_kernel(route_kernel<BF16>, (int)(need < most ? need : most), kRouteWarps * 32, smem, stream,
+                                      false, p);
+  return e == cudaSuccess ? EP_OK : cuda_fail(e, "route launch");
 }
 
 }  // namespace
@@ -839,13 +845,7 @@ ep_status_t launch_route(const RouteArgs &a, cudaStream_t stream) {
     if (a.num_topk <= 8) return a.bf16 ? launch_lanes<true, 8>(p, stream) : launch_lanes<false, 8>(p, stream);
     return a.bf16 ? launch_lanes<true, 16>(p, stream) : launch_lanes<false, 16>(p, stream);
   }
-  auto kernel = a.bf16 ? route_kernel<true> : route_kernel<false>;
-  int grid;
-  size_t smem;
-  const ep_status_t s = route_grid(kernel, a.num_tokens, a.num_experts, di, &grid, &smem);
-  if (s != EP_OK) return s;
-  const cudaError_t e = launch_kernel(kernel, grid, kRouteWarps * 32, smem, stream, false, p);
-  return e == cudaSuccess ? EP_OK : cuda_fail(e, "route launch");
+  return a.bf16 ? launch_warps<true>(p, di, stream) : launch_warps<false>(p, di, stream);
 }
 
 ep_status_t launch_route_backward(const RouteBackwardArgs &a, cudaStream_t stream) {

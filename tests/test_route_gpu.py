@@ -9,6 +9,7 @@ A gradient adds differences of such terms, so the same bound on the sum of
 the absolute values of its terms; bf16 gradients add their rounding, 2^-8.
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -191,6 +192,33 @@ def test_no_tokens_and_other_streams():
         ep.ep_route(y, 8, score="sigmoid", out=out)
     s.synchronize()
     assert torch.equal(out.topk_idx, want.topk_idx) and torch.equal(out.topk_weights, want.topk_weights)
+
+
+def test_threads_with_other_counts_of_experts():
+    """Calls with more and with fewer experts from several threads at once:
+    none refuses another's launch, whose shared memory goes by its experts."""
+    errors, results = [], {}
+
+    def go(name, x):
+        try:
+            out = ep.ep_route(x, 4)
+            for _ in range(4000):
+                ep.ep_route(x, 4, out=out)
+            results[name] = out
+        except ep.EPError as e:
+            errors.append(str(e))
+
+    x = {n: make_logits(8, n, torch.float32, n).to(DEV) for n in (4096, 3100, 4095, 3073)}
+    want = {n: ep.ep_route(v, 4) for n, v in x.items()}
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=go, args=item) for item in x.items()]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    assert all(torch.equal(results[n].topk_idx, want[n].topk_idx) for n in x)
 
 
 def test_many_tokens_feed_the_layout():
