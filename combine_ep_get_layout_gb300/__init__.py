@@ -670,12 +670,20 @@ def _refuse_tensors(*wanted):
 
 
 def _product_sizes(x, w, layout, activation):
-    """(capacity, hidden, width, wide) of rows and weights, checked."""
+    """(capacity, hidden, width, wide) of rows and weights, checked, and the
+    layout's tensors where they are."""
     bf = torch.bfloat16
     if not (x.dtype is bf and w.dtype is bf and x.is_cuda and x.get_device() == w.get_device()
             and x.is_contiguous() and w.is_contiguous()):
         _want(x, "x", bf)
         _want(w, "w", bf, x.device)
+    i = x.get_device()
+    if not (layout.num_rows_per_expert.get_device() == i and layout.expert_offset.get_device() == i
+            and layout.error_word.get_device() == i):
+        for name in ("num_rows_per_expert", "expert_offset", "error_word"):
+            at = getattr(layout, name).device
+            if at != x.device:
+                raise ValueError(f"layout.{name} is on {at}, expected {x.device}")
     if x.dim() != 2 or w.dim() != 3:
         raise ValueError("x must be [recv_capacity, hidden] and w [num_experts, outputs, hidden]")
     cap, H = x.shape

@@ -142,6 +142,38 @@ def test_the_binding_checks_tensors():
         ep.ep_adapter_product(torch.zeros((4, 64)), bf, bf, bf, torch.zeros(4, dtype=torch.int64))
 
 
+class OnDevice:
+    """A tensor as the binding looks at it, on a device that need not be there."""
+
+    def __init__(self, shape, index, dtype=torch.bfloat16):
+        self.shape, self.dtype, self.is_cuda, self.index = torch.Size(shape), dtype, True, index
+        self.device = torch.device("cuda", index)
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.mark.parametrize("away", ["num_rows_per_expert", "expert_offset", "error_word"])
+@pytest.mark.parametrize("where", ["cuda:1", "cpu"])
+def test_a_layout_of_another_device_is_refused(away, where):
+    """The kernels read the layout's tensors where the rows are."""
+    x, w, grad = OnDevice((8, 64), 0), OnDevice((4, 32, 64), 0), OnDevice((8, 32), 0)
+    there = {n: OnDevice((1,), 0, torch.int32) for n in
+             ("num_rows_per_expert", "expert_offset", "token_slot", "error_word", "workspace")}
+    there[away] = OnDevice((1,), 1, torch.int32) if where == "cuda:1" else torch.zeros(1, dtype=torch.int32)
+    lay = ep.ExpandedLayout(**there, num_tokens=4, num_topk=2, num_experts=4, expert_alignment=1)
+    with pytest.raises(ValueError, match=f"layout.{away} is on {where}, expected cuda:0"):
+        ep.ep_expert_product(x, w, lay)
+    with pytest.raises(ValueError, match=f"layout.{away} is on {where}, expected cuda:0"):
+        ep.ep_expert_product_backward(grad, x, w, lay)
+
+
 @pytest.mark.parametrize("cls", [N.ep_route_args_t, N.ep_route_backward_args_t, N.ep_expert_product_args_t,
                                  N.ep_expert_product_backward_args_t, N.ep_adapter_product_args_t])
 def test_packed_arguments_are_the_structures_bytes(cls):
