@@ -269,7 +269,7 @@ __device__ __forceinline__ uint32_t not_finite(const uint4 &w) {
 }
 
 // kAdapter: the infinities and NaN of the up-projections, which the gathering
-// warps left out, added to 32 rows c ... of output `at` that this warp wrote
+// warps replaced, added to 32 rows c ... of output `at` that this warp wrote
 // (a sum with one of them is that one, whatever the rest was rounded to).
 __device__ __forceinline__ void add_odd(const Params &p, const Tile &t, int c, int at) {
   const int32_t *plan = p.plan + (int64_t)t.part * kPlanWords;
@@ -545,8 +545,11 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     // swizzled order that a tile's copy would give them: eight lanes take the
     // eight pieces of a row, so a lane stays with one adapter in a step.  An
     // up-projection meets every row of the tile, and in other adapters' rows
-    // zeros, which would make NaN of what is not finite: that is put to zero
-    // here, the tile is noted, and the results' warps add it to its own rows.
+    // zeros, which would make NaN of what is not finite: 2^-64 of its sign
+    // takes its place here, the tile is noted, and the results' warps add it
+    // to its own rows.  (Not zero: an infinite low value would make NaN of
+    // that; times 2^-64 it is the infinity that the product is, and a finite
+    // one is too little to be seen beside an infinity.)
     griddep_wait();
     Walker<F> walk(p);
     Tile t;
@@ -568,7 +571,10 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         if (odd != 0u) {
           for (int j = 0; j < 8; ++j) {
             uint32_t *w = reinterpret_cast<uint32_t *>(at(j));
-            for (int i = 0; i < 4; ++i) w[i] &= ~((not_finite(w[i]) >> 15) * 0xffffu);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t which = (not_finite(w[i]) >> 15) * 0xffffu;
+              w[i] = (w[i] & ~(which & 0x7fff7fffu)) | (which & 0x1f801f80u);
+            }
           }
           atom_max_cluster(map_shared(smem_addr(&s_bar.odd), rank), n);  // where the results are finished
         }

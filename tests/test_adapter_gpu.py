@@ -137,6 +137,33 @@ def test_an_up_projection_that_is_not_finite_stays_with_its_rows(T, H, N, A, r, 
     assert torch.equal(got.nan_to_num(nan=7.0), ep.ep_adapter_product(x, w, a, b, idx, s).nan_to_num(nan=7.0))
 
 
+@pytest.mark.parametrize("T,H,N,A,r", [(3, 512, 136, 3, 8), (32, 4096, 520, 24, 16), (300, 256, 512, 40, 24),
+                                       (1100, 4096, 128, 5, 32)])
+def test_infinite_low_values_meet_infinite_up_projections(T, H, N, A, r):
+    """Infinity times infinity is infinity, of the product's sign: a low value
+    that overflows meets an infinite up-projection, and finite ones."""
+    x, w, a, b, idx, s = make(T, H, N, A, r, T + 1, "rows")
+    idx[0], idx[1], idx[2] = 1, 1, 0
+    i = r - 2
+    a[1, i] = 0.0
+    a[1, i, 0] = 3e38
+    x[:, 0] = 0.25
+    x[0, 0], x[1, 0] = 16.0, -16.0  # times 3e38 and a scale of 0.5 or more: infinite
+    clean = ep.ep_adapter_product(x, w, a, b, idx, s)
+    finite = b[1, :, i].clone()
+    assert bool((finite != 0).all())
+    b[1, 5, i], b[1, 70, i], b[1, N - 1, i] = math.inf, -math.inf, math.inf
+    got = ep.ep_adapter_product(x, w, a, b, idx, s)
+    sign = b[1, :, i].double().sign() * math.inf
+    assert torch.equal(got[0].double(), sign) and torch.equal(got[1].double(), -sign)
+    own = (idx == 1).nonzero()[:, 0]
+    own = own[own > 1]  # their low value is finite and positive
+    for n in (5, 70, N - 1):
+        assert bool((got[own, n].double() == sign[n]).all())
+    rest = (idx != 1).nonzero()[:, 0]
+    assert len(rest) and torch.isfinite(clean[rest]).all() and torch.equal(got[rest], clean[rest])
+
+
 def test_no_rows_and_another_stream():
     x, w, a, b, idx, s = make(0, 64, 32, 2, 8, 5, "rows")
     assert ep.ep_adapter_product(x, w, a, b, idx, s).shape == (0, 32)
