@@ -65,6 +65,20 @@ __global__ void __launch_bounds__(256) gate_backward_kernel(GateParams p) {
   }
 }
 
+// Where no row may be computed: a layout that has some all the same is flagged.
+__global__ void __launch_bounds__(256) flag_rows_kernel(const int32_t *rows, int E, uint32_t *error_word) {
+  griddep_wait();
+  griddep_launch_dependents();
+  bool some = false;
+  for (int e = threadIdx.x; e < E; e += 256) some = some || rows[e] != 0;
+  if (some) set_error(error_word, EP_ERRBIT_CAPACITY);
+}
+
+ep_status_t launch_flag_rows(const Params &p, cudaStream_t stream) {
+  const cudaError_t e = launch_kernel(flag_rows_kernel, 1, 256, 0, stream, false, p.rows, p.E, p.error_word);
+  return e == cudaSuccess ? EP_OK : cuda_fail(e, "flag_rows launch");
+}
+
 // Rows [rows][length] read with the outer dimension contiguous: blocks of 64
 // of a row by 64 rows, two blocks a copy where the length allows it.
 ep_status_t block_map(CUtensorMap *map, bool *blocks, const void *rows, int length, int cap) {
@@ -122,13 +136,13 @@ ep_status_t launch_rows_form(Params &p, const void *rows, cudaStream_t stream) {
 
 ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
   const int most = a.num_tokens < a.recv_capacity ? a.num_tokens : a.recv_capacity;  // rows of one expert
-  if (most == 0) return EP_OK;
   Params p = {};
   p.most_rows = most;
   p.rows = a.num_rows_per_expert;
   p.offset = a.expert_offset;
   p.error_word = a.error_word;
   p.E = a.num_experts;
+  if (most == 0) return launch_flag_rows(p, stream);
   p.cap = a.recv_capacity;
   p.width = a.width;
   p.wide = a.gated ? 2 * a.width : a.width;
@@ -154,6 +168,7 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
   p.cap = a.recv_capacity;
   p.wide = wide;
   p.hidden = a.hidden;
+  if (most == 0 && a.grad_w == nullptr) return launch_flag_rows(p, stream);  // else the weights' gradient flags them
   if (a.gated && most > 0) {
     const GateParams q{a.grad, a.preact, a.grad_preact, p.offset, a.num_experts, a.recv_capacity, a.width};
     const DeviceInfo *di = current_device_info();

@@ -337,6 +337,33 @@ def test_a_capacity_that_cuts_an_expert(counts, cap, H, width, act):
         close(grad_w[e], want, tol)
 
 
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("what", ["no capacity", "no tokens"])
+def test_rows_that_are_all_skipped_are_flagged(what, act):
+    """A capacity of no rows, and a layout whose num_tokens says none: the
+    layout's rows are skipped and flagged as any others, and gradients of the
+    weights are zero."""
+    lay, x, used, g = rows_and_layout(64, 2, 4, 64, 1, 6)
+    w = weights(g, 4, 64, 64)
+    width = 32 if act else 64
+    if what == "no capacity":
+        x = x[:0]
+    else:
+        lay.num_tokens = 0
+    out = torch.full((x.shape[0], width), 7.0, dtype=torch.bfloat16, device=DEV)
+    pre = torch.full((x.shape[0], 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    ep.ep_expert_product(x, w, lay, activation=act, out=out, preact=pre)
+    assert lay.errors() == ep.EP_ERRBIT_CAPACITY and bool((out == 7.0).all()) and bool((pre == 7.0).all())
+    for need_x, need_w in ((True, False), (False, True), (True, True)):
+        lay.error_word.zero_()
+        grad_x = torch.full((x.shape[0], 64), 7.0, dtype=torch.bfloat16, device=DEV) if need_x else None
+        _, grad_w = ep.ep_expert_product_backward(out, x, w, lay, activation=act, preact=pre if act else None,
+                                                  grad_x=grad_x, need_x=need_x, need_w=need_w)
+        assert lay.errors() == ep.EP_ERRBIT_CAPACITY
+        assert not need_x or bool((grad_x == 7.0).all())
+        assert not need_w or bool((grad_w == 0).all())
+
+
 def test_another_stream():
     lay, x, used, g = rows_and_layout(512, 4, 8, 512, 1, 8)
     w = weights(g, 8, 512, 512)
