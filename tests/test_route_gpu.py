@@ -194,6 +194,31 @@ def test_no_tokens_and_other_streams():
     assert torch.equal(out.topk_idx, want.topk_idx) and torch.equal(out.topk_weights, want.topk_weights)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,Gk,top,K", [(8, 1, 1, 1, 3), (33, 1, 1, 1, 8), (40, 5, 2, 2, 6), (60, 3, 2, 1, 4), (60, 15, 6, 2, 16)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_a_token_goes_to_the_same_experts_in_any_batch(E, G, Gk, top, K, score, bias):
+    """Many near ties: the logits come in pairs a few units in the last place
+    apart, with the same bias.  Few tokens and many take different kernels,
+    which compare the same keys."""
+    g = torch.Generator().manual_seed(E + K)
+    half = E // 2
+    x = make_logits(6000, E, torch.float32, E + G)
+    x[:, half:2 * half] = x[:, :half] * (1.0 + torch.randint(-3, 4, (6000, half), generator=g) * 2.0 ** -23)
+    x[::7].masked_fill_(torch.rand(x[::7].shape, generator=g) < 0.3, -math.inf)
+    b = None
+    if bias:
+        b = torch.randn(E, generator=g) * 0.05
+        b[half:2 * half] = b[:half]
+        b = b.to(DEV)
+    x = x.to(DEV)
+    how = dict(score=score, bias=b, num_groups=G, topk_groups=Gk, group_top=top)
+    whole = ep.ep_route(x, K, **how).topk_idx
+    for n in (1, 700, 4096):
+        part = torch.cat([ep.ep_route(x[i:i + n], K, **how).topk_idx for i in range(0, 6000 if n > 1 else 20, n)])
+        assert torch.equal(part, whole[:len(part)]), int((part != whole[:len(part)]).any(1).sum())
+
+
 def test_threads_with_other_counts_of_experts():
     """Calls with more and with fewer experts from several threads at once:
     none refuses another's launch, whose shared memory goes by its experts."""
