@@ -25,10 +25,10 @@
 // library's product).  A step of 64 x 256 columns takes the tensor cores 512
 // cycles; the copies, the issue and the results have to stay below that.
 // Dense 8192 x 4096 x 4096: 148 us, 1859 TFLOP/s (burst).  Few rows: reading
-// the weights, 24 tokens top-6 of 64 experts, 4096 -> 2 x 1408, 191 us, 6.9
-// TB/s.  Many: the power limit (1370 W), 4096 tokens 421 to 457 us sustained
-// at 1.3 GHz, 358 to 371 us in a burst.  8192 tokens top-8 of 256 experts, 512 ->
-// 7168: 477 to 505 us, 6 TB/s.
+// the weights, 24 tokens top-6 of 64 experts, 4096 -> 2 x 1408, 191 to 198 us,
+// 6.7 to 6.9 TB/s.  Many: the power limit (1370 W), 4096 tokens 421 to 457 us
+// sustained at 1.3 GHz, 358 to 371 us in a burst.  8192 tokens top-8 of 256
+// experts, 512 -> 7168: 477 to 505 us, 6 TB/s.
 #pragma once
 
 #include <atomic>
@@ -205,6 +205,8 @@ struct Walker {
   }
 };
 
+// __expf errs by up to 2 + 1.17 |g| units in the last place (its documented
+// bound): 2^-16 before it overflows, where the result is rounded to 2^-9.
 __device__ __forceinline__ float silu_of(float g) { return g / (1.0f + __expf(-g)); }
 
 // Barriers of two warps; the first also gives whether both say `ok`.

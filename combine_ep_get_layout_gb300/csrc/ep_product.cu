@@ -21,6 +21,8 @@ namespace {
 
 // The gradient of silu(g) * u for the rows of the layout, kept in bf16 as the
 // preactivations are: it is an operand of two products on the tensor cores.
+// (The gradients are then 2.3e-3 from 64 bits, with 32 bits between 1.7e-3;
+// __expf is accurate to 2^-16, as in silu_of.)
 // One pass over flat rows: 22 000 rows of 1408, 311 MB, 43 us (rows by expert
 // and block: 73 us, since experts differ in their rows).
 struct GateParams {

@@ -533,6 +533,8 @@ typedef enum {
  * are offered the remaining slots are -1 with weight 0.  Without a bias, and
  * with one group or group_top 1, the logits themselves are compared (the
  * scores rise with them), so scores that round together stay distinct.
+ * Scores are otherwise compared as fp32 holds them (below 2^-126 as 0), the
+ * same for a token in any batch.
  *   logits  [T] rows of E, row_stride >= E elements apart (row_stride is in
  *           elements), fp32 (4-byte aligned) or bf16 (2-byte aligned)
  *   bias    [E] fp32 or NULL
@@ -596,7 +598,7 @@ typedef enum {
  *   out[s] = bf16(silu(h[0:width]) * h[width:2*width])   EP_ACT_SWIGLU
  * with silu(g) = g / (1 + exp(-g)).  Padding rows and rows past the last are
  * not written.  Rows at or past recv_capacity are skipped and set
- * EP_ERRBIT_CAPACITY.
+ * EP_ERRBIT_CAPACITY, also where that is all of them.
  *   x       [recv_capacity * hidden] bf16
  *   layout  num_rows_per_expert, expert_offset and error_word are used; an
  *           expert has at most num_tokens rows (a token names it once), more
