@@ -33,8 +33,10 @@ __all__ = ["EPError", "Layout", "Dispatched", "ep_layout_workspace_bytes",
            "ep_expanded_layout_workspace_bytes", "ep_get_layout_expanded",
            "ep_dispatch_expanded", "ep_combine_expanded", "Routing", "ep_route",
            "ep_route_backward", "ep_expert_product", "ep_expert_product_backward",
-           "ep_adapter_workspace_bytes", "ep_adapter_product", "ep_selftest_bounded_waits",
-           "library_path"]
+           "ep_adapter_workspace_bytes", "ep_adapter_product", "Balance", "ep_balance_workspace_bytes",
+           "ep_balance_loss", "ep_balance_loss_backward", "ep_layer_norm", "ep_layer_norm_workspace_bytes",
+           "ep_layer_norm_backward", "ep_dense_product", "ep_dense_workspace_bytes",
+           "ep_dense_product_backward", "ep_selftest_bounded_waits", "library_path"]
 
 
 class EPError(RuntimeError):
@@ -829,6 +831,329 @@ def ep_adapter_product(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, l
         out.data_ptr(), workspace.data_ptr(), nbytes, 0 if error_word is None else error_word.data_ptr()),
         stream)
     return out
+
+
+# ------------------- the block around the layer: losses, norm, shared product
+
+@dataclass
+class Balance:
+    """A batch's balance and z loss, and what they were made of."""
+    losses: torch.Tensor  # fp32 [2]: balance, z
+    counts: torch.Tensor  # int32 [S, E]: choices of each expert
+    probs: torch.Tensor   # fp32 [S, E]: its mean score
+    slopes: torch.Tensor  # fp32 [S, E]: the balance loss's derivative for a token's score
+
+
+_TYPES = {torch.float32: N.EP_TYPE_FP32, torch.bfloat16: N.EP_TYPE_BF16}
+_DENSE_ACTIVATIONS = {None: N.EP_ACT_NONE, "swiglu": N.EP_ACT_SWIGLU, "relu": N.EP_ACT_RELU, "silu": N.EP_ACT_SILU,
+                      "gelu": N.EP_ACT_GELU, "gelu_tanh": N.EP_ACT_GELU_TANH}
+_balance_args = N.packer(N.ep_balance_loss_args_t)
+_balance_backward_args = N.packer(N.ep_balance_loss_backward_args_t)
+_norm_args = N.packer(N.ep_layer_norm_args_t)
+_norm_backward_args = N.packer(N.ep_layer_norm_backward_args_t)
+_dense_args = N.packer(N.ep_dense_product_args_t)
+_dense_backward_args = N.packer(N.ep_dense_product_backward_args_t)
+
+
+def _good(t, dtype, i, shape):
+    """A contiguous tensor of this type and shape on device ``i``."""
+    return t.dtype is dtype and t.get_device() == i and t.is_contiguous() and t.shape == shape
+
+
+def _address(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _given(t, name, dtype, dev, shape):
+    """An optional tensor, refused if it is not so."""
+    if t is not None and not (isinstance(t, torch.Tensor) and _good(t, dtype, dev.index, shape)):
+        _refuse_tensors((t, name, dtype, dev, shape))
+
+
+def _target(t, name, dtype, dev, shape, stream):
+    """An output: checked if it is given, else a new tensor."""
+    if t is None:
+        return _empty(shape, dtype, dev, stream)
+    _given(t, name, dtype, dev, shape)
+    return t
+
+
+def _scratch(workspace, nbytes, dev, stream):
+    """A workspace and its bytes."""
+    if workspace is None:
+        nbytes = max(nbytes, 16)
+        return _empty(nbytes, torch.uint8, dev, stream), nbytes
+    _want(workspace, "workspace", torch.uint8, dev)
+    return workspace, workspace.numel()
+
+
+def _rows(x: torch.Tensor, name: str, dtypes) -> tuple:
+    """Rows, their length and their distance in a matrix [T, H] of a type in
+    ``dtypes`` (rows may be apart, a row's entries may not)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    T, H = x.shape
+    apart, step = x.stride()
+    if (H > 1 and step != 1) or (T > 1 and apart < H):
+        raise ValueError(f"a row of {name} must be contiguous, and rows must not overlap")
+    return T, H, apart if T > 1 else H
+
+
+def _sequences(seq_offsets, dev) -> int:
+    if seq_offsets is None:
+        return 1
+    _want(seq_offsets, "seq_offsets", torch.int32, dev)
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+        raise ValueError("seq_offsets must be [num_sequences + 1]")
+    return seq_offsets.shape[0] - 1
+
+
+@lru_cache(maxsize=256)
+def ep_balance_workspace_bytes(num_tokens: int, num_experts: int, num_sequences: int) -> int:
+    return int(N.load().ep_balance_workspace_bytes(num_tokens, num_experts, num_sequences))
+
+
+def ep_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = "softmax",
+                    seq_offsets: Optional[torch.Tensor] = None, out: Optional[Balance] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> Balance:
+    """The router's balance and z loss, and each expert's counts, from the
+    gate's logits (as ``ep_route`` takes them) and the choice (int64 [T, K]).
+
+    With ``seq_offsets`` (int32 [S + 1], ascending) the sequences
+    ``[seq_offsets[s], seq_offsets[s + 1])`` are balanced one by one and the
+    losses averaged; tokens in none of them take no part.  ``score`` is
+    "softmax", or "sigmoid" (divided by its sum).  ``losses`` are the mean of
+    E times the sum of each expert's share of the choices times its mean score
+    (1 when balanced), and the mean square of the logits' log-sum-exp.
+    """
+    T, E, apart = _logits_sizes(logits)
+    dev, i = logits.device, logits.get_device()
+    S = _sequences(seq_offsets, dev)
+    if topk_idx.dim() != 2 or not _good(topk_idx, torch.int64, i, (T, topk_idx.shape[1])):
+        _refuse_tensors((topk_idx, "topk_idx", torch.int64, dev, (T, topk_idx.shape[-1])))
+    if out is None:
+        out = Balance(_empty(2, torch.float32, dev, stream), _empty((S, E), torch.int32, dev, stream),
+                      _empty((S, E), torch.float32, dev, stream), _empty((S, E), torch.float32, dev, stream))
+    else:
+        _refuse_tensors((out.losses, "losses", torch.float32, dev, (2,)), (out.counts, "counts", torch.int32, dev, (S, E)),
+                        (out.probs, "probs", torch.float32, dev, (S, E)),
+                        (out.slopes, "slopes", torch.float32, dev, (S, E)))
+    workspace, nbytes = _scratch(workspace, ep_balance_workspace_bytes(T, E, S) if workspace is None else 0, dev, stream)
+    _launch(i, "ep_balance_loss", _balance_args(
+        logits.data_ptr(), _LOGITS[logits.dtype], apart, topk_idx.data_ptr(), T, E, topk_idx.shape[1], _SCORES[score],
+        _address(seq_offsets), S, out.losses.data_ptr(), out.counts.data_ptr(), out.probs.data_ptr(),
+        out.slopes.data_ptr(), workspace.data_ptr(), nbytes), stream)
+    return out
+
+
+def ep_balance_loss_backward(grad_losses: torch.Tensor, logits: torch.Tensor, balance: Balance, score: str = "softmax",
+                             seq_offsets: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of ``ep_balance_loss``'s losses for the logits ([T, E],
+    the logits' dtype), given theirs (fp32 [2]) and what the forward call
+    returned, plus ``add`` ([T, E], for one what ``ep_route_backward`` gave;
+    ``out`` may be the same tensor).  The choice is held fixed."""
+    T, E, apart = _logits_sizes(logits)
+    dev, i = logits.device, logits.get_device()
+    S = _sequences(seq_offsets, dev)
+    if not (_good(grad_losses, torch.float32, i, (2,)) and _good(balance.slopes, torch.float32, i, (S, E))):
+        _refuse_tensors((grad_losses, "grad_losses", torch.float32, dev, (2,)),
+                        (balance.slopes, "balance.slopes", torch.float32, dev, (S, E)))
+    _given(add, "add", logits.dtype, dev, (T, E))
+    out = _target(out, "out", logits.dtype, dev, (T, E), stream)
+    _launch(i, "ep_balance_loss_backward", _balance_backward_args(
+        grad_losses.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], apart, T, E, _SCORES[score],
+        _address(seq_offsets), S, balance.slopes.data_ptr(), _address(add), out.data_ptr()), stream)
+    return out
+
+
+def _norm_params(weight, bias, H, dev) -> torch.dtype:
+    """The type of a norm's weight and bias, checked."""
+    dtype = torch.float32
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            if t.dtype not in _TYPES:
+                raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+            dtype = t.dtype
+            break
+    _given(weight, "weight", dtype, dev, (H,))
+    _given(bias, "bias", dtype, dev, (H,))
+    return dtype
+
+
+def ep_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                  rstd: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Layer norm of the rows of ``x`` (bf16 or fp32 [T, H]; rows may be a
+    slice of wider ones), times ``weight`` plus ``bias`` (fp32 or bf16 [H],
+    both alike).  Returns [T, H] in x's type; ``mean`` and ``rstd`` (fp32 [T])
+    receive the rows' statistics, which the backward pass needs."""
+    T, H, apart = _rows(x, "x", _TYPES)
+    dev = x.device
+    params = _norm_params(weight, bias, H, dev)
+    _given(mean, "mean", torch.float32, dev, (T,))
+    _given(rstd, "rstd", torch.float32, dev, (T,))
+    out = _target(out, "out", x.dtype, dev, (T, H), stream)
+    _launch(dev.index, "ep_layer_norm", _norm_args(
+        x.data_ptr(), _TYPES[x.dtype], apart, T, H, _address(weight), _address(bias), _TYPES[params], eps, out.data_ptr(),
+        _address(mean), _address(rstd)), stream)
+    return out
+
+
+@lru_cache(maxsize=256)
+def ep_layer_norm_workspace_bytes(num_rows: int, hidden: int) -> int:
+    return int(N.load().ep_layer_norm_workspace_bytes(num_rows, hidden))
+
+
+def ep_layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                           weight: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                           grad_x: Optional[torch.Tensor] = None, grad_weight: Optional[torch.Tensor] = None,
+                           grad_bias: Optional[torch.Tensor] = None, need_x: bool = True, need_params: bool = True,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """(grad_x, grad_weight, grad_bias) of ``ep_layer_norm`` for the output's
+    gradient ``grad`` ([T, H], x's type) and the statistics that the forward
+    call kept; what is not needed is None.  ``add`` ([T, H], x's type: the
+    gradient of a residual around the norm) is added to grad_x.  The
+    parameters' gradients (fp32 sums over the rows) have the weight's type,
+    fp32 without one, or that of the tensors given for them."""
+    T, H, apart = _rows(x, "x", _TYPES)
+    dev, i = x.device, x.get_device()
+    dtype, f32 = x.dtype, torch.float32
+    if not (_good(grad, dtype, i, (T, H)) and _good(mean, f32, i, (T,)) and _good(rstd, f32, i, (T,))):
+        _refuse_tensors((grad, "grad", dtype, dev, (T, H)), (mean, "mean", f32, dev, (T,)), (rstd, "rstd", f32, dev, (T,)))
+    params = _norm_params(weight, None, H, dev)
+    if weight is None and need_params and (grad_weight is not None or grad_bias is not None):
+        params = _norm_params(grad_weight, grad_bias, H, dev)
+    _given(add, "add", dtype, dev, (T, H))
+    grad_x = _target(grad_x, "grad_x", dtype, dev, (T, H), stream) if need_x else None
+    nbytes = 0
+    if need_params:
+        grad_weight = _target(grad_weight, "grad_weight", params, dev, (H,), stream)
+        grad_bias = _target(grad_bias, "grad_bias", params, dev, (H,), stream)
+        workspace, nbytes = _scratch(workspace, ep_layer_norm_workspace_bytes(T, H) if workspace is None else 0, dev, stream)
+    else:
+        grad_weight = grad_bias = workspace = None
+    _launch(i, "ep_layer_norm_backward", _norm_backward_args(
+        grad.data_ptr(), x.data_ptr(), _TYPES[dtype], apart, T, H, mean.data_ptr(), rstd.data_ptr(), _address(weight),
+        _TYPES[params], _address(add), _address(grad_x), _address(grad_weight), _address(grad_bias), _address(workspace),
+        nbytes), stream)
+    return grad_x, grad_weight, grad_bias
+
+
+def _dense_sizes(x, w, activation) -> tuple:
+    """(rows, hidden, x's row distance, width, wide) of a shared product."""
+    bf = torch.bfloat16
+    T, H, apart = _rows(x, "x", (bf,))
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be [outputs, hidden]")
+    wide = w.shape[0]
+    if not _good(w, bf, x.get_device(), (wide, H)):
+        _refuse_tensors((w, "w", bf, x.device, (wide, H)))
+    if activation == "swiglu":
+        if wide % 2:
+            raise ValueError("w must have an even number of outputs with swiglu")
+        return T, H, apart, wide // 2, wide
+    return T, H, apart, wide, wide
+
+
+def ep_dense_product(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                     activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, preact: Optional[torch.Tensor] = None,
+                     out_dtype: torch.dtype = torch.bfloat16, error_word: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """act(x w^T + bias) + residual, a product shared by all rows.
+
+    ``x`` bf16 [T, H] (rows may be a slice of wider ones, a multiple of 8
+    apart), ``w`` bf16 [N, H], ``bias`` fp32 or bf16 [N].  ``activation`` is
+    None, "relu", "silu", "gelu" (by erf), "gelu_tanh", or "swiglu": silu of
+    the first half of the outputs times the second, [T, N/2].  ``residual``
+    (bf16 like the output's shape) may be ``out``.  The output is bf16, or
+    fp32 with ``out_dtype`` (a gate's logits); sums are fp32, rounded once.
+    ``preact`` (bf16 [T, N]) receives x w^T + bias, which the backward pass of
+    an activation needs."""
+    act = _DENSE_ACTIVATIONS[activation]
+    T, H, apart, width, wide = _dense_sizes(x, w, activation)
+    bf, dev = torch.bfloat16, x.device
+    bias_type = N.EP_TYPE_FP32
+    if bias is not None:
+        if bias.dtype not in _TYPES:
+            raise TypeError(f"bias must be float32 or bfloat16, got {bias.dtype}")
+        _given(bias, "bias", bias.dtype, dev, (wide,))
+        bias_type = _TYPES[bias.dtype]
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _TYPES:
+        raise TypeError(f"the output must be float32 or bfloat16, not {out_dtype}")
+    _given(residual, "residual", bf, dev, (T, width))
+    _given(preact, "preact", bf, dev, (T, wide))
+    if error_word is not None:
+        _want(error_word, "error_word", torch.int32, dev)
+    out = _target(out, "out", out_dtype, dev, (T, width), stream)
+    _launch(dev.index, "ep_dense_product", _dense_args(
+        x.data_ptr(), apart, T, H, w.data_ptr(), width, _address(bias), bias_type, act, _address(residual),
+        out.data_ptr(), _TYPES[out_dtype], _address(preact), _address(error_word)), stream)
+    return out
+
+
+@lru_cache(maxsize=256)
+def ep_dense_workspace_bytes(num_rows: int, hidden: int, width: int, activation: Optional[str] = None) -> int:
+    return int(N.load().ep_dense_workspace_bytes(num_rows, hidden, width, _DENSE_ACTIVATIONS[activation]))
+
+
+def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tensor, activation: Optional[str] = None,
+                              preact: Optional[torch.Tensor] = None, bias_dtype: Optional[torch.dtype] = None,
+                              grad_x: Optional[torch.Tensor] = None, grad_w: Optional[torch.Tensor] = None,
+                              grad_bias: Optional[torch.Tensor] = None, need_x: bool = True, need_w: bool = True,
+                              grad_preact: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              error_word: Optional[torch.Tensor] = None, stream=None):
+    """(grad_x, grad_w, grad_bias) of ``ep_dense_product`` for the output's
+    gradient ``grad`` ([T, width], bf16 or fp32); what is not needed is None.
+    The bias's is computed for a ``bias_dtype`` (or a ``grad_bias`` tensor).
+    With an activation ``preact`` is what the forward pass kept;
+    ``grad_preact`` (bf16 [T, N], allocated when not given) receives its
+    gradient, rounded as the products take it.  A residual's gradient is
+    ``grad`` itself."""
+    act = _DENSE_ACTIVATIONS[activation]
+    T, H, apart, width, wide = _dense_sizes(x, w, activation)
+    bf, dev, i = torch.bfloat16, x.device, x.get_device()
+    if not isinstance(grad, torch.Tensor) or grad.dtype not in _TYPES:
+        raise TypeError("grad must be a float32 or bfloat16 tensor")
+    if not _good(grad, grad.dtype, i, (T, width)):
+        _refuse_tensors((grad, "grad", grad.dtype, dev, (T, width)))
+    if act != N.EP_ACT_NONE:
+        if preact is None:
+            raise ValueError(f"{activation} needs preact")
+        _given(preact, "preact", bf, dev, (T, wide))
+    else:
+        preact = None
+    if (act != N.EP_ACT_NONE or grad.dtype is not bf) and (need_x or need_w):
+        grad_preact = _target(grad_preact, "grad_preact", bf, dev, (T, wide), stream)
+    else:
+        grad_preact = None
+    grad_x = _target(grad_x, "grad_x", bf, dev, (T, H), stream) if need_x else None
+    grad_w = _target(grad_w, "grad_w", bf, dev, (wide, H), stream) if need_w else None
+    if grad_bias is not None:
+        bias_dtype = grad_bias.dtype
+    if bias_dtype is not None:
+        if bias_dtype not in _TYPES:
+            raise TypeError(f"the bias must be float32 or bfloat16, not {bias_dtype}")
+        grad_bias = _target(grad_bias, "grad_bias", bias_dtype, dev, (wide,), stream)
+    if error_word is not None:
+        _want(error_word, "error_word", torch.int32, dev)
+    workspace, nbytes = _scratch(
+        workspace, ep_dense_workspace_bytes(T, H, width, activation) if workspace is None else 0, dev, stream)
+    _launch(i, "ep_dense_product_backward", _dense_backward_args(
+        grad.data_ptr(), _TYPES[grad.dtype], x.data_ptr(), apart, T, H, w.data_ptr(), width, act, _address(preact),
+        _address(grad_preact), _address(grad_x), _address(grad_w), _address(grad_bias),
+        N.EP_TYPE_FP32 if bias_dtype is None else _TYPES[bias_dtype], workspace.data_ptr(), nbytes, _address(error_word)),
+        stream)
+    return grad_x, grad_w, grad_bias
 
 
 def ep_selftest_bounded_waits(device=None, stream=None) -> dict:

@@ -42,6 +42,13 @@ EP_LOGITS_FP32 = 0
 EP_LOGITS_BF16 = 1
 EP_ACT_NONE = 0
 EP_ACT_SWIGLU = 1
+EP_ACT_RELU = 2
+EP_ACT_SILU = 3
+EP_ACT_GELU = 4
+EP_ACT_GELU_TANH = 5
+EP_TYPE_FP32 = 0
+EP_TYPE_BF16 = 1
+EP_MAX_SEQUENCES = 65536
 EP_MAX_RANK = 128
 
 ABI_VERSION = 2  # EP_ABI_VERSION of the header these bindings mirror
@@ -162,6 +169,64 @@ class ep_adapter_product_args_t(C.Structure):
     ]
 
 
+class ep_balance_loss_args_t(C.Structure):
+    _fields_ = [
+        ("logits", C.c_void_p), ("logits_type", C.c_int), ("row_stride", C.c_int64),
+        ("topk_idx", C.c_void_p), ("num_tokens", C.c_int), ("num_experts", C.c_int),
+        ("num_topk", C.c_int), ("score", C.c_int), ("seq_offsets", C.c_void_p),
+        ("num_sequences", C.c_int), ("losses", C.c_void_p), ("counts", C.c_void_p),
+        ("probs", C.c_void_p), ("slopes", C.c_void_p), ("workspace", C.c_void_p),
+        ("workspace_bytes", C.c_size_t),
+    ]
+
+
+class ep_balance_loss_backward_args_t(C.Structure):
+    _fields_ = [
+        ("grad_losses", C.c_void_p), ("logits", C.c_void_p), ("logits_type", C.c_int),
+        ("row_stride", C.c_int64), ("num_tokens", C.c_int), ("num_experts", C.c_int),
+        ("score", C.c_int), ("seq_offsets", C.c_void_p), ("num_sequences", C.c_int),
+        ("slopes", C.c_void_p), ("add", C.c_void_p), ("grad_logits", C.c_void_p),
+    ]
+
+
+class ep_layer_norm_args_t(C.Structure):
+    _fields_ = [
+        ("x", C.c_void_p), ("type", C.c_int), ("row_stride", C.c_int64), ("num_rows", C.c_int),
+        ("hidden", C.c_int), ("weight", C.c_void_p), ("bias", C.c_void_p), ("param_type", C.c_int),
+        ("eps", C.c_float), ("out", C.c_void_p), ("mean", C.c_void_p), ("rstd", C.c_void_p),
+    ]
+
+
+class ep_layer_norm_backward_args_t(C.Structure):
+    _fields_ = [
+        ("grad", C.c_void_p), ("x", C.c_void_p), ("type", C.c_int), ("row_stride", C.c_int64),
+        ("num_rows", C.c_int), ("hidden", C.c_int), ("mean", C.c_void_p), ("rstd", C.c_void_p),
+        ("weight", C.c_void_p), ("param_type", C.c_int), ("add", C.c_void_p), ("grad_x", C.c_void_p),
+        ("grad_weight", C.c_void_p), ("grad_bias", C.c_void_p), ("workspace", C.c_void_p),
+        ("workspace_bytes", C.c_size_t),
+    ]
+
+
+class ep_dense_product_args_t(C.Structure):
+    _fields_ = [
+        ("x", C.c_void_p), ("row_stride", C.c_int64), ("num_rows", C.c_int), ("hidden", C.c_int),
+        ("w", C.c_void_p), ("width", C.c_int), ("bias", C.c_void_p), ("bias_type", C.c_int),
+        ("activation", C.c_int), ("residual", C.c_void_p), ("out", C.c_void_p), ("out_type", C.c_int),
+        ("preact", C.c_void_p), ("error_word", C.c_void_p),
+    ]
+
+
+class ep_dense_product_backward_args_t(C.Structure):
+    _fields_ = [
+        ("grad", C.c_void_p), ("grad_type", C.c_int), ("x", C.c_void_p), ("row_stride", C.c_int64),
+        ("num_rows", C.c_int), ("hidden", C.c_int), ("w", C.c_void_p), ("width", C.c_int),
+        ("activation", C.c_int), ("preact", C.c_void_p), ("grad_preact", C.c_void_p),
+        ("grad_x", C.c_void_p), ("grad_w", C.c_void_p), ("grad_bias", C.c_void_p),
+        ("bias_type", C.c_int), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+        ("error_word", C.c_void_p),
+    ]
+
+
 # name -> (restype, argtypes); mirrors include/ep_gb300.h
 _p, _i, _sz = C.c_void_p, C.c_int, C.c_size_t
 _LP = C.POINTER(ep_layout_t)
@@ -185,6 +250,15 @@ SIGNATURES = {
     "ep_expert_product_backward": (_i, [C.POINTER(ep_expert_product_backward_args_t), _p]),
     "ep_adapter_workspace_bytes": (_sz, [_i, _i, _i]),
     "ep_adapter_product": (_i, [C.POINTER(ep_adapter_product_args_t), _p]),
+    "ep_balance_workspace_bytes": (_sz, [_i, _i, _i]),
+    "ep_balance_loss": (_i, [C.POINTER(ep_balance_loss_args_t), _p]),
+    "ep_balance_loss_backward": (_i, [C.POINTER(ep_balance_loss_backward_args_t), _p]),
+    "ep_layer_norm": (_i, [C.POINTER(ep_layer_norm_args_t), _p]),
+    "ep_layer_norm_workspace_bytes": (_sz, [_i, _i]),
+    "ep_layer_norm_backward": (_i, [C.POINTER(ep_layer_norm_backward_args_t), _p]),
+    "ep_dense_product": (_i, [C.POINTER(ep_dense_product_args_t), _p]),
+    "ep_dense_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "ep_dense_product_backward": (_i, [C.POINTER(ep_dense_product_backward_args_t), _p]),
     "ep_selftest_bounded_waits": (_i, [_p, _p, _p, _p]),
     "ep_status_str": (C.c_char_p, [_i]),
     "ep_last_error": (C.c_char_p, []),

@@ -1,5 +1,6 @@
 // Host-side internals of the operators around the path (router, experts'
-// products, low-rank adapters): the checked arguments each launcher takes.
+// products, low-rank adapters; balance loss, layer norm, shared product): the
+// checked arguments each launcher takes.
 // Not part of the public interface.
 #pragma once
 
@@ -82,5 +83,104 @@ struct AdapterArgs {
   uint32_t *error_word;  // or null
 };
 ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream);
+
+// ---- balance loss (ep_balance.cu)
+size_t balance_workspace_bytes(int num_tokens, int num_experts, int num_sequences);
+struct BalanceArgs {
+  const void *logits;
+  bool bf16;
+  int64_t row_stride;
+  const int64_t *topk_idx;
+  int num_tokens, num_experts, num_topk;
+  bool sigmoid;
+  const int32_t *seq_offsets;  // [S + 1] or null: one sequence
+  int num_sequences;
+  float *losses;
+  int32_t *counts;
+  float *probs, *slopes;
+  void *workspace;
+};
+ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream);
+
+struct BalanceBackwardArgs {
+  const float *grad_losses;
+  const void *logits;
+  bool bf16;
+  int64_t row_stride;
+  int num_tokens, num_experts;
+  bool sigmoid;
+  const int32_t *seq_offsets;
+  int num_sequences;
+  const float *slopes;
+  const void *add;    // logits' type, rows E apart, or null
+  void *grad_logits;  // the same
+};
+ep_status_t launch_balance_backward(const BalanceBackwardArgs &a, cudaStream_t stream);
+
+// ---- layer norm (ep_norm.cu)
+struct NormArgs {
+  const void *x;
+  bool bf16;
+  int64_t row_stride;
+  int num_rows, hidden;
+  const void *weight, *bias;  // or null
+  bool param_bf16;
+  float eps;
+  void *out;
+  float *mean, *rstd;  // or null
+};
+ep_status_t launch_norm(const NormArgs &a, cudaStream_t stream);
+
+size_t norm_workspace_bytes(int num_rows, int hidden);
+struct NormBackwardArgs {
+  const void *grad, *x;
+  bool bf16;
+  int64_t row_stride;  // of x
+  int num_rows, hidden;
+  const float *mean, *rstd;
+  const void *weight;  // or null
+  bool param_bf16;
+  const void *add;                         // or null
+  void *grad_x, *grad_weight, *grad_bias;  // or null
+  float *workspace;
+};
+ep_status_t launch_norm_backward(const NormBackwardArgs &a, cudaStream_t stream);
+
+// ---- product shared by all rows (ep_dense.cu)
+struct DenseArgs {
+  const uint16_t *x;
+  int64_t row_stride;
+  int num_rows, hidden;
+  const uint16_t *w;  // [wide, hidden], wide = width, or 2 * width (EP_ACT_SWIGLU)
+  int width;
+  const void *bias;  // [wide] or null
+  bool bias_bf16;
+  ep_activation_t activation;
+  const uint16_t *residual;  // [T, width] or null
+  void *out;
+  bool out_bf16;
+  uint16_t *preact;  // [T, wide] or null
+  uint32_t *error_word;
+};
+ep_status_t launch_dense(const DenseArgs &a, cudaStream_t stream);
+
+size_t dense_workspace_bytes(int num_rows, int hidden, int width, ep_activation_t activation);
+struct DenseBackwardArgs {
+  const void *grad;
+  bool grad_bf16;
+  const uint16_t *x;
+  int64_t row_stride;
+  int num_rows, hidden;
+  const uint16_t *w;
+  int width;
+  ep_activation_t activation;
+  const uint16_t *preact;
+  uint16_t *grad_preact, *grad_x, *grad_w;  // grad_x, grad_w or null
+  void *grad_bias;                          // or null
+  bool bias_bf16;
+  void *workspace;
+  uint32_t *error_word;
+};
+ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t stream);
 
 }  // namespace ep

@@ -587,7 +587,12 @@ ep_status_t ep_route_backward(const ep_route_backward_args_t *args, ep_stream_t 
 
 typedef enum {
     EP_ACT_NONE = 0,
-    EP_ACT_SWIGLU = 1 /* silu(first half) * second half of the outputs */
+    EP_ACT_SWIGLU = 1, /* silu(first half) * second half of the outputs */
+    /* ep_dense_product only */
+    EP_ACT_RELU = 2,
+    EP_ACT_SILU = 3,
+    EP_ACT_GELU = 4,
+    EP_ACT_GELU_TANH = 5
 } ep_activation_t;
 
 /*
@@ -701,6 +706,242 @@ typedef struct {
     uint32_t *error_word;
 } ep_adapter_product_args_t;
 ep_status_t ep_adapter_product(const ep_adapter_product_args_t *args, ep_stream_t stream);
+
+/* Types of the operators of the block around the layer. */
+typedef enum {
+    EP_TYPE_FP32 = 0,
+    EP_TYPE_BF16 = 1
+} ep_type_t;
+
+#define EP_MAX_SEQUENCES 65536
+
+/* Bytes of device workspace ep_balance_loss needs (no initial contents; 0
+ * for sizes it refuses). */
+size_t ep_balance_workspace_bytes(int num_tokens, int num_experts, int num_sequences);
+
+/*
+ * The losses that keep a router balanced, and each expert's counts.  The
+ * batch is one sequence, or the sequences [seq_offsets[s], seq_offsets[s+1])
+ * of its tokens; tokens in none of them (a padded batch's end) take no part.
+ * For the tokens t of sequence s, n_s of them, S' sequences with a token, N
+ * tokens in them:
+ *   p         softmax(l), or sigmoid(l) divided by its sum over the experts
+ *   counts[s,e]  choices of e: (t, k) with topk_idx[t,k] == e; others, and
+ *             indices outside [0, E), count for nobody
+ *   probs[s,e]   the mean of p[t,e], 0 for an empty sequence
+ *   balance   1/S' sum_s E sum_e counts[s,e] / C_s * probs[s,e], C_s the
+ *             choices of s: 1 when experts or scores are balanced
+ *   z         1/N sum_t log(sum_e exp(l[t,e]))^2
+ *   losses    balance, z
+ *   slopes[s,e]  E counts[s,e] / (S' C_s n_s): the derivative of the balance
+ *             loss for each p[t,e] of s, which the backward pass needs
+ * Logits of -infinity or NaN are experts not offered (p = 0), +infinity
+ * counts as the largest finite number, as for ep_route; a token without
+ * offered experts adds 0.  Sums in fp32, those over tokens in a fixed order:
+ * the same inputs give the same bits.
+ *   logits as for ep_route; topk_idx [T*K] int64
+ *   seq_offsets [S+1] int32 ascending in [0, T], or NULL (S = 1); where they
+ *             are not, the losses are NaN and the rest is unspecified
+ *   losses [2] fp32, counts [S*E] int32, probs and slopes [S*E] fp32: written
+ *   workspace >= ep_balance_workspace_bytes(T, E, S) bytes, 16-byte aligned;
+ *             calls sharing one must be ordered
+ * 1 <= S <= EP_MAX_SEQUENCES, T, E and K as for ep_route.
+ */
+typedef struct {
+    const void *logits;
+    ep_logits_t logits_type;
+    int64_t row_stride;
+    const int64_t *topk_idx;
+    int num_tokens;
+    int num_experts;
+    int num_topk;
+    ep_score_t score;
+    const int32_t *seq_offsets;
+    int num_sequences;
+    float *losses;
+    int32_t *counts;
+    float *probs;
+    float *slopes;
+    void *workspace;
+    size_t workspace_bytes;
+} ep_balance_loss_args_t;
+ep_status_t ep_balance_loss(const ep_balance_loss_args_t *args, ep_stream_t stream);
+
+/*
+ * The gradient of grad_losses[0] * balance + grad_losses[1] * z for the
+ * logits, the choice held fixed, plus `add` (the gradient that ep_route_backward
+ * gave, for one) when given.  Logits that are not offered and tokens outside
+ * every sequence receive 0 (plus `add`).
+ *   grad_losses [2] fp32; slopes as ep_balance_loss gave them; logits,
+ *   seq_offsets and sizes as there
+ *   add, grad_logits [T*E] in the logits' type, rows E apart; they may be the
+ *   same memory
+ */
+typedef struct {
+    const float *grad_losses;
+    const void *logits;
+    ep_logits_t logits_type;
+    int64_t row_stride;
+    int num_tokens;
+    int num_experts;
+    ep_score_t score;
+    const int32_t *seq_offsets;
+    int num_sequences;
+    const float *slopes;
+    const void *add;
+    void *grad_logits;
+} ep_balance_loss_backward_args_t;
+ep_status_t ep_balance_loss_backward(const ep_balance_loss_backward_args_t *args, ep_stream_t stream);
+
+/*
+ * Layer norm of rows:
+ *   mean[t] = sum_h x[t,h] / H,  rstd[t] = 1 / sqrt(sum_h (x[t,h] - mean)^2 / H + eps)
+ *   out[t,h] = (x[t,h] - mean) * rstd * weight[h] + bias[h]
+ * in fp32, rounded once.
+ *   x      [T] rows of H, row_stride >= H elements apart, of `type`
+ *   weight, bias [H] of `param_type`, or NULL (1 and 0)
+ *   out    [T*H] of `type`; may be x when its rows are H apart
+ *   mean, rstd [T] fp32 or NULL (not kept): what the backward pass needs
+ * T >= 0, 1 <= H <= EP_MAX_HIDDEN, eps > 0.  Arrays are aligned to their
+ * elements; with 16-byte aligned rows (H and row_stride of whole 16 bytes)
+ * they are read and written 16 bytes at a time.
+ */
+typedef struct {
+    const void *x;
+    ep_type_t type;
+    int64_t row_stride;
+    int num_rows;
+    int hidden;
+    const void *weight;
+    const void *bias;
+    ep_type_t param_type;
+    float eps;
+    void *out;
+    float *mean;
+    float *rstd;
+} ep_layer_norm_args_t;
+ep_status_t ep_layer_norm(const ep_layer_norm_args_t *args, ep_stream_t stream);
+
+/* Bytes of device workspace ep_layer_norm_backward needs for the gradients
+ * of weight and bias (no initial contents; 0 for sizes it refuses). */
+size_t ep_layer_norm_workspace_bytes(int num_rows, int hidden);
+
+/*
+ * The gradients of ep_layer_norm, with n = (x - mean) * rstd and g = grad:
+ *   grad_x[t] = rstd (g w - mean_h(g w) - n mean_h(g w n)) + add[t]
+ *   grad_weight[h] = sum_t g n,   grad_bias[h] = sum_t g
+ * in fp32, the sums over rows in a fixed order, each rounded once.
+ *   grad, grad_x [T*H] of `type`, add [T*H] of `type` or NULL (the gradient
+ *   of a residual around the norm); grad_x may be grad or add
+ *   x, row_stride, weight as for ep_layer_norm; mean, rstd [T] fp32
+ *   grad_x NULL: not computed; grad_weight, grad_bias [H] of `param_type`,
+ *   NULL: not computed.  Without rows they are 0.
+ *   workspace >= ep_layer_norm_workspace_bytes(T, H) bytes, 16-byte aligned,
+ *   when grad_weight or grad_bias is given; calls sharing one must be ordered
+ */
+typedef struct {
+    const void *grad;
+    const void *x;
+    ep_type_t type;
+    int64_t row_stride;
+    int num_rows;
+    int hidden;
+    const float *mean;
+    const float *rstd;
+    const void *weight;
+    ep_type_t param_type;
+    const void *add;
+    void *grad_x;
+    void *grad_weight;
+    void *grad_bias;
+    void *workspace;
+    size_t workspace_bytes;
+} ep_layer_norm_backward_args_t;
+ep_status_t ep_layer_norm_backward(const ep_layer_norm_backward_args_t *args, ep_stream_t stream);
+
+/*
+ * A product shared by all rows, with its epilogue:
+ *   z[t] = x[t] w^T + bias                    fp32
+ *   out[t] = act(z[t]) + residual[t]          rounded once
+ * with act one of EP_ACT_NONE, EP_ACT_RELU (max(z, 0)), EP_ACT_SILU
+ * (z / (1 + exp(-z))), EP_ACT_GELU (z (1 + erf(z / sqrt 2)) / 2),
+ * EP_ACT_GELU_TANH (z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2) and
+ * EP_ACT_SWIGLU (silu of the first half of z times the second).
+ *   x        [T] rows of `hidden`, row_stride >= hidden elements apart (a
+ *            multiple of 8), bf16
+ *   w        [wide * hidden] bf16, wide = width, or 2 * width with
+ *            EP_ACT_SWIGLU
+ *   bias     [wide] of bias_type, or NULL
+ *   residual [T * width] bf16, or NULL; may be out when that is bf16
+ *   out      [T * width] of out_type (EP_TYPE_FP32: a gate's logits)
+ *   preact   [T * wide] bf16 or NULL: bf16(z), what the backward pass of an
+ *            activation needs
+ *   error_word [1] or NULL: EP_ERRBIT_TIMEOUT
+ * hidden and width are multiples of 8 in [8, EP_MAX_HIDDEN]; x, w, residual,
+ * out and preact are 16-byte aligned, bias to its elements.
+ */
+typedef struct {
+    const void *x;
+    int64_t row_stride;
+    int num_rows;
+    int hidden;
+    const void *w;
+    int width;
+    const void *bias;
+    ep_type_t bias_type;
+    ep_activation_t activation;
+    const void *residual;
+    void *out;
+    ep_type_t out_type;
+    void *preact;
+    uint32_t *error_word;
+} ep_dense_product_args_t;
+ep_status_t ep_dense_product(const ep_dense_product_args_t *args, ep_stream_t stream);
+
+/* Bytes of device workspace ep_dense_product_backward needs (no initial
+ * contents; 0 for sizes it refuses). */
+size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activation_t activation);
+
+/*
+ * The gradients of ep_dense_product.  With d the gradient of z, act'(z) grad
+ * (z as kept in preact; at 0 EP_ACT_RELU has the derivative 0):
+ *   grad_x[t] = bf16(d[t] w),  grad_w = bf16(sum_t d[t]^T x[t]),
+ *   grad_bias = sum_t d[t]     (fp32 sums of d before it is rounded)
+ * The two products take d in bf16: `grad` itself for EP_ACT_NONE with a bf16
+ * gradient, else rounded into grad_preact.  A residual's gradient is `grad`.
+ *   grad   [T * width] of grad_type (the type of `out`)
+ *   preact [T * wide] bf16 (not with EP_ACT_NONE)
+ *   grad_preact [T * wide] bf16: written, then read (not with EP_ACT_NONE and
+ *          a bf16 gradient)
+ *   grad_x [T * hidden], grad_w [wide * hidden] bf16, grad_bias [wide] of
+ *          bias_type: NULL: not computed.  grad_w and grad_bias are 0
+ *          without rows.
+ *   workspace >= ep_dense_workspace_bytes(...) bytes, 16-byte aligned; calls
+ *          sharing one must be ordered
+ * The rest as for ep_dense_product.  The sums run in a fixed order: the same
+ * inputs give the same bits.
+ */
+typedef struct {
+    const void *grad;
+    ep_type_t grad_type;
+    const void *x;
+    int64_t row_stride;
+    int num_rows;
+    int hidden;
+    const void *w;
+    int width;
+    ep_activation_t activation;
+    const void *preact;
+    void *grad_preact;
+    void *grad_x;
+    void *grad_w;
+    void *grad_bias;
+    ep_type_t bias_type;
+    void *workspace;
+    size_t workspace_bytes;
+    uint32_t *error_word;
+} ep_dense_product_backward_args_t;
+ep_status_t ep_dense_product_backward(const ep_dense_product_backward_args_t *args, ep_stream_t stream);
 
 /*
  * Self-test of the bounded device waits (the pages have no counterpart: the
