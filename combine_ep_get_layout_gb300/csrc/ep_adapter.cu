@@ -519,7 +519,7 @@ ep_status_t launch_adapter(const AdapterArgs &a, cudaStream_t stream) {
   const uint32_t wb[] = {kInner, 128, 1};
   s = encode_map(&p.a, a.w, 3, wd, ws_, wb);
   if (s != EP_OK) return s;
-  s = row_maps(p, a.x, a.hidden, a.num_rows);
+  s = row_maps(p, a.x, a.hidden, a.num_rows, a.hidden);
   if (s != EP_OK) return s;
   return launch_form<kAdapter>(p, (int64_t)tiles * p.a_tiles, stream);
 }

@@ -6,21 +6,16 @@
 //
 // bf16 operands, sums in fp32, results rounded once.  d is an operand of two
 // products and kept in bf16; the bias's gradient is summed before that.
-#include "ep_device.cuh"
-#include "ep_ops.h"
+#include "ep_pair.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kTile = 32;
 constexpr int kMaxSlices = 64;  // of the rows, for the bias's gradient
 
 __device__ __forceinline__ float value_of(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ __forceinline__ uint16_t rounded(float v) { return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu); }
-__device__ __forceinline__ float load_value(const void *p, bool bf16, int64_t i) {
-  return bf16 ? value_of(static_cast<const uint16_t *>(p)[i]) : static_cast<const float *>(p)[i];
-}
 __device__ __forceinline__ void store_value(void *p, bool bf16, int64_t i, float v) {
   if (bf16)
     static_cast<uint16_t *>(p)[i] = rounded(v);
@@ -28,91 +23,24 @@ __device__ __forceinline__ void store_value(void *p, bool bf16, int64_t i, float
     static_cast<float *>(p)[i] = v;
 }
 
-constexpr float kRootHalf = 0.70710678118654752f;      // 1 / sqrt 2
-constexpr float kRootTwoPi = 0.79788456080286536f;     // sqrt(2 / pi)
-constexpr float kRootOneTwoPi = 0.39894228040143268f;  // 1 / sqrt(2 pi)
-constexpr float kCubic = 0.044715f;
-
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
-
-__device__ __forceinline__ float activate(ep_activation_t act, float z) {
-  switch (act) {
-    case EP_ACT_RELU:
-      return z < 0.0f ? 0.0f : z;
-    case EP_ACT_SILU:
-      return z * sigmoid(z);
-    case EP_ACT_GELU:
-      return 0.5f * z * erfcf(-z * kRootHalf);
-    case EP_ACT_GELU_TANH:
-      return z * sigmoid(2.0f * kRootTwoPi * (z + kCubic * z * z * z));
-    default:
-      return z;
-  }
-}
-
-__device__ __forceinline__ float slope(ep_activation_t act, float z) {
+// act'(z)
+__device__ __forceinline__ float slope_of(ep_activation_t act, float z) {
   float s;
   switch (act) {
     case EP_ACT_RELU:
       return z > 0.0f ? 1.0f : 0.0f;
     case EP_ACT_SILU:
-      s = sigmoid(z);
+      s = sigmoid_of(z);
       return s * (1.0f + z * (1.0f - s));
     case EP_ACT_GELU:
       return 0.5f * erfcf(-z * kRootHalf) + z * kRootOneTwoPi * __expf(-0.5f * z * z);
     case EP_ACT_GELU_TANH:
-      s = sigmoid(2.0f * kRootTwoPi * (z + kCubic * z * z * z));
+      s = tanh_gate(z);
       z = fminf(fmaxf(z, -16.0f), 16.0f);  // s (1 - s) is 0 there; z^2 stays finite
       return s + z * s * (1.0f - s) * 2.0f * kRootTwoPi * (1.0f + 3.0f * kCubic * z * z);
     default:
       return 1.0f;
   }
-}
-
-// sum over k of a(row, k) b(col, k), each matrix by its two strides.
-struct Operand {
-  const uint16_t *p;
-  int64_t outer, inner;
-  int count;
-};
-
-__device__ float tile_sum(const Operand &a, const Operand &b, int row0, int col0, int K) {
-  __shared__ float s_a[kTile][kTile + 1], s_b[kTile][kTile + 1];
-  const int x = threadIdx.x, y = threadIdx.y;
-  float sum = 0.0f;
-  for (int k0 = 0; k0 < K; k0 += kTile) {
-    s_a[y][x] = row0 + y < a.count && k0 + x < K ? value_of(a.p[(row0 + y) * a.outer + (k0 + x) * a.inner]) : 0.0f;
-    s_b[y][x] = col0 + y < b.count && k0 + x < K ? value_of(b.p[(col0 + y) * b.outer + (k0 + x) * b.inner]) : 0.0f;
-    __syncthreads();
-    for (int k = 0; k < kTile; ++k) sum += s_a[y][k] * s_b[x][k];
-    __syncthreads();
-  }
-  return sum;
-}
-
-__global__ void __launch_bounds__(kTile *kTile) dense_kernel(DenseArgs p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const bool gated = p.activation == EP_ACT_SWIGLU;
-  const int tiles = (p.width - 1) / kTile + 1;
-  const int row0 = blockIdx.x / tiles * kTile, col0 = blockIdx.x % tiles * kTile;
-  const Operand x{p.x, p.row_stride, 1, p.num_rows}, w{p.w, p.hidden, 1, p.width};
-  const int64_t t = row0 + threadIdx.y;
-  const int n = col0 + threadIdx.x;
-  float z = tile_sum(x, w, row0, col0, p.hidden), u = 0.0f;
-  if (gated) {
-    const Operand other{p.w + (int64_t)p.width * p.hidden, p.hidden, 1, p.width};
-    u = tile_sum(x, other, row0, col0, p.hidden);
-  }
-  if (t >= p.num_rows || n >= p.width) return;
-  const int64_t wide = gated ? 2 * p.width : p.width;
-  if (p.bias != nullptr) z += load_value(p.bias, p.bias_bf16, n);
-  if (p.bias != nullptr && gated) u += load_value(p.bias, p.bias_bf16, p.width + n);
-  if (p.preact != nullptr) p.preact[t * wide + n] = rounded(z);
-  if (p.preact != nullptr && gated) p.preact[t * wide + p.width + n] = rounded(u);
-  float y = gated ? z * sigmoid(z) * u : activate(p.activation, z);
-  if (p.residual != nullptr) y += value_of(p.residual[t * p.width + n]);
-  store_value(p.out, p.out_bf16, t * p.width + n, y);
 }
 
 // d, rounded, and a slice of the rows' part of the bias's gradient; a column
@@ -126,15 +54,15 @@ __global__ void __launch_bounds__(256) dense_gradient_kernel(DenseBackwardArgs p
   if (n >= p.width) return;
   float sum = 0.0f, other = 0.0f;
   for (int64_t t = slice; t < p.num_rows; t += slices) {
-    float d = load_value(p.grad, p.grad_bf16, t * p.width + n);
+    float d = load_param(p.grad, p.grad_bf16, t * p.width + n);
     if (gated) {
-      const float g = value_of(p.preact[t * wide + n]), u = value_of(p.preact[t * wide + p.width + n]), s = sigmoid(g);
+      const float g = value_of(p.preact[t * wide + n]), u = value_of(p.preact[t * wide + p.width + n]), s = sigmoid_of(g);
       const float du = d * g * s;
       d *= u * s * (1.0f + g * (1.0f - s));
       other += du;
       if (p.grad_preact != nullptr) p.grad_preact[t * wide + p.width + n] = rounded(du);
     } else if (p.activation != EP_ACT_NONE) {
-      d *= slope(p.activation, value_of(p.preact[t * wide + n]));
+      d *= slope_of(p.activation, value_of(p.preact[t * wide + n]));
     }
     if (p.grad_preact != nullptr) p.grad_preact[t * wide + n] = rounded(d);
     sum += d;
@@ -154,37 +82,39 @@ __global__ void __launch_bounds__(256) dense_bias_kernel(const float *sums, int 
   store_value(out, bf16, n, sum);
 }
 
-__global__ void __launch_bounds__(kTile *kTile) dense_product_kernel(Operand a, Operand b, int K, uint16_t *out) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tiles = (b.count - 1) / kTile + 1;
-  const int row0 = blockIdx.x / tiles * kTile, col0 = blockIdx.x % tiles * kTile;
-  const float v = tile_sum(a, b, row0, col0, K);
-  const int64_t row = row0 + threadIdx.y;
-  const int col = col0 + threadIdx.x;
-  if (row < a.count && col < b.count) out[row * b.count + col] = rounded(v);
-}
-
 int slices_of(int rows) { return rows < kMaxSlices ? rows : kMaxSlices; }
 
-cudaError_t launch_tiles(const Operand &a, const Operand &b, int K, uint16_t *out, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(((a.count - 1) / kTile + 1) * ((b.count - 1) / kTile + 1));
-  cfg.blockDim = dim3(kTile, kTile);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, dense_product_kernel, a, b, K, out);
+// What the products of a call share: one expert with every row.
+Params params_of(int rows, int wide, int width, int hidden, uint32_t *error_word) {
+  Params p = {};
+  p.most_rows = p.cap = rows;
+  p.error_word = error_word;
+  p.E = 1;
+  p.wide = wide;
+  p.width = width;
+  p.hidden = hidden;
+  return p;
 }
 
 }  // namespace
 
 ep_status_t launch_dense(const DenseArgs &a, cudaStream_t stream) {
   if (a.num_rows == 0) return EP_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(((a.num_rows - 1) / kTile + 1) * ((a.width - 1) / kTile + 1));
-  cfg.blockDim = dim3(kTile, kTile);
-  cfg.stream = stream;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, dense_kernel, a);
-  return e == cudaSuccess ? EP_OK : cuda_fail(e, "dense launch");
+  const bool pairs = a.activation == EP_ACT_SWIGLU;
+  Params p = params_of(a.num_rows, pairs ? 2 * a.width : a.width, a.width, a.hidden, a.error_word);
+  p.inner = a.hidden;
+  p.a_tiles = up(a.width, pairs ? 128 : 256);
+  p.out = static_cast<uint16_t *>(a.out);
+  p.preact = a.preact;
+  p.bias = a.bias;
+  p.bias_bf16 = a.bias_bf16;
+  p.residual = a.residual;
+  p.activation = a.activation;
+  p.out_fp32 = !a.out_bf16;
+  const ep_status_t s = weight_map(p, pairs ? kDenseGated : kDense, a.w, p.wide, a.hidden);
+  if (s != EP_OK) return s;
+  return pairs ? launch_rows_form<kDenseGated>(p, a.x, a.row_stride, stream)
+               : launch_rows_form<kDense>(p, a.x, a.row_stride, stream);
 }
 
 size_t dense_workspace_bytes(int num_rows, int hidden, int width, ep_activation_t activation) {
@@ -201,12 +131,37 @@ ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t strea
   if (e == cudaSuccess && a.grad_bias != nullptr)
     e = launch_kernel(dense_bias_kernel, (wide - 1) / 256 + 1, 256, 0, stream, false, (const float *)sums, slices, wide,
                       a.grad_bias, a.bias_bf16);
+  if (e != cudaSuccess) return cuda_fail(e, "dense_backward launch");
   const uint16_t *d = made ? a.grad_preact : static_cast<const uint16_t *>(a.grad);
-  if (e == cudaSuccess && a.grad_x != nullptr && a.num_rows > 0)
-    e = launch_tiles(Operand{d, wide, 1, a.num_rows}, Operand{a.w, 1, a.hidden, a.hidden}, wide, a.grad_x, stream);
-  if (e == cudaSuccess && a.grad_w != nullptr)
-    e = launch_tiles(Operand{d, 1, wide, wide}, Operand{a.x, 1, a.row_stride, a.hidden}, a.num_rows, a.grad_w, stream);
-  return e == cudaSuccess ? EP_OK : cuda_fail(e, "dense_backward launch");
+  if (a.grad_x != nullptr && a.num_rows > 0) {
+    Params p = params_of(a.num_rows, wide, a.hidden, a.hidden, a.error_word);
+    p.inner = wide;
+    p.a_tiles = up(a.hidden, 256);
+    p.out = a.grad_x;
+    ep_status_t s = weight_map(p, kDenseGradX, a.w, wide, a.hidden);
+    if (s == EP_OK) s = launch_rows_form<kDenseGradX>(p, d, wide, stream);
+    if (s != EP_OK) return s;
+  }
+  if (a.grad_w != nullptr) {
+    Params p = params_of(a.num_rows, wide, a.width, a.hidden, a.error_word);
+    p.parts = 1;
+    p.max_cols = kMaxCols;
+    p.a_tiles = up(wide, 256);
+    p.b_tiles = up(a.hidden, 256);
+    p.out = a.grad_w;
+    // without rows nothing is copied: the maps only need an address
+    const bool any = a.num_rows > 0;
+    const int rows = any ? a.num_rows : 1;
+    ep_status_t s = block_map(&p.a, &p.a_blocks, any ? d : a.grad_w, wide, rows, wide);
+    const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)wide, 1};
+    const uint64_t strides[] = {a.hidden * kSize, (uint64_t)wide * a.hidden * kSize};
+    const uint32_t box[] = {64, 32, 1};
+    if (s == EP_OK) s = encode_map(&p.grad, a.grad_w, 3, dims, strides, box);
+    if (s == EP_OK) s = block_map(&p.b[0], &p.b_blocks, any ? a.x : a.grad_w, a.hidden, rows, any ? a.row_stride : a.hidden);
+    if (s == EP_OK) s = launch_form<kDenseGradW>(p, (int64_t)p.a_tiles * p.b_tiles, stream);
+    if (s != EP_OK) return s;
+  }
+  return EP_OK;
 }
 
 }  // namespace ep

@@ -1,6 +1,7 @@
 // Products of ragged groups of rows on the tensor cores, for pairs of CTAs:
-// the kernel behind the experts' products, their gradients and the adapters'
-// projection (each includes the forms it launches).
+// the kernel behind the experts' products, their gradients, the adapters'
+// projection and the product shared by all rows (each includes the forms it
+// launches).
 //
 // A pair of CTAs computes a tile of 256 x up to 256: A, the operand with 256
 // rows, is the weights (so the ragged number of an expert's rows meets the
@@ -12,6 +13,9 @@
 //                    up-projections of the adapters that the tile's rows name,
 //                    side by side, B = the rows' low-rank factors in their
 //                    adapter's columns, zero in the others
+//   kDense, kDenseGated, kDenseGradX, kDenseGradW
+//                    the first four with one expert that has every row, and
+//                    the first two with bias, activation and residual
 // An inner step is 64 elements, a 128-byte row of shared memory in the
 // 128-byte swizzle; the transposed operands are read with their outer
 // dimension contiguous, so nothing is ever transposed in memory.
@@ -42,7 +46,12 @@ namespace ep {
 
 namespace {
 
-enum Form { kPlain, kGated, kGradX, kGradW, kAdapter };
+enum Form { kPlain, kGated, kGradX, kGradW, kAdapter, kDense, kDenseGated, kDenseGradX, kDenseGradW };
+__host__ __device__ constexpr bool gated(Form f) { return f == kGated || f == kDenseGated; }
+__host__ __device__ constexpr bool grad_x(Form f) { return f == kGradX || f == kDenseGradX; }
+__host__ __device__ constexpr bool grad_w(Form f) { return f == kGradW || f == kDenseGradW; }
+__host__ __device__ constexpr bool dense(Form f) { return f == kDense || f == kDenseGated; }  // with the epilogue
+__host__ __device__ constexpr bool single(Form f) { return f >= kAdapter; }  // one expert, its rows known to the host
 
 // Warps: 0 and 3 copies of A and B, 1 products, 2 row ends (kGradW), 4-11
 // results; kAdapter: 12-15 gather the adapters.
@@ -60,7 +69,7 @@ constexpr int kPlanWords = 1 + 2 * kMaxCols;
 constexpr int kPitch = 80;                       // bytes of a staged row: 64 and 16 against bank conflicts
 constexpr int kStagedRows = 16;                  // of a result warp at a time
 constexpr int kExchangeBytes = 8 * 32 * 4;       // kGated: 8 columns of a warp, fp32
-__host__ __device__ constexpr int staging_of(Form f) { return f == kGradW ? 32 * 128 : kStagedRows * kPitch; }
+__host__ __device__ constexpr int staging_of(Form f) { return grad_w(f) ? 32 * 128 : kStagedRows * kPitch; }
 constexpr int kResultWarps = 8;
 constexpr int kMaxParts = 4;         // pairs of a cluster, which share the inner dimension of one tile
 
@@ -92,6 +101,11 @@ struct Params {
   const int32_t *plan;   // kPlanWords a tile of rows
   const uint16_t *low;   // [rows][rank], scaled
   int rank;
+  // kDense, kDenseGated
+  const void *bias;          // [wide] or null
+  const uint16_t *residual;  // [rows][width] or null
+  int activation;
+  bool bias_bf16, out_fp32;
 };
 
 struct Barriers {
@@ -128,9 +142,9 @@ struct Walker {
 
   // The most columns that a tile has (the whole warp calls it).
   __device__ static int most_cols(const Params &p) {
-    if (F == kGradW) return kMaxCols;
+    if (grad_w(F)) return kMaxCols;
     // with so few rows the counts need not be read
-    if (F == kAdapter || p.most_rows <= 64) return most_cols_of(limits(p));
+    if (single(F) || p.most_rows <= 64) return most_cols_of(limits(p));
     const int n = widest_tile(limits(p), p.offset, p.rows, p.E, threadIdx.x & 31, 32);
     return max(kColumnStep, __reduce_max_sync(0xffffffffu, n));
   }
@@ -141,15 +155,15 @@ struct Walker {
     chunk = c;
     const int e = c * 32 + lane;
     rows = first = mine = 0;
-    if (F == kAdapter) {
+    if (single(F)) {
       rows = e == 0 ? p.cap : 0;
-      mine = p.a_tiles * tiles_of(limits(p), rows);
+      if (e == 0) mine = grad_w(F) ? p.a_tiles * p.b_tiles : p.a_tiles * tiles_of(limits(p), rows);
     } else if (e < p.E) {
       first = p.offset[e];
       const int n = p.rows[e];
       rows = rows_within(limits(p), first, n);
       if (rows != n && blockIdx.x == 0 && threadIdx.x < 32) set_error(p.error_word, EP_ERRBIT_CAPACITY);
-      mine = F == kGradW ? p.a_tiles * p.b_tiles : p.a_tiles * tiles_of(limits(p), rows);
+      mine = grad_w(F) ? p.a_tiles * p.b_tiles : p.a_tiles * tiles_of(limits(p), rows);
     }
     prefix = mine;
 #pragma unroll
@@ -176,7 +190,7 @@ struct Walker {
     const int n = __shfl_sync(0xffffffffu, rows, src);
     t.e = chunk * 32 + src;
     t.first = __shfl_sync(0xffffffffu, first, src);
-    if (F == kGradW) {
+    if (grad_w(F)) {
       t.a0 = at / p.b_tiles * 256;
       t.b0 = at % p.b_tiles * 256;
       t.count = n;
@@ -184,15 +198,15 @@ struct Walker {
       t.steps = ceil_div(n, kInner);
     } else {
       const int tiles = tiles_of(limits(p), n);
-      if (F == kAdapter) {
+      if (single(F)) {
         // eight tiles of rows go along A together, so the pairs running at
         // once share rows as well as weights
         const int band = at / (8 * p.a_tiles), in = at - band * 8 * p.a_tiles, high = min(8, tiles - band * 8);
         t.part = band * 8 + in % high;
-        t.a0 = in / high * 256;
+        t.a0 = in / high * (gated(F) ? 128 : 256);
       } else {
         t.part = at % tiles;
-        t.a0 = at / tiles * (F == kGated ? 128 : 256);
+        t.a0 = at / tiles * (gated(F) ? 128 : 256);
       }
       t.b0 = 0;
       int from;
@@ -303,6 +317,93 @@ __device__ __forceinline__ void add_odd(const Params &p, const Tile &t, int c, i
   }
 }
 
+// ------------------------------------------------ the epilogue of kDense
+
+constexpr float kRootHalf = 0.70710678118654752f;      // 1 / sqrt 2
+constexpr float kRootTwoPi = 0.79788456080286536f;     // sqrt(2 / pi)
+constexpr float kRootOneTwoPi = 0.39894228040143268f;  // 1 / sqrt(2 pi)
+constexpr float kCubic = 0.044715f;
+
+__device__ __forceinline__ float load_param(const void *p, bool bf16, int64_t i) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16) : static_cast<const float *>(p)[i];
+}
+
+__device__ __forceinline__ float sigmoid_of(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+// tanh(u) = 2 sigmoid(2 u) - 1
+__device__ __forceinline__ float tanh_gate(float z) { return sigmoid_of(2.0f * kRootTwoPi * (z + kCubic * z * z * z)); }
+
+__device__ __forceinline__ void activate(int act, float (&v)[32]) {
+  if (act == EP_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+  } else if (act == EP_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = silu_of(v[j]);
+  } else if (act == EP_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.5f * v[j] * erfcf(-v[j] * kRootHalf);
+  } else if (act == EP_ACT_GELU_TANH) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= tanh_gate(v[j]);
+  }
+}
+
+// The residual of COUNT rows of 32 outputs from `at` on, 16 bytes a lane and
+// row: four lanes a row.
+template <int COUNT>
+__device__ __forceinline__ void load_residual(int4 (&r)[4], const Params &p, int64_t row, int rows, int at, int lane) {
+  const int n = at + (lane & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < COUNT / 8; ++i) {
+    const int c = (lane >> 2) + i * 8;
+    if (c < rows && n < p.width) r[i] = *reinterpret_cast<const int4 *>(p.residual + (row + c) * p.width + n);
+  }
+}
+
+// ... added to a row's value a lane and output, through the staging buffer.
+template <int COUNT>
+__device__ __forceinline__ void add_residual(float *v, const int4 (&r)[4], char *stage, int lane) {
+#pragma unroll
+  for (int h = 0; h < COUNT / 16; ++h) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<int4 *>(stage + ((lane >> 2) + i * 8) * kPitch + (lane & 3) * 16) = r[2 * h + i];
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      v[h * 16 + c] += __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t *>(stage + c * kPitch + lane * 2) << 16);
+    __syncwarp();
+  }
+}
+
+template <int COUNT>
+__device__ __forceinline__ void store_out(const float *v, char *stage, const Params &p, int64_t row, int rows, int at,
+                                          int lane) {
+  if (!p.out_fp32) {
+    store_transposed<COUNT>(v, stage, p.out + row * p.width, p.width, rows, at, p.width, lane);
+    return;
+  }
+  float *out = reinterpret_cast<float *>(p.out) + row * p.width;
+  constexpr int kRows = 8, kWide = 144;  // of 128 bytes; 16 against bank conflicts
+  static_assert(kRows * kWide <= kStagedRows * kPitch, "");
+  const int n = at + (lane & 7) * 4;
+#pragma unroll
+  for (int r = 0; r < COUNT; r += kRows) {
+    if (r >= rows) return;
+#pragma unroll
+    for (int c = 0; c < kRows; ++c) *reinterpret_cast<float *>(stage + c * kWide + lane * 4) = v[r + c];
+    __syncwarp();
+#pragma unroll
+    for (int c = lane >> 3; c < kRows; c += 4) {
+      if (r + c < rows && n < p.width)
+        *reinterpret_cast<float4 *>(out + (int64_t)(r + c) * p.width + n) =
+            *reinterpret_cast<const float4 *>(stage + c * kWide + (lane & 7) * 16);
+    }
+    __syncwarp();
+  }
+}
+
 template <Form F>
 __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_constant__ Params p) {
   extern __shared__ char s_raw[];
@@ -311,7 +412,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
   char *staging = ring + p.ring_bytes / 1024 * 1024;
   char *exchange = staging + kResultWarps * staging_of(F);
   // [parts - 1][columns / 4][128][4]: the other pairs' results
-  float4 *joined = reinterpret_cast<float4 *>(exchange + (F == kGated ? kResultWarps * kExchangeBytes : 0));
+  float4 *joined = reinterpret_cast<float4 *>(exchange + (gated(F) ? kResultWarps * kExchangeBytes : 0));
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // A cluster is one pair, or the pairs that share a tile (`part`: which of them).
   const uint32_t rank = cluster_rank() & 1u, lead = cluster_rank() & ~1u, both = 3u << lead;
@@ -381,8 +482,8 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       const int b_rows = t.cols / 2;
       const uint32_t bytes = kABytes + b_rows * 128;
-      const int a0 = t.a0 + (int)rank * (F == kGated ? 64 : 128);
-      const int b0 = (F == kGradW ? t.b0 : t.first) + (int)rank * b_rows;
+      const int a0 = t.a0 + (int)rank * (gated(F) ? 64 : 128);
+      const int b0 = (grad_w(F) ? t.b0 : t.first) + (int)rank * b_rows;
       const int k1 = last_step(t);
       for (int k = first_step(t); k < k1; ++k) {
         if (!__all_sync(0xffffffffu, mbar_wait_pair(&s_bar.empty[stage], phase ^ 1))) {
@@ -393,7 +494,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           const uint32_t a = smem_addr(ring + (size_t)stage * stage_bytes), b = a + kABytes;
           // both CTAs' copies complete on the leading CTA's barrier, but those
           // of a last step whose rows end raggedly go by the row ends
-          const bool last = F == kGradW && t.count % 16 != 0 && k == t.steps - 1;
+          const bool last = grad_w(F) && t.count % 16 != 0 && k == t.steps - 1;
           const uint32_t bar = last ? map_shared(smem_addr(&s_bar.ends[stage]), lead | rank)
                                     : map_shared(smem_addr(&s_bar.full[stage]), lead);
           if (is_a) {
@@ -407,11 +508,11 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           }
           const int at = k * kInner;
           if (is_a) {
-            if (F == kPlain || F == kAdapter) {
+            if (F == kPlain || F == kAdapter || F == kDense) {
               tile_load_3d(a, &p.a, at, a0, t.e, bar);
-            } else if (F == kGated) {
+            } else if (gated(F)) {
               tile_load_4d(a, &p.a, at, a0, 0, t.e, bar);
-            } else if (F == kGradX) {
+            } else if (grad_x(F)) {
               if (p.a_blocks) {
                 tile_load_4d(a, &p.a, 0, at, a0 / 64, t.e, bar);
               } else {
@@ -424,7 +525,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
               tile_load_2d(a, &p.a, a0, t.first + at, bar);
               tile_load_2d(a + 8192, &p.a, a0 + 64, t.first + at, bar);
             }
-          } else if (F != kGradW) {
+          } else if (!grad_w(F)) {
             tile_load_2d(b, &p.b[b_rows / 16 - 1], at, b0, bar);
           } else if (p.b_blocks) {
             tile_load_3d(b, &p.b[0], 0, t.first + at, b0 / 64, bar);
@@ -459,28 +560,28 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     const uint32_t ring_addr = smem_addr(ring);
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       if (t.steps == 0) continue;  // an expert without rows (kGradW): zeros are written
-      const uint32_t idesc = mma_desc(t.cols, F == kGradX || F == kGradW, F == kGradW);
+      const uint32_t idesc = mma_desc(t.cols, grad_x(F) || grad_w(F), grad_w(F));
       const uint32_t d = tmem + acc * kMaxCols;
       ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1));
       tc_fence_after();
       const int k0 = first_step(t), k1 = last_step(t);
       for (int k = k0; ok && k < k1; ++k) {
         ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
-        if (F == kGradW && ok && k == t.steps - 1 && t.count % 16 != 0) {
+        if (grad_w(F) && ok && k == t.steps - 1 && t.count % 16 != 0) {
           ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.fixed[stage], (trims >> stage) & 1u));
           trims ^= 1u << stage;
         }
         if (!ok) break;
         tc_fence_after();
         const uint32_t addr = ring_addr + (uint32_t)(stage * stage_bytes);
-        const uint32_t a = F == kGradX || F == kGradW ? outer_desc(addr, 8192) : inner_desc(addr);
-        const uint32_t b = F == kGradW ? outer_desc(addr + kABytes, 8192) : inner_desc(addr + kABytes);
-        const int parts = F == kGradW ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
+        const uint32_t a = grad_x(F) || grad_w(F) ? outer_desc(addr, 8192) : inner_desc(addr);
+        const uint32_t b = grad_w(F) ? outer_desc(addr + kABytes, 8192) : inner_desc(addr + kABytes);
+        const int parts = grad_w(F) ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (j < parts)
-              mma_pair(d, a + j * ((F == kGradX || F == kGradW ? 2048 : 32) >> 4), b + j * ((F == kGradW ? 2048 : 32) >> 4),
+              mma_pair(d, a + j * ((grad_x(F) || grad_w(F) ? 2048 : 32) >> 4), b + j * ((grad_w(F) ? 2048 : 32) >> 4),
                        idesc, k > k0 || j > 0);
           commit_pair(&s_bar.empty[stage], both);
           if (F != kAdapter && k == k1 - 1) commit_pair(&s_bar.acc_full[acc], both);
@@ -517,7 +618,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-  } else if (warp == 2 && F == kGradW) {
+  } else if (warp == 2 && grad_w(F)) {
     // ---------------------------------------------------------- row ends
     // The last step of an expert reads rows of the next one: they are zeroed
     // in both operands (both, since what lies there may be NaN).
@@ -673,7 +774,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.acc_empty[a]), lead));
     };
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
-      if (F == kGradW && t.steps == 0) {  // an expert without rows
+      if (grad_w(F) && t.steps == 0) {  // an expert without rows
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
 #pragma unroll
@@ -686,8 +787,16 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
             store_block(stage_buf, t, c);
         continue;
       }
+      float bias = 0.0f;
+      int4 ahead[4];  // kDense: the residual of the next 32 rows
+      if (dense(F) && part == 0) {
+        const int at = gated(F) ? t.a0 + (int)rank * 64 + (quarter & 1) * 32 : t.a0 + (int)rank * 128 + quarter * 32;
+        if (p.bias != nullptr && at + lane < p.width)
+          bias = load_param(p.bias, p.bias_bf16, (gated(F) && quarter >= 2 ? p.width : 0) + at + lane);
+        if (F == kDense && p.residual != nullptr) load_residual<32>(ahead, p, t.first + half * 32, t.count - half * 32, at, lane);
+      }
       ok = mbar_wait_pair(&s_bar.acc_full[acc], acc_phase);
-      if (F != kGradW && p.parts > 1) {
+      if (!grad_w(F) && p.parts > 1) {
         if (part > 0) {
           // this pair's sums go to the first pair's CTA with the same rows
           ok = ok && mbar_wait_cluster(&s_bar.part_empty, part_phase ^ 1);
@@ -712,10 +821,10 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         }
         ok = ok && mbar_wait_cluster(&s_bar.part_full, part_phase);
       }
-      ok = F == kGated ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
+      ok = gated(F) ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      if (F == kGradW) {
+      if (grad_w(F)) {
         // a row of the gradient a lane; 64 columns are staged in the swizzled
         // order and stored as a tile
         for (int c = half * 64; c < t.cols; c += 128) {
@@ -742,7 +851,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         float v[32];
         tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
         if (c + 64 >= t.cols) release(acc);
-        if (F != kGradW && p.parts > 1) {
+        if (!grad_w(F) && p.parts > 1) {
           // the parts are added in their order
           for (int q = 0; q + 1 < p.parts; ++q) {
             const float4 *more = joined + (q * p.max_cols + c) * 32 + quarter * 32 + lane;
@@ -757,24 +866,43 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           }
         }
         const int left = t.count - c;  // rows of this chunk (not kGradW)
-        if (F == kPlain || F == kGradX || F == kAdapter) {
+        if (F == kDense) {
+          const int at = t.a0 + (int)rank * 128 + quarter * 32;
+          const int64_t row = t.first + c;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += bias;
+          if (p.preact != nullptr)
+            store_transposed<32>(v, stage_buf, p.preact + row * p.width, p.width, left, at, p.width, lane);
+          activate(p.activation, v);
+          if (p.residual != nullptr) {
+            add_residual<32>(v, ahead, stage_buf, lane);
+            load_residual<32>(ahead, p, row + 64, left - 64, at, lane);
+          }
+          store_out<32>(v, stage_buf, p, row, left, at, lane);
+        } else if (F == kPlain || grad_x(F) || F == kAdapter) {
           const int at = t.a0 + (int)rank * 128 + quarter * 32;
           const int64_t row = t.first + c;
           store_transposed<32>(v, stage_buf, p.out + row * p.width, p.width, left, at, p.width, lane);
           if (F == kPlain && p.preact != nullptr)
             store_transposed<32>(v, stage_buf, p.preact + row * p.width, p.width, left, at, p.width, lane);
-        } else if (F == kGated) {
+        } else if (gated(F)) {
           // lanes 0-63 hold the gate, lanes 64-127 what it multiplies: warps
           // w and w + 2 exchange half of their columns and finish half each
           const int at = t.a0 + (int)rank * 64 + (quarter & 1) * 32;
           const int64_t row = t.first + c;
           const bool gate = quarter < 2;
+          if (F == kDenseGated) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += bias;
+          }
           if (p.preact != nullptr)
             store_transposed<32>(v, stage_buf, p.preact + row * p.wide + (gate ? 0 : p.width), p.wide, left, at,
                                  p.width, lane);
           float *give = reinterpret_cast<float *>(exchange + w * kExchangeBytes);
           const float *take = reinterpret_cast<const float *>(exchange + (w ^ 2) * kExchangeBytes);
           const int id = 1 + half * 2 + (quarter & 1);
+          const int skip = gate ? 0 : 16;  // the rows that this warp finishes
+          if (F == kDenseGated && p.residual != nullptr) load_residual<16>(ahead, p, row + skip, left - skip, at, lane);
           float o[16];
 #pragma unroll
           for (int r = 0; r < 16; r += 8) {
@@ -788,8 +916,12 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
             }
             pair_barrier(id);  // before the next columns overwrite what the other warp reads
           }
-          const int skip = gate ? 0 : 16;
-          store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);
+          if (F == kDenseGated) {
+            if (p.residual != nullptr) add_residual<16>(o, ahead, stage_buf, lane);
+            store_out<16>(o, stage_buf, p, row + skip, left - skip, at, lane);
+          } else {
+            store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);
+          }
         }
       }
       if (t.cols <= half * 32) release(acc);  // no columns for this warp
@@ -797,7 +929,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         __syncwarp();  // what other lanes wrote
         for (int c = half * 32; c < t.cols; c += 64) add_odd(p, t, c, t.a0 + (int)rank * 128 + quarter * 32 + lane);
       }
-      if (F != kGradW && p.parts > 1) {
+      if (!grad_w(F) && p.parts > 1) {
         __syncwarp();
         if (lane == 0)
           for (int q = 1; q < p.parts; ++q)
@@ -808,7 +940,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       if (acc == 0) acc_phase ^= 1;
     }
   }
-  if (F == kGradW && warp >= 4 && lane == 0) bulk_wait<0>();
+  if (grad_w(F) && warp >= 4 && lane == 0) bulk_wait<0>();
   if (!ok) {
     // A wait gave up (it never should): what this CTA started lands well
     // within the time waited here, then everything is given back.
@@ -920,7 +1052,7 @@ ep_status_t launch_form(Params &p, int64_t tiles, cudaStream_t stream) {
   const int cols = p.max_cols;
   // The ring takes what is left of shared memory.
   const int limit = shared_limit(di);
-  const int fixed = 1024 + kResultWarps * staging_of(F) + (F == kGated ? kResultWarps * kExchangeBytes : 0) +
+  const int fixed = 1024 + kResultWarps * staging_of(F) + (gated(F) ? kResultWarps * kExchangeBytes : 0) +
                     (p.parts - 1) * cols * 128 * 4;
   p.ring_bytes = limit - fixed;
   const size_t smem = (size_t)limit;
@@ -945,15 +1077,71 @@ ep_status_t launch_form(Params &p, int64_t tiles, cudaStream_t stream) {
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "product launch");
 }
 
-// Rows [rows][length] by halves of B of every height that a tile may have.
-ep_status_t row_maps(Params &p, const void *rows, int length, int cap) {
-  const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {length * kSize};
+// Rows of `length`, `pitch` elements apart, by halves of B of every height
+// that a tile may have.
+ep_status_t row_maps(Params &p, const void *rows, int length, int cap, int64_t pitch) {
+  const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {pitch * kSize};
   for (int i = 0; i < p.max_cols / 32; ++i) {
     const uint32_t box[] = {kInner, 16u * (i + 1)};
     const ep_status_t s = encode_map(&p.b[i], rows, 2, dims, strides, box);
     if (s != EP_OK) return s;
   }
   return EP_OK;
+}
+
+// Rows of `length`, `pitch` elements apart, read with the outer dimension
+// contiguous: blocks of 64 of a row by 64 rows, two blocks a copy where the
+// length allows it.
+[[maybe_unused]] ep_status_t block_map(CUtensorMap *map, bool *blocks, const void *rows, int length, int cap, int64_t pitch) {
+  *blocks = length % 64 == 0;
+  if (*blocks) {
+    const uint64_t dims[] = {64, (uint64_t)cap, (uint64_t)length / 64}, strides[] = {pitch * kSize, 64 * kSize};
+    const uint32_t box[] = {64, kInner, 2};
+    return encode_map(map, rows, 3, dims, strides, box);
+  }
+  const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {pitch * kSize};
+  const uint32_t box[] = {64, kInner};
+  return encode_map(map, rows, 2, dims, strides, box);
+}
+
+// The weights [E][wide][hidden] as A of a form.
+[[maybe_unused]] ep_status_t weight_map(Params &p, Form form, const void *w, int wide, int hidden) {
+  const uint64_t E = p.E, n = wide, h = hidden;
+  if (form == kPlain || form == kDense) {
+    const uint64_t dims[] = {h, n, E}, strides[] = {h * kSize, n * h * kSize};
+    const uint32_t box[] = {kInner, 128, 1};
+    return encode_map(&p.a, w, 3, dims, strides, box);
+  }
+  if (gated(form)) {
+    const uint64_t dims[] = {h, n / 2, 2, E}, strides[] = {h * kSize, n / 2 * h * kSize, n * h * kSize};
+    const uint32_t box[] = {kInner, 64, 2, 1};
+    return encode_map(&p.a, w, 4, dims, strides, box);
+  }
+  p.a_blocks = hidden % 64 == 0;
+  if (p.a_blocks) {
+    const uint64_t dims[] = {64, n, h / 64, E}, strides[] = {h * kSize, 64 * kSize, n * h * kSize};
+    const uint32_t box[] = {64, kInner, 2, 1};
+    return encode_map(&p.a, w, 4, dims, strides, box);
+  }
+  const uint64_t dims[] = {h, n, E}, strides[] = {h * kSize, n * h * kSize};
+  const uint32_t box[] = {64, kInner, 1};
+  return encode_map(&p.a, w, 3, dims, strides, box);
+}
+
+// A product whose columns are the experts' rows (`pitch` elements apart), cut
+// and launched.
+template <Form F>
+ep_status_t launch_rows_form(Params &p, const void *rows, int64_t pitch, cudaStream_t stream) {
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
+  Cut c;
+  ep_status_t s = choose<F>(di, p.cap, p.E, p.most_rows, p.a_tiles, p.inner, &c);
+  if (s != EP_OK) return s;
+  p.max_cols = c.cols;
+  p.parts = c.parts;
+  s = row_maps(p, rows, p.inner, p.cap, pitch);
+  if (s != EP_OK) return s;
+  return launch_form<F>(p, most_tiles(p.cap, p.E, c.cols) * p.a_tiles, stream);
 }
 
 }  // namespace

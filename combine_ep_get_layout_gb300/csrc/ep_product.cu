@@ -81,59 +81,6 @@ ep_status_t launch_flag_rows(const Params &p, cudaStream_t stream) {
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "flag_rows launch");
 }
 
-// Rows [rows][length] read with the outer dimension contiguous: blocks of 64
-// of a row by 64 rows, two blocks a copy where the length allows it.
-ep_status_t block_map(CUtensorMap *map, bool *blocks, const void *rows, int length, int cap) {
-  *blocks = length % 64 == 0;
-  if (*blocks) {
-    const uint64_t dims[] = {64, (uint64_t)cap, (uint64_t)length / 64}, strides[] = {length * kSize, 64 * kSize};
-    const uint32_t box[] = {64, kInner, 2};
-    return encode_map(map, rows, 3, dims, strides, box);
-  }
-  const uint64_t dims[] = {(uint64_t)length, (uint64_t)cap}, strides[] = {length * kSize};
-  const uint32_t box[] = {64, kInner};
-  return encode_map(map, rows, 2, dims, strides, box);
-}
-
-// The weights [E][wide][hidden] as A of a form.
-ep_status_t weight_map(Params &p, Form form, const void *w, int wide, int hidden) {
-  const uint64_t E = p.E, n = wide, h = hidden;
-  if (form == kPlain) {
-    const uint64_t dims[] = {h, n, E}, strides[] = {h * kSize, n * h * kSize};
-    const uint32_t box[] = {kInner, 128, 1};
-    return encode_map(&p.a, w, 3, dims, strides, box);
-  }
-  if (form == kGated) {
-    const uint64_t dims[] = {h, n / 2, 2, E}, strides[] = {h * kSize, n / 2 * h * kSize, n * h * kSize};
-    const uint32_t box[] = {kInner, 64, 2, 1};
-    return encode_map(&p.a, w, 4, dims, strides, box);
-  }
-  p.a_blocks = hidden % 64 == 0;
-  if (p.a_blocks) {
-    const uint64_t dims[] = {64, n, h / 64, E}, strides[] = {h * kSize, 64 * kSize, n * h * kSize};
-    const uint32_t box[] = {64, kInner, 2, 1};
-    return encode_map(&p.a, w, 4, dims, strides, box);
-  }
-  const uint64_t dims[] = {h, n, E}, strides[] = {h * kSize, n * h * kSize};
-  const uint32_t box[] = {64, kInner, 1};
-  return encode_map(&p.a, w, 3, dims, strides, box);
-}
-
-// A product whose columns are the experts' rows, cut and launched.
-template <Form F>
-ep_status_t launch_rows_form(Params &p, const void *rows, cudaStream_t stream) {
-  const DeviceInfo *di = current_device_info();
-  if (di == nullptr) return EP_ERR_CUDA;
-  Cut c;
-  ep_status_t s = choose<F>(di, p.cap, p.E, p.most_rows, p.a_tiles, p.inner, &c);
-  if (s != EP_OK) return s;
-  p.max_cols = c.cols;
-  p.parts = c.parts;
-  s = row_maps(p, rows, p.inner, p.cap);
-  if (s != EP_OK) return s;
-  return launch_form<F>(p, most_tiles(p.cap, p.E, c.cols) * p.a_tiles, stream);
-}
-
 }  // namespace
 
 ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
@@ -154,7 +101,7 @@ ep_status_t launch_product(const ProductArgs &a, cudaStream_t stream) {
   p.preact = a.preact;
   const ep_status_t s = weight_map(p, a.gated ? kGated : kPlain, a.w, p.wide, a.hidden);
   if (s != EP_OK) return s;
-  return a.gated ? launch_rows_form<kGated>(p, a.x, stream) : launch_rows_form<kPlain>(p, a.x, stream);
+  return a.gated ? launch_rows_form<kGated>(p, a.x, a.hidden, stream) : launch_rows_form<kPlain>(p, a.x, a.hidden, stream);
 }
 
 ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t stream) {
@@ -186,7 +133,7 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     p.a_tiles = up(a.hidden, 256);
     p.out = a.grad_x;
     ep_status_t s = weight_map(p, kGradX, a.w, wide, a.hidden);
-    if (s == EP_OK) s = launch_rows_form<kGradX>(p, g, stream);
+    if (s == EP_OK) s = launch_rows_form<kGradX>(p, g, wide, stream);
     if (s != EP_OK) return s;
   }
   if (a.grad_w != nullptr) {
@@ -197,12 +144,12 @@ ep_status_t launch_product_backward(const ProductBackwardArgs &a, cudaStream_t s
     p.out = a.grad_w;
     // without rows nothing is copied: the maps only need an address
     const int cap = most > 0 ? a.recv_capacity : 1;
-    ep_status_t s = block_map(&p.a, &p.a_blocks, most > 0 ? g : a.grad_w, wide, cap);
+    ep_status_t s = block_map(&p.a, &p.a_blocks, most > 0 ? g : a.grad_w, wide, cap, wide);
     const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)wide, (uint64_t)a.num_experts};
     const uint64_t strides[] = {a.hidden * kSize, (uint64_t)wide * a.hidden * kSize};
     const uint32_t box[] = {64, 32, 1};
     if (s == EP_OK) s = encode_map(&p.grad, a.grad_w, 3, dims, strides, box);
-    if (s == EP_OK) s = block_map(&p.b[0], &p.b_blocks, most > 0 ? a.x : a.grad_w, a.hidden, cap);
+    if (s == EP_OK) s = block_map(&p.b[0], &p.b_blocks, most > 0 ? a.x : a.grad_w, a.hidden, cap, a.hidden);
     if (s == EP_OK)
       s = launch_form<kGradW>(p, (int64_t)a.num_experts * p.a_tiles * p.b_tiles, stream);
     if (s != EP_OK) return s;
