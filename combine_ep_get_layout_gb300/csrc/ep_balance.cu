@@ -8,9 +8,14 @@
 //   d l: softmax p (slope - sum p slope), sigmoid the same times 1 - sigmoid(l)
 //        + 2/N log-sum-exp softmax(l)
 //
-// The sums over tokens run in a fixed order: a block's part of a sequence
-// first (a "segment"; block b's of sequence s is segment b + s, since later
-// blocks hold later sequences), then the segments.
+// Bound by memory: one pass over the logits.  A row belongs to L lanes of a
+// warp, V columns each, so that a row's sums take log2 L exchanges and the
+// columns' sums stay in registers over all rows of a lane.  The sums over
+// tokens run in a fixed order: a block's part of a sequence first (a
+// "segment"; block b's of sequence s is segment b + s, since later blocks
+// hold later sequences), then the segments.
+#include <algorithm>
+
 #include "ep_device.cuh"
 #include "ep_ops.h"
 
@@ -19,15 +24,343 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlocks = 456;      // that share the tokens: three an SM
+constexpr int kTokenStep = 32;    // a block's tokens come in these
+constexpr int kLanesMost = 1024;  // experts that a warp's lanes hold
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kMost = 3.402823466e38f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kTiny = -200.0f;  // 2^-200 is 0
 
-// A logit in fp32: NaN counts as masked, +infinity as the largest number.
-__device__ __forceinline__ float load_logit(const void *p, bool bf16, int64_t i) {
-  float v = bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16) : static_cast<const float *>(p)[i];
-  v = v != v ? kNegInf : v;
-  return fminf(v, 3.402823466e38f);
+__device__ __forceinline__ float value_of(const void *p, bool bf16, int64_t i) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16) : static_cast<const float *>(p)[i];
 }
 
+// A logit in fp32: NaN counts as masked, +infinity as the largest number.
+__device__ __forceinline__ float offered(float v) { return fminf(v != v ? kNegInf : v, kMost); }
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ int offset_of(const int32_t *offsets, int T, int s) {
+  return offsets == nullptr ? (s == 0 ? 0 : T) : min(max(offsets[s], 0), T);
+}
+
+// The first sequence that ends behind token t (S: none).  Within the bounds
+// of `offsets` whatever they hold.
+__device__ __forceinline__ int sequence_of(const int32_t *offsets, int T, int S, int t) {
+  int low = 0, high = S;
+  while (low < high) {
+    const int mid = (low + high) / 2;
+    if (offset_of(offsets, T, mid + 1) > t)
+      high = mid;
+    else
+      low = mid + 1;
+  }
+  return low;
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// A row's V columns of a lane: by pieces of 16 bytes where rows allow it
+// (WIDE), by the same columns one by one where they do not.
+template <bool BF16, int L, int V, bool WIDE>
+struct Columns {
+  static constexpr int kPiece = BF16 ? 8 : 4, kCount = V / kPiece;
+  int E, lane;
+  __device__ int column(int i, int j) const { return (i * L + lane) * kPiece + j; }
+  // Columns past the last expert read `none`.
+  __device__ void load(const char *row, float none, float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      if (WIDE) {
+        int4 f = make_int4(0, 0, 0, 0);
+        const bool there = column(i, 0) < E;
+        if (there) f = *reinterpret_cast<const int4 *>(row + column(i, 0) * (BF16 ? 2 : 4));
+        const int w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          const float x = !BF16 ? __int_as_float(w[j % 4]) : j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+          v[i * kPiece + j] = there ? x : none;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) v[i * kPiece + j] = column(i, j) < E ? value_of(row, BF16, column(i, j)) : none;
+      }
+    }
+  }
+  __device__ void store(char *row, const float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      if (WIDE) {
+        int w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = BF16 ? (int)pack_bf16x2(v[i * kPiece + 2 * j % kPiece], v[i * kPiece + (2 * j + 1) % kPiece])
+                      : __float_as_int(v[i * kPiece + j % kPiece]);
+        if (column(i, 0) < E)
+          *reinterpret_cast<int4 *>(row + column(i, 0) * (BF16 ? 2 : 4)) = make_int4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          if (column(i, j) >= E) continue;
+          const float x = v[i * kPiece + j];
+          if (BF16)
+            reinterpret_cast<uint16_t *>(row)[column(i, j)] = (uint16_t)(pack_bf16x2(x, 0.0f) & 0xffffu);
+          else
+            reinterpret_cast<float *>(row)[column(i, j)] = x;
+        }
+      }
+    }
+  }
+  __device__ void floats(const float *row, float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i)
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) v[i * kPiece + j] = column(i, j) < E ? __ldg(row + column(i, j)) : 0.0f;
+  }
+};
+
+// A row's scores over L lanes: p = e inv; softmax = soft inv_soft (kSigmoid;
+// else e inv too), side = 1 - sigmoid.
+template <int V, bool SIGMOID, bool GRAD>
+struct Scores {
+  float e[V];
+  float soft[SIGMOID && GRAD ? V : 1], side[SIGMOID && GRAD ? V : 1];
+  float inv, inv_soft, lse;
+};
+
+// Rows with logits of at least 2^100 or without one of at least 2^-100 or so
+// (a sum that is no positive finite number, or a largest logit that the
+// product with log2 e could overflow): everything relative to the largest.
+template <int L, int V, bool SIGMOID, bool GRAD>
+__device__ __forceinline__ void far_scores(const float (&l)[V], Scores<V, SIGMOID, GRAD> &s) {
+  float m = kNegInf, sum = 0.0f, soft = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) m = fmaxf(m, offered(l[j]));
+  m = lanes_max<L>(m);
+  const float k = fminf(m, 0.0f);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float x = offered(l[j]);
+    const bool there = x > kNegInf;
+    const float e = there ? exp2_approx(fmaxf((x - m) * kLog2e, kTiny)) : 0.0f;
+    soft += e;
+    if (SIGMOID) {
+      const float u = exp2_approx(fmaxf(-fabsf(x) * kLog2e, kTiny)), r = 1.0f / (1.0f + u);
+      s.e[j] = there ? exp2_approx(fmaxf((fminf(x, 0.0f) - k) * kLog2e, kTiny)) * r : 0.0f;
+      if (GRAD) {
+        s.soft[GRAD ? j : 0] = e;
+        s.side[GRAD ? j : 0] = x >= 0.0f ? u * r : r;
+      }
+    } else {
+      s.e[j] = e;
+    }
+    sum += s.e[j];
+  }
+  sum = lanes_sum<L>(sum);
+  soft = lanes_sum<L>(soft);
+  s.inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  s.inv_soft = soft > 0.0f ? 1.0f / soft : 0.0f;
+  s.lse = soft > 0.0f ? m + logf(soft) : 0.0f;
+}
+
+// All lanes of the warp call it.  Exponentials are approximate (2 ulp, and
+// the rounding of their argument); NaN and -infinity become 0 through the
+// maximum with kTiny, which takes the other operand of a NaN.
+//   softmax: 2^(l log2 e - c), c = m log2 e rounded once, which cancels in p
+//   sigmoid: E = e^l, sigmoid E / (1 + E); one exponential serves both scores
+template <int L, int V, bool SIGMOID, bool GRAD>
+__device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID, GRAD> &s) {
+  float sum = 0.0f, soft = 0.0f, c = 0.0f;
+  bool near;
+  if (SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float e = exp2_approx(fmaxf(l[j] * kLog2e, kTiny)), r = rcp_approx(1.0f + e);
+      s.e[j] = e * r;
+      sum += s.e[j];
+      soft += e;
+      if (GRAD) {
+        s.soft[GRAD ? j : 0] = e;
+        s.side[GRAD ? j : 0] = r;
+      }
+    }
+    sum = lanes_sum<L>(sum);
+    soft = lanes_sum<L>(soft);
+    near = soft > 1e-30f && soft < 1e30f;
+  } else {
+    float m = kNegInf;
+#pragma unroll
+    for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
+    m = lanes_max<L>(m);
+    near = fabsf(m) < 1e30f;
+    c = m * kLog2e;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      s.e[j] = exp2_approx(fmaxf(fmaf(l[j], kLog2e, -c), kTiny));
+      sum += s.e[j];
+    }
+    sum = lanes_sum<L>(sum);
+    soft = sum;
+  }
+  if (!__all_sync(0xffffffffu, near)) {
+    far_scores<L, V, SIGMOID, GRAD>(l, s);
+    return;
+  }
+  s.inv = 1.0f / sum;
+  s.inv_soft = SIGMOID ? 1.0f / soft : s.inv;
+  s.lse = fmaf(c, kLn2, logf(soft));
+}
+
+// Tokens of a block, and blocks.
+int tokens_of(int T) { return std::max(kTokenStep, ((T - 1) / kBlocks + kTokenStep) / kTokenStep * kTokenStep); }
+int blocks_of(int T) { return T == 0 ? 0 : (T - 1) / tokens_of(T) + 1; }
+
+struct Parts {
+  float *probs;     // [segments][E]
+  int32_t *counts;  // [segments][E]
+  int32_t *chosen;  // [segments]
+  float *z;         // [blocks]
+  float *balance;   // [S][column blocks]
+  int32_t *head;    // sequences with tokens, whether offsets are out of order, tickets of the join
+  int tokens, blocks;
+};
+
+// Sequences with tokens, and whether the offsets are out of order.
+__device__ void look_at_offsets(const int32_t *offsets, int T, int S, int32_t *head) {
+  int full = 0, bad = 0;
+  for (int s = threadIdx.x; s < S; s += blockDim.x) {
+    full += offset_of(offsets, T, s + 1) > offset_of(offsets, T, s);
+    if (offsets != nullptr) bad |= offsets[s] < 0 || offsets[s] > offsets[s + 1] || offsets[s + 1] > T;
+  }
+  __shared__ int s_full[32], s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
+  full = __reduce_add_sync(0xffffffffu, full);
+  if ((threadIdx.x & 31) == 0) s_full[threadIdx.x / 32] = full;
+  __syncthreads();
+  if (bad) atomicOr(&s_bad, 1);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < (int)blockDim.x / 32; ++i) full += s_full[i];
+    head[0] = full;
+    head[1] = s_bad;
+    head[2] = 0;
+  }
+  __syncthreads();
+}
+
+// The choices of rows a ... b, counted in shared memory and written with
+// their number.
+__device__ void count_choices(const BalanceArgs &p, int a, int b, int64_t segment, int32_t *s_counts, const Parts &parts) {
+  __shared__ int s_chosen;
+  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) s_counts[e] = 0;
+  if (threadIdx.x == 0) s_chosen = 0;
+  __syncthreads();
+  int chosen = 0;
+  for (int64_t i = (int64_t)a * p.num_topk + threadIdx.x; i < (int64_t)b * p.num_topk; i += blockDim.x) {
+    const int64_t e = p.topk_idx[i];
+    if (e >= 0 && e < p.num_experts) {
+      atomicAdd(&s_counts[e], 1);
+      ++chosen;
+    }
+  }
+  chosen = __reduce_add_sync(0xffffffffu, chosen);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&s_chosen, chosen);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) parts.counts[segment * p.num_experts + e] = s_counts[e];
+  if (threadIdx.x == 0) parts.chosen[segment] = s_chosen;
+}
+
+template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(BalanceArgs p, Parts parts) {
+  extern __shared__ float s_probs[];  // [warps][experts], and the counts
+  __shared__ float s_z[kWarps];
+  constexpr int kRows = kThreads / L;  // at a time
+  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row = threadIdx.x / L;
+  const Columns<BF16, L, V, WIDE> columns{E, (int)threadIdx.x % L};
+  const int t0 = blockIdx.x * parts.tokens, t1 = t0 + min(T - t0, parts.tokens);
+  const int64_t apart = p.row_stride * (BF16 ? 2 : 4);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x == 0) look_at_offsets(p.seq_offsets, T, S, parts.head);
+  float z = 0.0f;
+  for (int s = sequence_of(p.seq_offsets, T, S, t0); s < S; ++s) {
+    const int a = max(t0, offset_of(p.seq_offsets, T, s)), b = min(t1, offset_of(p.seq_offsets, T, s + 1));
+    if (a >= t1) break;
+    if (a >= b) continue;
+    const int64_t segment = blockIdx.x + s;
+    float acc[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+    const char *from = static_cast<const char *>(p.logits) + a * apart;
+    for (int i = 0; i < b - a; i += kRows) {
+      const bool here = i + row < b - a;
+      float l[V];
+      if (here) {
+        columns.load(from + (i + row) * apart, kNegInf, l);
+      } else {  // all lanes take part in the exchanges
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] = 0.0f;
+      }
+      Scores<V, SIGMOID, false> sc;
+      scores_of<L>(l, sc);
+      const float inv = here ? sc.inv : 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = fmaf(sc.e[j], inv, acc[j]);
+      if (here && columns.lane == 0) z = fmaf(sc.lse, sc.lse, z);
+    }
+    // the warp's rows, then the warps
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    }
+    if (lane < L) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = columns.column(i / columns.kPiece, i % columns.kPiece);
+        if (c < E) s_probs[warp * E + c] = acc[i];
+      }
+    }
+    count_choices(p, a, b, segment, reinterpret_cast<int32_t *>(s_probs + kWarps * E), parts);
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      float sum = s_probs[e];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) sum += s_probs[w * E + e];
+      parts.probs[segment * E + e] = sum;
+    }
+    __syncthreads();
+  }
+  // (only a row's first lane has added to z)
+  z = lanes_sum<32>(z);
+  if (lane == 0) s_z[warp] = z;
+  __syncthreads();
+  if (threadIdx.x == 0 && t0 < t1) {
+    for (int w = 1; w < kWarps; ++w) z += s_z[w];
+    parts.z[blockIdx.x] = z;
+  }
+}
+
+// More experts than a warp's lanes hold: a block a row at a time.
 template <typename Op>
 __device__ __forceinline__ float block_reduce(float v, float *s, Op op) {
 #pragma unroll
@@ -61,12 +394,12 @@ struct Row {
 __device__ Row row_of(const void *logits, bool bf16, int64_t at, int E, bool sigmoid, float *s) {
   Row r;
   float m = kNegInf, sum = 0.0f, sig = 0.0f;
-  for (int e = threadIdx.x; e < E; e += kThreads) m = fmaxf(m, load_logit(logits, bf16, at + e));
+  for (int e = threadIdx.x; e < E; e += kThreads) m = fmaxf(m, offered(value_of(logits, bf16, at + e)));
   r.m = block_reduce(m, s, Max());
   r.k = fminf(r.m, 0.0f);
   if (r.m > kNegInf) {
     for (int e = threadIdx.x; e < E; e += kThreads) {
-      const float l = load_logit(logits, bf16, at + e);
+      const float l = offered(value_of(logits, bf16, at + e));
       sum += expf(l - r.m);
       if (sigmoid) sig += l > kNegInf ? expf(fminf(l, 0.0f) - r.k) / (1.0f + expf(-fabsf(l))) : 0.0f;
     }
@@ -76,111 +409,162 @@ __device__ Row row_of(const void *logits, bool bf16, int64_t at, int E, bool sig
   return r;
 }
 
-__device__ __forceinline__ int offset_of(const int32_t *offsets, int T, int s) {
-  return offsets == nullptr ? (s == 0 ? 0 : T) : min(max(offsets[s], 0), T);
-}
-
-constexpr int kTokens = 64;  // of a block
-
-int blocks_of(int T) { return (T + kTokens - 1) / kTokens; }
-
-struct Parts {
-  float *probs;    // [segments][E]
-  int32_t *counts; // [segments][E]
-  float *z;        // [segments]
-};
-
-__global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs p, Parts parts) {
-  __shared__ float s_reduce[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) balance_rows_kernel(BalanceArgs p, Parts parts) {
+  __shared__ float s_reduce[kWarps];
   __shared__ float s_probs[EP_MAX_EXPERTS];
   __shared__ int32_t s_counts[EP_MAX_EXPERTS];
   griddep_wait();
   griddep_launch_dependents();
-  const int t0 = blockIdx.x * kTokens, t1 = min(p.num_tokens, t0 + kTokens);
-  for (int s = 0; s < p.num_sequences; ++s) {
-    const int a = max(t0, offset_of(p.seq_offsets, p.num_tokens, s));
-    const int b = min(t1, offset_of(p.seq_offsets, p.num_tokens, s + 1));
+  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
+  if (blockIdx.x == 0) look_at_offsets(p.seq_offsets, T, S, parts.head);
+  const int t0 = blockIdx.x * parts.tokens, t1 = t0 + min(T - t0, parts.tokens);
+  float z = 0.0f;
+  for (int s = sequence_of(p.seq_offsets, T, S, t0); s < S; ++s) {
+    const int a = max(t0, offset_of(p.seq_offsets, T, s)), b = min(t1, offset_of(p.seq_offsets, T, s + 1));
+    if (a >= t1) break;
     if (a >= b) continue;
-    for (int e = threadIdx.x; e < p.num_experts; e += kThreads) {
-      s_probs[e] = 0.0f;
-      s_counts[e] = 0;
-    }
-    __syncthreads();
-    float z = 0.0f;
+    const int64_t segment = blockIdx.x + s;
+    for (int e = threadIdx.x; e < E; e += kThreads) s_probs[e] = 0.0f;  // each thread its own
     for (int t = a; t < b; ++t) {
       const int64_t at = t * p.row_stride;
-      const Row r = row_of(p.logits, p.bf16, at, p.num_experts, p.sigmoid, s_reduce);
-      for (int e = threadIdx.x; e < p.num_experts; e += kThreads) {
-        const float l = load_logit(p.logits, p.bf16, at + e);
+      const Row r = row_of(p.logits, p.bf16, at, E, p.sigmoid, s_reduce);
+      for (int e = threadIdx.x; e < E; e += kThreads) {
+        const float l = offered(value_of(p.logits, p.bf16, at + e));
         s_probs[e] += p.sigmoid ? r.sigmoid(l) : r.softmax(l);
       }
       z += r.lse() * r.lse();
     }
-    for (int64_t i = (int64_t)a * p.num_topk + threadIdx.x; i < (int64_t)b * p.num_topk; i += kThreads) {
-      const int64_t e = p.topk_idx[i];
-      if (e >= 0 && e < p.num_experts) atomicAdd(&s_counts[e], 1);
-    }
+    count_choices(p, a, b, segment, s_counts, parts);
+    for (int e = threadIdx.x; e < E; e += kThreads) parts.probs[segment * E + e] = s_probs[e];
     __syncthreads();
-    const int64_t segment = blockIdx.x + s;
-    for (int e = threadIdx.x; e < p.num_experts; e += kThreads) {
-      parts.probs[segment * p.num_experts + e] = s_probs[e];
-      parts.counts[segment * p.num_experts + e] = s_counts[e];
+  }
+  if (threadIdx.x == 0 && t0 < t1) parts.z[blockIdx.x] = z;
+}
+
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
+
+// A sequence's segments, 32 experts a block: 32 warps take every 32nd
+// segment, then are added in their order.  The block that ends last adds up
+// the losses.
+__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs p, Parts parts) {
+  __shared__ float s_probs[kJoinWarps][33], s_reduce[kJoinWarps];
+  __shared__ int s_counts[kJoinWarps][33], s_chosen[kJoinWarps], s_last;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
+  const int s = blockIdx.x / tiles, e = blockIdx.x % tiles * 32 + threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int a = offset_of(p.seq_offsets, T, s), b = offset_of(p.seq_offsets, T, s + 1);
+  const int b0 = a / parts.tokens, b1 = b > a ? (b - 1) / parts.tokens : b0 - 1;
+  const int full = parts.head[0];
+  float prob = 0.0f;
+  int count = 0, chosen = 0;
+  if (e < E) {
+#pragma unroll 4
+    for (int i = b0 + warp; i <= b1; i += kJoinWarps) {
+      prob += parts.probs[(int64_t)(i + s) * E + e];
+      count += parts.counts[(int64_t)(i + s) * E + e];
     }
-    if (threadIdx.x == 0) parts.z[segment] = z;
-    __syncthreads();
+  }
+  for (int i = b0 + threadIdx.x; i <= b1; i += kJoinThreads) chosen += parts.chosen[i + s];
+  s_probs[warp][lane] = prob;
+  s_counts[warp][lane] = count;
+  chosen = __reduce_add_sync(0xffffffffu, chosen);
+  if (lane == 0) s_chosen[warp] = chosen;
+  __syncthreads();
+  if (warp == 0) {
+    chosen = __reduce_add_sync(0xffffffffu, s_chosen[lane]);
+    for (int w = 1; w < kJoinWarps; ++w) {
+      prob += s_probs[w][lane];
+      count += s_counts[w][lane];
+    }
+    float part = 0.0f;
+    if (e < E) {
+      const int64_t at = (int64_t)s * E + e;
+      const float mean = b > a ? prob / (b - a) : 0.0f;
+      const float share = chosen > 0 ? (float)E * count / chosen / full : 0.0f;
+      p.probs[at] = mean;
+      p.counts[at] = count;
+      p.slopes[at] = b > a ? share / (b - a) : 0.0f;
+      part = share * mean;
+    }
+    part = lanes_sum<32>(part);
+    if (lane == 0) {
+      parts.balance[blockIdx.x] = part;
+      __threadfence();
+      s_last = atomicAdd(parts.head + 2, 1) == (int)gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  float balance = 0.0f, z = 0.0f;
+  for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += kJoinThreads) balance += __ldcg(parts.balance + i);
+  for (int i = threadIdx.x; i < parts.blocks; i += kJoinThreads) z += parts.z[i];
+  balance = block_reduce(balance, s_reduce, Sum());
+  z = block_reduce(z, s_reduce, Sum());
+  if (threadIdx.x == 0) {
+    const int tokens = offset_of(p.seq_offsets, T, S) - offset_of(p.seq_offsets, T, 0);
+    const float nan = __int_as_float(0x7fffffff);
+    const bool bad = parts.head[1] != 0;
+    p.losses[0] = bad ? nan : balance;
+    p.losses[1] = bad ? nan : tokens > 0 ? z / tokens : 0.0f;
   }
 }
 
-__global__ void __launch_bounds__(kThreads) balance_join_kernel(BalanceArgs p, Parts parts) {
-  __shared__ float s_reduce[kThreads / 32];
-  __shared__ int s_bad;
+// Without tokens nobody else looks at the offsets.
+__global__ void __launch_bounds__(kThreads) balance_empty_kernel(BalanceArgs p, Parts parts) {
   griddep_wait();
   griddep_launch_dependents();
-  const int E = p.num_experts, S = p.num_sequences;
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  int full = 0;
-  bool bad = false;
-  for (int s = 0; s < S; ++s) {
-    const int a = offset_of(p.seq_offsets, p.num_tokens, s), b = offset_of(p.seq_offsets, p.num_tokens, s + 1);
-    full += b > a;
-    if (p.seq_offsets != nullptr)
-      bad = bad || p.seq_offsets[s] < 0 || p.seq_offsets[s] > p.seq_offsets[s + 1] || p.seq_offsets[s + 1] > p.num_tokens;
-  }
-  float balance = 0.0f, z = 0.0f;
-  int tokens = 0;
-  for (int s = 0; s < S; ++s) {
-    const int a = offset_of(p.seq_offsets, p.num_tokens, s), b = offset_of(p.seq_offsets, p.num_tokens, s + 1);
-    const int b0 = a / kTokens, b1 = b > a ? (b - 1) / kTokens : b0 - 1;
-    float chosen = 0.0f;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float prob = 0.0f;
-      int count = 0;
-      for (int i = b0; i <= b1; ++i) {
-        prob += parts.probs[(int64_t)(i + s) * E + e];
-        count += parts.counts[(int64_t)(i + s) * E + e];
+  look_at_offsets(p.seq_offsets, p.num_tokens, p.num_sequences, parts.head);
+}
+
+// The gradients' rows of a block.
+constexpr int kGradRows = 64;
+
+template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads, 2) balance_backward_kernel(BalanceBackwardArgs p) {
+  constexpr int kRows = kThreads / L, kSize = BF16 ? 2 : 4;
+  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
+  const Columns<BF16, L, V, WIDE> columns{E, (int)threadIdx.x % L};
+  const int row = threadIdx.x / L;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int first = offset_of(p.seq_offsets, T, 0), last = offset_of(p.seq_offsets, T, S);
+  const float db = p.grad_losses[0], dz = p.grad_losses[1] * 2.0f / max(1, last - first);
+  for (int64_t t0 = (int64_t)blockIdx.x * kGradRows; t0 < T; t0 += (int64_t)gridDim.x * kGradRows) {
+    float slope[V];
+    int end = -1;  // of the sequence whose slopes are held
+    for (int i = 0; i < kGradRows; i += kRows) {
+      const int64_t t64 = t0 + i + row;
+      const bool here = t64 < T;
+      const int64_t t = here ? t64 : T - 1;  // all lanes take part in the exchanges
+      if (t >= end) {
+        const int s = sequence_of(p.seq_offsets, T, S, (int)t);
+        end = s < S ? offset_of(p.seq_offsets, T, s + 1) : INT32_MAX;
+        if (s < S) columns.floats(p.slopes + (int64_t)s * E, slope);
       }
-      p.probs[(int64_t)s * E + e] = b > a ? prob / (b - a) : 0.0f;
-      p.counts[(int64_t)s * E + e] = count;
-      chosen += count;
+      const bool inside = end < INT32_MAX && t >= first;
+      float l[V], add[V];
+      columns.load(static_cast<const char *>(p.logits) + t * p.row_stride * kSize, kNegInf, l);
+      if (p.add != nullptr) columns.load(static_cast<const char *>(p.add) + t * E * kSize, 0.0f, add);
+      Scores<V, SIGMOID, true> sc;
+      scores_of<L>(l, sc);
+      float dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) dot = fmaf(sc.e[j], slope[j], dot);
+      dot = lanes_sum<L>(dot) * sc.inv;
+      const float scale = db * sc.inv, tail = fminf(fmaxf(dz * sc.lse * sc.inv_soft, -kMost), kMost);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float d = sc.e[j] * scale * (slope[j] - dot);
+        if (SIGMOID) d *= sc.side[SIGMOID ? j : 0];
+        d = fmaf(SIGMOID ? sc.soft[SIGMOID ? j : 0] : sc.e[j], tail, d);
+        d = inside ? d : 0.0f;
+        l[j] = p.add != nullptr ? add[j] + d : d;
+      }
+      if (here) columns.store(static_cast<char *>(p.grad_logits) + t * E * kSize, l);
     }
-    if (b > a) {
-      tokens += b - a;
-      for (int i = b0; i <= b1; ++i) z += parts.z[i + s];
-    }
-    chosen = block_reduce(chosen, s_reduce, Sum());
-    float part = 0.0f;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      const float share = chosen > 0.0f ? (float)E * p.counts[(int64_t)s * E + e] / chosen / full : 0.0f;
-      p.slopes[(int64_t)s * E + e] = b > a ? share / (b - a) : 0.0f;
-      part += share * p.probs[(int64_t)s * E + e];
-    }
-    balance += block_reduce(part, s_reduce, Sum());
-  }
-  if (threadIdx.x == 0) {
-    const float nan = __int_as_float(0x7fffffff);
-    p.losses[0] = bad ? nan : balance;
-    p.losses[1] = bad ? nan : tokens > 0 ? z / tokens : 0.0f;
   }
 }
 
@@ -191,16 +575,15 @@ __device__ __forceinline__ void store_grad(void *p, bool bf16, int64_t i, float 
     static_cast<float *>(p)[i] = v;
 }
 
-__global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceBackwardArgs p) {
-  __shared__ float s_reduce[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) balance_backward_rows_kernel(BalanceBackwardArgs p) {
+  __shared__ float s_reduce[kWarps];
   griddep_wait();
   griddep_launch_dependents();
-  const int E = p.num_experts, S = p.num_sequences;
-  const int first = offset_of(p.seq_offsets, p.num_tokens, 0), last = offset_of(p.seq_offsets, p.num_tokens, S);
+  const int E = p.num_experts, S = p.num_sequences, T = p.num_tokens;
+  const int first = offset_of(p.seq_offsets, T, 0), last = offset_of(p.seq_offsets, T, S);
   const float db = p.grad_losses[0], dz = p.grad_losses[1] * 2.0f / max(1, last - first);
-  for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-    int s = 0;
-    while (s < S && offset_of(p.seq_offsets, p.num_tokens, s + 1) <= t) ++s;
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    const int s = sequence_of(p.seq_offsets, T, S, (int)t);
     const bool inside = s < S && t >= first;
     Row r = {};
     float dot = 0.0f;
@@ -209,20 +592,18 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceBackw
     if (inside) {
       r = row_of(p.logits, p.bf16, t * p.row_stride, E, p.sigmoid, s_reduce);
       for (int e = threadIdx.x; e < E; e += kThreads)
-        dot += score(load_logit(p.logits, p.bf16, t * p.row_stride + e)) * slope[e];
+        dot += score(offered(value_of(p.logits, p.bf16, t * p.row_stride + e))) * slope[e];
       dot = block_reduce(dot, s_reduce, Sum());
     }
     for (int e = threadIdx.x; e < E; e += kThreads) {
       float d = 0.0f;
       if (inside) {
-        const float l = load_logit(p.logits, p.bf16, t * p.row_stride + e);
+        const float l = offered(value_of(p.logits, p.bf16, t * p.row_stride + e));
         d = db * score(l) * (slope[e] - dot);
         if (p.sigmoid) d *= 1.0f / (1.0f + expf(l));
         d += dz * r.lse() * r.softmax(l);
       }
-      if (p.add != nullptr)
-        d += p.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.add)[t * E + e] << 16)
-                    : static_cast<const float *>(p.add)[t * E + e];
+      if (p.add != nullptr) d += value_of(p.add, p.bf16, t * E + e);
       store_grad(p.grad_logits, p.bf16, t * E + e, d);
     }
   }
@@ -230,28 +611,100 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceBackw
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
+Parts parts_of(const BalanceArgs &a) {
+  const size_t E = a.num_experts, segments = (size_t)blocks_of(a.num_tokens) + a.num_sequences;
+  char *at = static_cast<char *>(a.workspace);
+  const auto take = [&](size_t bytes) {
+    char *p = at;
+    at += round16(bytes);
+    return p;
+  };
+  Parts p;
+  p.head = reinterpret_cast<int32_t *>(take(16));
+  p.probs = reinterpret_cast<float *>(take(segments * E * 4));
+  p.counts = reinterpret_cast<int32_t *>(take(segments * E * 4));
+  p.chosen = reinterpret_cast<int32_t *>(take(segments * 4));
+  p.z = reinterpret_cast<float *>(take(segments * 4));
+  p.balance = reinterpret_cast<float *>(take(a.num_sequences * ((E + 31) / 32) * 4));
+  p.tokens = tokens_of(a.num_tokens);
+  p.blocks = blocks_of(a.num_tokens);
+  return p;
+}
+
+// Rows of whole 16 bytes.
+bool wide_rows(const void *p, int64_t stride, int E, bool bf16) {
+  const int piece = bf16 ? 8 : 4;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % piece == 0 && E % piece == 0;
+}
+
+template <bool BF16, int L, int V>
+cudaError_t launch_lanes(const BalanceArgs &a, const Parts &parts, bool wide, cudaStream_t stream) {
+  const size_t smem = (size_t)(kWarps + 1) * a.num_experts * 4;
+  const auto kernel = wide ? (a.sigmoid ? balance_kernel<BF16, L, V, true, true> : balance_kernel<BF16, L, V, true, false>)
+                           : (a.sigmoid ? balance_kernel<BF16, L, V, false, true> : balance_kernel<BF16, L, V, false, false>);
+  return launch_kernel(kernel, parts.blocks, kThreads, smem, stream, false, a, parts);
+}
+
+template <bool BF16>
+cudaError_t launch_lanes_of(const BalanceArgs &a, const Parts &parts, cudaStream_t stream) {
+  const bool wide = wide_rows(a.logits, a.row_stride, a.num_experts, a.bf16);
+  const int E = a.num_experts;
+  if (E <= 64) return launch_lanes<BF16, 8, 8>(a, parts, wide, stream);
+  if (E <= 128) return launch_lanes<BF16, 8, 16>(a, parts, wide, stream);
+  if (E <= 256) return launch_lanes<BF16, 8, 32>(a, parts, wide, stream);
+  if (E <= 512) return launch_lanes<BF16, 16, 32>(a, parts, wide, stream);
+  return launch_lanes<BF16, 32, 32>(a, parts, wide, stream);
+}
+
+template <bool BF16, int L, int V>
+cudaError_t launch_grad(const BalanceBackwardArgs &a, bool wide, cudaStream_t stream) {
+  const auto kernel =
+      wide ? (a.sigmoid ? balance_backward_kernel<BF16, L, V, true, true> : balance_backward_kernel<BF16, L, V, true, false>)
+           : (a.sigmoid ? balance_backward_kernel<BF16, L, V, false, true> : balance_backward_kernel<BF16, L, V, false, false>);
+  const int need = (a.num_tokens - 1) / kGradRows + 1, most = 1 << 20;
+  return launch_kernel(kernel, need < most ? need : most, kThreads, 0, stream, false, a);
+}
+
+template <bool BF16>
+cudaError_t launch_grad_of(const BalanceBackwardArgs &a, cudaStream_t stream) {
+  const int E = a.num_experts;
+  const bool wide = wide_rows(a.logits, a.row_stride, E, a.bf16) && wide_rows(a.add, E, E, a.bf16) &&
+                    wide_rows(a.grad_logits, E, E, a.bf16);
+  if (E <= 64) return launch_grad<BF16, 8, 8>(a, wide, stream);
+  if (E <= 128) return launch_grad<BF16, 8, 16>(a, wide, stream);
+  if (E <= 256) return launch_grad<BF16, 16, 16>(a, wide, stream);
+  if (E <= 512) return launch_grad<BF16, 32, 16>(a, wide, stream);
+  return launch_grad<BF16, 32, 32>(a, wide, stream);
+}
+
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int S) {
   const size_t segments = (size_t)blocks_of(T) + S;
-  return 2 * round16(segments * E * 4) + round16(segments * 4);
+  return 16 + 2 * round16(segments * E * 4) + 2 * round16(segments * 4) + round16((size_t)S * ((E + 31) / 32) * 4);
 }
 
 ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
-  const size_t segments = (size_t)blocks_of(a.num_tokens) + a.num_sequences, matrix = round16(segments * a.num_experts * 4);
-  char *at = static_cast<char *>(a.workspace);
-  const Parts parts{reinterpret_cast<float *>(at), reinterpret_cast<int32_t *>(at + matrix),
-                    reinterpret_cast<float *>(at + 2 * matrix)};
-  cudaError_t e = cudaSuccess;
-  if (a.num_tokens > 0) e = launch_kernel(balance_kernel, blocks_of(a.num_tokens), kThreads, 0, stream, false, a, parts);
-  if (e == cudaSuccess) e = launch_kernel(balance_join_kernel, 1, kThreads, 0, stream, false, a, parts);
+  const Parts parts = parts_of(a);
+  cudaError_t e;
+  if (a.num_tokens == 0)
+    e = launch_kernel(balance_empty_kernel, 1, kThreads, 0, stream, false, a, parts);
+  else if (a.num_experts > kLanesMost)
+    e = launch_kernel(balance_rows_kernel, parts.blocks, kThreads, 0, stream, false, a, parts);
+  else
+    e = a.bf16 ? launch_lanes_of<true>(a, parts, stream) : launch_lanes_of<false>(a, parts, stream);
+  const int64_t grid = (int64_t)a.num_sequences * ((a.num_experts + 31) / 32);
+  if (e == cudaSuccess) e = launch_kernel(balance_join_kernel, (int)grid, kJoinThreads, 0, stream, false, a, parts);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance launch");
 }
 
 ep_status_t launch_balance_backward(const BalanceBackwardArgs &a, cudaStream_t stream) {
   if (a.num_tokens == 0) return EP_OK;
-  const int grid = a.num_tokens < 65536 ? a.num_tokens : 65536;
-  const cudaError_t e = launch_kernel(balance_backward_kernel, grid, kThreads, 0, stream, false, a);
+  cudaError_t e;
+  if (a.num_experts > kLanesMost)
+    e = launch_kernel(balance_backward_rows_kernel, a.num_tokens < 65536 ? a.num_tokens : 65536, kThreads, 0, stream, false, a);
+  else
+    e = a.bf16 ? launch_grad_of<true>(a, stream) : launch_grad_of<false>(a, stream);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance_backward launch");
 }
 
