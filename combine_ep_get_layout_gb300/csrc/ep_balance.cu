@@ -10,11 +10,14 @@
 //
 // Bound by memory: one pass over the logits.  A row belongs to L lanes of a
 // warp, V columns each, so that a row's sums take log2 L exchanges and the
-// columns' sums stay in registers over all rows of a lane.  The sums over
+// columns' sums stay in registers over all rows of a lane.  A lane copies its
+// pieces of the rows ahead (cp.async) to shared memory that only it reads,
+// so they need no barrier.  The sums over
 // tokens run in a fixed order: a block's part of a sequence first (a
 // "segment"; block b's of sequence s is segment b + s, since later blocks
 // hold later sequences), then the segments.
 #include <algorithm>
+#include <atomic>
 
 #include "ep_device.cuh"
 #include "ep_ops.h"
@@ -25,9 +28,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocks = 456;      // that share the tokens: three an SM
 constexpr int kTokenStep = 32;    // a block's tokens come in these
 constexpr int kLanesMost = 1024;  // experts that a warp's lanes hold
+constexpr int kChoices = 4;       // of a thread in a pass: EP_MAX_TOPK rows of 8 lanes
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMost = 3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -79,27 +82,47 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
+__device__ __forceinline__ void copy_piece(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's groups are in flight.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // A row's V columns of a lane: by pieces of 16 bytes where rows allow it
-// (WIDE), by the same columns one by one where they do not.
+// (WIDE: through shared memory, `here` the lane's place, a block's threads
+// apart), by the same columns one by one where they do not.
 template <bool BF16, int L, int V, bool WIDE>
 struct Columns {
   static constexpr int kPiece = BF16 ? 8 : 4, kCount = V / kPiece;
   int E, lane;
   __device__ int column(int i, int j) const { return (i * L + lane) * kPiece + j; }
-  // Columns past the last expert read `none`.
-  __device__ void load(const char *row, float none, float (&v)[V]) const {
+  __device__ void fetch(char *here, const char *row) const {
+    if (!WIDE) return;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i)
+      if (column(i, 0) < E) copy_piece(smem_addr(here) + i * kThreads * 16, row + column(i, 0) * (BF16 ? 2 : 4));
+  }
+  // Where no copy comes: -infinity, or 0 of either type.
+  __device__ void clear(char *here, bool masked) const {
+    const int w = !masked ? 0 : BF16 ? (int)0xff80ff80u : (int)0xff800000u;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i)
+      if (WIDE && column(i, 0) >= E) *reinterpret_cast<int4 *>(here + i * kThreads * 16) = make_int4(w, w, w, w);
+  }
+  // Columns past the last expert read what `clear` put there, or `none`.
+  __device__ void load(const char *here, const char *row, float none, float (&v)[V]) const {
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
       if (WIDE) {
-        int4 f = make_int4(0, 0, 0, 0);
-        const bool there = column(i, 0) < E;
-        if (there) f = *reinterpret_cast<const int4 *>(row + column(i, 0) * (BF16 ? 2 : 4));
+        const int4 f = *reinterpret_cast<const int4 *>(here + i * kThreads * 16);
         const int w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
-          const float x = !BF16 ? __int_as_float(w[j % 4]) : j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-          v[i * kPiece + j] = there ? x : none;
-        }
+        for (int j = 0; j < kPiece; ++j)
+          v[i * kPiece + j] = !BF16 ? __int_as_float(w[j % 4]) : j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
       } else {
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) v[i * kPiece + j] = column(i, j) < E ? value_of(row, BF16, column(i, j)) : none;
@@ -225,14 +248,18 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
     far_scores<L, V, SIGMOID, GRAD>(l, s);
     return;
   }
-  s.inv = 1.0f / sum;
-  s.inv_soft = SIGMOID ? 1.0f / soft : s.inv;
+  s.inv = rcp_approx(sum);
+  s.inv_soft = SIGMOID ? rcp_approx(soft) : s.inv;
   s.lse = fmaf(c, kLn2, logf(soft));
 }
 
-// Tokens of a block, and blocks.
-int tokens_of(int T) { return std::max(kTokenStep, ((T - 1) / kBlocks + kTokenStep) / kTokenStep * kTokenStep); }
-int blocks_of(int T) { return T == 0 ? 0 : (T - 1) / tokens_of(T) + 1; }
+// Blocks that share the tokens: all at once on the SMs, two each, or three
+// where a lane has 16 columns or fewer (65 536 tokens, 256 experts: 411
+// blocks 28 us, 293 us at most two an SM 22).
+int blocks_at_once(int E) { return E <= 128 ? 456 : 304; }
+
+int tokens_of(int T, int blocks) { return std::max(kTokenStep, ((T - 1) / blocks + kTokenStep) / kTokenStep * kTokenStep); }
+int blocks_of(int T, int blocks) { return T == 0 ? 0 : (T - 1) / tokens_of(T, blocks) + 1; }
 
 struct Parts {
   float *probs;     // [segments][E]
@@ -267,94 +294,158 @@ __device__ void look_at_offsets(const int32_t *offsets, int T, int S, int32_t *h
   __syncthreads();
 }
 
-// The choices of rows a ... b, counted in shared memory and written with
-// their number.
-__device__ void count_choices(const BalanceArgs &p, int a, int b, int64_t segment, int32_t *s_counts, const Parts &parts) {
-  __shared__ int s_chosen;
-  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) s_counts[e] = 0;
-  if (threadIdx.x == 0) s_chosen = 0;
-  __syncthreads();
-  int chosen = 0;
-  for (int64_t i = (int64_t)a * p.num_topk + threadIdx.x; i < (int64_t)b * p.num_topk; i += blockDim.x) {
-    const int64_t e = p.topk_idx[i];
-    if (e >= 0 && e < p.num_experts) {
-      atomicAdd(&s_counts[e], 1);
-      ++chosen;
-    }
-  }
-  chosen = __reduce_add_sync(0xffffffffu, chosen);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&s_chosen, chosen);
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) parts.counts[segment * p.num_experts + e] = s_counts[e];
-  if (threadIdx.x == 0) parts.chosen[segment] = s_chosen;
-}
+// Passes of rows in shared memory: up to 64 KB (16 columns a lane in fp32),
+// 96 KB (32).
+template <bool BF16, int V>
+constexpr int ahead() { return V > 16 && !BF16 ? 3 : 4; }
+template <bool BF16, int V>
+constexpr int pass_bytes() { return kThreads * V * (BF16 ? 2 : 4); }
 
 template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(BalanceArgs p, Parts parts) {
-  extern __shared__ float s_probs[];  // [warps][experts], and the counts
+  extern __shared__ int4 s_rows[];  // [ahead][pieces][threads], then [warps][experts] sums and [experts] counts
   __shared__ float s_z[kWarps];
-  constexpr int kRows = kThreads / L;  // at a time
-  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row = threadIdx.x / L;
+  __shared__ int s_chosen[kWarps];
+  constexpr int kRows = kThreads / L, kAhead = ahead<BF16, V>(), kPass = pass_bytes<BF16, V>();
+  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, K = p.num_topk;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Columns<BF16, L, V, WIDE> columns{E, (int)threadIdx.x % L};
-  const int t0 = blockIdx.x * parts.tokens, t1 = t0 + min(T - t0, parts.tokens);
+  float *s_probs = reinterpret_cast<float *>(reinterpret_cast<char *>(s_rows) + (WIDE ? kAhead * kPass : 0));
+  int *s_counts = reinterpret_cast<int *>(s_probs + kWarps * E);
+  char *mine = reinterpret_cast<char *>(s_rows + threadIdx.x);
+  const int t0 = (int)blockIdx.x < parts.blocks ? blockIdx.x * parts.tokens : 0, count = min(T - t0, parts.tokens), row = threadIdx.x / L;
   const int64_t apart = p.row_stride * (BF16 ? 2 : 4);
+  const char *from = static_cast<const char *>(p.logits) + (t0 + row) * apart;
+  for (int e = threadIdx.x; e < E; e += kThreads) s_counts[e] = 0;
+  for (int i = 0; i < kAhead; ++i) columns.clear(mine + i * kPass, true);
   griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x == 0) look_at_offsets(p.seq_offsets, T, S, parts.head);
-  float z = 0.0f;
-  for (int s = sequence_of(p.seq_offsets, T, S, t0); s < S; ++s) {
-    const int a = max(t0, offset_of(p.seq_offsets, T, s)), b = min(t1, offset_of(p.seq_offsets, T, s + 1));
-    if (a >= t1) break;
-    if (a >= b) continue;
-    const int64_t segment = blockIdx.x + s;
-    float acc[V];
+  if (blockIdx.x == parts.blocks) {  // the last block has no rows
+    look_at_offsets(p.seq_offsets, T, S, parts.head);
+    return;
+  }
+  // passes number the rows from t0 on
+  const int64_t pass_apart = kRows * apart;
+  int to_fetch = row;
+  const char *next = from;
+  const auto fetch = [&](int slot) {
+    if (to_fetch < count) columns.fetch(mine + slot * kPass, next);
+    to_fetch += kRows;
+    next += pass_apart;
+    copies_commit();
+  };
+  for (int i = 0; WIDE && i < kAhead; ++i) fetch(i);
+  // the choices of a pass's rows, kThreads apart: read a pass ahead
+  int64_t choice[kChoices];
+  int choice_row[kChoices];
+  const int64_t *choices = p.topk_idx + (int64_t)t0 * K + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = 0.0f;
-    const char *from = static_cast<const char *>(p.logits) + a * apart;
-    for (int i = 0; i < b - a; i += kRows) {
-      const bool here = i + row < b - a;
-      float l[V];
-      if (here) {
-        columns.load(from + (i + row) * apart, kNegInf, l);
-      } else {  // all lanes take part in the exchanges
+  for (int i = 0; i < kChoices; ++i) {
+    const int at = threadIdx.x + i * kThreads;
+    choice_row[i] = at < kRows * K ? at / K : count;
+  }
+  const auto read_choices = [&](int first) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) l[j] = 0.0f;
-      }
-      Scores<V, SIGMOID, false> sc;
-      scores_of<L>(l, sc);
+    for (int i = 0; i < kChoices; ++i) {
+      if (i * kThreads >= kRows * K) break;
+      choice[i] = choice_row[i] < count - first ? choices[i * kThreads] : -1;
+    }
+    choices += kRows * K;
+  };
+  read_choices(0);
+  int s = sequence_of(p.seq_offsets, T, S, t0), chosen = 0;
+  // this block's rows of sequence s, from t0 on
+  int a = s < S ? max(t0, offset_of(p.seq_offsets, T, s)) - t0 : count;
+  int b = s < S ? min(t0 + count, offset_of(p.seq_offsets, T, s + 1)) - t0 : count;
+  float acc[V], z = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+  __syncthreads();
+  int slot = 0;
+  for (int done = 0; done < count; done += kRows, from += pass_apart) {
+    const int r = done + row, behind = done + kRows;
+    float l[V];
+    if (WIDE) copies_wait<kAhead - 1>();
+    columns.load(mine + slot * kPass, r < count ? from : from - row * apart, kNegInf, l);
+    if (r >= count) {  // all lanes take part in the exchanges
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[j] = 0.0f;
+    }
+    if (WIDE) fetch(slot);
+    if (++slot == kAhead) slot = 0;
+    int now[kChoices];
+#pragma unroll
+    for (int i = 0; i < kChoices; ++i) {
+      if (i * kThreads >= kRows * K) break;
+      now[i] = choice[i] >= 0 && choice[i] < E ? (int)choice[i] : -1;
+    }
+    if (behind < count) read_choices(behind);
+    Scores<V, SIGMOID, false> sc;
+    scores_of<L>(l, sc);
+    // the sequences that the pass's rows belong to: mostly one
+    while (a < behind && s < S) {
+      const bool here = r >= a && r < b;
       const float inv = here ? sc.inv : 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] = fmaf(sc.e[j], inv, acc[j]);
       if (here && columns.lane == 0) z = fmaf(sc.lse, sc.lse, z);
-    }
-    // the warp's rows, then the warps
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-#pragma unroll
-      for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-    }
-    if (lane < L) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = columns.column(i / columns.kPiece, i % columns.kPiece);
-        if (c < E) s_probs[warp * E + c] = acc[i];
+      for (int i = 0; i < kChoices; ++i) {
+        if (i * kThreads >= kRows * K) break;
+        const int of = done + choice_row[i];
+        if (now[i] >= 0 && of >= a && of < b) {
+          atomicAdd(&s_counts[now[i]], 1);
+          ++chosen;
+        }
       }
-    }
-    count_choices(p, a, b, segment, reinterpret_cast<int32_t *>(s_probs + kWarps * E), parts);
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float sum = s_probs[e];
+      if (b > behind || (b == behind && b < count)) break;
+      // the sequence, or the block, ends here: its segment.  The warp's rows,
+      // then the warps.
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) sum += s_probs[w * E + e];
-      parts.probs[segment * E + e] = sum;
+      for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+      }
+      if (lane < L) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int c = columns.column(j / columns.kPiece, j % columns.kPiece);
+          if (c < E) s_probs[warp * E + c] = acc[j];
+        }
+      }
+      chosen = __reduce_add_sync(0xffffffffu, chosen);
+      if (lane == 0) s_chosen[warp] = chosen;
+      __syncthreads();
+      const int64_t segment = (int64_t)blockIdx.x + s;
+      for (int e = threadIdx.x; e < E; e += kThreads) {
+        float sum = s_probs[e];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) sum += s_probs[w * E + e];
+        parts.probs[segment * E + e] = sum;
+        parts.counts[segment * E + e] = s_counts[e];
+        s_counts[e] = 0;
+      }
+      if (threadIdx.x == 0) {
+        for (int w = 1; w < kWarps; ++w) chosen += s_chosen[w];
+        parts.chosen[segment] = chosen;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+      chosen = 0;
+      do {  // the next one with rows
+        ++s;
+        a = s < S ? max(t0, offset_of(p.seq_offsets, T, s)) - t0 : count;
+        b = s < S ? min(t0 + count, offset_of(p.seq_offsets, T, s + 1)) - t0 : count;
+      } while (s < S && a < count && a >= b);
+      if (a >= count) s = S;
     }
-    __syncthreads();
   }
   // (only a row's first lane has added to z)
   z = lanes_sum<32>(z);
   if (lane == 0) s_z[warp] = z;
   __syncthreads();
-  if (threadIdx.x == 0 && t0 < t1) {
+  if (threadIdx.x == 0) {
     for (int w = 1; w < kWarps; ++w) z += s_z[w];
     parts.z[blockIdx.x] = z;
   }
@@ -409,6 +500,28 @@ __device__ Row row_of(const void *logits, bool bf16, int64_t at, int E, bool sig
   return r;
 }
 
+// The choices of rows a ... b, counted in shared memory and written with
+// their number.
+__device__ void count_choices(const BalanceArgs &p, int a, int b, int64_t segment, int32_t *s_counts, const Parts &parts) {
+  __shared__ int s_chosen;
+  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) s_counts[e] = 0;
+  if (threadIdx.x == 0) s_chosen = 0;
+  __syncthreads();
+  int chosen = 0;
+  for (int64_t i = (int64_t)a * p.num_topk + threadIdx.x; i < (int64_t)b * p.num_topk; i += blockDim.x) {
+    const int64_t e = p.topk_idx[i];
+    if (e >= 0 && e < p.num_experts) {
+      atomicAdd(&s_counts[e], 1);
+      ++chosen;
+    }
+  }
+  chosen = __reduce_add_sync(0xffffffffu, chosen);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&s_chosen, chosen);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) parts.counts[segment * p.num_experts + e] = s_counts[e];
+  if (threadIdx.x == 0) parts.chosen[segment] = s_chosen;
+}
+
 __global__ void __launch_bounds__(kThreads) balance_rows_kernel(BalanceArgs p, Parts parts) {
   __shared__ float s_reduce[kWarps];
   __shared__ float s_probs[EP_MAX_EXPERTS];
@@ -416,7 +529,10 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(BalanceArgs p, P
   griddep_wait();
   griddep_launch_dependents();
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
-  if (blockIdx.x == 0) look_at_offsets(p.seq_offsets, T, S, parts.head);
+  if (blockIdx.x == parts.blocks) {  // the last block has no rows
+    look_at_offsets(p.seq_offsets, T, S, parts.head);
+    return;
+  }
   const int t0 = blockIdx.x * parts.tokens, t1 = t0 + min(T - t0, parts.tokens);
   float z = 0.0f;
   for (int s = sequence_of(p.seq_offsets, T, S, t0); s < S; ++s) {
@@ -444,53 +560,68 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(BalanceArgs p, P
 constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
 
 // A sequence's segments, 32 experts a block: 32 warps take every 32nd
-// segment, then are added in their order.  The block that ends last adds up
-// the losses.
+// segment, then a warp an expert adds those up (in the order of a shuffled
+// tree).  Block 0 adds up z too; the block that ends last, the balance loss.
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs p, Parts parts) {
-  __shared__ float s_probs[kJoinWarps][33], s_reduce[kJoinWarps];
+  __shared__ float s_probs[kJoinWarps][33], s_part[kJoinWarps], s_z[kJoinWarps];
   __shared__ int s_counts[kJoinWarps][33], s_chosen[kJoinWarps], s_last;
+  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
+  const int s = blockIdx.x / tiles, first = blockIdx.x % tiles * 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   griddep_wait();
   griddep_launch_dependents();
-  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
-  const int s = blockIdx.x / tiles, e = blockIdx.x % tiles * 32 + threadIdx.x % 32;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int a = offset_of(p.seq_offsets, T, s), b = offset_of(p.seq_offsets, T, s + 1);
   const int b0 = a / parts.tokens, b1 = b > a ? (b - 1) / parts.tokens : b0 - 1;
   const int full = parts.head[0];
-  float prob = 0.0f;
+  float prob = 0.0f, z = 0.0f;
   int count = 0, chosen = 0;
-  if (e < E) {
-#pragma unroll 4
+  for (int i = b0 + threadIdx.x; i <= b1; i += kJoinThreads) chosen += parts.chosen[i + s];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < parts.blocks; i += kJoinThreads) z += parts.z[i];
+  if (first + lane < E) {
+    const int64_t from = (int64_t)s * E + first + lane;
+#pragma unroll 8
     for (int i = b0 + warp; i <= b1; i += kJoinWarps) {
-      prob += parts.probs[(int64_t)(i + s) * E + e];
-      count += parts.counts[(int64_t)(i + s) * E + e];
+      prob += parts.probs[from + (int64_t)i * E];
+      count += parts.counts[from + (int64_t)i * E];
     }
   }
-  for (int i = b0 + threadIdx.x; i <= b1; i += kJoinThreads) chosen += parts.chosen[i + s];
   s_probs[warp][lane] = prob;
   s_counts[warp][lane] = count;
   chosen = __reduce_add_sync(0xffffffffu, chosen);
-  if (lane == 0) s_chosen[warp] = chosen;
+  z = lanes_sum<32>(z);
+  if (lane == 0) {
+    s_chosen[warp] = chosen;
+    s_z[warp] = z;
+  }
   __syncthreads();
-  if (warp == 0) {
-    chosen = __reduce_add_sync(0xffffffffu, s_chosen[lane]);
-    for (int w = 1; w < kJoinWarps; ++w) {
-      prob += s_probs[w][lane];
-      count += s_counts[w][lane];
-    }
-    float part = 0.0f;
-    if (e < E) {
-      const int64_t at = (int64_t)s * E + e;
-      const float mean = b > a ? prob / (b - a) : 0.0f;
-      const float share = chosen > 0 ? (float)E * count / chosen / full : 0.0f;
+  prob = lanes_sum<32>(s_probs[lane][warp]);
+  count = __reduce_add_sync(0xffffffffu, s_counts[lane][warp]);
+  chosen = __reduce_add_sync(0xffffffffu, s_chosen[lane]);
+  const int e = first + warp;
+  float part = 0.0f;
+  if (e < E) {
+    const int64_t at = (int64_t)s * E + e;
+    const float mean = b > a ? prob / (b - a) : 0.0f;
+    const float share = chosen > 0 ? (float)E * count / chosen / full : 0.0f;
+    if (lane == 0) {
       p.probs[at] = mean;
       p.counts[at] = count;
       p.slopes[at] = b > a ? share / (b - a) : 0.0f;
-      part = share * mean;
     }
-    part = lanes_sum<32>(part);
+    part = share * mean;
+  }
+  if (lane == 0) s_part[warp] = part;
+  __syncthreads();
+  if (warp == 0) {
+    part = lanes_sum<32>(s_part[lane]);
+    z = lanes_sum<32>(s_z[lane]);
     if (lane == 0) {
       parts.balance[blockIdx.x] = part;
+      if (blockIdx.x == 0) {
+        const int tokens = offset_of(p.seq_offsets, T, S) - offset_of(p.seq_offsets, T, 0);
+        p.losses[1] = parts.head[1] != 0 ? __int_as_float(0x7fffffff) : tokens > 0 ? z / tokens : 0.0f;
+      }
       __threadfence();
       s_last = atomicAdd(parts.head + 2, 1) == (int)gridDim.x - 1;
     }
@@ -498,18 +629,14 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  float balance = 0.0f, z = 0.0f;
+  float balance = 0.0f;
   for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += kJoinThreads) balance += __ldcg(parts.balance + i);
-  for (int i = threadIdx.x; i < parts.blocks; i += kJoinThreads) z += parts.z[i];
-  balance = block_reduce(balance, s_reduce, Sum());
-  z = block_reduce(z, s_reduce, Sum());
-  if (threadIdx.x == 0) {
-    const int tokens = offset_of(p.seq_offsets, T, S) - offset_of(p.seq_offsets, T, 0);
-    const float nan = __int_as_float(0x7fffffff);
-    const bool bad = parts.head[1] != 0;
-    p.losses[0] = bad ? nan : balance;
-    p.losses[1] = bad ? nan : tokens > 0 ? z / tokens : 0.0f;
-  }
+  balance = lanes_sum<32>(balance);
+  if (lane == 0) s_part[warp] = balance;
+  __syncthreads();
+  if (warp != 0) return;
+  balance = lanes_sum<32>(s_part[lane]);
+  if (lane == 0) p.losses[0] = parts.head[1] != 0 ? __int_as_float(0x7fffffff) : balance;
 }
 
 // Without tokens nobody else looks at the offsets.
@@ -519,52 +646,79 @@ __global__ void __launch_bounds__(kThreads) balance_empty_kernel(BalanceArgs p, 
   look_at_offsets(p.seq_offsets, p.num_tokens, p.num_sequences, parts.head);
 }
 
-// The gradients' rows of a block.
-constexpr int kGradRows = 64;
-
 template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads, 2) balance_backward_kernel(BalanceBackwardArgs p) {
-  constexpr int kRows = kThreads / L, kSize = BF16 ? 2 : 4;
+__global__ void __launch_bounds__(kThreads, 2) balance_backward_kernel(BalanceBackwardArgs p, int tokens) {
+  extern __shared__ int4 s_rows[];  // [ahead][logits, add][pieces][threads]
+  constexpr int kRows = kThreads / L, kSize = BF16 ? 2 : 4, kPass = pass_bytes<BF16, V>();
+  constexpr int kAhead = V > 16 && !BF16 ? 1 : 3;
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
   const Columns<BF16, L, V, WIDE> columns{E, (int)threadIdx.x % L};
-  const int row = threadIdx.x / L;
+  char *mine = reinterpret_cast<char *>(s_rows + threadIdx.x);
+  const int t0 = blockIdx.x * tokens, count = min(T - t0, tokens), row = threadIdx.x / L;
+  const int64_t apart = p.row_stride * kSize, packed = (int64_t)E * kSize;
+  const char *from = static_cast<const char *>(p.logits) + (t0 + row) * apart;
+  const char *add_from = static_cast<const char *>(p.add) + (t0 + row) * packed;
+  char *out = static_cast<char *>(p.grad_logits) + (t0 + row) * packed;
+  for (int i = 0; i < kAhead; ++i) {
+    columns.clear(mine + i * 2 * kPass, true);
+    columns.clear(mine + (i * 2 + 1) * kPass, false);
+  }
   griddep_wait();
   griddep_launch_dependents();
+  const int64_t pass_apart = kRows * apart, pass_packed = kRows * packed;
+  int to_fetch = row;
+  const char *next = from, *next_add = add_from;
+  const auto fetch = [&](int slot) {
+    if (to_fetch < count) {
+      columns.fetch(mine + slot * 2 * kPass, next);
+      if (p.add != nullptr) columns.fetch(mine + (slot * 2 + 1) * kPass, next_add);
+    }
+    to_fetch += kRows;
+    next += pass_apart;
+    next_add += pass_packed;
+    copies_commit();
+  };
+  for (int i = 0; WIDE && i < kAhead; ++i) fetch(i);
   const int first = offset_of(p.seq_offsets, T, 0), last = offset_of(p.seq_offsets, T, S);
   const float db = p.grad_losses[0], dz = p.grad_losses[1] * 2.0f / max(1, last - first);
-  for (int64_t t0 = (int64_t)blockIdx.x * kGradRows; t0 < T; t0 += (int64_t)gridDim.x * kGradRows) {
-    float slope[V];
-    int end = -1;  // of the sequence whose slopes are held
-    for (int i = 0; i < kGradRows; i += kRows) {
-      const int64_t t64 = t0 + i + row;
-      const bool here = t64 < T;
-      const int64_t t = here ? t64 : T - 1;  // all lanes take part in the exchanges
-      if (t >= end) {
-        const int s = sequence_of(p.seq_offsets, T, S, (int)t);
-        end = s < S ? offset_of(p.seq_offsets, T, s + 1) : INT32_MAX;
-        if (s < S) columns.floats(p.slopes + (int64_t)s * E, slope);
-      }
-      const bool inside = end < INT32_MAX && t >= first;
-      float l[V], add[V];
-      columns.load(static_cast<const char *>(p.logits) + t * p.row_stride * kSize, kNegInf, l);
-      if (p.add != nullptr) columns.load(static_cast<const char *>(p.add) + t * E * kSize, 0.0f, add);
-      Scores<V, SIGMOID, true> sc;
-      scores_of<L>(l, sc);
-      float dot = 0.0f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) dot = fmaf(sc.e[j], slope[j], dot);
-      dot = lanes_sum<L>(dot) * sc.inv;
-      const float scale = db * sc.inv, tail = fminf(fmaxf(dz * sc.lse * sc.inv_soft, -kMost), kMost);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float d = sc.e[j] * scale * (slope[j] - dot);
-        if (SIGMOID) d *= sc.side[SIGMOID ? j : 0];
-        d = fmaf(SIGMOID ? sc.soft[SIGMOID ? j : 0] : sc.e[j], tail, d);
-        d = inside ? d : 0.0f;
-        l[j] = p.add != nullptr ? add[j] + d : d;
-      }
-      if (here) columns.store(static_cast<char *>(p.grad_logits) + t * E * kSize, l);
+  float slope[V];
+  int end = -1, slot = 0;  // of the sequence whose slopes are held
+  for (int done = 0; done < count; done += kRows, from += pass_apart, add_from += pass_packed, out += pass_packed) {
+    const int r = done + row, t = t0 + r;
+    const bool there = r < count;
+    if (there && t >= end) {
+      const int s = sequence_of(p.seq_offsets, T, S, t);
+      end = s < S ? offset_of(p.seq_offsets, T, s + 1) : INT32_MAX;
+      if (s < S) columns.floats(p.slopes + (int64_t)s * E, slope);
     }
+    const bool inside = there && end < INT32_MAX && t >= first;
+    const char *here = mine + slot * 2 * kPass;
+    float l[V], add[V];
+    if (WIDE) copies_wait<kAhead - 1>();
+    columns.load(here, there ? from : from - row * apart, kNegInf, l);
+    if (p.add != nullptr) columns.load(here + kPass, there ? add_from : add_from - row * packed, 0.0f, add);
+    if (!there) {  // all lanes take part in the exchanges
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[j] = 0.0f;
+    }
+    if (WIDE) fetch(slot);
+    if (++slot == kAhead) slot = 0;
+    Scores<V, SIGMOID, true> sc;
+    scores_of<L>(l, sc);
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) dot = fmaf(sc.e[j], slope[j], dot);
+    dot = lanes_sum<L>(dot) * sc.inv;
+    const float scale = db * sc.inv, tail = fminf(fmaxf(dz * sc.lse * sc.inv_soft, -kMost), kMost);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float d = sc.e[j] * scale * (slope[j] - dot);
+      if (SIGMOID) d *= sc.side[SIGMOID ? j : 0];
+      d = fmaf(SIGMOID ? sc.soft[SIGMOID ? j : 0] : sc.e[j], tail, d);
+      d = inside ? d : 0.0f;
+      l[j] = p.add != nullptr ? add[j] + d : d;
+    }
+    if (there) columns.store(out, l);
   }
 }
 
@@ -612,7 +766,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_rows_kernel(Balance
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 Parts parts_of(const BalanceArgs &a) {
-  const size_t E = a.num_experts, segments = (size_t)blocks_of(a.num_tokens) + a.num_sequences;
+  const size_t E = a.num_experts, segments = (size_t)blocks_of(a.num_tokens, blocks_at_once(a.num_experts)) + a.num_sequences;
   char *at = static_cast<char *>(a.workspace);
   const auto take = [&](size_t bytes) {
     char *p = at;
@@ -626,8 +780,8 @@ Parts parts_of(const BalanceArgs &a) {
   p.chosen = reinterpret_cast<int32_t *>(take(segments * 4));
   p.z = reinterpret_cast<float *>(take(segments * 4));
   p.balance = reinterpret_cast<float *>(take(a.num_sequences * ((E + 31) / 32) * 4));
-  p.tokens = tokens_of(a.num_tokens);
-  p.blocks = blocks_of(a.num_tokens);
+  p.tokens = tokens_of(a.num_tokens, blocks_at_once(a.num_experts));
+  p.blocks = blocks_of(a.num_tokens, blocks_at_once(a.num_experts));
   return p;
 }
 
@@ -637,62 +791,98 @@ bool wide_rows(const void *p, int64_t stride, int E, bool bf16) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % piece == 0 && E % piece == 0;
 }
 
+// The limit of shared memory belongs to the kernel: set once, to the most that
+// any call needs.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel *kernel, size_t bytes, std::atomic<bool> *ready) {
+  if (*ready) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  *ready = e == cudaSuccess;
+  return e;
+}
+
+template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
+cudaError_t launch_lanes_as(const BalanceArgs &a, const Parts &parts, int device, cudaStream_t stream) {
+  static std::atomic<bool> ready[64];
+  const auto smem = [](int experts) {
+    return (size_t)(WIDE ? ahead<BF16, V>() * pass_bytes<BF16, V>() : 0) + (size_t)(kWarps + 1) * experts * 4;
+  };
+  const auto kernel = balance_kernel<BF16, L, V, WIDE, SIGMOID>;
+  const cudaError_t e = allow_shared(kernel, smem(L * V), &ready[device]);
+  return e != cudaSuccess ? e : launch_kernel(kernel, parts.blocks + 1, kThreads, smem(a.num_experts), stream, false, a, parts);
+}
+
 template <bool BF16, int L, int V>
-cudaError_t launch_lanes(const BalanceArgs &a, const Parts &parts, bool wide, cudaStream_t stream) {
-  const size_t smem = (size_t)(kWarps + 1) * a.num_experts * 4;
-  const auto kernel = wide ? (a.sigmoid ? balance_kernel<BF16, L, V, true, true> : balance_kernel<BF16, L, V, true, false>)
-                           : (a.sigmoid ? balance_kernel<BF16, L, V, false, true> : balance_kernel<BF16, L, V, false, false>);
-  return launch_kernel(kernel, parts.blocks, kThreads, smem, stream, false, a, parts);
+cudaError_t launch_lanes(const BalanceArgs &a, const Parts &parts, bool wide, int device, cudaStream_t stream) {
+  if (wide)
+    return a.sigmoid ? launch_lanes_as<BF16, L, V, true, true>(a, parts, device, stream)
+                     : launch_lanes_as<BF16, L, V, true, false>(a, parts, device, stream);
+  return a.sigmoid ? launch_lanes_as<BF16, L, V, false, true>(a, parts, device, stream)
+                   : launch_lanes_as<BF16, L, V, false, false>(a, parts, device, stream);
 }
 
 template <bool BF16>
-cudaError_t launch_lanes_of(const BalanceArgs &a, const Parts &parts, cudaStream_t stream) {
+cudaError_t launch_lanes_of(const BalanceArgs &a, const Parts &parts, int device, cudaStream_t stream) {
   const bool wide = wide_rows(a.logits, a.row_stride, a.num_experts, a.bf16);
   const int E = a.num_experts;
-  if (E <= 64) return launch_lanes<BF16, 8, 8>(a, parts, wide, stream);
-  if (E <= 128) return launch_lanes<BF16, 8, 16>(a, parts, wide, stream);
-  if (E <= 256) return launch_lanes<BF16, 8, 32>(a, parts, wide, stream);
-  if (E <= 512) return launch_lanes<BF16, 16, 32>(a, parts, wide, stream);
-  return launch_lanes<BF16, 32, 32>(a, parts, wide, stream);
+  if (E <= 64) return launch_lanes<BF16, 8, 8>(a, parts, wide, device, stream);
+  if (E <= 128) return launch_lanes<BF16, 8, 16>(a, parts, wide, device, stream);
+  if (E <= 256) return launch_lanes<BF16, 8, 32>(a, parts, wide, device, stream);
+  if (E <= 512) return launch_lanes<BF16, 16, 32>(a, parts, wide, device, stream);
+  return launch_lanes<BF16, 32, 32>(a, parts, wide, device, stream);
+}
+
+constexpr int kGradBlocks = 304;  // two an SM
+
+template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
+cudaError_t launch_grad_as(const BalanceBackwardArgs &a, int device, cudaStream_t stream) {
+  static std::atomic<bool> ready[64];
+  const size_t smem = WIDE ? (size_t)(V > 16 && !BF16 ? 1 : 3) * 2 * pass_bytes<BF16, V>() : 0;
+  const auto kernel = balance_backward_kernel<BF16, L, V, WIDE, SIGMOID>;
+  const cudaError_t e = allow_shared(kernel, smem, &ready[device]);
+  return e != cudaSuccess ? e : launch_kernel(kernel, blocks_of(a.num_tokens, kGradBlocks), kThreads, smem, stream, false, a,
+                                                     tokens_of(a.num_tokens, kGradBlocks));
 }
 
 template <bool BF16, int L, int V>
-cudaError_t launch_grad(const BalanceBackwardArgs &a, bool wide, cudaStream_t stream) {
-  const auto kernel =
-      wide ? (a.sigmoid ? balance_backward_kernel<BF16, L, V, true, true> : balance_backward_kernel<BF16, L, V, true, false>)
-           : (a.sigmoid ? balance_backward_kernel<BF16, L, V, false, true> : balance_backward_kernel<BF16, L, V, false, false>);
-  const int need = (a.num_tokens - 1) / kGradRows + 1, most = 1 << 20;
-  return launch_kernel(kernel, need < most ? need : most, kThreads, 0, stream, false, a);
+cudaError_t launch_grad(const BalanceBackwardArgs &a, bool wide, int device, cudaStream_t stream) {
+  if (wide)
+    return a.sigmoid ? launch_grad_as<BF16, L, V, true, true>(a, device, stream)
+                     : launch_grad_as<BF16, L, V, true, false>(a, device, stream);
+  return a.sigmoid ? launch_grad_as<BF16, L, V, false, true>(a, device, stream)
+                   : launch_grad_as<BF16, L, V, false, false>(a, device, stream);
 }
 
 template <bool BF16>
-cudaError_t launch_grad_of(const BalanceBackwardArgs &a, cudaStream_t stream) {
+cudaError_t launch_grad_of(const BalanceBackwardArgs &a, int device, cudaStream_t stream) {
   const int E = a.num_experts;
   const bool wide = wide_rows(a.logits, a.row_stride, E, a.bf16) && wide_rows(a.add, E, E, a.bf16) &&
                     wide_rows(a.grad_logits, E, E, a.bf16);
-  if (E <= 64) return launch_grad<BF16, 8, 8>(a, wide, stream);
-  if (E <= 128) return launch_grad<BF16, 8, 16>(a, wide, stream);
-  if (E <= 256) return launch_grad<BF16, 16, 16>(a, wide, stream);
-  if (E <= 512) return launch_grad<BF16, 32, 16>(a, wide, stream);
-  return launch_grad<BF16, 32, 32>(a, wide, stream);
+  if (E <= 64) return launch_grad<BF16, 8, 8>(a, wide, device, stream);
+  if (E <= 128) return launch_grad<BF16, 8, 16>(a, wide, device, stream);
+  if (E <= 256) return launch_grad<BF16, 16, 16>(a, wide, device, stream);
+  if (E <= 512) return launch_grad<BF16, 32, 16>(a, wide, device, stream);
+  return launch_grad<BF16, 32, 32>(a, wide, device, stream);
 }
 
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int S) {
-  const size_t segments = (size_t)blocks_of(T) + S;
+  const size_t segments = (size_t)blocks_of(T, blocks_at_once(E)) + S;
   return 16 + 2 * round16(segments * E * 4) + 2 * round16(segments * 4) + round16((size_t)S * ((E + 31) / 32) * 4);
 }
 
 ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
   const Parts parts = parts_of(a);
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
   cudaError_t e;
   if (a.num_tokens == 0)
     e = launch_kernel(balance_empty_kernel, 1, kThreads, 0, stream, false, a, parts);
   else if (a.num_experts > kLanesMost)
-    e = launch_kernel(balance_rows_kernel, parts.blocks, kThreads, 0, stream, false, a, parts);
+    e = launch_kernel(balance_rows_kernel, parts.blocks + 1, kThreads, 0, stream, false, a, parts);
   else
-    e = a.bf16 ? launch_lanes_of<true>(a, parts, stream) : launch_lanes_of<false>(a, parts, stream);
+    e = a.bf16 ? launch_lanes_of<true>(a, parts, di->device, stream) : launch_lanes_of<false>(a, parts, di->device, stream);
   const int64_t grid = (int64_t)a.num_sequences * ((a.num_experts + 31) / 32);
   if (e == cudaSuccess) e = launch_kernel(balance_join_kernel, (int)grid, kJoinThreads, 0, stream, false, a, parts);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance launch");
@@ -700,11 +890,13 @@ ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
 
 ep_status_t launch_balance_backward(const BalanceBackwardArgs &a, cudaStream_t stream) {
   if (a.num_tokens == 0) return EP_OK;
+  const DeviceInfo *di = current_device_info();
+  if (di == nullptr) return EP_ERR_CUDA;
   cudaError_t e;
   if (a.num_experts > kLanesMost)
     e = launch_kernel(balance_backward_rows_kernel, a.num_tokens < 65536 ? a.num_tokens : 65536, kThreads, 0, stream, false, a);
   else
-    e = a.bf16 ? launch_grad_of<true>(a, stream) : launch_grad_of<false>(a, stream);
+    e = a.bf16 ? launch_grad_of<true>(a, di->device, stream) : launch_grad_of<false>(a, di->device, stream);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance_backward launch");
 }
 
