@@ -201,9 +201,11 @@ ep_status_t launch_dense(const DenseArgs &a, cudaStream_t stream) {
   p.bias_bf16 = a.bias_bf16;
   p.residual = a.residual;
   p.activation = a.activation;
-  p.out_fp32 = !a.out_bf16;
   const ep_status_t s = weight_map(p, pairs ? kDenseGated : kDense, a.w, p.wide, a.hidden);
   if (s != EP_OK) return s;
+  if (!a.out_bf16)
+    return pairs ? launch_rows_form<kDenseGated32>(p, a.x, a.row_stride, stream)
+                 : launch_rows_form<kDense32>(p, a.x, a.row_stride, stream);
   return pairs ? launch_rows_form<kDenseGated>(p, a.x, a.row_stride, stream)
                : launch_rows_form<kDense>(p, a.x, a.row_stride, stream);
 }

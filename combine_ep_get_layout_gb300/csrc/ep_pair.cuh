@@ -16,6 +16,11 @@
 //   kDense, kDenseGated, kDenseGradX, kDenseGradW
 //                    the first four with one expert that has every row, and
 //                    the first two with bias, activation and residual
+//   kDense32, kDenseGated32
+//                    those two for results kept in fp32.  The tensor cores
+//                    cut off what does not fit beside a growing sum: over
+//                    7168 inner elements an error of 8e-6.  So their sums of
+//                    kRun steps are added up in registers, rounded: 6e-7.
 // An inner step is 64 elements, a 128-byte row of shared memory in the
 // 128-byte swizzle; the transposed operands are read with their outer
 // dimension contiguous, so nothing is ever transposed in memory.
@@ -46,11 +51,12 @@ namespace ep {
 
 namespace {
 
-enum Form { kPlain, kGated, kGradX, kGradW, kAdapter, kDense, kDenseGated, kDenseGradX, kDenseGradW };
-__host__ __device__ constexpr bool gated(Form f) { return f == kGated || f == kDenseGated; }
+enum Form { kPlain, kGated, kGradX, kGradW, kAdapter, kDense, kDenseGated, kDense32, kDenseGated32, kDenseGradX, kDenseGradW };
+__host__ __device__ constexpr bool gated(Form f) { return f == kGated || f == kDenseGated || f == kDenseGated32; }
 __host__ __device__ constexpr bool grad_x(Form f) { return f == kGradX || f == kDenseGradX; }
 __host__ __device__ constexpr bool grad_w(Form f) { return f == kGradW || f == kDenseGradW; }
-__host__ __device__ constexpr bool dense(Form f) { return f == kDense || f == kDenseGated; }  // with the epilogue
+__host__ __device__ constexpr bool dense(Form f) { return f >= kDense && f <= kDenseGated32; }  // with the epilogue
+__host__ __device__ constexpr bool runs(Form f) { return f == kDense32 || f == kDenseGated32; }
 __host__ __device__ constexpr bool single(Form f) { return f >= kAdapter; }  // one expert, its rows known to the host
 
 // Warps: 0 and 3 copies of A and B, 1 products, 2 row ends (kGradW), 4-11
@@ -60,6 +66,8 @@ __host__ __device__ constexpr int threads_of(Form f) { return f == kAdapter ? 38
 constexpr int kInner = 64;           // elements of an inner step
 constexpr int kABytes = 128 * 128;   // a CTA's half of A for one step
 constexpr int kMaxCols = 256;        // columns of a tile
+constexpr int kRun = 8;              // steps that kDense32 sums in tensor memory
+__host__ __device__ constexpr int most_cols_of_form(Form f) { return runs(f) ? 128 : kMaxCols; }  // sums in 64 registers
 constexpr int kTmemCols = 512;       // two tiles: one computed, one read out
 constexpr int kMaxStages = 12;
 constexpr int kSideStages = 4;
@@ -101,11 +109,11 @@ struct Params {
   const int32_t *plan;   // kPlanWords a tile of rows
   const uint16_t *low;   // [rows][rank], scaled
   int rank;
-  // kDense, kDenseGated
+  // kDense and the like
   const void *bias;          // [wide] or null
   const uint16_t *residual;  // [rows][width] or null
   int activation;
-  bool bias_bf16, out_fp32;
+  bool bias_bf16;
 };
 
 struct Barriers {
@@ -395,10 +403,10 @@ __device__ __forceinline__ void add_residual(float *v, const int4 (&r)[4], char 
   }
 }
 
-template <int COUNT>
+template <Form F, int COUNT>
 __device__ __forceinline__ void store_out(const float *v, char *stage, const Params &p, int64_t row, int rows, int at,
                                           int lane) {
-  if (!p.out_fp32) {
+  if (!runs(F)) {
     store_transposed<COUNT>(v, stage, p.out + row * p.width, p.width, rows, at, p.width, lane);
     return;
   }
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           }
           const int at = k * kInner;
           if (is_a) {
-            if (F == kPlain || F == kAdapter || F == kDense) {
+            if (F == kPlain || F == kAdapter || (dense(F) && !gated(F))) {
               tile_load_3d(a, &p.a, at, a0, t.e, bar);
             } else if (gated(F)) {
               tile_load_4d(a, &p.a, at, a0, 0, t.e, bar);
@@ -579,62 +587,65 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     for (int n = pair; ok && walk.find(n, t); n += pairs) {
       if (t.steps == 0) continue;  // an expert without rows (kGradW): zeros are written
       const uint32_t idesc = mma_desc(t.cols, grad_x(F) || grad_w(F), grad_w(F));
-      const uint32_t d = tmem + acc * kMaxCols;
-      ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1));
-      tc_fence_after();
-      const int k0 = first_step(t), k1 = last_step(t);
-      for (int k = k0; ok && k < k1; ++k) {
-        ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
-        if (grad_w(F) && ok && k == t.steps - 1 && t.count % 16 != 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.fixed[stage], (trims >> stage) & 1u));
-          trims ^= 1u << stage;
-        }
-        if (!ok) break;
+      const int end = last_step(t);
+      for (int k0 = first_step(t), k1; ok && k0 < end; k0 = k1) {  // one run, or runs of kRun
+        k1 = runs(F) ? min(end, k0 + kRun) : end;
+        const uint32_t d = tmem + acc * kMaxCols;
+        ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_empty[acc], acc_phase ^ 1));
         tc_fence_after();
-        const uint32_t addr = ring_addr + (uint32_t)(stage * stage_bytes);
-        const uint32_t a = grad_x(F) || grad_w(F) ? outer_desc(addr, 8192) : inner_desc(addr);
-        const uint32_t b = grad_w(F) ? outer_desc(addr + kABytes, 8192) : inner_desc(addr + kABytes);
-        const int parts = grad_w(F) ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
-        if (elect_one()) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < parts)
-              mma_pair(d, a + j * ((grad_x(F) || grad_w(F) ? 2048 : 32) >> 4), b + j * ((grad_w(F) ? 2048 : 32) >> 4),
-                       idesc, k > k0 || j > 0);
-          commit_pair(&s_bar.empty[stage], both);
-          if (F != kAdapter && k == k1 - 1) commit_pair(&s_bar.acc_full[acc], both);
-        }
-        __syncwarp();
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-      if (F == kAdapter && ok) {
-        if (n == pair) griddep_wait();
-        const int length = p.rank * load_made(p.plan + (int64_t)t.part * kPlanWords);  // of the adapters side by side
-        for (int k = part; ok && k * kInner < length; k += p.parts) {
-          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_full[side_stage], side_phase));
+        for (int k = k0; ok && k < k1; ++k) {
+          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.full[stage], phase));
+          if (grad_w(F) && ok && k == t.steps - 1 && t.count % 16 != 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.fixed[stage], (trims >> stage) & 1u));
+            trims ^= 1u << stage;
+          }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t addr = smem_addr(side) + (uint32_t)(side_stage * stage_bytes);
-          const uint32_t a = inner_desc(addr), b = inner_desc(addr + kABytes);
-          const int parts = min(4, ceil_div(length - k * kInner, 16));
+          const uint32_t addr = ring_addr + (uint32_t)(stage * stage_bytes);
+          const uint32_t a = grad_x(F) || grad_w(F) ? outer_desc(addr, 8192) : inner_desc(addr);
+          const uint32_t b = grad_w(F) ? outer_desc(addr + kABytes, 8192) : inner_desc(addr + kABytes);
+          const int parts = grad_w(F) ? min(4, ceil_div(t.count - k * kInner, 16)) : 4;
           if (elect_one()) {
-            for (int j = 0; j < parts; ++j) mma_pair(d, a + j * 2, b + j * 2, idesc, true);
-            commit_pair(&s_bar.side_empty[side_stage], both);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < parts)
+                mma_pair(d, a + j * ((grad_x(F) || grad_w(F) ? 2048 : 32) >> 4), b + j * ((grad_w(F) ? 2048 : 32) >> 4),
+                         idesc, k > k0 || j > 0);
+            commit_pair(&s_bar.empty[stage], both);
+            if (F != kAdapter && k == k1 - 1) commit_pair(&s_bar.acc_full[acc], both);
           }
           __syncwarp();
-          if (++side_stage == side_stages) {
-            side_stage = 0;
-            side_phase ^= 1;
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
           }
         }
-        if (ok && elect_one()) commit_pair(&s_bar.acc_full[acc], both);
-        __syncwarp();
+        if (F == kAdapter && ok) {
+          if (n == pair) griddep_wait();
+          const int length = p.rank * load_made(p.plan + (int64_t)t.part * kPlanWords);  // of the adapters side by side
+          for (int k = part; ok && k * kInner < length; k += p.parts) {
+            ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.side_full[side_stage], side_phase));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t addr = smem_addr(side) + (uint32_t)(side_stage * stage_bytes);
+            const uint32_t a = inner_desc(addr), b = inner_desc(addr + kABytes);
+            const int parts = min(4, ceil_div(length - k * kInner, 16));
+            if (elect_one()) {
+              for (int j = 0; j < parts; ++j) mma_pair(d, a + j * 2, b + j * 2, idesc, true);
+              commit_pair(&s_bar.side_empty[side_stage], both);
+            }
+            __syncwarp();
+            if (++side_stage == side_stages) {
+              side_stage = 0;
+              side_phase ^= 1;
+            }
+          }
+          if (ok && elect_one()) commit_pair(&s_bar.acc_full[acc], both);
+          __syncwarp();
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
       }
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1;
     }
   } else if (warp == 2 && grad_w(F)) {
     // ---------------------------------------------------------- row ends
@@ -811,9 +822,36 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         const int at = gated(F) ? t.a0 + (int)rank * 64 + (quarter & 1) * 32 : t.a0 + (int)rank * 128 + quarter * 32;
         if (p.bias != nullptr && at + lane < p.width)
           bias = load_param(p.bias, p.bias_bf16, (gated(F) && quarter >= 2 ? p.width : 0) + at + lane);
-        if (F == kDense && p.residual != nullptr) load_residual<32>(ahead, p, t.first + half * 32, t.count - half * 32, at, lane);
+        if (!gated(F) && p.residual != nullptr) load_residual<32>(ahead, p, t.first + half * 32, t.count - half * 32, at, lane);
       }
-      ok = mbar_wait_pair(&s_bar.acc_full[acc], acc_phase);
+      constexpr int kHeld = runs(F) ? most_cols_of_form(F) / 64 : 1;
+      float held[kHeld][32];  // kDense32: this warp's sums of the runs so far
+      if (runs(F)) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) held[i][j] = 0.0f;
+        const int end = last_step(t);
+        for (int k = first_step(t); ok && k < end; k += kRun) {
+          ok = __all_sync(0xffffffffu, mbar_wait_pair(&s_bar.acc_full[acc], acc_phase));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) {
+            const int c = half * 32 + i * 64;
+            if (c >= t.cols) break;
+            float v[32];
+            tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) held[i][j] += v[j];
+          }
+          release(acc);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+        }
+      } else {
+        ok = mbar_wait_pair(&s_bar.acc_full[acc], acc_phase);
+      }
       if (!grad_w(F) && p.parts > 1) {
         if (part > 0) {
           // this pair's sums go to the first pair's CTA with the same rows
@@ -821,18 +859,27 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
           const uint32_t to = map_shared(smem_addr(joined + (part - 1) * p.max_cols * 32 + quarter * 32 + lane), rank);
-          for (int c = half * 32; c < t.cols; c += 64) {
+#pragma unroll(runs(F) ? kHeld : 1)
+          for (int i = 0; i < (runs(F) ? kHeld : kMaxCols / 64); ++i) {
+            const int c = half * 32 + i * 64;
+            if (c >= t.cols) break;
             float v[32];
-            tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+            if (runs(F)) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = held[i % kHeld][j];
+            } else {
+              tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+            }
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
               store_cluster(to + (uint32_t)(c + j) * 512, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
           }
-          release(acc);
+          if (!runs(F)) release(acc);
           __syncwarp();
           fence_cluster();  // every lane's stores, before one arrives for all
           if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.part_full), rank));
           part_phase ^= 1;
+          if (runs(F)) continue;
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
           continue;
@@ -865,10 +912,18 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
         if (acc == 0) acc_phase ^= 1;
         continue;
       }
-      for (int c = half * 32; c < t.cols; c += 64) {
+#pragma unroll(runs(F) ? kHeld : 1)
+      for (int i = 0; i < (runs(F) ? kHeld : kMaxCols / 64); ++i) {
+        const int c = half * 32 + i * 64;
+        if (c >= t.cols) break;
         float v[32];
-        tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
-        if (c + 64 >= t.cols) release(acc);
+        if (runs(F)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = held[i % kHeld][j];
+        } else {
+          tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+          if (c + 64 >= t.cols) release(acc);
+        }
         if (!grad_w(F) && p.parts > 1) {
           // the parts are added in their order
           for (int q = 0; q + 1 < p.parts; ++q) {
@@ -884,7 +939,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           }
         }
         const int left = t.count - c;  // rows of this chunk (not kGradW)
-        if (F == kDense) {
+        if (dense(F) && !gated(F)) {
           const int at = t.a0 + (int)rank * 128 + quarter * 32;
           const int64_t row = t.first + c;
 #pragma unroll
@@ -896,7 +951,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
             add_residual<32>(v, ahead, stage_buf, lane);
             load_residual<32>(ahead, p, row + 64, left - 64, at, lane);
           }
-          store_out<32>(v, stage_buf, p, row, left, at, lane);
+          store_out<F, 32>(v, stage_buf, p, row, left, at, lane);
         } else if (F == kPlain || grad_x(F) || F == kAdapter) {
           const int at = t.a0 + (int)rank * 128 + quarter * 32;
           const int64_t row = t.first + c;
@@ -909,7 +964,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           const int at = t.a0 + (int)rank * 64 + (quarter & 1) * 32;
           const int64_t row = t.first + c;
           const bool gate = quarter < 2;
-          if (F == kDenseGated) {
+          if (dense(F)) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += bias;
           }
@@ -920,7 +975,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
           const float *take = reinterpret_cast<const float *>(exchange + (w ^ 2) * kExchangeBytes);
           const int id = 1 + half * 2 + (quarter & 1);
           const int skip = gate ? 0 : 16;  // the rows that this warp finishes
-          if (F == kDenseGated && p.residual != nullptr) load_residual<16>(ahead, p, row + skip, left - skip, at, lane);
+          if (dense(F) && p.residual != nullptr) load_residual<16>(ahead, p, row + skip, left - skip, at, lane);
           float o[16];
 #pragma unroll
           for (int r = 0; r < 16; r += 8) {
@@ -934,15 +989,15 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
             }
             pair_barrier(id);  // before the next columns overwrite what the other warp reads
           }
-          if (F == kDenseGated) {
+          if (dense(F)) {
             if (p.residual != nullptr) add_residual<16>(o, ahead, stage_buf, lane);
-            store_out<16>(o, stage_buf, p, row + skip, left - skip, at, lane);
+            store_out<F, 16>(o, stage_buf, p, row + skip, left - skip, at, lane);
           } else {
             store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);
           }
         }
       }
-      if (t.cols <= half * 32) release(acc);  // no columns for this warp
+      if (!runs(F) && t.cols <= half * 32) release(acc);  // no columns for this warp
       if (F == kAdapter && *static_cast<volatile int *>(&s_bar.odd) >= n) {
         __syncwarp();  // what other lanes wrote
         for (int c = half * 32; c < t.cols; c += 64) add_odd(p, t, c, t.a0 + (int)rank * 128 + quarter * 32 + lane);
@@ -954,6 +1009,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
             mbar_arrive_cluster_relaxed(map_shared(smem_addr(&s_bar.part_empty), 2 * q + rank));
         part_phase ^= 1;
       }
+      if (runs(F)) continue;
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
@@ -1037,7 +1093,7 @@ ep_status_t choose(const DeviceInfo *di, int rows, int experts, int most, int a_
   const int used = rows < experts ? rows : experts, mean = up(rows, used);
   const int64_t likely = experts == 1 ? most : mean + (int64_t)(2.0f * sqrtf((float)mean));
   int64_t least = -1;
-  for (int cut = kMaxCols; cut >= 32; cut -= 32) {
+  for (int cut = most_cols_of_form(F); cut >= 32; cut -= 32) {
     // the rows of a single expert go to tiles of about equal size
     const int need = experts == 1 ? up(most, up(most, cut)) : most < cut ? most : cut;
     const int cols = up(need, 32) * 32;
@@ -1049,7 +1105,7 @@ ep_status_t choose(const DeviceInfo *di, int rows, int experts, int most, int a_
       if (parts > 1 && (tiles > clusters || steps < 2 * parts)) break;
       const int64_t copies = (kABytes + cols / 2 * 128) / 58, products = 2 * cols;
       const int64_t count = used * ((likely + cols - 1) / cols) * a_tiles, waves = (count + clusters - 1) / clusters;
-      if (experts > 1 && waves > 1 && cut < kMaxCols) continue;  // too uncertain to leave the widest for
+      if (experts > 1 && waves > 1 && cut < most_cols_of_form(F)) continue;  // too uncertain to leave the widest for
       const int64_t cost =
           waves * (up(steps, parts) * (copies > products ? copies : products) + 2000 + 10 * cols) +
           (parts > 1 ? 1000 + parts * 10 * cols : 0);
@@ -1125,7 +1181,7 @@ ep_status_t row_maps(Params &p, const void *rows, int length, int cap, int64_t p
 // The weights [E][wide][hidden] as A of a form.
 [[maybe_unused]] ep_status_t weight_map(Params &p, Form form, const void *w, int wide, int hidden) {
   const uint64_t E = p.E, n = wide, h = hidden;
-  if (form == kPlain || form == kDense) {
+  if (form == kPlain || (dense(form) && !gated(form))) {
     const uint64_t dims[] = {h, n, E}, strides[] = {h * kSize, n * h * kSize};
     const uint32_t box[] = {kInner, 128, 1};
     return encode_map(&p.a, w, 3, dims, strides, box);
