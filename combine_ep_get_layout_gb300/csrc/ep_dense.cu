@@ -175,6 +175,50 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dense_bias_kernel(const float
     static_cast<float *>(out)[n] = sum;
 }
 
+// The weights' gradient of few tiles of 256 x 256: pairs take segments of the
+// rows, whose sums a second kernel adds.  That costs about 16 steps of 64
+// rows, so it has to save more (with the bias's kernel): 8192 rows 7168 -> 256
+// (28 tiles) 42 us, by two segments 35; 512 -> 512 (4 tiles) 38 us, by
+// sixteen 17; 128 -> 128 (one) 37 us, by sixteen 10; 333 rows 512 -> 1408
+// stay whole, 8.5 us.
+constexpr int kPairs = 76;          // that run at once
+constexpr int kLeastSteps = 8;      // of a segment
+constexpr int kSegmentsCost = 16;   // steps
+
+struct Segments {
+  int count, rows;
+};
+
+Segments segments_of(int rows, int wide, int hidden) {
+  const int tiles = up(wide, 256) * up(hidden, 256), steps = up(rows, kInner);
+  int most = tiles < kPairs ? kPairs / tiles : 1;
+  if (most > steps / kLeastSteps) most = steps / kLeastSteps;
+  if (most < 2 || steps - up(steps, most) < kSegmentsCost) return Segments{1, rows};
+  const int each = up(steps, most);
+  return Segments{up(steps, each), each * kInner};
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t sums_bytes(int rows, int width, int wide) { return round256((size_t)slices_of(rows, width).slices * wide * sizeof(float)); }
+
+// The segments' sums added up in their order, eight elements a thread.
+__global__ void __launch_bounds__(256) dense_segments_kernel(const float *parts, int segments, int64_t count, uint16_t *out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= count) return;
+  float v[8] = {};
+#pragma unroll 4
+  for (int i = 0; i < segments; ++i) {
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(parts + i * count + at));
+    const float4 b = __ldcg(reinterpret_cast<const float4 *>(parts + i * count + at) + 1);
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+    v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+  *reinterpret_cast<int4 *>(out + at) = pack8(v);
+}
+
 // What the products of a call share: one expert with every row.
 Params params_of(int rows, int wide, int width, int hidden, uint32_t *error_word) {
   Params p = {};
@@ -211,7 +255,9 @@ ep_status_t launch_dense(const DenseArgs &a, cudaStream_t stream) {
 }
 
 size_t dense_workspace_bytes(int num_rows, int hidden, int width, ep_activation_t activation) {
-  return (size_t)slices_of(num_rows, width).slices * (activation == EP_ACT_SWIGLU ? 2 : 1) * width * sizeof(float);
+  const int wide = activation == EP_ACT_SWIGLU ? 2 * width : width;
+  const int segments = segments_of(num_rows, wide, hidden).count;
+  return sums_bytes(num_rows, width, wide) + (segments > 1 ? (size_t)segments * wide * hidden * sizeof(float) : 0);
 }
 
 ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t stream) {
@@ -250,13 +296,27 @@ ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t strea
     // without rows nothing is copied: the maps only need an address
     const bool any = a.num_rows > 0;
     const int rows = any ? a.num_rows : 1;
+    const Segments seg = segments_of(a.num_rows, wide, a.hidden);
+    const bool parts = seg.count > 1;
+    float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + sums_bytes(a.num_rows, a.width, wide));
     ep_status_t s = block_map(&p.a, &p.a_blocks, any ? d : a.grad_w, wide, rows, wide);
-    const uint64_t dims[] = {(uint64_t)a.hidden, (uint64_t)wide, 1};
-    const uint64_t strides[] = {a.hidden * kSize, (uint64_t)wide * a.hidden * kSize};
+    // (fp32 as two bf16 each)
+    const uint64_t each = parts ? 2 : 1, columns = each * a.hidden;
+    const uint64_t dims[] = {columns, (uint64_t)wide, (uint64_t)seg.count};
+    const uint64_t strides[] = {columns * kSize, (uint64_t)wide * columns * kSize};
     const uint32_t box[] = {64, 32, 1};
-    if (s == EP_OK) s = encode_map(&p.grad, a.grad_w, 3, dims, strides, box);
+    if (s == EP_OK) s = encode_map(&p.grad, parts ? (const void *)part : a.grad_w, 3, dims, strides, box);
     if (s == EP_OK) s = block_map(&p.b[0], &p.b_blocks, any ? a.x : a.grad_w, a.hidden, rows, any ? a.row_stride : a.hidden);
-    if (s == EP_OK) s = launch_form<kDenseGradW>(p, (int64_t)p.a_tiles * p.b_tiles, stream);
+    const int64_t tiles = (int64_t)p.a_tiles * p.b_tiles * seg.count;
+    p.segments = seg.count;
+    p.rows_each = seg.rows;
+    if (s == EP_OK) s = parts ? launch_form<kDenseGradWPart>(p, tiles, stream) : launch_form<kDenseGradW>(p, tiles, stream);
+    if (s == EP_OK && parts) {
+      const int64_t count = (int64_t)wide * a.hidden;
+      e = launch_kernel(dense_segments_kernel, (int)((count / 8 + 255) / 256), 256, 0, stream, false, (const float *)part,
+                        seg.count, count, a.grad_w);
+      if (e != cudaSuccess) return cuda_fail(e, "dense_segments launch");
+    }
     if (s != EP_OK) return s;
   }
   return EP_OK;

@@ -21,6 +21,8 @@
 //                    cut off what does not fit beside a growing sum: over
 //                    7168 inner elements an error of 8e-6.  So their sums of
 //                    kRun steps are added up in registers, rounded: 6e-7.
+//   kDenseGradWPart  kDenseGradW by segments of the rows, p.rows_each long:
+//                    the sums of each in fp32, joined by another kernel
 // An inner step is 64 elements, a 128-byte row of shared memory in the
 // 128-byte swizzle; the transposed operands are read with their outer
 // dimension contiguous, so nothing is ever transposed in memory.
@@ -51,10 +53,10 @@ namespace ep {
 
 namespace {
 
-enum Form { kPlain, kGated, kGradX, kGradW, kAdapter, kDense, kDenseGated, kDense32, kDenseGated32, kDenseGradX, kDenseGradW };
+enum Form { kPlain, kGated, kGradX, kGradW, kAdapter, kDense, kDenseGated, kDense32, kDenseGated32, kDenseGradX, kDenseGradW, kDenseGradWPart };
 __host__ __device__ constexpr bool gated(Form f) { return f == kGated || f == kDenseGated || f == kDenseGated32; }
 __host__ __device__ constexpr bool grad_x(Form f) { return f == kGradX || f == kDenseGradX; }
-__host__ __device__ constexpr bool grad_w(Form f) { return f == kGradW || f == kDenseGradW; }
+__host__ __device__ constexpr bool grad_w(Form f) { return f == kGradW || f == kDenseGradW || f == kDenseGradWPart; }
 __host__ __device__ constexpr bool dense(Form f) { return f >= kDense && f <= kDenseGated32; }  // with the epilogue
 __host__ __device__ constexpr bool runs(Form f) { return f == kDense32 || f == kDenseGated32; }
 __host__ __device__ constexpr bool single(Form f) { return f >= kAdapter; }  // one expert, its rows known to the host
@@ -98,7 +100,8 @@ struct Params {
   int a_tiles;   // tiles along A
   int b_tiles;   // kGradW: tiles along B (hidden)
   int hidden;    // kGradW
-  CUtensorMap grad;  // kGradW: the gradient [E][wide][hidden], boxes of 64 x 32
+  int segments, rows_each;  // kDenseGradWPart
+  CUtensorMap grad;  // kGradW: the gradient [E][wide][hidden], boxes of 64 x 32; kDenseGradWPart: [segments][wide][2 hidden]
   uint16_t *out, *preact;
   int max_cols;         // rows of a tile, at most
   int most_rows;        // of an expert, at most
@@ -165,7 +168,10 @@ struct Walker {
     rows = first = mine = 0;
     if (single(F)) {
       rows = e == 0 ? p.cap : 0;
-      if (e == 0) mine = grad_w(F) ? p.a_tiles * p.b_tiles : p.a_tiles * tiles_of(limits(p), rows);
+      if (e == 0) {
+        mine = !grad_w(F) ? p.a_tiles * tiles_of(limits(p), rows) : p.a_tiles * p.b_tiles;
+        if (F == kDenseGradWPart) mine *= p.segments;
+      }
     } else if (e < p.E) {
       first = p.offset[e];
       const int n = p.rows[e];
@@ -199,11 +205,17 @@ struct Walker {
     t.e = chunk * 32 + src;
     t.first = __shfl_sync(0xffffffffu, first, src);
     if (grad_w(F)) {
-      t.a0 = at / p.b_tiles * 256;
-      t.b0 = at % p.b_tiles * 256;
+      const int tiles = p.a_tiles * p.b_tiles, in = F == kDenseGradWPart ? at % tiles : at;
+      t.a0 = in / p.b_tiles * 256;
+      t.b0 = in % p.b_tiles * 256;
       t.count = n;
+      if (F == kDenseGradWPart) {
+        t.e = at / tiles;
+        t.first = t.e * p.rows_each;
+        t.count = min(p.rows_each, n - t.first);
+      }
       t.cols = kMaxCols;
-      t.steps = ceil_div(n, kInner);
+      t.steps = ceil_div(t.count, kInner);
     } else {
       const int tiles = tiles_of(limits(p), n);
       if (single(F)) {
@@ -794,7 +806,8 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const auto store_block = [&](char *from, const Tile &t, int c) {  // kGradW: 32 rows of 64 columns
       const int col = t.b0 + c, row = t.a0 + (int)rank * 128 + quarter * 32;
-      if (col < p.hidden && row < p.wide) tile_store_3d(&p.grad, smem_addr(from), col, row, t.e);
+      if (col < p.hidden && row < p.wide)
+        tile_store_3d(&p.grad, smem_addr(from), F == kDenseGradWPart ? 2 * col : col, row, t.e);
       bulk_commit();
     };
     const auto release = [&](int a) {  // this warp has read its columns of accumulator a
@@ -889,6 +902,26 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
       ok = gated(F) ? pair_agree(1 + half * 2 + (quarter & 1), ok) : __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      if (F == kDenseGradWPart) {
+        // as below, 32 columns of fp32 at a time
+        for (int c = half * 32; c < t.cols; c += 64) {
+          float v[32];
+          tmem_load32(tmem + acc * kMaxCols + c + lane_base, v);
+          if (c + 64 >= t.cols) release(acc);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4 *>(stage_buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) store_block(stage_buf, t, c);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+        continue;
+      }
       if (grad_w(F)) {
         // a row of the gradient a lane; 64 columns are staged in the swizzled
         // order and stored as a tile
