@@ -937,7 +937,7 @@ def ep_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = "
     S = _sequences(seq_offsets, dev)
     if topk_idx.dim() != 2 or not _good(topk_idx, torch.int64, i, (T, topk_idx.shape[1])):
         _refuse_tensors((topk_idx, "topk_idx", torch.int64, dev, (T, topk_idx.shape[-1])))
-    if out is None:
+    if out is None:  # (views of one tensor take longer than tensors of their own)
         out = Balance(_empty(2, torch.float32, dev, stream), _empty((S, E), torch.int32, dev, stream),
                       _empty((S, E), torch.float32, dev, stream), _empty((S, E), torch.float32, dev, stream))
     else:
@@ -1132,10 +1132,13 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
         _given(preact, "preact", bf, dev, (T, wide))
     else:
         preact = None
-    if (act != N.EP_ACT_NONE or grad.dtype is not bf) and (need_x or need_w):
-        grad_preact = _target(grad_preact, "grad_preact", bf, dev, (T, wide), stream)
-    else:
+    kept = 0  # bytes of the scratch tensor for grad_preact
+    if not ((act != N.EP_ACT_NONE or grad.dtype is not bf) and (need_x or need_w)):
         grad_preact = None
+    elif grad_preact is None:
+        kept = (T * wide * 2 + 255) // 256 * 256
+    else:
+        _given(grad_preact, "grad_preact", bf, dev, (T, wide))
     grad_x = _target(grad_x, "grad_x", bf, dev, (T, H), stream) if need_x else None
     grad_w = _target(grad_w, "grad_w", bf, dev, (wide, H), stream) if need_w else None
     if grad_bias is not None:
@@ -1146,13 +1149,20 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
         grad_bias = _target(grad_bias, "grad_bias", bias_dtype, dev, (wide,), stream)
     if error_word is not None:
         _want(error_word, "error_word", torch.int32, dev)
-    workspace, nbytes = _scratch(
-        workspace, ep_dense_workspace_bytes(T, H, width, activation) if workspace is None else 0, dev, stream)
+    if workspace is None:
+        nbytes = max(ep_dense_workspace_bytes(T, H, width, activation), 16)
+        scratch = _empty(kept + nbytes, torch.uint8, dev, stream)
+        made = scratch.data_ptr()
+        at = made + kept
+    else:
+        _want(workspace, "workspace", torch.uint8, dev)
+        at, nbytes = workspace.data_ptr(), workspace.numel()
+        scratch = _empty(kept, torch.uint8, dev, stream) if kept else None
+        made = _address(scratch)
     _launch(i, "ep_dense_product_backward", _dense_backward_args(
         grad.data_ptr(), _TYPES[grad.dtype], x.data_ptr(), apart, T, H, w.data_ptr(), width, act, _address(preact),
-        _address(grad_preact), _address(grad_x), _address(grad_w), _address(grad_bias),
-        N.EP_TYPE_FP32 if bias_dtype is None else _TYPES[bias_dtype], workspace.data_ptr(), nbytes, _address(error_word)),
-        stream)
+        made if kept else _address(grad_preact), _address(grad_x), _address(grad_w), _address(grad_bias),
+        N.EP_TYPE_FP32 if bias_dtype is None else _TYPES[bias_dtype], at, nbytes, _address(error_word)), stream)
     return grad_x, grad_w, grad_bias
 
 
