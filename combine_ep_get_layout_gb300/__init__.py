@@ -1070,7 +1070,7 @@ def ep_dense_product(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tens
     """act(x w^T + bias) + residual, a product shared by all rows.
 
     ``x`` bf16 [T, H] (rows may be a slice of wider ones, a multiple of 8
-    apart), ``w`` bf16 [N, H], ``bias`` fp32 or bf16 [N].  ``activation`` is
+    apart; H is one too), ``w`` bf16 [N, H], ``bias`` fp32 or bf16 [N].  ``activation`` is
     None, "relu", "silu", "gelu" (by erf), "gelu_tanh", or "swiglu": silu of
     the first half of the outputs times the second, [T, N/2].  ``residual``
     (bf16 like the output's shape) may be ``out``.  The output is bf16, or
@@ -1116,8 +1116,8 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
     gradient ``grad`` ([T, width], bf16 or fp32); what is not needed is None.
     The bias's is computed for a ``bias_dtype`` (or a ``grad_bias`` tensor).
     With an activation ``preact`` is what the forward pass kept;
-    ``grad_preact`` (bf16 [T, N], allocated when not given) receives its
-    gradient, rounded as the products take it.  A residual's gradient is
+    ``grad_preact`` (bf16 [T, N], N rounded up to a multiple of 8, allocated
+    when not given) receives its gradient, rounded as the products take it.  A residual's gradient is
     ``grad`` itself."""
     act = _DENSE_ACTIVATIONS[activation]
     T, H, apart, width, wide = _dense_sizes(x, w, activation)
@@ -1133,12 +1133,13 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
     else:
         preact = None
     kept = 0  # bytes of the scratch tensor for grad_preact
-    if not ((act != N.EP_ACT_NONE or grad.dtype is not bf) and (need_x or need_w)):
+    pitch = (wide + 7) // 8 * 8
+    if not ((act != N.EP_ACT_NONE or grad.dtype is not bf or width % 8) and (need_x or need_w)):
         grad_preact = None
     elif grad_preact is None:
-        kept = (T * wide * 2 + 255) // 256 * 256
+        kept = (T * pitch * 2 + 255) // 256 * 256
     else:
-        _given(grad_preact, "grad_preact", bf, dev, (T, wide))
+        _given(grad_preact, "grad_preact", bf, dev, (T, pitch))
     grad_x = _target(grad_x, "grad_x", bf, dev, (T, H), stream) if need_x else None
     grad_w = _target(grad_w, "grad_w", bf, dev, (wide, H), stream) if need_w else None
     if grad_bias is not None:

@@ -67,7 +67,7 @@ ep_status_t check_eights(const char *fn, const char *name, int v) {
 ep_status_t check_dense(const char *fn, int T, int H, int width, int act, int64_t stride) {
   EP_CHECK(check_size(fn, "num_rows", T, 0, INT32_MAX));
   EP_CHECK(check_eights(fn, "hidden", H));
-  EP_CHECK(check_eights(fn, "width", width));
+  EP_CHECK(check_size(fn, "width", width, 1, EP_MAX_HIDDEN));
   if (act < EP_ACT_NONE || act > EP_ACT_GELU_TANH) return fail(EP_ERR_INVALID_ARG, "%s: unknown activation %d", fn, act);
   EP_CHECK(check_stride(fn, stride, "hidden", H));
   if (stride % 8 != 0)
@@ -208,7 +208,7 @@ ep_status_t ep_dense_product(const ep_dense_product_args_t *args, ep_stream_t st
 }
 
 size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activation_t activation) {
-  if (num_rows < 0 || hidden < 8 || hidden > EP_MAX_HIDDEN || width < 8 || width > EP_MAX_HIDDEN) return 0;
+  if (num_rows < 0 || hidden < 8 || hidden > EP_MAX_HIDDEN || width < 1 || width > EP_MAX_HIDDEN) return 0;
   return dense_workspace_bytes(num_rows, hidden, width, activation);
 }
 
@@ -227,7 +227,7 @@ ep_status_t ep_dense_product_backward(const ep_dense_product_backward_args_t *ar
   EP_CHECK(check_ptr(fn, "w", x.w, 16, any && x.grad_x != nullptr));
   EP_CHECK(check_ptr(fn, "preact", x.preact, 16, any && act));
   EP_CHECK(check_ptr(fn, "grad_preact", x.grad_preact, 16,
-                     any && products && (act || x.grad_type == EP_TYPE_FP32)));
+                     any && products && (act || x.grad_type == EP_TYPE_FP32 || x.width % 8 != 0)));
   EP_CHECK(check_ptr(fn, "grad_x", x.grad_x, 16, false));
   EP_CHECK(check_ptr(fn, "grad_w", x.grad_w, 16, false));
   EP_CHECK(check_ptr(fn, "grad_bias", x.grad_bias, size_of(x.bias_type), false));

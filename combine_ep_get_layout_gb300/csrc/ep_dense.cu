@@ -151,6 +151,37 @@ __global__ void __launch_bounds__(32 * kRowLanes, GATED ? 2 : 3) dense_gradient_
   }
 }
 
+// Rows that are not of whole 16 bytes: a column a thread (64 rows a block).
+template <bool GATED>
+__global__ void __launch_bounds__(kWide) dense_gradient_any_kernel(DenseBackwardArgs p, float *sums, Slices cut, int64_t pitch) {
+  const int slice = blockIdx.x / cut.columns, n = blockIdx.x % cut.columns * kWide + threadIdx.x;
+  const int64_t wide = (GATED ? 2 : 1) * (int64_t)p.width;
+  const int64_t first = (int64_t)slice * cut.rows, last = min(first + cut.rows, (int64_t)p.num_rows);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (n >= p.width) return;
+  const auto put = [&](int64_t i, float v) { p.grad_preact[i] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu); };
+  float sum = 0.0f, other = 0.0f;
+#pragma unroll 4
+  for (int64_t t = first; t < last; ++t) {
+    float d = load_param(p.grad, p.grad_bf16, t * p.width + n);
+    if (GATED) {
+      const float g = load_param(p.preact, true, t * wide + n), u = load_param(p.preact, true, t * wide + p.width + n);
+      const float s = sigmoid_of(g), du = d * g * s;
+      d *= u * s * (1.0f + g * (1.0f - s));
+      other += du;
+      if (p.grad_preact != nullptr) put(t * pitch + p.width + n, du);
+    } else if (p.activation != EP_ACT_NONE) {
+      d *= slope_of(p.activation, load_param(p.preact, true, t * wide + n));
+    }
+    if (p.grad_preact != nullptr) put(t * pitch + n, d);
+    sum += d;
+  }
+  if (p.grad_bias == nullptr) return;
+  sums[slice * wide + n] = sum;
+  if (GATED) sums[slice * wide + p.width + n] = other;
+}
+
 constexpr int kJoinWarps = 8;
 
 // The slices by eight warps, then those in their order; a column a lane.
@@ -264,13 +295,19 @@ ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t strea
   const bool pairs = a.activation == EP_ACT_SWIGLU;
   const int wide = pairs ? 2 * a.width : a.width;
   const Slices cut = slices_of(a.num_rows, a.width);
-  const bool made = a.activation != EP_ACT_NONE || !a.grad_bf16;  // d is not `grad` itself
+  const bool any_width = a.width % 8 != 0;
+  const bool made = a.activation != EP_ACT_NONE || !a.grad_bf16 || wide % 8 != 0;  // d is not `grad` itself
+  const int64_t pitch = made ? up(wide, 8) * 8 : wide;                             // between d's rows
   float *sums = static_cast<float *>(a.workspace);
   cudaError_t e = cudaSuccess;
   if (a.num_rows > 0 && (a.grad_bias != nullptr || (made && a.grad_preact != nullptr))) {
     const auto kernel = pairs ? (a.grad_bf16 ? dense_gradient_kernel<true, true> : dense_gradient_kernel<true, false>)
                               : (a.grad_bf16 ? dense_gradient_kernel<false, true> : dense_gradient_kernel<false, false>);
-    e = launch_kernel(kernel, cut.columns * cut.slices, 32 * kRowLanes, 0, stream, false, a, sums, cut);
+    if (any_width)
+      e = launch_kernel(pairs ? dense_gradient_any_kernel<true> : dense_gradient_any_kernel<false>, cut.columns * cut.slices,
+                        kWide, 0, stream, false, a, sums, cut, pitch);
+    else
+      e = launch_kernel(kernel, cut.columns * cut.slices, 32 * kRowLanes, 0, stream, false, a, sums, cut);
   }
   if (e == cudaSuccess && a.grad_bias != nullptr)
     e = launch_kernel(dense_bias_kernel, up(wide, 32), 32 * kJoinWarps, 0, stream, false, (const float *)sums, cut.slices,
@@ -283,7 +320,7 @@ ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t strea
     p.a_tiles = up(a.hidden, 256);
     p.out = a.grad_x;
     ep_status_t s = weight_map(p, kDenseGradX, a.w, wide, a.hidden);
-    if (s == EP_OK) s = launch_rows_form<kDenseGradX>(p, d, wide, stream);
+    if (s == EP_OK) s = launch_rows_form<kDenseGradX>(p, d, pitch, stream);
     if (s != EP_OK) return s;
   }
   if (a.grad_w != nullptr) {
@@ -299,7 +336,7 @@ ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t strea
     const Segments seg = segments_of(a.num_rows, wide, a.hidden);
     const bool parts = seg.count > 1;
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + sums_bytes(a.num_rows, a.width, wide));
-    ep_status_t s = block_map(&p.a, &p.a_blocks, any ? d : a.grad_w, wide, rows, wide);
+    ep_status_t s = block_map(&p.a, &p.a_blocks, any ? d : a.grad_w, wide, rows, any ? pitch : up(wide, 8) * 8);
     // (fp32 as two bf16 each)
     const uint64_t each = parts ? 2 : 1, columns = each * a.hidden;
     const uint64_t dims[] = {columns, (uint64_t)wide, (uint64_t)seg.count};

@@ -259,10 +259,17 @@ __device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0
 
 // A warp's 32 lanes hold outputs n (one a lane) of COUNT rows v[0..), `rows`
 // of them real: out[row][n] through the staging buffer, 64 bytes of a row at
-// a time.
-template <int COUNT>
+// a time; or, where rows are not of whole 16 bytes (ANY: they may not be),
+// straight from the registers, 2 bytes a lane.
+template <int COUNT, bool ANY = false>
 __device__ __forceinline__ void store_transposed(const float *v, char *stage, uint16_t *out, int64_t pitch, int rows,
                                                  int n, int limit, int lane) {
+  if (ANY && pitch % 8 != 0) {
+#pragma unroll
+    for (int c = 0; c < COUNT; ++c)
+      if (c < rows && n + lane < limit) out[c * pitch + n + lane] = (uint16_t)(pack_bf16x2(v[c], 0.0f) & 0xffffu);
+    return;
+  }
   constexpr int kRows = COUNT < kStagedRows ? COUNT : kStagedRows;
   const int part = lane & 3;
 #pragma unroll
@@ -392,6 +399,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[32]) {
 template <int COUNT>
 __device__ __forceinline__ void load_residual(int4 (&r)[4], const Params &p, int64_t row, int rows, int at, int lane) {
   const int n = at + (lane & 3) * 8;
+  if (p.width % 8 != 0) return;
 #pragma unroll
   for (int i = 0; i < COUNT / 8; ++i) {
     const int c = (lane >> 2) + i * 8;
@@ -399,9 +407,17 @@ __device__ __forceinline__ void load_residual(int4 (&r)[4], const Params &p, int
   }
 }
 
-// ... added to a row's value a lane and output, through the staging buffer.
+// ... added to a row's value a lane and output, through the staging buffer
+// (or, where rows are not of whole 16 bytes, read here).
 template <int COUNT>
-__device__ __forceinline__ void add_residual(float *v, const int4 (&r)[4], char *stage, int lane) {
+__device__ __forceinline__ void add_residual(float *v, const int4 (&r)[4], char *stage, const Params &p, int64_t row, int rows,
+                                             int at, int lane) {
+  if (p.width % 8 != 0) {
+#pragma unroll
+    for (int c = 0; c < COUNT; ++c)
+      if (c < rows && at + lane < p.width) v[c] += __uint_as_float((uint32_t)p.residual[(row + c) * p.width + at + lane] << 16);
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < COUNT / 16; ++h) {
 #pragma unroll
@@ -419,10 +435,16 @@ template <Form F, int COUNT>
 __device__ __forceinline__ void store_out(const float *v, char *stage, const Params &p, int64_t row, int rows, int at,
                                           int lane) {
   if (!runs(F)) {
-    store_transposed<COUNT>(v, stage, p.out + row * p.width, p.width, rows, at, p.width, lane);
+    store_transposed<COUNT, true>(v, stage, p.out + row * p.width, p.width, rows, at, p.width, lane);
     return;
   }
   float *out = reinterpret_cast<float *>(p.out) + row * p.width;
+  if (p.width % 4 != 0) {
+#pragma unroll
+    for (int c = 0; c < COUNT; ++c)
+      if (c < rows && at + lane < p.width) out[(int64_t)c * p.width + at + lane] = v[c];
+    return;
+  }
   constexpr int kRows = 8, kWide = 144;  // of 128 bytes; 16 against bank conflicts
   static_assert(kRows * kWide <= kStagedRows * kPitch, "");
   const int n = at + (lane & 7) * 4;
@@ -978,10 +1000,10 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] += bias;
           if (p.preact != nullptr)
-            store_transposed<32>(v, stage_buf, p.preact + row * p.width, p.width, left, at, p.width, lane);
+            store_transposed<32, true>(v, stage_buf, p.preact + row * p.width, p.width, left, at, p.width, lane);
           activate(p.activation, v);
           if (p.residual != nullptr) {
-            add_residual<32>(v, ahead, stage_buf, lane);
+            add_residual<32>(v, ahead, stage_buf, p, row, left, at, lane);
             load_residual<32>(ahead, p, row + 64, left - 64, at, lane);
           }
           store_out<F, 32>(v, stage_buf, p, row, left, at, lane);
@@ -1001,9 +1023,18 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += bias;
           }
-          if (p.preact != nullptr)
-            store_transposed<32>(v, stage_buf, p.preact + row * p.wide + (gate ? 0 : p.width), p.wide, left, at,
-                                 p.width, lane);
+          if (p.preact != nullptr) {
+            // (a half may start off 16 bytes where a row does not)
+            uint16_t *to = p.preact + row * p.wide + (gate ? 0 : p.width);
+            if (dense(F) && p.width % 8 != 0) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j < left && at + lane < p.width)
+                  to[(int64_t)j * p.wide + at + lane] = (uint16_t)(pack_bf16x2(v[j], 0.0f) & 0xffffu);
+            } else {
+              store_transposed<32>(v, stage_buf, to, p.wide, left, at, p.width, lane);
+            }
+          }
           float *give = reinterpret_cast<float *>(exchange + w * kExchangeBytes);
           const float *take = reinterpret_cast<const float *>(exchange + (w ^ 2) * kExchangeBytes);
           const int id = 1 + half * 2 + (quarter & 1);
@@ -1023,7 +1054,7 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
             pair_barrier(id);  // before the next columns overwrite what the other warp reads
           }
           if (dense(F)) {
-            if (p.residual != nullptr) add_residual<16>(o, ahead, stage_buf, lane);
+            if (p.residual != nullptr) add_residual<16>(o, ahead, stage_buf, p, row + skip, left - skip, at, lane);
             store_out<F, 16>(o, stage_buf, p, row + skip, left - skip, at, lane);
           } else {
             store_transposed<16>(o, stage_buf, p.out + (row + skip) * p.width, p.width, left - skip, at, p.width, lane);

@@ -877,8 +877,10 @@ ep_status_t ep_layer_norm_backward(const ep_layer_norm_backward_args_t *args, ep
  *   preact   [T * wide] bf16 or NULL: bf16(z), what the backward pass of an
  *            activation needs
  *   error_word [1] or NULL: EP_ERRBIT_TIMEOUT
- * hidden and width are multiples of 8 in [8, EP_MAX_HIDDEN]; x, w, residual,
- * out and preact are 16-byte aligned, bias to its elements.
+ * hidden is a multiple of 8 in [8, EP_MAX_HIDDEN], width in
+ * [1, EP_MAX_HIDDEN] (a gate may have any number of experts; with multiples of
+ * 8 the outputs are written 16 bytes at a time); x, w, residual, out and
+ * preact are 16-byte aligned, bias to its elements.
  */
 typedef struct {
     const void *x;
@@ -908,11 +910,12 @@ size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activati
  *   grad_x[t] = bf16(d[t] w),  grad_w = bf16(sum_t d[t]^T x[t]),
  *   grad_bias = sum_t d[t]     (fp32 sums of d before it is rounded)
  * The two products take d in bf16: `grad` itself for EP_ACT_NONE with a bf16
- * gradient, else rounded into grad_preact.  A residual's gradient is `grad`.
+ * gradient and a width of a multiple of 8, else rounded into grad_preact.  A
+ * residual's gradient is `grad`.
  *   grad   [T * width] of grad_type (the type of `out`)
  *   preact [T * wide] bf16 (not with EP_ACT_NONE)
- *   grad_preact [T * wide] bf16: written, then read (not with EP_ACT_NONE and
- *          a bf16 gradient)
+ *   grad_preact [T] rows of wide, rounded up to a multiple of 8, bf16: written
+ *          (but for what that adds), then read; NULL where d is `grad` itself
  *   grad_x [T * hidden], grad_w [wide * hidden] bf16, grad_bias [wide] of
  *          bias_type: NULL: not computed.  grad_w and grad_bias are 0
  *          without rows.

@@ -96,8 +96,8 @@ def test_norm_backward_refuses(lib, kw, needle, status):
 
 PRODUCT = [
     (dict(num_rows=-1), "num_rows", BAD), (dict(hidden=4), "hidden", BAD), (dict(hidden=60), "multiple of 8", BAD),
-    (dict(hidden=16392, row_stride=16392), "hidden", LIMIT), (dict(width=0), "width", BAD), (dict(width=12), "multiple of 8", BAD),
-    (dict(width=16392), "width", LIMIT), (dict(activation=6), "activation", BAD), (dict(activation=-1), "activation", BAD),
+    (dict(hidden=16392, row_stride=16392), "hidden", LIMIT), (dict(width=0), "width", BAD), (dict(width=-8), "width", BAD),
+    (dict(width=16385), "width", LIMIT), (dict(activation=6), "activation", BAD), (dict(activation=-1), "activation", BAD),
     (dict(row_stride=56), "row_stride", BAD), (dict(row_stride=68), "multiple of 8", BAD), (dict(bias_type=2), "bias_type", BAD),
     (dict(x=P + 8), "x is not 16-byte", BAD), (dict(w=None), "w is NULL", BAD), (dict(w=P + 2), "w is not 16-byte", BAD),
     (dict(error_word=P + 2), "error_word", BAD),
@@ -119,6 +119,7 @@ def test_dense_refuses(lib, kw, needle, status):
 @pytest.mark.parametrize("kw,needle,status", PRODUCT + [
     (dict(grad_type=2), "grad_type", BAD), (dict(grad=None), "grad is NULL", BAD), (dict(preact=None), "preact is NULL", BAD),
     (dict(grad_preact=None), "grad_preact is NULL", BAD), (dict(activation=0, grad_type=0, grad_preact=None), "grad_preact is NULL", BAD),
+    (dict(activation=0, width=60, grad_preact=None), "grad_preact is NULL", BAD),
     (dict(grad_x=P + 8), "grad_x", BAD), (dict(grad_w=P + 2), "grad_w", BAD), (dict(grad_bias=P + 2), "grad_bias", BAD),
     (dict(workspace=None), "workspace is NULL", BAD), (dict(workspace_bytes=16), "workspace_bytes", BAD),
 ])

@@ -104,7 +104,8 @@ def check_backward(grad, x, w, act, preact, got, bias):
 
 SHAPES = [(1, 8, 8), (1, 512, 256), (2, 64, 128), (5, 72, 40), (17, 136, 264), (31, 2048, 136), (33, 256, 520), (64, 1024, 96),
           (100, 96, 2056), (129, 128, 128), (255, 264, 248), (256, 512, 256), (300, 512, 1032), (513, 4096, 64), (700, 192, 200),
-          (1021, 1000, 328), (2050, 64, 72), (8, 16384, 16), (9, 16, 16384)]
+          (1021, 1000, 328), (2050, 64, 72), (8, 16384, 16), (9, 16, 16384), (1, 8, 1), (40, 64, 3), (33, 256, 60), (700, 128, 225),
+          (300, 512, 259), (1500, 64, 130), (5, 72, 1001)]
 
 
 @pytest.mark.parametrize("T,H,W", SHAPES)
@@ -140,7 +141,8 @@ def test_every_row_counts():
     """Small whole numbers: every sum is exact, so a row or an inner element
     that is left out, or taken twice, shows."""
     g = torch.Generator(device=DEV).manual_seed(2)
-    for T, H, W in ((1, 64, 8), (37, 72, 24), (1000, 200, 136), (4100, 136, 264), (513, 1032, 8), (9000, 64, 64)):
+    for T, H, W in ((1, 64, 8), (37, 72, 24), (1000, 200, 136), (4100, 136, 264), (513, 1032, 8), (9000, 64, 64), (800, 72, 61),
+                    (1300, 136, 299)):
         x = torch.randint(-2, 3, (T, H), generator=g, device=DEV).to(BF16)
         w = torch.randint(-2, 3, (W, H), generator=g, device=DEV).to(BF16)
         bias = torch.randint(-9, 10, (W,), generator=g, device=DEV).to(F32)
@@ -320,7 +322,7 @@ def test_refusals():
     for error, call in [
             (TypeError, lambda: ep.ep_dense_product(x.float(), w)), (TypeError, lambda: ep.ep_dense_product(x, w.float())),
             (ValueError, lambda: ep.ep_dense_product(x, w[:, :32])), (ValueError, lambda: ep.ep_dense_product(x, w[0])),
-            (ep.EPError, lambda: ep.ep_dense_product(x, w[:39])), (ep.EPError, lambda: ep.ep_dense_product(x[:, :60].contiguous(), w[:, :60].contiguous())),
+            (ep.EPError, lambda: ep.ep_dense_product(x, w[:0])), (ep.EPError, lambda: ep.ep_dense_product(x[:, :60].contiguous(), w[:, :60].contiguous())),
             (ValueError, lambda: ep.ep_dense_product(x.T, w)), (KeyError, lambda: ep.ep_dense_product(x, w, activation="tanh")),
             (ValueError, lambda: ep.ep_dense_product(x, w, bias[:8])), (TypeError, lambda: ep.ep_dense_product(x, w, bias.half())),
             (ValueError, lambda: ep.ep_dense_product(x, w, residual=residual[:5])),
