@@ -19,8 +19,8 @@
 #include <algorithm>
 #include <atomic>
 
-#include "ep_device.cuh"
 #include "ep_ops.h"
+#include "ep_tc.cuh"
 
 namespace ep {
 
@@ -94,12 +94,12 @@ __device__ __forceinline__ void copies_wait() {
 
 // A row's V columns of a lane: by pieces of 16 bytes where rows allow it
 // (WIDE: through shared memory, `here` the lane's place, a block's threads
-// apart), by the same columns one by one where they do not.
+// apart), else one by one, neighbours in neighbouring lanes.
 template <bool BF16, int L, int V, bool WIDE>
 struct Columns {
   static constexpr int kPiece = BF16 ? 8 : 4, kCount = V / kPiece;
   int E, lane;
-  __device__ int column(int i, int j) const { return (i * L + lane) * kPiece + j; }
+  __device__ int column(int i, int j) const { return WIDE ? (i * L + lane) * kPiece + j : (i * kPiece + j) * L + lane; }
   __device__ void fetch(char *here, const char *row) const {
     if (!WIDE) return;
 #pragma unroll
@@ -253,13 +253,29 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
   s.lse = fmaf(c, kLn2, logf(soft));
 }
 
-// Blocks that share the tokens: all at once on the SMs, two each, or three
-// where a lane has 16 columns or fewer (65 536 tokens, 256 experts: 411
-// blocks 28 us, 293 us at most two an SM 22).
-int blocks_at_once(int E) { return E <= 128 ? 456 : 304; }
+// How the tokens are shared.  Many: by blocks that are all on the SMs at once,
+// two each, or three where a lane has 16 columns or fewer (65 536 tokens, 256
+// experts: 411 blocks 28 us, 293 us at most two an SM 22).  Few, up to five
+// passes of a block's rows: by one cluster, which joins its parts itself and
+// saves a launch, 3.4 us of the host's (1021 tokens, 64 experts in a graph 6.8
+// us, 7.0 with the launch).
+struct Cut {
+  int tokens, blocks;  // of a block, and blocks
+  bool joined;
+};
 
-int tokens_of(int T, int blocks) { return std::max(kTokenStep, ((T - 1) / blocks + kTokenStep) / kTokenStep * kTokenStep); }
-int blocks_of(int T, int blocks) { return T == 0 ? 0 : (T - 1) / tokens_of(T, blocks) + 1; }
+constexpr int kPasses = 5;
+constexpr int kJoinedCounts = 65536;  // sequences times experts, at most, of a cluster
+
+Cut cut_of(int T, int E, int S) {
+  if (T == 0) return Cut{kTokenStep, 0, false};
+  const int rows = E <= 256 ? 32 : E <= 512 ? 16 : 8;  // of a pass
+  const int each = ((T - 1) / kClusterMost + rows) / rows * rows;
+  if (E <= kLanesMost && each <= kPasses * rows && (int64_t)S * E <= kJoinedCounts) return Cut{each, (T - 1) / each + 1, true};
+  const int blocks = E <= 128 ? 456 : 304;
+  const int tokens = std::max(kTokenStep, ((T - 1) / blocks + kTokenStep) / kTokenStep * kTokenStep);
+  return Cut{tokens, (T - 1) / tokens + 1, false};
+}
 
 struct Parts {
   float *probs;     // [segments][E]
@@ -269,10 +285,12 @@ struct Parts {
   float *balance;   // [S][column blocks]
   int32_t *head;    // sequences with tokens, whether offsets are out of order, tickets of the join
   int tokens, blocks;
+  bool joined;
 };
 
-// Sequences with tokens, and whether the offsets are out of order.
-__device__ void look_at_offsets(const int32_t *offsets, int T, int S, int32_t *head) {
+// Sequences with tokens (x), and whether the offsets are out of order (y),
+// for all threads of a block.
+__device__ int2 look_at_offsets(const int32_t *offsets, int T, int S) {
   int full = 0, bad = 0;
   for (int s = threadIdx.x; s < S; s += blockDim.x) {
     full += offset_of(offsets, T, s + 1) > offset_of(offsets, T, s);
@@ -285,13 +303,76 @@ __device__ void look_at_offsets(const int32_t *offsets, int T, int S, int32_t *h
   __syncthreads();
   if (bad) atomicOr(&s_bad, 1);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < (int)blockDim.x / 32; ++i) full += s_full[i];
-    head[0] = full;
-    head[1] = s_bad;
-    head[2] = 0;
+  full = 0;
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) full += s_full[i];
+  return make_int2(full, s_bad);
+}
+
+// The same for the joining kernel, whose tickets start at 0.
+__device__ void write_head(const BalanceArgs &p, const Parts &parts) {
+  const int2 v = look_at_offsets(p.seq_offsets, p.num_tokens, p.num_sequences);
+  if (threadIdx.x != 0) return;
+  parts.head[0] = v.x;
+  parts.head[1] = v.y;
+  parts.head[2] = 0;
+}
+
+// An expert's count and mean score in a sequence, and its share of the loss,
+// from the segments' sums.
+__device__ __forceinline__ float finish_expert(const BalanceArgs &p, int s, int e, int tokens, float prob, int count, int chosen,
+                                               int full) {
+  const int64_t at = (int64_t)s * p.num_experts + e;
+  const float mean = tokens > 0 ? prob / tokens : 0.0f;
+  const float share = chosen > 0 ? (float)p.num_experts * count / chosen / full : 0.0f;
+  p.probs[at] = mean;
+  p.counts[at] = count;
+  p.slopes[at] = tokens > 0 ? share / tokens : 0.0f;
+  return share * mean;
+}
+
+__device__ __forceinline__ float loss_of(float v, int bad) { return bad != 0 ? __int_as_float(0x7fffffff) : v; }
+
+// The whole grid is one cluster: its blocks join the segments and the losses.
+__device__ void join_in_cluster(const BalanceArgs &p, const Parts &parts, float z) {
+  __shared__ float s_losses[2], s_balance[kWarps];
+  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
+  const int2 head = look_at_offsets(p.seq_offsets, T, S);
+  cluster_sync();  // the segments in global memory
+  float balance = 0.0f;
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < S * E; i += gridDim.x * kThreads) {
+    const int s = i / E, e = i - s * E;
+    const int a = offset_of(p.seq_offsets, T, s), b = offset_of(p.seq_offsets, T, s + 1);
+    const int b0 = a / parts.tokens, b1 = b > a ? (b - 1) / parts.tokens : b0 - 1;
+    float prob = 0.0f;
+    int count = 0, chosen = 0;
+#pragma unroll 4
+    for (int k = b0; k <= b1; ++k) {
+      prob += __ldcg(parts.probs + (int64_t)(k + s) * E + e);
+      count += __ldcg(parts.counts + (int64_t)(k + s) * E + e);
+      chosen += __ldcg(parts.chosen + k + s);
+    }
+    balance += finish_expert(p, s, e, b - a, prob, count, chosen, head.x);
   }
+  balance = lanes_sum<32>(balance);
+  if (threadIdx.x % 32 == 0) s_balance[threadIdx.x / 32] = balance;
   __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kWarps; ++w) balance += s_balance[w];
+    s_losses[0] = balance;
+    s_losses[1] = z;
+  }
+  cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    balance = z = 0.0f;
+    for (int b = 0; b < (int)gridDim.x; ++b) {
+      balance += load_cluster(map_shared(smem_addr(&s_losses[0]), b));
+      z += load_cluster(map_shared(smem_addr(&s_losses[1]), b));
+    }
+    const int tokens = offset_of(p.seq_offsets, T, S) - offset_of(p.seq_offsets, T, 0);
+    p.losses[0] = loss_of(balance, head.y);
+    p.losses[1] = loss_of(tokens > 0 ? z / tokens : 0.0f, head.y);
+  }
+  cluster_sync();  // before a block whose losses are read ends
 }
 
 // Passes of rows in shared memory: up to 64 KB (16 columns a lane in fp32),
@@ -321,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == parts.blocks) {  // the last block has no rows
-    look_at_offsets(p.seq_offsets, T, S, parts.head);
+    write_head(p, parts);
     return;
   }
   // passes number the rows from t0 on
@@ -447,8 +528,9 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < kWarps; ++w) z += s_z[w];
-    parts.z[blockIdx.x] = z;
+    if (!parts.joined) parts.z[blockIdx.x] = z;
   }
+  if (parts.joined) join_in_cluster(p, parts, z);
 }
 
 // More experts than a warp's lanes hold: a block a row at a time.
@@ -530,7 +612,7 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(BalanceArgs p, P
   griddep_launch_dependents();
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
   if (blockIdx.x == parts.blocks) {  // the last block has no rows
-    look_at_offsets(p.seq_offsets, T, S, parts.head);
+    write_head(p, parts);
     return;
   }
   const int t0 = blockIdx.x * parts.tokens, t1 = t0 + min(T - t0, parts.tokens);
@@ -568,10 +650,12 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
   const int s = blockIdx.x / tiles, first = blockIdx.x % tiles * 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  griddep_wait();
-  griddep_launch_dependents();
+  // (the offsets are no work of the kernel ahead, which started after all that
+  // was before it had ended)
   const int a = offset_of(p.seq_offsets, T, s), b = offset_of(p.seq_offsets, T, s + 1);
   const int b0 = a / parts.tokens, b1 = b > a ? (b - 1) / parts.tokens : b0 - 1;
+  griddep_wait();
+  griddep_launch_dependents();
   const int full = parts.head[0];
   float prob = 0.0f, z = 0.0f;
   int count = 0, chosen = 0;
@@ -600,17 +684,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   chosen = __reduce_add_sync(0xffffffffu, s_chosen[lane]);
   const int e = first + warp;
   float part = 0.0f;
-  if (e < E) {
-    const int64_t at = (int64_t)s * E + e;
-    const float mean = b > a ? prob / (b - a) : 0.0f;
-    const float share = chosen > 0 ? (float)E * count / chosen / full : 0.0f;
-    if (lane == 0) {
-      p.probs[at] = mean;
-      p.counts[at] = count;
-      p.slopes[at] = b > a ? share / (b - a) : 0.0f;
-    }
-    part = share * mean;
-  }
+  if (e < E && lane == 0) part = finish_expert(p, s, e, b - a, prob, count, chosen, full);
   if (lane == 0) s_part[warp] = part;
   __syncthreads();
   if (warp == 0) {
@@ -620,7 +694,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
       parts.balance[blockIdx.x] = part;
       if (blockIdx.x == 0) {
         const int tokens = offset_of(p.seq_offsets, T, S) - offset_of(p.seq_offsets, T, 0);
-        p.losses[1] = parts.head[1] != 0 ? __int_as_float(0x7fffffff) : tokens > 0 ? z / tokens : 0.0f;
+        p.losses[1] = loss_of(tokens > 0 ? z / tokens : 0.0f, parts.head[1]);
       }
       __threadfence();
       s_last = atomicAdd(parts.head + 2, 1) == (int)gridDim.x - 1;
@@ -636,14 +710,14 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   __syncthreads();
   if (warp != 0) return;
   balance = lanes_sum<32>(s_part[lane]);
-  if (lane == 0) p.losses[0] = parts.head[1] != 0 ? __int_as_float(0x7fffffff) : balance;
+  if (lane == 0) p.losses[0] = loss_of(balance, parts.head[1]);
 }
 
 // Without tokens nobody else looks at the offsets.
 __global__ void __launch_bounds__(kThreads) balance_empty_kernel(BalanceArgs p, Parts parts) {
   griddep_wait();
   griddep_launch_dependents();
-  look_at_offsets(p.seq_offsets, p.num_tokens, p.num_sequences, parts.head);
+  write_head(p, parts);
 }
 
 template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
@@ -766,7 +840,8 @@ __global__ void __launch_bounds__(kThreads) balance_backward_rows_kernel(Balance
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 Parts parts_of(const BalanceArgs &a) {
-  const size_t E = a.num_experts, segments = (size_t)blocks_of(a.num_tokens, blocks_at_once(a.num_experts)) + a.num_sequences;
+  const Cut cut = cut_of(a.num_tokens, a.num_experts, a.num_sequences);
+  const size_t E = a.num_experts, segments = (size_t)cut.blocks + a.num_sequences;
   char *at = static_cast<char *>(a.workspace);
   const auto take = [&](size_t bytes) {
     char *p = at;
@@ -780,8 +855,9 @@ Parts parts_of(const BalanceArgs &a) {
   p.chosen = reinterpret_cast<int32_t *>(take(segments * 4));
   p.z = reinterpret_cast<float *>(take(segments * 4));
   p.balance = reinterpret_cast<float *>(take(a.num_sequences * ((E + 31) / 32) * 4));
-  p.tokens = tokens_of(a.num_tokens, blocks_at_once(a.num_experts));
-  p.blocks = blocks_of(a.num_tokens, blocks_at_once(a.num_experts));
+  p.tokens = cut.tokens;
+  p.blocks = cut.blocks;
+  p.joined = cut.joined;
   return p;
 }
 
@@ -809,7 +885,9 @@ cudaError_t launch_lanes_as(const BalanceArgs &a, const Parts &parts, int device
   };
   const auto kernel = balance_kernel<BF16, L, V, WIDE, SIGMOID>;
   const cudaError_t e = allow_shared(kernel, smem(L * V), &ready[device]);
-  return e != cudaSuccess ? e : launch_kernel(kernel, parts.blocks + 1, kThreads, smem(a.num_experts), stream, false, a, parts);
+  if (e != cudaSuccess) return e;
+  if (parts.joined) return launch_clusters(kernel, parts.blocks, kThreads, smem(a.num_experts), stream, parts.blocks, a, parts);
+  return launch_kernel(kernel, parts.blocks + 1, kThreads, smem(a.num_experts), stream, false, a, parts);
 }
 
 template <bool BF16, int L, int V>
@@ -840,8 +918,9 @@ cudaError_t launch_grad_as(const BalanceBackwardArgs &a, int device, cudaStream_
   const size_t smem = WIDE ? (size_t)(V > 16 && !BF16 ? 1 : 3) * 2 * pass_bytes<BF16, V>() : 0;
   const auto kernel = balance_backward_kernel<BF16, L, V, WIDE, SIGMOID>;
   const cudaError_t e = allow_shared(kernel, smem, &ready[device]);
-  return e != cudaSuccess ? e : launch_kernel(kernel, blocks_of(a.num_tokens, kGradBlocks), kThreads, smem, stream, false, a,
-                                                     tokens_of(a.num_tokens, kGradBlocks));
+  if (e != cudaSuccess) return e;
+  const int tokens = std::max(kTokenStep, ((a.num_tokens - 1) / kGradBlocks + kTokenStep) / kTokenStep * kTokenStep);
+  return launch_kernel(kernel, (a.num_tokens - 1) / tokens + 1, kThreads, smem, stream, false, a, tokens);
 }
 
 template <bool BF16, int L, int V>
@@ -868,7 +947,7 @@ cudaError_t launch_grad_of(const BalanceBackwardArgs &a, int device, cudaStream_
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int S) {
-  const size_t segments = (size_t)blocks_of(T, blocks_at_once(E)) + S;
+  const size_t segments = (size_t)cut_of(T, E, S).blocks + S;
   return 16 + 2 * round16(segments * E * 4) + 2 * round16(segments * 4) + round16((size_t)S * ((E + 31) / 32) * 4);
 }
 
@@ -883,6 +962,7 @@ ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
     e = launch_kernel(balance_rows_kernel, parts.blocks + 1, kThreads, 0, stream, false, a, parts);
   else
     e = a.bf16 ? launch_lanes_of<true>(a, parts, di->device, stream) : launch_lanes_of<false>(a, parts, di->device, stream);
+  if (e == cudaSuccess && parts.joined) return EP_OK;
   const int64_t grid = (int64_t)a.num_sequences * ((a.num_experts + 31) / 32);
   if (e == cudaSuccess) e = launch_kernel(balance_join_kernel, (int)grid, kJoinThreads, 0, stream, false, a, parts);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance launch");

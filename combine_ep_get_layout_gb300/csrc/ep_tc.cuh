@@ -54,6 +54,22 @@ __device__ __forceinline__ void store_cluster(uint32_t cluster_addr, float4 v) {
                : "memory");
 }
 
+// After a cluster_sync, of what no one writes until the next: loads of a loop
+// stay in flight together.
+__device__ __forceinline__ float load_cluster(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
+  return v;
+}
+
+__device__ __forceinline__ float4 load_cluster4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr));
+  return v;
+}
+
 // Done when it returns: whoever is told of it afterwards sees the new value.
 __device__ __forceinline__ void atom_max_cluster(uint32_t cluster_addr, int v) {
   int old;
