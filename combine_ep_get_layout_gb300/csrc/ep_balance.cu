@@ -9,8 +9,9 @@
 //        + 2/N log-sum-exp softmax(l)
 //
 // Bound by memory: one pass over the logits.  A row belongs to L lanes of a
-// warp, V columns each, so that a row's sums take log2 L exchanges and the
-// columns' sums stay in registers over all rows of a lane.  A lane copies its
+// warp (beyond 1024 experts to a whole block), V columns each, so that a row's
+// sums take log2 L exchanges and the columns' sums stay in registers over all
+// rows of a lane.  A lane copies its
 // pieces of the rows ahead (cp.async) to shared memory that only it reads,
 // so they need no barrier.  The sums over
 // tokens run in a fixed order: a block's part of a sequence first (a
@@ -68,18 +69,44 @@ __device__ __forceinline__ int sequence_of(const int32_t *offsets, int T, int S,
   return low;
 }
 
+// Over a row's lanes, the same in all of them; L = kThreads: the block.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (L > 32) {
+    __shared__ float s[kWarps];
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = s[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v += s[w];
+  }
   return v;
 }
 
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (L > 32) {
+    __shared__ float s[kWarps];
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = s[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v = fmaxf(v, s[w]);
+  }
   return v;
+}
+
+// Whether all lanes that take part in a row's exchanges say so: of the warp,
+// or of the block.
+template <int L>
+__device__ __forceinline__ bool all_of(bool v) {
+  return L > 32 ? __syncthreads_and(v) != 0 : __all_sync(0xffffffffu, v) != 0;
 }
 
 __device__ __forceinline__ void copy_piece(uint32_t dst, const void *src) {
@@ -205,7 +232,7 @@ __device__ __forceinline__ void far_scores(const float (&l)[V], Scores<V, SIGMOI
   s.lse = soft > 0.0f ? m + logf(soft) : 0.0f;
 }
 
-// All lanes of the warp call it.  Exponentials are approximate (2 ulp, and
+// All lanes of the warp (L = kThreads: of the block) call it.  Exponentials are approximate (2 ulp, and
 // the rounding of their argument); NaN and -infinity become 0 through the
 // maximum with kTiny, which takes the other operand of a NaN.
 //   softmax: 2^(l log2 e - c), c = m log2 e rounded once, which cancels in p
@@ -244,7 +271,7 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
     sum = lanes_sum<L>(sum);
     soft = sum;
   }
-  if (!__all_sync(0xffffffffu, near)) {
+  if (!all_of<L>(near)) {
     far_scores<L, V, SIGMOID, GRAD>(l, s);
     return;
   }
@@ -384,7 +411,8 @@ constexpr int pass_bytes() { return kThreads * V * (BF16 ? 2 : 4); }
 
 template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(BalanceArgs p, Parts parts) {
-  extern __shared__ int4 s_rows[];  // [ahead][pieces][threads], then [warps][experts] sums and [experts] counts
+  // [ahead][pieces][threads], then [warps][experts] sums (within a warp's rows) and [experts] counts
+  extern __shared__ int4 s_rows[];
   __shared__ float s_z[kWarps];
   __shared__ int s_chosen[kWarps];
   constexpr int kRows = kThreads / L, kAhead = ahead<BF16, V>(), kPass = pass_bytes<BF16, V>();
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Columns<BF16, L, V, WIDE> columns{E, (int)threadIdx.x % L};
   float *s_probs = reinterpret_cast<float *>(reinterpret_cast<char *>(s_rows) + (WIDE ? kAhead * kPass : 0));
-  int *s_counts = reinterpret_cast<int *>(s_probs + kWarps * E);
+  int *s_counts = reinterpret_cast<int *>(s_probs + (L > 32 ? 0 : kWarps * E));
   char *mine = reinterpret_cast<char *>(s_rows + threadIdx.x);
   const int t0 = (int)blockIdx.x < parts.blocks ? blockIdx.x * parts.tokens : 0, count = min(T - t0, parts.tokens), row = threadIdx.x / L;
   const int64_t apart = p.row_stride * (BF16 ? 2 : 4);
@@ -487,22 +515,25 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
 #pragma unroll
         for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
       }
+      const int64_t segment = (int64_t)blockIdx.x + s;
       if (lane < L) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int c = columns.column(j / columns.kPiece, j % columns.kPiece);
-          if (c < E) s_probs[warp * E + c] = acc[j];
+          if (L > 32 && c < E) parts.probs[segment * E + c] = acc[j];
+          if (L <= 32 && c < E) s_probs[warp * E + c] = acc[j];
         }
       }
       chosen = __reduce_add_sync(0xffffffffu, chosen);
       if (lane == 0) s_chosen[warp] = chosen;
       __syncthreads();
-      const int64_t segment = (int64_t)blockIdx.x + s;
       for (int e = threadIdx.x; e < E; e += kThreads) {
-        float sum = s_probs[e];
+        if (L <= 32) {
+          float sum = s_probs[e];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) sum += s_probs[w * E + e];
-        parts.probs[segment * E + e] = sum;
+          for (int w = 1; w < kWarps; ++w) sum += s_probs[w * E + e];
+          parts.probs[segment * E + e] = sum;
+        }
         parts.counts[segment * E + e] = s_counts[e];
         s_counts[e] = 0;
       }
@@ -531,112 +562,6 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
     if (!parts.joined) parts.z[blockIdx.x] = z;
   }
   if (parts.joined) join_in_cluster(p, parts, z);
-}
-
-// More experts than a warp's lanes hold: a block a row at a time.
-template <typename Op>
-__device__ __forceinline__ float block_reduce(float v, float *s, Op op) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s[0];
-  for (int i = 1; i < (int)blockDim.x / 32; ++i) v = op(v, s[i]);
-  return v;
-}
-
-struct Sum {
-  __device__ float operator()(float a, float b) const { return a + b; }
-};
-struct Max {
-  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-
-// What a row's scores need: softmax e^(l - m) / soft, sigmoid scores
-// e^(min(l, 0) - k) / (1 + e^-|l|) / sig.
-struct Row {
-  float m, soft, k, sig;
-  __device__ float softmax(float l) const { return soft > 0.0f ? expf(l - m) / soft : 0.0f; }
-  __device__ float sigmoid(float l) const {
-    return sig > 0.0f && l > kNegInf ? expf(fminf(l, 0.0f) - k) / (1.0f + expf(-fabsf(l))) / sig : 0.0f;
-  }
-  __device__ float lse() const { return soft > 0.0f ? m + logf(soft) : 0.0f; }
-};
-
-__device__ Row row_of(const void *logits, bool bf16, int64_t at, int E, bool sigmoid, float *s) {
-  Row r;
-  float m = kNegInf, sum = 0.0f, sig = 0.0f;
-  for (int e = threadIdx.x; e < E; e += kThreads) m = fmaxf(m, offered(value_of(logits, bf16, at + e)));
-  r.m = block_reduce(m, s, Max());
-  r.k = fminf(r.m, 0.0f);
-  if (r.m > kNegInf) {
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      const float l = offered(value_of(logits, bf16, at + e));
-      sum += expf(l - r.m);
-      if (sigmoid) sig += l > kNegInf ? expf(fminf(l, 0.0f) - r.k) / (1.0f + expf(-fabsf(l))) : 0.0f;
-    }
-  }
-  r.soft = block_reduce(sum, s, Sum());
-  r.sig = block_reduce(sig, s, Sum());
-  return r;
-}
-
-// The choices of rows a ... b, counted in shared memory and written with
-// their number.
-__device__ void count_choices(const BalanceArgs &p, int a, int b, int64_t segment, int32_t *s_counts, const Parts &parts) {
-  __shared__ int s_chosen;
-  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) s_counts[e] = 0;
-  if (threadIdx.x == 0) s_chosen = 0;
-  __syncthreads();
-  int chosen = 0;
-  for (int64_t i = (int64_t)a * p.num_topk + threadIdx.x; i < (int64_t)b * p.num_topk; i += blockDim.x) {
-    const int64_t e = p.topk_idx[i];
-    if (e >= 0 && e < p.num_experts) {
-      atomicAdd(&s_counts[e], 1);
-      ++chosen;
-    }
-  }
-  chosen = __reduce_add_sync(0xffffffffu, chosen);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&s_chosen, chosen);
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x) parts.counts[segment * p.num_experts + e] = s_counts[e];
-  if (threadIdx.x == 0) parts.chosen[segment] = s_chosen;
-}
-
-__global__ void __launch_bounds__(kThreads) balance_rows_kernel(BalanceArgs p, Parts parts) {
-  __shared__ float s_reduce[kWarps];
-  __shared__ float s_probs[EP_MAX_EXPERTS];
-  __shared__ int32_t s_counts[EP_MAX_EXPERTS];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences;
-  if (blockIdx.x == parts.blocks) {  // the last block has no rows
-    write_head(p, parts);
-    return;
-  }
-  const int t0 = blockIdx.x * parts.tokens, t1 = t0 + min(T - t0, parts.tokens);
-  float z = 0.0f;
-  for (int s = sequence_of(p.seq_offsets, T, S, t0); s < S; ++s) {
-    const int a = max(t0, offset_of(p.seq_offsets, T, s)), b = min(t1, offset_of(p.seq_offsets, T, s + 1));
-    if (a >= t1) break;
-    if (a >= b) continue;
-    const int64_t segment = blockIdx.x + s;
-    for (int e = threadIdx.x; e < E; e += kThreads) s_probs[e] = 0.0f;  // each thread its own
-    for (int t = a; t < b; ++t) {
-      const int64_t at = t * p.row_stride;
-      const Row r = row_of(p.logits, p.bf16, at, E, p.sigmoid, s_reduce);
-      for (int e = threadIdx.x; e < E; e += kThreads) {
-        const float l = offered(value_of(p.logits, p.bf16, at + e));
-        s_probs[e] += p.sigmoid ? r.sigmoid(l) : r.softmax(l);
-      }
-      z += r.lse() * r.lse();
-    }
-    count_choices(p, a, b, segment, s_counts, parts);
-    for (int e = threadIdx.x; e < E; e += kThreads) parts.probs[segment * E + e] = s_probs[e];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0 && t0 < t1) parts.z[blockIdx.x] = z;
 }
 
 constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
@@ -796,47 +721,6 @@ __global__ void __launch_bounds__(kThreads, 2) balance_backward_kernel(BalanceBa
   }
 }
 
-__device__ __forceinline__ void store_grad(void *p, bool bf16, int64_t i, float v) {
-  if (bf16)
-    static_cast<uint16_t *>(p)[i] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
-  else
-    static_cast<float *>(p)[i] = v;
-}
-
-__global__ void __launch_bounds__(kThreads) balance_backward_rows_kernel(BalanceBackwardArgs p) {
-  __shared__ float s_reduce[kWarps];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int E = p.num_experts, S = p.num_sequences, T = p.num_tokens;
-  const int first = offset_of(p.seq_offsets, T, 0), last = offset_of(p.seq_offsets, T, S);
-  const float db = p.grad_losses[0], dz = p.grad_losses[1] * 2.0f / max(1, last - first);
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int s = sequence_of(p.seq_offsets, T, S, (int)t);
-    const bool inside = s < S && t >= first;
-    Row r = {};
-    float dot = 0.0f;
-    const float *slope = p.slopes + (int64_t)min(s, S - 1) * E;
-    const auto score = [&](float l) { return p.sigmoid ? r.sigmoid(l) : r.softmax(l); };
-    if (inside) {
-      r = row_of(p.logits, p.bf16, t * p.row_stride, E, p.sigmoid, s_reduce);
-      for (int e = threadIdx.x; e < E; e += kThreads)
-        dot += score(offered(value_of(p.logits, p.bf16, t * p.row_stride + e))) * slope[e];
-      dot = block_reduce(dot, s_reduce, Sum());
-    }
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float d = 0.0f;
-      if (inside) {
-        const float l = offered(value_of(p.logits, p.bf16, t * p.row_stride + e));
-        d = db * score(l) * (slope[e] - dot);
-        if (p.sigmoid) d *= 1.0f / (1.0f + expf(l));
-        d += dz * r.lse() * r.softmax(l);
-      }
-      if (p.add != nullptr) d += value_of(p.add, p.bf16, t * E + e);
-      store_grad(p.grad_logits, p.bf16, t * E + e, d);
-    }
-  }
-}
-
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 Parts parts_of(const BalanceArgs &a) {
@@ -881,7 +765,7 @@ template <bool BF16, int L, int V, bool WIDE, bool SIGMOID>
 cudaError_t launch_lanes_as(const BalanceArgs &a, const Parts &parts, int device, cudaStream_t stream) {
   static std::atomic<bool> ready[64];
   const auto smem = [](int experts) {
-    return (size_t)(WIDE ? ahead<BF16, V>() * pass_bytes<BF16, V>() : 0) + (size_t)(kWarps + 1) * experts * 4;
+    return (size_t)(WIDE ? ahead<BF16, V>() * pass_bytes<BF16, V>() : 0) + (size_t)(L > 32 ? 1 : kWarps + 1) * experts * 4;
   };
   const auto kernel = balance_kernel<BF16, L, V, WIDE, SIGMOID>;
   const cudaError_t e = allow_shared(kernel, smem(L * V), &ready[device]);
@@ -907,7 +791,8 @@ cudaError_t launch_lanes_of(const BalanceArgs &a, const Parts &parts, int device
   if (E <= 128) return launch_lanes<BF16, 8, 16>(a, parts, wide, device, stream);
   if (E <= 256) return launch_lanes<BF16, 8, 32>(a, parts, wide, device, stream);
   if (E <= 512) return launch_lanes<BF16, 16, 32>(a, parts, wide, device, stream);
-  return launch_lanes<BF16, 32, 32>(a, parts, wide, device, stream);
+  if (E <= kLanesMost) return launch_lanes<BF16, 32, 32>(a, parts, wide, device, stream);
+  return launch_lanes<BF16, kThreads, EP_MAX_EXPERTS / kThreads>(a, parts, wide, device, stream);
 }
 
 constexpr int kGradBlocks = 304;  // two an SM
@@ -941,7 +826,8 @@ cudaError_t launch_grad_of(const BalanceBackwardArgs &a, int device, cudaStream_
   if (E <= 128) return launch_grad<BF16, 8, 16>(a, wide, device, stream);
   if (E <= 256) return launch_grad<BF16, 16, 16>(a, wide, device, stream);
   if (E <= 512) return launch_grad<BF16, 32, 16>(a, wide, device, stream);
-  return launch_grad<BF16, 32, 32>(a, wide, device, stream);
+  if (E <= kLanesMost) return launch_grad<BF16, 32, 32>(a, wide, device, stream);
+  return launch_grad<BF16, kThreads, EP_MAX_EXPERTS / kThreads>(a, wide, device, stream);
 }
 
 }  // namespace
@@ -958,8 +844,6 @@ ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
   cudaError_t e;
   if (a.num_tokens == 0)
     e = launch_kernel(balance_empty_kernel, 1, kThreads, 0, stream, false, a, parts);
-  else if (a.num_experts > kLanesMost)
-    e = launch_kernel(balance_rows_kernel, parts.blocks + 1, kThreads, 0, stream, false, a, parts);
   else
     e = a.bf16 ? launch_lanes_of<true>(a, parts, di->device, stream) : launch_lanes_of<false>(a, parts, di->device, stream);
   if (e == cudaSuccess && parts.joined) return EP_OK;
@@ -972,11 +856,7 @@ ep_status_t launch_balance_backward(const BalanceBackwardArgs &a, cudaStream_t s
   if (a.num_tokens == 0) return EP_OK;
   const DeviceInfo *di = current_device_info();
   if (di == nullptr) return EP_ERR_CUDA;
-  cudaError_t e;
-  if (a.num_experts > kLanesMost)
-    e = launch_kernel(balance_backward_rows_kernel, a.num_tokens < 65536 ? a.num_tokens : 65536, kThreads, 0, stream, false, a);
-  else
-    e = a.bf16 ? launch_grad_of<true>(a, di->device, stream) : launch_grad_of<false>(a, di->device, stream);
+  const cudaError_t e = a.bf16 ? launch_grad_of<true>(a, di->device, stream) : launch_grad_of<false>(a, di->device, stream);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance_backward launch");
 }
 
