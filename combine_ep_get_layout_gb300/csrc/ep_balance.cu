@@ -569,12 +569,16 @@ constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
 // A sequence's segments, 32 experts a block: 32 warps take every 32nd
 // segment, then a warp an expert adds those up (in the order of a shuffled
 // tree).  Block 0 adds up z too; the block that ends last, the balance loss.
+// SHORT: many sequences of few segments each, a warp a sequence and 32 experts
+// (16 384 sequences of 4 tokens, 64 experts: 59 us, the other way 513).
+template <bool SHORT>
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs p, Parts parts) {
   __shared__ float s_probs[kJoinWarps][33], s_part[kJoinWarps], s_z[kJoinWarps];
   __shared__ int s_counts[kJoinWarps][33], s_chosen[kJoinWarps], s_last;
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
-  const int s = blockIdx.x / tiles, first = blockIdx.x % tiles * 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t job = SHORT ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x;
+  const int s = min((int)(job / tiles), S - 1), first = job < (int64_t)S * tiles ? (int)(job % tiles) * 32 : E;
   // (the offsets are no work of the kernel ahead, which started after all that
   // was before it had ended)
   const int a = offset_of(p.seq_offsets, T, s), b = offset_of(p.seq_offsets, T, s + 1);
@@ -584,13 +588,13 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   const int full = parts.head[0];
   float prob = 0.0f, z = 0.0f;
   int count = 0, chosen = 0;
-  for (int i = b0 + threadIdx.x; i <= b1; i += kJoinThreads) chosen += parts.chosen[i + s];
+  for (int i = b0 + (SHORT ? lane : (int)threadIdx.x); i <= b1; i += SHORT ? 32 : kJoinThreads) chosen += parts.chosen[i + s];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < parts.blocks; i += kJoinThreads) z += parts.z[i];
   if (first + lane < E) {
     const int64_t from = (int64_t)s * E + first + lane;
 #pragma unroll 8
-    for (int i = b0 + warp; i <= b1; i += kJoinWarps) {
+    for (int i = b0 + (SHORT ? 0 : warp); i <= b1; i += SHORT ? 1 : kJoinWarps) {
       prob += parts.probs[from + (int64_t)i * E];
       count += parts.counts[from + (int64_t)i * E];
     }
@@ -603,13 +607,18 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
     s_chosen[warp] = chosen;
     s_z[warp] = z;
   }
-  __syncthreads();
-  prob = lanes_sum<32>(s_probs[lane][warp]);
-  count = __reduce_add_sync(0xffffffffu, s_counts[lane][warp]);
-  chosen = __reduce_add_sync(0xffffffffu, s_chosen[lane]);
-  const int e = first + warp;
   float part = 0.0f;
-  if (e < E && lane == 0) part = finish_expert(p, s, e, b - a, prob, count, chosen, full);
+  if (SHORT) {
+    if (first + lane < E) part = finish_expert(p, s, first + lane, b - a, prob, count, chosen, full);
+    part = lanes_sum<32>(part);
+  } else {
+    __syncthreads();
+    prob = lanes_sum<32>(s_probs[lane][warp]);
+    count = __reduce_add_sync(0xffffffffu, s_counts[lane][warp]);
+    chosen = __reduce_add_sync(0xffffffffu, s_chosen[lane]);
+    const int e = first + warp;
+    if (e < E && lane == 0) part = finish_expert(p, s, e, b - a, prob, count, chosen, full);
+  }
   if (lane == 0) s_part[warp] = part;
   __syncthreads();
   if (warp == 0) {
@@ -847,8 +856,13 @@ ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
   else
     e = a.bf16 ? launch_lanes_of<true>(a, parts, di->device, stream) : launch_lanes_of<false>(a, parts, di->device, stream);
   if (e == cudaSuccess && parts.joined) return EP_OK;
-  const int64_t grid = (int64_t)a.num_sequences * ((a.num_experts + 31) / 32);
-  if (e == cudaSuccess) e = launch_kernel(balance_join_kernel, (int)grid, kJoinThreads, 0, stream, false, a, parts);
+  // more jobs than the SMs take at once, and on average at most eight segments each
+  const int64_t jobs = (int64_t)a.num_sequences * ((a.num_experts + 31) / 32);
+  const bool many = jobs > 2 * di->num_sms && parts.blocks <= 7 * a.num_sequences;
+  if (e == cudaSuccess)
+    e = many ? launch_kernel(balance_join_kernel<true>, (int)((jobs + kJoinWarps - 1) / kJoinWarps), kJoinThreads, 0, stream,
+                             false, a, parts)
+             : launch_kernel(balance_join_kernel<false>, (int)jobs, kJoinThreads, 0, stream, false, a, parts);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance launch");
 }
 

@@ -144,7 +144,8 @@ def test_one_sequence(T, E, K, dtype, score):
 @pytest.mark.parametrize("T,E,offsets", [
     (100, 64, [0, 40, 40, 97]), (100, 64, [3, 4, 90]), (700, 24, [0, 1, 2, 3, 333, 333, 334, 700]),
     (5, 8, [0, 0, 0, 5]), (50, 128, [50, 50]), (50, 128, [0, 0]), (300, 256, list(range(0, 301, 3))),
-    (4096, 32, [0, 1000, 1001, 4000]), (1500, 1300, [7, 700, 1400]), (900, 8, [0, 256, 512, 768])])
+    (4096, 32, [0, 1000, 1001, 4000]), (1500, 1300, [7, 700, 1400]), (900, 8, [0, 256, 512, 768]),
+    (5000, 100, list(range(0, 5001, 10))), (3000, 40, [0, 2000, 2000, *range(2001, 2900)])])
 def test_sequences(T, E, offsets, score):
     l, idx = make(T, E, min(4, E), torch.float32, seed=T, masked=0.1)
     add = torch.randn((T, E), device=DEV) * 1e-3
