@@ -894,11 +894,14 @@ def _rows(x: torch.Tensor, name: str, dtypes) -> tuple:
         raise TypeError(f"{name} must be a torch.Tensor")
     if x.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    T, H = x.shape
+    T, H = shape
+    if x.is_contiguous():
+        return T, H, H
     apart, step = x.stride()
     if (H > 1 and step != 1) or (T > 1 and apart < H):
         raise ValueError(f"a row of {name} must be contiguous, and rows must not overlap")
@@ -995,14 +998,22 @@ def ep_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     both alike).  Returns [T, H] in x's type; ``mean`` and ``rstd`` (fp32 [T])
     receive the rows' statistics, which the backward pass needs."""
     T, H, apart = _rows(x, "x", _TYPES)
-    dev = x.device
-    params = _norm_params(weight, bias, H, dev)
-    _given(mean, "mean", torch.float32, dev, (T,))
-    _given(rstd, "rstd", torch.float32, dev, (T,))
-    out = _target(out, "out", x.dtype, dev, (T, H), stream)
-    _launch(dev.index, "ep_layer_norm", _norm_args(
-        x.data_ptr(), _TYPES[x.dtype], apart, T, H, _address(weight), _address(bias), _TYPES[params], eps, out.data_ptr(),
-        _address(mean), _address(rstd)), stream)
+    dev, i, dtype, f32 = x.device, x.get_device(), x.dtype, torch.float32
+    first = bias if weight is None else weight
+    params = f32 if first is None else first.dtype
+    if not (params in _TYPES and (weight is None or _good(weight, params, i, (H,)))
+            and (bias is None or _good(bias, params, i, (H,)))
+            and (mean is None or _good(mean, f32, i, (T,))) and (rstd is None or _good(rstd, f32, i, (T,)))):
+        _norm_params(weight, bias, H, dev)
+        _refuse_tensors((mean, "mean", f32, dev, (T,)), (rstd, "rstd", f32, dev, (T,)))
+    if out is None:
+        out = _empty((T, H), dtype, dev, stream)
+    elif not _good(out, dtype, i, (T, H)):
+        _refuse_tensors((out, "out", dtype, dev, (T, H)))
+    _launch(i, "ep_layer_norm", _norm_args(
+        x.data_ptr(), _TYPES[dtype], apart, T, H, 0 if weight is None else weight.data_ptr(),
+        0 if bias is None else bias.data_ptr(), _TYPES[params], eps, out.data_ptr(), 0 if mean is None else mean.data_ptr(),
+        0 if rstd is None else rstd.data_ptr()), stream)
     return out
 
 
@@ -1079,25 +1090,30 @@ def ep_dense_product(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tens
     an activation needs."""
     act = _DENSE_ACTIVATIONS[activation]
     T, H, apart, width, wide = _dense_sizes(x, w, activation)
-    bf, dev = torch.bfloat16, x.device
+    bf, dev, i = torch.bfloat16, x.device, x.get_device()
     bias_type = N.EP_TYPE_FP32
     if bias is not None:
         if bias.dtype not in _TYPES:
             raise TypeError(f"bias must be float32 or bfloat16, got {bias.dtype}")
-        _given(bias, "bias", bias.dtype, dev, (wide,))
+        if not _good(bias, bias.dtype, i, (wide,)):
+            _refuse_tensors((bias, "bias", bias.dtype, dev, (wide,)))
         bias_type = _TYPES[bias.dtype]
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _TYPES:
         raise TypeError(f"the output must be float32 or bfloat16, not {out_dtype}")
-    _given(residual, "residual", bf, dev, (T, width))
-    _given(preact, "preact", bf, dev, (T, wide))
+    if not ((residual is None or _good(residual, bf, i, (T, width))) and (preact is None or _good(preact, bf, i, (T, wide)))):
+        _refuse_tensors((residual, "residual", bf, dev, (T, width)), (preact, "preact", bf, dev, (T, wide)))
     if error_word is not None:
         _want(error_word, "error_word", torch.int32, dev)
-    out = _target(out, "out", out_dtype, dev, (T, width), stream)
-    _launch(dev.index, "ep_dense_product", _dense_args(
-        x.data_ptr(), apart, T, H, w.data_ptr(), width, _address(bias), bias_type, act, _address(residual),
-        out.data_ptr(), _TYPES[out_dtype], _address(preact), _address(error_word)), stream)
+    if out is None:
+        out = _empty((T, width), out_dtype, dev, stream)
+    elif not _good(out, out_dtype, i, (T, width)):
+        _refuse_tensors((out, "out", out_dtype, dev, (T, width)))
+    _launch(i, "ep_dense_product", _dense_args(
+        x.data_ptr(), apart, T, H, w.data_ptr(), width, 0 if bias is None else bias.data_ptr(), bias_type, act,
+        0 if residual is None else residual.data_ptr(), out.data_ptr(), _TYPES[out_dtype],
+        0 if preact is None else preact.data_ptr(), 0 if error_word is None else error_word.data_ptr()), stream)
     return out
 
 
