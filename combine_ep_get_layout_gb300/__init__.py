@@ -873,7 +873,7 @@ def _given(t, name, dtype, dev, shape):
 def _target(t, name, dtype, dev, shape, stream):
     """An output: checked if it is given, else a new tensor."""
     if t is None:
-        return _empty(shape, dtype, dev, stream)
+        return torch.empty(shape, dtype=dtype, device=dev) if stream is None else _empty(shape, dtype, dev, stream)
     _given(t, name, dtype, dev, shape)
     return t
 
@@ -881,8 +881,7 @@ def _target(t, name, dtype, dev, shape, stream):
 def _scratch(workspace, nbytes, dev, stream):
     """A workspace and its bytes."""
     if workspace is None:
-        nbytes = max(nbytes, 16)
-        return _empty(nbytes, torch.uint8, dev, stream), nbytes
+        return _empty(nbytes or 16, torch.uint8, dev, stream), nbytes or 16
     _want(workspace, "workspace", torch.uint8, dev)
     return workspace, workspace.numel()
 
@@ -968,11 +967,15 @@ def ep_balance_loss_backward(grad_losses: torch.Tensor, logits: torch.Tensor, ba
     if not (_good(grad_losses, torch.float32, i, (2,)) and _good(balance.slopes, torch.float32, i, (S, E))):
         _refuse_tensors((grad_losses, "grad_losses", torch.float32, dev, (2,)),
                         (balance.slopes, "balance.slopes", torch.float32, dev, (S, E)))
-    _given(add, "add", logits.dtype, dev, (T, E))
-    out = _target(out, "out", logits.dtype, dev, (T, E), stream)
+    dtype, shape = logits.dtype, (T, E)
+    if not ((add is None or _good(add, dtype, i, shape)) and (out is None or _good(out, dtype, i, shape))):
+        _refuse_tensors((add, "add", dtype, dev, shape), (out, "out", dtype, dev, shape))
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
     _launch(i, "ep_balance_loss_backward", _balance_backward_args(
-        grad_losses.data_ptr(), logits.data_ptr(), _LOGITS[logits.dtype], apart, T, E, _SCORES[score],
-        _address(seq_offsets), S, balance.slopes.data_ptr(), _address(add), out.data_ptr()), stream)
+        grad_losses.data_ptr(), logits.data_ptr(), _LOGITS[dtype], apart, T, E, _SCORES[score],
+        0 if seq_offsets is None else seq_offsets.data_ptr(), S, balance.slopes.data_ptr(),
+        0 if add is None else add.data_ptr(), out.data_ptr()), stream)
     return out
 
 
@@ -1038,11 +1041,19 @@ def ep_layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tens
     dtype, f32 = x.dtype, torch.float32
     if not (_good(grad, dtype, i, (T, H)) and _good(mean, f32, i, (T,)) and _good(rstd, f32, i, (T,))):
         _refuse_tensors((grad, "grad", dtype, dev, (T, H)), (mean, "mean", f32, dev, (T,)), (rstd, "rstd", f32, dev, (T,)))
-    params = _norm_params(weight, None, H, dev)
+    params = f32 if weight is None else weight.dtype
+    if weight is not None and not (params in _TYPES and _good(weight, params, i, (H,))):
+        _norm_params(weight, None, H, dev)
     if weight is None and need_params and (grad_weight is not None or grad_bias is not None):
         params = _norm_params(grad_weight, grad_bias, H, dev)
-    _given(add, "add", dtype, dev, (T, H))
-    grad_x = _target(grad_x, "grad_x", dtype, dev, (T, H), stream) if need_x else None
+    if add is not None and not _good(add, dtype, i, (T, H)):
+        _refuse_tensors((add, "add", dtype, dev, (T, H)))
+    if not need_x:
+        grad_x = None
+    elif grad_x is None:
+        grad_x = _empty((T, H), dtype, dev, stream)
+    elif not _good(grad_x, dtype, i, (T, H)):
+        _refuse_tensors((grad_x, "grad_x", dtype, dev, (T, H)))
     nbytes = 0
     if need_params:
         grad_weight = _target(grad_weight, "grad_weight", params, dev, (H,), stream)
@@ -1140,30 +1151,42 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
     bf, dev, i = torch.bfloat16, x.device, x.get_device()
     if not isinstance(grad, torch.Tensor) or grad.dtype not in _TYPES:
         raise TypeError("grad must be a float32 or bfloat16 tensor")
-    if not _good(grad, grad.dtype, i, (T, width)):
-        _refuse_tensors((grad, "grad", grad.dtype, dev, (T, width)))
-    if act != N.EP_ACT_NONE:
+    given = grad.dtype
+    if not _good(grad, given, i, (T, width)):
+        _refuse_tensors((grad, "grad", given, dev, (T, width)))
+    if act:
         if preact is None:
             raise ValueError(f"{activation} needs preact")
-        _given(preact, "preact", bf, dev, (T, wide))
+        if not _good(preact, bf, i, (T, wide)):
+            _refuse_tensors((preact, "preact", bf, dev, (T, wide)))
     else:
         preact = None
     kept = 0  # bytes of the scratch tensor for grad_preact
     pitch = (wide + 7) // 8 * 8
-    if not ((act != N.EP_ACT_NONE or grad.dtype is not bf or width % 8) and (need_x or need_w)):
+    if not ((act or given is not bf or width % 8) and (need_x or need_w)):
         grad_preact = None
     elif grad_preact is None:
         kept = (T * pitch * 2 + 255) // 256 * 256
     else:
         _given(grad_preact, "grad_preact", bf, dev, (T, pitch))
-    grad_x = _target(grad_x, "grad_x", bf, dev, (T, H), stream) if need_x else None
-    grad_w = _target(grad_w, "grad_w", bf, dev, (wide, H), stream) if need_w else None
+    x_at = w_at = bias_at = 0
+    if need_x:
+        grad_x = _target(grad_x, "grad_x", bf, dev, (T, H), stream)
+        x_at = grad_x.data_ptr()
+    else:
+        grad_x = None
+    if need_w:
+        grad_w = _target(grad_w, "grad_w", bf, dev, (wide, H), stream)
+        w_at = grad_w.data_ptr()
+    else:
+        grad_w = None
     if grad_bias is not None:
         bias_dtype = grad_bias.dtype
     if bias_dtype is not None:
         if bias_dtype not in _TYPES:
             raise TypeError(f"the bias must be float32 or bfloat16, not {bias_dtype}")
         grad_bias = _target(grad_bias, "grad_bias", bias_dtype, dev, (wide,), stream)
+        bias_at = grad_bias.data_ptr()
     if error_word is not None:
         _want(error_word, "error_word", torch.int32, dev)
     if workspace is None:
@@ -1177,8 +1200,8 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
         scratch = _empty(kept, torch.uint8, dev, stream) if kept else None
         made = _address(scratch)
     _launch(i, "ep_dense_product_backward", _dense_backward_args(
-        grad.data_ptr(), _TYPES[grad.dtype], x.data_ptr(), apart, T, H, w.data_ptr(), width, act, _address(preact),
-        made if kept else _address(grad_preact), _address(grad_x), _address(grad_w), _address(grad_bias),
+        grad.data_ptr(), _TYPES[given], x.data_ptr(), apart, T, H, w.data_ptr(), width, act,
+        0 if preact is None else preact.data_ptr(), made if kept else _address(grad_preact), x_at, w_at, bias_at,
         N.EP_TYPE_FP32 if bias_dtype is None else _TYPES[bias_dtype], at, nbytes, _address(error_word)), stream)
     return grad_x, grad_w, grad_bias
 
