@@ -959,8 +959,8 @@ def ep_balance_loss_backward(grad_losses: torch.Tensor, logits: torch.Tensor, ba
                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient of ``ep_balance_loss``'s losses for the logits ([T, E],
     the logits' dtype), given theirs (fp32 [2]) and what the forward call
-    returned, plus ``add`` ([T, E], for one what ``ep_route_backward`` gave;
-    ``out`` may be the same tensor).  The choice is held fixed."""
+    returned, plus ``add`` ([T, E], for one what ``ep_route_backward`` gave).
+    ``out`` may be ``add`` or ``logits``.  The choice is held fixed."""
     T, E, apart = _logits_sizes(logits)
     dev, i = logits.device, logits.get_device()
     S = _sequences(seq_offsets, dev)

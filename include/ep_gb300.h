@@ -775,7 +775,7 @@ ep_status_t ep_balance_loss(const ep_balance_loss_args_t *args, ep_stream_t stre
  *   grad_losses [2] fp32; slopes as ep_balance_loss gave them; logits,
  *   seq_offsets and sizes as there
  *   add, grad_logits [T*E] in the logits' type, rows E apart; they may be the
- *   same memory
+ *   same memory, and grad_logits may be logits whose rows are E apart
  */
 typedef struct {
     const float *grad_losses;

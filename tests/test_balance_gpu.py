@@ -145,7 +145,8 @@ def test_one_sequence(T, E, K, dtype, score):
     (100, 64, [0, 40, 40, 97]), (100, 64, [3, 4, 90]), (700, 24, [0, 1, 2, 3, 333, 333, 334, 700]),
     (5, 8, [0, 0, 0, 5]), (50, 128, [50, 50]), (50, 128, [0, 0]), (300, 256, list(range(0, 301, 3))),
     (4096, 32, [0, 1000, 1001, 4000]), (1500, 1300, [7, 700, 1400]), (900, 8, [0, 256, 512, 768]),
-    (5000, 100, list(range(0, 5001, 10))), (3000, 40, [0, 2000, 2000, *range(2001, 2900)])])
+    (5000, 100, list(range(0, 5001, 10))), (3000, 40, [0, 2000, 2000, *range(2001, 2900)]),
+    (300, 16, [0] * 900 + [7] * 50 + list(range(8, 290)) + [290] * 700), (1281, 64, [0, 640, 1281]), (1280, 64, [1, 640, 1279])])
 def test_sequences(T, E, offsets, score):
     l, idx = make(T, E, min(4, E), torch.float32, seed=T, masked=0.1)
     add = torch.randn((T, E), device=DEV) * 1e-3
@@ -251,6 +252,36 @@ def test_offsets_out_of_order_are_loud(offsets):
     assert torch.isnan(b.losses).all()
     ep.ep_balance_loss_backward(torch.ones(2, device=DEV), l, b, seq_offsets=off)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("E", [16, 300, 2048])
+def test_offsets_out_of_order_in_a_large_batch(E):
+    l, idx = make(4000, E, 2, torch.float32)
+    for offsets in ([0, 3000, 10, 4000], [5, 2 ** 31 - 1, -3, 4000], [4000, 0], [3999, 4001], [0, 1, 0, 1, 0, 1, 4000]):
+        off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        b = ep.ep_balance_loss(l, idx, seq_offsets=off)
+        assert torch.isnan(b.losses).all()
+        ep.ep_balance_loss_backward(torch.ones(2, device=DEV), l, b, seq_offsets=off)
+    torch.cuda.synchronize()
+
+
+def test_given_tensors_are_used_again():
+    for T, E in ((900, 64), (5000, 256), (300, 1500)):
+        shared = torch.empty(ep.ep_balance_workspace_bytes(T, E, 3), dtype=torch.uint8, device=DEV).fill_(255)
+        off = torch.tensor([0, T // 3, T // 3, T], dtype=torch.int32, device=DEV)
+        out = None
+        for seed in range(3):
+            l, idx = make(T, E, 3, torch.float32, seed=seed)
+            want = ep.ep_balance_loss(l, idx, seq_offsets=off)
+            got = ep.ep_balance_loss(l, idx, seq_offsets=off, out=out, workspace=shared)
+            assert out is None or got is out
+            out = got
+            for name in ("losses", "counts", "probs", "slopes"):
+                assert torch.equal(getattr(got, name), getattr(want, name))
+            g = torch.tensor([1.0, 0.1], device=DEV)
+            d = ep.ep_balance_loss_backward(g, l, got, seq_offsets=off)
+            mine = l.clone()  # the gradient over the logits themselves
+            assert torch.equal(ep.ep_balance_loss_backward(g, mine, got, seq_offsets=off, out=mine), d)
 
 
 def test_gradient_by_differences():

@@ -176,6 +176,26 @@ def test_parts_and_given_tensors():
     assert all(p is m and torch.equal(p, q) for p, m, q in zip(got, mine, full))
 
 
+def test_given_outputs_set_the_type():
+    x, w, bias, residual = make(77, 128, 96, "relu", F32, True)
+    for dtype in (F32, BF16):
+        out = torch.full((77, 96), 5.0, dtype=dtype, device=DEV)
+        assert ep.ep_dense_product(x, w, bias, activation="relu", residual=residual, out=out) is out
+        check_forward(x, w, bias, "relu", residual, out)
+
+
+def test_the_widest():
+    """16 384 outputs, and as many gates beside them."""
+    for act in (None, "swiglu"):
+        x, w, bias, residual = make(3, 64, 16384, act, BF16, True)
+        preact = torch.empty((3, w.shape[0]), dtype=BF16, device=DEV)
+        out = ep.ep_dense_product(x, w, bias, activation=act, residual=residual, preact=preact)
+        check_forward(x, w, bias, act, residual, out, preact)
+        grad = torch.randn((3, 16384), device=DEV)
+        got = ep.ep_dense_product_backward(grad, x, w, activation=act, preact=preact if act else None, bias_dtype=BF16)
+        check_backward(grad, x, w, act, preact, got, bias)
+
+
 def test_residual_in_place():
     for act in (None, "swiglu"):
         x, w, bias, residual = make(333, 512, 264, act, F32, True)
