@@ -565,38 +565,75 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
 }
 
 constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
+constexpr int kAtOnce = 15;  // segments that a lane reads at once: 480 of a sequence by 32 warps
 
-// A sequence's segments, 32 experts a block: 32 warps take every 32nd
-// segment, then a warp an expert adds those up (in the order of a shuffled
-// tree).  Block 0 adds up z too; the block that ends last, the balance loss.
-// SHORT: many sequences of few segments each, a warp a sequence and 32 experts
-// (16 384 sequences of 4 tokens, 64 experts: 59 us, the other way 513).
-template <bool SHORT>
-__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs p, Parts parts) {
-  __shared__ float s_probs[kJoinWarps][33], s_part[kJoinWarps], s_z[kJoinWarps];
-  __shared__ int s_counts[kJoinWarps][33], s_chosen[kJoinWarps], s_last;
+// How the segments are joined: 32 experts of a sequence are a job of `warps`
+// warps (a power of two).  Few segments are joined by one cluster, whose
+// blocks add up the losses in its shared memory; else the block that ends last
+// does it, 2 us later, where eight SMs would take longer to read them (65 536
+// tokens, 256 experts, one sequence, 0.6 MB: the whole call 17.9 us, the other
+// way 20.7; 16 384 of 1000, 2.4 MB: 29.8 and 28.5).
+constexpr int64_t kClusterBytes = 1 << 20;
+
+struct Join {
+  int warps, blocks;
+  bool cluster;
+};
+
+Join join_of(const Cut &cut, int E, int S) {
+  const int64_t jobs = (int64_t)S * ((E + 31) / 32);
+  Join j;
+  j.cluster = jobs <= kClusterMost * kJoinWarps && ((int64_t)cut.blocks + S) * E * 8 <= kClusterBytes;
+  j.warps = 1;
+  if (j.cluster) {
+    const int each = (int)((jobs + kClusterMost - 1) / kClusterMost);  // jobs of a block
+    while (2 * j.warps * each <= kJoinWarps) j.warps *= 2;
+  } else {
+    const int mean = cut.blocks / S + 1;
+    while (j.warps < kJoinWarps && j.warps * kAtOnce < mean) j.warps *= 2;
+  }
+  const int of_block = kJoinWarps / j.warps;
+  j.blocks = (int)((jobs + of_block - 1) / of_block);
+  return j;
+}
+
+// Block 0 adds up z too.
+__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs p, Parts parts, Join join) {
+  __shared__ float s_probs[kJoinWarps][32], s_part[kJoinWarps], s_z[kJoinWarps], s_loss;
+  __shared__ int s_counts[kJoinWarps][32], s_chosen[kJoinWarps], s_last;
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t job = SHORT ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x;
-  const int s = min((int)(job / tiles), S - 1), first = job < (int64_t)S * tiles ? (int)(job % tiles) * 32 : E;
+  const int of_block = kJoinWarps / join.warps, sub = warp % join.warps;
+  const int64_t job = (int64_t)blockIdx.x * of_block + warp / join.warps;
+  const bool some = job < (int64_t)S * tiles;
+  const int s = some ? (int)(job / tiles) : 0, e = some ? (int)(job % tiles) * 32 + lane : E;
   // (the offsets are no work of the kernel ahead, which started after all that
   // was before it had ended)
   const int a = offset_of(p.seq_offsets, T, s), b = offset_of(p.seq_offsets, T, s + 1);
-  const int b0 = a / parts.tokens, b1 = b > a ? (b - 1) / parts.tokens : b0 - 1;
+  const int b0 = a / parts.tokens, b1 = some && b > a ? (b - 1) / parts.tokens : b0 - 1;
   griddep_wait();
   griddep_launch_dependents();
-  const int full = parts.head[0];
+  const int full = parts.head[0], bad = parts.head[1];
   float prob = 0.0f, z = 0.0f;
   int count = 0, chosen = 0;
-  for (int i = b0 + (SHORT ? lane : (int)threadIdx.x); i <= b1; i += SHORT ? 32 : kJoinThreads) chosen += parts.chosen[i + s];
+  for (int i = b0 + sub * 32 + lane; i <= b1; i += join.warps * 32) chosen += parts.chosen[i + s];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < parts.blocks; i += kJoinThreads) z += parts.z[i];
-  if (first + lane < E) {
-    const int64_t from = (int64_t)s * E + first + lane;
-#pragma unroll 8
-    for (int i = b0 + (SHORT ? 0 : warp); i <= b1; i += SHORT ? 1 : kJoinWarps) {
-      prob += parts.probs[from + (int64_t)i * E];
-      count += parts.counts[from + (int64_t)i * E];
+  const int64_t from = (int64_t)s * E + e;
+  for (int i = b0 + sub; i <= b1; i += join.warps * kAtOnce) {
+    float v[kAtOnce];
+    int c[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int at = i + k * join.warps;
+      const bool there = e < E && at <= b1;
+      v[k] = there ? parts.probs[from + (int64_t)at * E] : 0.0f;
+      c[k] = there ? parts.counts[from + (int64_t)at * E] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      prob += v[k];
+      count += c[k];
     }
   }
   s_probs[warp][lane] = prob;
@@ -607,44 +644,58 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
     s_chosen[warp] = chosen;
     s_z[warp] = z;
   }
+  __syncthreads();
   float part = 0.0f;
-  if (SHORT) {
-    if (first + lane < E) part = finish_expert(p, s, first + lane, b - a, prob, count, chosen, full);
-    part = lanes_sum<32>(part);
-  } else {
-    __syncthreads();
-    prob = lanes_sum<32>(s_probs[lane][warp]);
-    count = __reduce_add_sync(0xffffffffu, s_counts[lane][warp]);
-    chosen = __reduce_add_sync(0xffffffffu, s_chosen[lane]);
-    const int e = first + warp;
-    if (e < E && lane == 0) part = finish_expert(p, s, e, b - a, prob, count, chosen, full);
+  if (sub == 0 && some) {  // the job's warps in their order
+    for (int w = 1; w < join.warps; ++w) {
+      prob += s_probs[warp + w][lane];
+      count += s_counts[warp + w][lane];
+      chosen += s_chosen[warp + w];
+    }
+    if (e < E) part = finish_expert(p, s, e, b - a, prob, count, chosen, full);
   }
+  part = lanes_sum<32>(part);
   if (lane == 0) s_part[warp] = part;
   __syncthreads();
   if (warp == 0) {
     part = lanes_sum<32>(s_part[lane]);
     z = lanes_sum<32>(s_z[lane]);
-    if (lane == 0) {
-      parts.balance[blockIdx.x] = part;
-      if (blockIdx.x == 0) {
-        const int tokens = offset_of(p.seq_offsets, T, S) - offset_of(p.seq_offsets, T, 0);
-        p.losses[1] = loss_of(tokens > 0 ? z / tokens : 0.0f, parts.head[1]);
-      }
-      __threadfence();
-      s_last = atomicAdd(parts.head + 2, 1) == (int)gridDim.x - 1;
+    if (lane == 0 && blockIdx.x == 0) {
+      const int tokens = offset_of(p.seq_offsets, T, S) - offset_of(p.seq_offsets, T, 0);
+      p.losses[1] = loss_of(tokens > 0 ? z / tokens : 0.0f, bad);
     }
+  }
+  float balance = 0.0f;
+  if (join.cluster) {
+    if (threadIdx.x == 0) s_loss = part;
+    cluster_sync();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      float v[kClusterMost];
+#pragma unroll
+      for (int k = 0; k < kClusterMost; ++k)
+        v[k] = k < (int)gridDim.x ? load_cluster(map_shared(smem_addr(&s_loss), k)) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kClusterMost; ++k) balance += v[k];
+      p.losses[0] = loss_of(balance, bad);
+    }
+    cluster_sync();  // before a block whose loss is read ends
+    return;
+  }
+  if (threadIdx.x == 0) {
+    parts.balance[blockIdx.x] = part;
+    __threadfence();
+    s_last = atomicAdd(parts.head + 2, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  float balance = 0.0f;
   for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += kJoinThreads) balance += __ldcg(parts.balance + i);
   balance = lanes_sum<32>(balance);
   if (lane == 0) s_part[warp] = balance;
   __syncthreads();
   if (warp != 0) return;
   balance = lanes_sum<32>(s_part[lane]);
-  if (lane == 0) p.losses[0] = loss_of(balance, parts.head[1]);
+  if (lane == 0) p.losses[0] = loss_of(balance, bad);
 }
 
 // Without tokens nobody else looks at the offsets.
@@ -856,13 +907,10 @@ ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
   else
     e = a.bf16 ? launch_lanes_of<true>(a, parts, di->device, stream) : launch_lanes_of<false>(a, parts, di->device, stream);
   if (e == cudaSuccess && parts.joined) return EP_OK;
-  // more jobs than the SMs take at once, and on average at most eight segments each
-  const int64_t jobs = (int64_t)a.num_sequences * ((a.num_experts + 31) / 32);
-  const bool many = jobs > 2 * di->num_sms && parts.blocks <= 7 * a.num_sequences;
+  const Join join = join_of(cut_of(a.num_tokens, a.num_experts, a.num_sequences), a.num_experts, a.num_sequences);
   if (e == cudaSuccess)
-    e = many ? launch_kernel(balance_join_kernel<true>, (int)((jobs + kJoinWarps - 1) / kJoinWarps), kJoinThreads, 0, stream,
-                             false, a, parts)
-             : launch_kernel(balance_join_kernel<false>, (int)jobs, kJoinThreads, 0, stream, false, a, parts);
+    e = join.cluster ? launch_clusters(balance_join_kernel, join.blocks, kJoinThreads, 0, stream, join.blocks, a, parts, join)
+                     : launch_kernel(balance_join_kernel, join.blocks, kJoinThreads, 0, stream, false, a, parts, join);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance launch");
 }
 
