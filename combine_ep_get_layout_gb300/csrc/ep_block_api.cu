@@ -39,7 +39,7 @@ ep_status_t check_workspace(const char *fn, const void *p, size_t bytes, size_t 
 }
 
 ep_status_t check_balance(const char *fn, int T, int E, int score, int type, int64_t stride, const int32_t *offsets, int S) {
-  EP_CHECK(check_size(fn, "num_tokens", T, 0, INT32_MAX));
+  EP_CHECK(check_size(fn, "num_tokens", T, 0, EP_MAX_ROWS));
   EP_CHECK(check_size(fn, "num_experts", E, 1, EP_MAX_EXPERTS));
   if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID)
     return fail(EP_ERR_INVALID_ARG, "%s: unknown score %d", fn, score);
@@ -51,7 +51,7 @@ ep_status_t check_balance(const char *fn, int T, int E, int score, int type, int
 }
 
 ep_status_t check_norm(const char *fn, int T, int H, int type, int param_type, int64_t stride) {
-  EP_CHECK(check_size(fn, "num_rows", T, 0, INT32_MAX));
+  EP_CHECK(check_size(fn, "num_rows", T, 0, EP_MAX_ROWS));
   EP_CHECK(check_size(fn, "hidden", H, 1, EP_MAX_HIDDEN));
   EP_CHECK(check_type(fn, "type", type));
   EP_CHECK(check_type(fn, "param_type", param_type));
@@ -65,13 +65,19 @@ ep_status_t check_eights(const char *fn, const char *name, int v) {
 }
 
 ep_status_t check_dense(const char *fn, int T, int H, int width, int act, int64_t stride) {
-  EP_CHECK(check_size(fn, "num_rows", T, 0, INT32_MAX));
+  EP_CHECK(check_size(fn, "num_rows", T, 0, EP_MAX_ROWS));
   EP_CHECK(check_eights(fn, "hidden", H));
   EP_CHECK(check_size(fn, "width", width, 1, EP_MAX_HIDDEN));
   if (act < EP_ACT_NONE || act > EP_ACT_GELU_TANH) return fail(EP_ERR_INVALID_ARG, "%s: unknown activation %d", fn, act);
   EP_CHECK(check_stride(fn, stride, "hidden", H));
   if (stride % 8 != 0)
     return fail(EP_ERR_INVALID_ARG, "%s: row_stride=%lld is not a multiple of 8", fn, (long long)stride);
+  return EP_OK;
+}
+
+// An output that is an operand which others still read.
+ep_status_t check_apart(const char *fn, const char *name, const void *p, const char *of, const void *q) {
+  if (p != nullptr && p == q) return fail(EP_ERR_INVALID_ARG, "%s: %s is %s", fn, name, of);
   return EP_OK;
 }
 
@@ -82,7 +88,7 @@ size_t size_of(int type) { return type == EP_TYPE_BF16 ? 2 : 4; }
 extern "C" {
 
 size_t ep_balance_workspace_bytes(int T, int E, int S) {
-  if (T < 0 || E < 1 || E > EP_MAX_EXPERTS || S < 1 || S > EP_MAX_SEQUENCES) return 0;
+  if (T < 0 || T > EP_MAX_ROWS || E < 1 || E > EP_MAX_EXPERTS || S < 1 || S > EP_MAX_SEQUENCES) return 0;
   return balance_workspace_bytes(T, E, S);
 }
 
@@ -125,6 +131,8 @@ ep_status_t ep_balance_loss_backward(const ep_balance_loss_backward_args_t *args
   EP_CHECK(check_ptr(fn, "slopes", x.slopes, 4, any));
   EP_CHECK(check_ptr(fn, "add", x.add, size, false));
   EP_CHECK(check_ptr(fn, "grad_logits", x.grad_logits, size, any));
+  if (any && x.grad_logits == x.logits && x.row_stride != x.num_experts && x.num_tokens > 1)
+    return fail(EP_ERR_INVALID_ARG, "%s: grad_logits is logits, whose rows are %lld apart", fn, (long long)x.row_stride);
   const BalanceBackwardArgs a{x.grad_losses, x.logits, x.logits_type == EP_LOGITS_BF16, x.row_stride, x.num_tokens,
                               x.num_experts, x.score == EP_SCORE_SIGMOID, x.seq_offsets, x.num_sequences, x.slopes,
                               x.add, x.grad_logits};
@@ -153,7 +161,7 @@ ep_status_t ep_layer_norm(const ep_layer_norm_args_t *args, ep_stream_t stream) 
 }
 
 size_t ep_layer_norm_workspace_bytes(int num_rows, int hidden) {
-  if (num_rows < 0 || hidden < 1 || hidden > EP_MAX_HIDDEN) return 0;
+  if (num_rows < 0 || num_rows > EP_MAX_ROWS || hidden < 1 || hidden > EP_MAX_HIDDEN) return 0;
   return norm_workspace_bytes(num_rows, hidden);
 }
 
@@ -200,6 +208,12 @@ ep_status_t ep_dense_product(const ep_dense_product_args_t *args, ep_stream_t st
   EP_CHECK(check_ptr(fn, "error_word", x.error_word, 4, false));
   if (any && x.residual == x.out && x.out_type == EP_TYPE_FP32)
     return fail(EP_ERR_INVALID_ARG, "%s: residual (bf16) is out (fp32)", fn);
+  if (any) {
+    EP_CHECK(check_apart(fn, "out", x.out, "x", x.x));
+    EP_CHECK(check_apart(fn, "out", x.out, "preact", x.preact));
+    EP_CHECK(check_apart(fn, "preact", x.preact, "x", x.x));
+    EP_CHECK(check_apart(fn, "preact", x.preact, "residual", x.residual));
+  }
   const DenseArgs a{static_cast<const uint16_t *>(x.x), x.row_stride, x.num_rows, x.hidden,
                     static_cast<const uint16_t *>(x.w), x.width, x.bias, x.bias_type == EP_TYPE_BF16, x.activation,
                     static_cast<const uint16_t *>(x.residual), x.out, x.out_type == EP_TYPE_BF16,
@@ -208,7 +222,9 @@ ep_status_t ep_dense_product(const ep_dense_product_args_t *args, ep_stream_t st
 }
 
 size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activation_t activation) {
-  if (num_rows < 0 || hidden < 8 || hidden > EP_MAX_HIDDEN || width < 1 || width > EP_MAX_HIDDEN) return 0;
+  if (num_rows < 0 || num_rows > EP_MAX_ROWS || hidden < 8 || hidden > EP_MAX_HIDDEN || hidden % 8 != 0 || width < 1 ||
+      width > EP_MAX_HIDDEN)
+    return 0;
   return dense_workspace_bytes(num_rows, hidden, width, activation);
 }
 
@@ -234,6 +250,16 @@ ep_status_t ep_dense_product_backward(const ep_dense_product_backward_args_t *ar
   EP_CHECK(check_ptr(fn, "error_word", x.error_word, 4, false));
   EP_CHECK(check_workspace(fn, x.workspace, x.workspace_bytes,
                            dense_workspace_bytes(x.num_rows, x.hidden, x.width, x.activation)));
+  if (any) {
+    EP_CHECK(check_apart(fn, "grad_x", x.grad_x, "grad", x.grad));
+    EP_CHECK(check_apart(fn, "grad_x", x.grad_x, "x", x.x));
+    EP_CHECK(check_apart(fn, "grad_x", x.grad_x, "grad_preact", x.grad_preact));
+    EP_CHECK(check_apart(fn, "grad_w", x.grad_w, "w", x.w));
+    EP_CHECK(check_apart(fn, "grad_w", x.grad_w, "x", x.x));
+    EP_CHECK(check_apart(fn, "grad_preact", x.grad_preact, "grad", x.grad));
+    EP_CHECK(check_apart(fn, "grad_preact", x.grad_preact, "preact", x.preact));
+    EP_CHECK(check_apart(fn, "grad_preact", x.grad_preact, "x", x.x));
+  }
   const DenseBackwardArgs a{x.grad, x.grad_type == EP_TYPE_BF16, static_cast<const uint16_t *>(x.x), x.row_stride,
                             x.num_rows, x.hidden, static_cast<const uint16_t *>(x.w), x.width, x.activation,
                             static_cast<const uint16_t *>(x.preact), static_cast<uint16_t *>(x.grad_preact),

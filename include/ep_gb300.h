@@ -714,6 +714,7 @@ typedef enum {
 } ep_type_t;
 
 #define EP_MAX_SEQUENCES 65536
+#define EP_MAX_ROWS (1 << 30) /* tokens or rows of a call of these operators */
 
 /* Bytes of device workspace ep_balance_loss needs (no initial contents; 0
  * for sizes it refuses). */
@@ -745,7 +746,7 @@ size_t ep_balance_workspace_bytes(int num_tokens, int num_experts, int num_seque
  *   losses [2] fp32, counts [S*E] int32, probs and slopes [S*E] fp32: written
  *   workspace >= ep_balance_workspace_bytes(T, E, S) bytes, 16-byte aligned;
  *             calls sharing one must be ordered
- * 1 <= S <= EP_MAX_SEQUENCES, T, E and K as for ep_route.
+ * 1 <= S <= EP_MAX_SEQUENCES, T <= EP_MAX_ROWS, T, E and K as for ep_route.
  */
 typedef struct {
     const void *logits;
@@ -802,7 +803,7 @@ ep_status_t ep_balance_loss_backward(const ep_balance_loss_backward_args_t *args
  *   weight, bias [H] of `param_type`, or NULL (1 and 0)
  *   out    [T*H] of `type`; may be x when its rows are H apart
  *   mean, rstd [T] fp32 or NULL (not kept): what the backward pass needs
- * T >= 0, 1 <= H <= EP_MAX_HIDDEN, eps > 0.  Arrays are aligned to their
+ * 0 <= T <= EP_MAX_ROWS, 1 <= H <= EP_MAX_HIDDEN, eps > 0.  Arrays are aligned to their
  * elements; with 16-byte aligned rows (H and row_stride of whole 16 bytes)
  * they are read and written 16 bytes at a time.
  */
@@ -877,10 +878,12 @@ ep_status_t ep_layer_norm_backward(const ep_layer_norm_backward_args_t *args, ep
  *   preact   [T * wide] bf16 or NULL: bf16(z), what the backward pass of an
  *            activation needs
  *   error_word [1] or NULL: EP_ERRBIT_TIMEOUT
- * hidden is a multiple of 8 in [8, EP_MAX_HIDDEN], width in
+ * T <= EP_MAX_ROWS, hidden is a multiple of 8 in [8, EP_MAX_HIDDEN], width in
  * [1, EP_MAX_HIDDEN] (a gate may have any number of experts; with multiples of
  * 8 the outputs are written 16 bytes at a time); x, w, residual, out and
- * preact are 16-byte aligned, bias to its elements.
+ * preact are 16-byte aligned, bias to its elements.  out and preact lie apart
+ * from the rest (but out from residual): where they begin at another's first
+ * byte the call is refused.
  */
 typedef struct {
     const void *x;
@@ -921,7 +924,9 @@ size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activati
  *          without rows.
  *   workspace >= ep_dense_workspace_bytes(...) bytes, 16-byte aligned; calls
  *          sharing one must be ordered
- * The rest as for ep_dense_product.  The sums run in a fixed order: the same
+ * The outputs and grad_preact lie apart from each other and from what is read;
+ * where they begin at its first byte the call is refused.  The rest as for
+ * ep_dense_product.  The sums run in a fixed order: the same
  * inputs give the same bits.
  */
 typedef struct {

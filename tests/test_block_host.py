@@ -158,3 +158,49 @@ def test_tensors_off_the_gpu_are_refused():
                  lambda: ep.ep_balance_loss(logits, idx), lambda: ep.ep_balance_loss_backward(torch.zeros(2), logits, b)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_too_many_rows(lib):
+    many = 2 ** 30 + 1
+    balance = dict(logits=P, row_stride=1, num_tokens=many, num_experts=1, num_sequences=1)
+    norm = dict(x=P, row_stride=1, num_rows=many, hidden=1)
+    dense = dict(x=P, row_stride=8, num_rows=many, hidden=8, w=P, width=1)
+    for fn, args in (("ep_balance_loss", dict(balance, num_topk=1)), ("ep_balance_loss_backward", balance),
+                     ("ep_layer_norm", dict(norm, eps=1e-5)), ("ep_layer_norm_backward", norm),
+                     ("ep_dense_product", dense), ("ep_dense_product_backward", dense)):
+        refused(lib, fn, getattr(N, fn + "_args_t")(**args), f"{many} > {2 ** 30}", LIMIT)
+    assert lib.ep_balance_workspace_bytes(many, 1, 1) == lib.ep_layer_norm_workspace_bytes(many, 1) == 0
+    assert lib.ep_dense_workspace_bytes(many, 8, 1, 0) == lib.ep_dense_workspace_bytes(5, 12, 8, 0) == 0
+
+
+AT = [P + i * 0x10000 for i in range(10)]
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(out=AT[0]), "out is x"), (dict(preact=AT[3]), "out is preact"), (dict(preact=AT[0]), "preact is x"),
+    (dict(preact=AT[4]), "preact is residual"),
+])
+def test_dense_refuses_an_output_that_is_an_operand(lib, kw, needle):
+    a = dict(x=AT[0], row_stride=64, num_rows=10, hidden=64, w=AT[1], width=64, bias=AT[2], activation=2, residual=AT[4],
+             out=AT[3], out_type=1, preact=AT[5])
+    a.update(kw)
+    refused(lib, "ep_dense_product", N.ep_dense_product_args_t(**a), needle, BAD)
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(grad_x=AT[0]), "grad_x is grad"), (dict(grad_x=AT[1]), "grad_x is x"), (dict(grad_x=AT[4]), "grad_x is grad_preact"),
+    (dict(grad_w=AT[2]), "grad_w is w"), (dict(grad_w=AT[1]), "grad_w is x"), (dict(grad_preact=AT[0]), "grad_preact is grad"),
+    (dict(grad_preact=AT[3]), "grad_preact is preact"), (dict(grad_preact=AT[1]), "grad_preact is x"),
+])
+def test_dense_backward_refuses_an_output_that_is_an_operand(lib, kw, needle):
+    a = dict(grad=AT[0], grad_type=1, x=AT[1], row_stride=64, num_rows=10, hidden=64, w=AT[2], width=64, activation=2,
+             preact=AT[3], grad_preact=AT[4], grad_x=AT[5], grad_w=AT[6], grad_bias=AT[7], workspace=AT[8],
+             workspace_bytes=1 << 24)
+    a.update(kw)
+    refused(lib, "ep_dense_product_backward", N.ep_dense_product_backward_args_t(**a), needle, BAD)
+
+
+def test_balance_backward_refuses_logits_apart_as_output(lib):
+    refused(lib, "ep_balance_loss_backward", N.ep_balance_loss_backward_args_t(
+        grad_losses=AT[0], logits=AT[1], row_stride=128, num_tokens=10, num_experts=64, num_sequences=1, slopes=AT[2],
+        grad_logits=AT[1]), "grad_logits is logits", BAD)
