@@ -197,9 +197,8 @@ struct Scores {
   float inv, inv_soft, lse;
 };
 
-// Rows with logits of at least 2^100 or without one of at least 2^-100 or so
-// (a sum that is no positive finite number, or a largest logit that the
-// product with log2 e could overflow): everything relative to the largest.
+// Rows whose largest logit is huge, or by sigmoid whose sum of e^l is near the
+// ends of fp32: everything relative to the largest.
 template <int L, int V, bool SIGMOID, bool GRAD>
 __device__ __forceinline__ void far_scores(const float (&l)[V], Scores<V, SIGMOID, GRAD> &s) {
   float m = kNegInf, sum = 0.0f, soft = 0.0f;
@@ -236,6 +235,7 @@ __device__ __forceinline__ void far_scores(const float (&l)[V], Scores<V, SIGMOI
 // the rounding of their argument); NaN and -infinity become 0 through the
 // maximum with kTiny, which takes the other operand of a NaN.
 //   softmax: 2^(l log2 e - c), c = m log2 e rounded once, which cancels in p
+//            (below 2^24 it is off by 1 at most, so no power overflows)
 //   sigmoid: E = e^l, sigmoid E / (1 + E); one exponential serves both scores
 template <int L, int V, bool SIGMOID, bool GRAD>
 __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID, GRAD> &s) {
@@ -261,7 +261,7 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
 #pragma unroll
     for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
     m = lanes_max<L>(m);
-    near = fabsf(m) < 1e30f;
+    near = fabsf(m) < 16777216.0f;
     c = m * kLog2e;
 #pragma unroll
     for (int j = 0; j < V; ++j) {

@@ -212,6 +212,33 @@ def test_an_infinite_logit_counts_as_the_largest():
         assert torch.equal(a.probs, b.probs) and torch.isfinite(a.probs).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("base", [1e5, 1e7, 1.7e7, 1e9, 1e12, 1e20, 0.9e30])
+def test_large_logits(base, dtype, score):
+    """Ties at the largest of huge logits (the rest far below it): scores are
+    quotients of few equal numbers, 64 roundings of 2^-24 and those of the
+    exponentials' 2 ulp."""
+    T, E = 40, 96
+    l = torch.full((T, E), base, device=DEV)
+    l[1::2, 5:] = base * 0.75
+    l[2::4] *= -1
+    l[3::4] *= -1
+    l = l.to(dtype)
+    idx = torch.zeros((T, 1), dtype=torch.int64, device=DEV)
+    b = ep.ep_balance_loss(l, idx, score=score)
+    losses, counts, probs, slopes = balance64(l, idx, score, None)
+    near = 2.0 ** -18
+    assert torch.equal(b.counts.long(), counts)
+    assert ((b.probs - probs).abs() <= near * probs).all()
+    for i in range(2):
+        assert abs(float(b.losses[i]) - min(float(losses[i]), math.inf)) <= near * float(losses[i]) or float(losses[i]) > 3e38
+    grad = (0.7, 1e-3)
+    got = ep.ep_balance_loss_backward(torch.tensor(grad, device=DEV), l, b, score=score)
+    want, size = gradient64(l, slopes, grad, score, None, None)
+    assert ((got.double() - want).abs() <= torch.finfo(dtype).eps / 2 * want.abs() + near * size + 1e-38).all()
+
+
 def test_choices_outside_and_named_twice():
     l, idx = make(40, 12, 3, torch.float32)
     idx[0] = torch.tensor([5, 5, 5], device=DEV)
