@@ -51,6 +51,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// Of normal numbers (beyond 2^126 it gives 0), without the scaling that the
+// others take.
+__device__ __forceinline__ float rcp_normal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ int offset_of(const int32_t *offsets, int T, int s) {
   return offsets == nullptr ? (s == 0 ? 0 : T) : min(max(offsets[s], 0), T);
 }
@@ -133,12 +141,16 @@ struct Columns {
     for (int i = 0; i < kCount; ++i)
       if (column(i, 0) < E) copy_piece(smem_addr(here) + i * kThreads * 16, row + column(i, 0) * (BF16 ? 2 : 4));
   }
-  // Where no copy comes: -infinity, or 0 of either type.
-  __device__ void clear(char *here, bool masked) const {
-    const int w = !masked ? 0 : BF16 ? (int)0xff80ff80u : (int)0xff800000u;
+  // Where no copy comes: past the last expert -infinity, or 0 of either type,
+  // and 0 in a row that is not `there` (its lanes take part in exchanges; what
+  // they hold decides how their neighbours compute).
+  __device__ void clear(char *here, bool masked, bool there) const {
 #pragma unroll
-    for (int i = 0; i < kCount; ++i)
-      if (WIDE && column(i, 0) >= E) *reinterpret_cast<int4 *>(here + i * kThreads * 16) = make_int4(w, w, w, w);
+    for (int i = 0; i < kCount; ++i) {
+      const bool past = column(i, 0) >= E;
+      const int w = !(masked && past) ? 0 : BF16 ? (int)0xff80ff80u : (int)0xff800000u;
+      if (WIDE && (past || !there)) *reinterpret_cast<int4 *>(here + i * kThreads * 16) = make_int4(w, w, w, w);
+    }
   }
   // Columns past the last expert read what `clear` put there, or `none`.
   __device__ void load(const char *here, const char *row, float none, float (&v)[V]) const {
@@ -244,7 +256,7 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
   if (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float e = exp2_approx(fmaxf(l[j] * kLog2e, kTiny)), r = rcp_approx(1.0f + e);
+      const float e = exp2_approx(fmaxf(l[j] * kLog2e, kTiny)), r = rcp_normal(1.0f + e);
       s.e[j] = e * r;
       sum += s.e[j];
       soft += e;
@@ -275,8 +287,8 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
     far_scores<L, V, SIGMOID, GRAD>(l, s);
     return;
   }
-  s.inv = rcp_approx(sum);
-  s.inv_soft = SIGMOID ? rcp_approx(soft) : s.inv;
+  s.inv = rcp_normal(sum);
+  s.inv_soft = SIGMOID ? rcp_normal(soft) : s.inv;
   s.lse = fmaf(c, kLn2, logf(soft));
 }
 
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
   const int64_t apart = p.row_stride * (BF16 ? 2 : 4);
   const char *from = static_cast<const char *>(p.logits) + (t0 + row) * apart;
   for (int e = threadIdx.x; e < E; e += kThreads) s_counts[e] = 0;
-  for (int i = 0; i < kAhead; ++i) columns.clear(mine + i * kPass, true);
+  for (int i = 0; i < kAhead; ++i) columns.clear(mine + i * kPass, true, row + i * kRows < count);
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == parts.blocks) {  // the last block has no rows
@@ -476,10 +488,6 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
     float l[V];
     if (WIDE) copies_wait<kAhead - 1>();
     columns.load(mine + slot * kPass, r < count ? from : from - row * apart, kNegInf, l);
-    if (r >= count) {  // all lanes take part in the exchanges
-#pragma unroll
-      for (int j = 0; j < V; ++j) l[j] = 0.0f;
-    }
     if (WIDE) fetch(slot);
     if (++slot == kAhead) slot = 0;
     int now[kChoices];
@@ -719,8 +727,8 @@ __global__ void __launch_bounds__(kThreads, 2) balance_backward_kernel(BalanceBa
   const char *add_from = static_cast<const char *>(p.add) + (t0 + row) * packed;
   char *out = static_cast<char *>(p.grad_logits) + (t0 + row) * packed;
   for (int i = 0; i < kAhead; ++i) {
-    columns.clear(mine + i * 2 * kPass, true);
-    columns.clear(mine + (i * 2 + 1) * kPass, false);
+    columns.clear(mine + i * 2 * kPass, true, row + i * kRows < count);
+    columns.clear(mine + (i * 2 + 1) * kPass, false, true);
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -756,10 +764,6 @@ __global__ void __launch_bounds__(kThreads, 2) balance_backward_kernel(BalanceBa
     if (WIDE) copies_wait<kAhead - 1>();
     columns.load(here, there ? from : from - row * apart, kNegInf, l);
     if (p.add != nullptr) columns.load(here + kPass, there ? add_from : add_from - row * packed, 0.0f, add);
-    if (!there) {  // all lanes take part in the exchanges
-#pragma unroll
-      for (int j = 0; j < V; ++j) l[j] = 0.0f;
-    }
     if (WIDE) fetch(slot);
     if (++slot == kAhead) slot = 0;
     Scores<V, SIGMOID, true> sc;
