@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(32 * kRowLanes, 4) dense_gradient_kernel(Dense
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float s = sigmoid_of(a[j]);
-          other[j] = d[j] * a[j] * s;
+          other[j] = d[j] * (a[j] * s);
           d[j] *= u[j] * s * (1.0f + a[j] * (1.0f - s));
           sum[GATED ? 1 : 0][j] += other[j];
         }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kWide) dense_gradient_any_kernel(DenseBackward
     float d = load_param(p.grad, p.grad_bf16, t * p.width + n);
     if (GATED) {
       const float g = load_param(p.preact, true, t * wide + n), u = load_param(p.preact, true, t * wide + p.width + n);
-      const float s = sigmoid_of(g), du = d * g * s;
+      const float s = sigmoid_of(g), du = d * (g * s);
       d *= u * s * (1.0f + g * (1.0f - s));
       other += du;
       if (p.grad_preact != nullptr) put(t * pitch + p.width + n, du);

@@ -258,6 +258,28 @@ def test_activations_far_out():
         assert ((got - d).abs() <= 2.0 ** -15)[ok].all() and torch.isfinite(got).all(), act
 
 
+@pytest.mark.parametrize("width", [8, 5])
+def test_swiglu_gradient_far_out(width):
+    """Large gates of either sign under large gradients: products whose value
+    is 0 have no infinite part."""
+    gate = torch.tensor([1e38, -1e38, 1e30, -1e30, 200.0, -200.0, -90.0, 0.0], device=DEV)
+    T = gate.numel()
+    x, w = torch.zeros((T, 64), dtype=BF16, device=DEV), torch.zeros((2 * width, 64), dtype=BF16, device=DEV)
+    preact = torch.cat([gate[:, None].expand(T, width), torch.full((T, width), 0.5, device=DEV)], 1).to(BF16)
+    for grad in (1.0, 1e4):
+        g, u = preact[:, 0].double(), 0.5
+        s = torch.sigmoid(g)
+        want = torch.cat([(grad * u * s * (1 + g * (1 - s)))[:, None], (grad * g * s)[:, None]], 1)
+        for i in range(T):
+            db = ep.ep_dense_product_backward(torch.full((1, width), grad, device=DEV), x[i:i + 1], w, activation="swiglu",
+                                              preact=preact[i:i + 1].clone(), bias_dtype=F32, need_x=False,
+                                              need_w=False)[2].view(2, width).double()
+            for h in range(2):
+                top = float(want[i, h])
+                if abs(top) < 3e38:
+                    assert ((db[h] - top).abs() <= 2.0 ** -15 * max(abs(top), grad)).all(), (grad, float(g[i]), h, db[h], top)
+
+
 def test_no_rows():
     x, w, bias, _ = make(0, 64, 40, None)
     assert ep.ep_dense_product(x, w, bias).shape == (0, 40)
