@@ -616,8 +616,12 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   const bool some = job < (int64_t)S * tiles;
   const int s = some ? (int)(job / tiles) : 0, e = some ? (int)(job % tiles) * 32 + lane : E;
   // (the offsets are no work of the kernel ahead, which started after all that
-  // was before it had ended)
-  const int a = offset_of(p.seq_offsets, T, s), b = offset_of(p.seq_offsets, T, s + 1);
+  // was before it had ended; from L2, which that reached)
+  int a = 0, b = T;
+  if (p.seq_offsets != nullptr) {
+    a = min(max(__ldcg(p.seq_offsets + s), 0), T);
+    b = min(max(__ldcg(p.seq_offsets + s + 1), 0), T);
+  }
   const int b0 = a / parts.tokens, b1 = some && b > a ? (b - 1) / parts.tokens : b0 - 1;
   griddep_wait();
   griddep_launch_dependents();
