@@ -51,14 +51,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// Of normal numbers (beyond 2^126 it gives 0), without the scaling that the
-// others take.
-__device__ __forceinline__ float rcp_normal(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 __device__ __forceinline__ int offset_of(const int32_t *offsets, int T, int s) {
   return offsets == nullptr ? (s == 0 ? 0 : T) : min(max(offsets[s], 0), T);
 }

@@ -196,6 +196,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
+// ... of normal numbers (beyond 2^126 it gives 0), without the scaling that
+// the others take.
+__device__ __forceinline__ float rcp_normal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // (a * c, b * c), rounded to nearest even, as one packed f32x2 multiply.
 __device__ __forceinline__ void mul2_rn(float a, float b, float c, float &ac, float &bc) {
   asm("{\n\t.reg .b64 t, k, u;\n\tmov.b64 t, {%2, %3};\n\tmov.b64 k, {%4, %4};\n\t"

@@ -355,19 +355,32 @@ __device__ __forceinline__ float load_param(const void *p, bool bf16, int64_t i)
   return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16) : static_cast<const float *>(p)[i];
 }
 
-__device__ __forceinline__ float sigmoid_of(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// e^z by the hardware's power of two (2 ulp), whose argument is rounded: off
+// by 2^-24 (4 + |z|), 2^-17 before it overflows; below 2^-126 it is 0.  With
+// it and rcp_normal a sigmoid is five instructions; with a division and
+// __expf, which scale what is not normal, it was some twenty, and results took
+// longer than their products where the inner dimension is short (8192 rows
+// 512 -> 2 x 512, SwiGLU: 13.8 us, before 20.5; 1024 rows 2048 -> 2048, SiLU:
+// 11.4, before 14.2).
+__device__ __forceinline__ float exp_quick(float z) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z * 1.4426950408889634f));
+  return r;
+}
+
+__device__ __forceinline__ float sigmoid_of(float z) { return rcp_normal(1.0f + exp_quick(-z)); }
 
 // The normal distribution's integral up to z, and e^(-z^2 / 2), by formula
 // 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions for
 // the error function at |z| / sqrt 2, of error 1.5e-7: half of that here, far
 // below the rounding of a bf16 result.
 __device__ __forceinline__ float normal_integral(float z, float &density) {
-  const float x = fabsf(z) * kRootHalf, t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
+  const float x = fabsf(z) * kRootHalf, t = rcp_normal(fmaf(0.3275911f, x, 1.0f));
   float poly = fmaf(1.061405429f, t, -1.453152027f);
   poly = fmaf(poly, t, 1.421413741f);
   poly = fmaf(poly, t, -0.284496736f);
   poly = fmaf(poly, t, 0.254829592f);
-  density = __expf(-x * x);
+  density = exp_quick(-x * x);
   const float tail = 0.5f * poly * t * density;
   return z < 0.0f ? tail : 1.0f - tail;
 }
@@ -381,7 +394,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[32]) {
     for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
   } else if (act == EP_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = silu_of(v[j]);
+    for (int j = 0; j < 32; ++j) v[j] *= sigmoid_of(v[j]);
   } else if (act == EP_ACT_GELU) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -1049,7 +1062,8 @@ __global__ void __launch_bounds__(threads_of(F), 1) product_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float other = take[j * 32 + lane];
-              o[r + j] = gate ? silu_of(v[r + j]) * other : silu_of(other) * v[16 + r + j];
+              const float z = gate ? v[r + j] : other, u = gate ? other : v[16 + r + j];
+              o[r + j] = (dense(F) ? z * sigmoid_of(z) : silu_of(z)) * u;
             }
             pair_barrier(id);  // before the next columns overwrite what the other warp reads
           }
