@@ -236,8 +236,8 @@ __device__ __forceinline__ void far_scores(const float (&l)[V], Scores<V, SIGMOI
 }
 
 // All lanes of the warp (L = kThreads: of the block) call it.  Exponentials are approximate (2 ulp, and
-// the rounding of their argument); NaN and -infinity become 0 through the
-// maximum with kTiny, which takes the other operand of a NaN.
+// the rounding of their argument); -infinity becomes 0; NaN makes the sum NaN,
+// which is not near either.
 //   softmax: 2^(l log2 e - c), c = m log2 e rounded once, which cancels in p
 //            (below 2^24 it is off by 1 at most, so no power overflows)
 //   sigmoid: E = e^l, sigmoid E / (1 + E); one exponential serves both scores
@@ -248,7 +248,7 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
   if (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float e = exp2_approx(fmaxf(l[j] * kLog2e, kTiny)), r = rcp_normal(1.0f + e);
+      const float e = exp2_approx(l[j] * kLog2e), r = rcp_normal(1.0f + e);
       s.e[j] = e * r;
       sum += s.e[j];
       soft += e;
@@ -265,15 +265,15 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
 #pragma unroll
     for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
     m = lanes_max<L>(m);
-    near = fabsf(m) < 16777216.0f;
     c = m * kLog2e;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      s.e[j] = exp2_approx(fmaxf(fmaf(l[j], kLog2e, -c), kTiny));
+      s.e[j] = exp2_approx(fmaf(l[j], kLog2e, -c));
       sum += s.e[j];
     }
     sum = lanes_sum<L>(sum);
     soft = sum;
+    near = fabsf(m) < 16777216.0f && sum > 0.0f;
   }
   if (!all_of<L>(near)) {
     far_scores<L, V, SIGMOID, GRAD>(l, s);
