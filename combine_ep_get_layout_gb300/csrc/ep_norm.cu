@@ -584,20 +584,24 @@ __global__ void __launch_bounds__(kMaxWarps * 16, 1) norm_backward_kernel(NormBa
   cluster_sync();  // before a block whose sums are read ends
 }
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 
-// The blocks' parts, added in their order by eight warps, then those; a
+// The blocks' parts, added in their order by sixteen warps, then those; a
 // column a lane.
 __global__ void __launch_bounds__(kJoinWarps * 32) norm_join_kernel(NormBackwardArgs p, int blocks) {
   __shared__ float s[kJoinWarps][32];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane;
-  float sum = 0.0f;
-  if (c < 2 * p.hidden) {
-#pragma unroll 8
-    for (int i = warp; i < blocks; i += kJoinWarps) sum += p.workspace[(int64_t)i * 2 * p.hidden + c];
+  constexpr int kEach = (kMaxBlocks + kJoinWarps - 1) / kJoinWarps;  // a warp's, all read at once
+  float v[kEach], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = warp + k * kJoinWarps;
+    v[k] = i < blocks && c < 2 * p.hidden ? p.workspace[(int64_t)i * 2 * p.hidden + c] : 0.0f;
   }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) sum += v[k];
   s[warp][lane] = sum;
   __syncthreads();
   if (warp != 0 || c >= 2 * p.hidden) return;
@@ -634,11 +638,12 @@ bool wide_rows(const void *p, int64_t stride, bool bf16) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * (bf16 ? 2 : 4) % 16 == 0;
 }
 
-// Few rows: their gradients are computed by one cluster if that takes at most
-// three rows a group.  It saves the kernel that joins the blocks' sums, 3.4 us
-// of the host's, where the device takes 0.9 us longer (13 rows of 4096 in a
-// graph 5.6 us instead of 4.7).
-constexpr int kRowsOfGroup = 3;
+// Few rows: their gradients are computed by one cluster, which saves the
+// kernel that joins the blocks' sums, 3.4 us of the host's, up to where the
+// device takes 1 to 2 us longer for it (in a graph, one cluster and two
+// kernels: 13 rows of 4096 5.5 and 4.6 us, 48 of 1024 5.1 and 3.5, 8 of 1024
+// 3.1 and 3.4; 96 of 1024 would be 7.1 and 3.7).
+int cluster_rows(int groups) { return 16 + 4 * groups; }
 
 template <typename Args>
 ep_status_t launch_rows(void (*kernel)(Args, Shape), const Args &a, const Shape &s, size_t smem, int rows, int most, const DeviceInfo *di,
@@ -674,7 +679,7 @@ ep_status_t launch_norm_backward_as(const NormBackwardArgs &a, const DeviceInfo 
   Shape s = shape_of(a.num_rows, a.hidden, U, kMaxWarps / 2, sms);
   if (params) {
     const Shape few = shape_of(a.num_rows, a.hidden, U, kMaxWarps / 2, kClusterMost);
-    if (a.num_rows <= kRowsOfGroup * kClusterMost * few.groups) {
+    if (a.num_rows <= cluster_rows(few.groups)) {
       s = few;
       s.joined = true;
       sms = kClusterMost;
