@@ -219,18 +219,27 @@ __global__ void __launch_bounds__(kWide) dense_gradient_any_kernel(DenseBackward
   if (GATED) sums[slice * wide + p.width + n] = other;
 }
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 
-// The slices by eight warps, then those in their order; a column a lane.
+// The slices by sixteen warps, ten of each read at once, then those in their
+// order; a column a lane.  (8192 rows, 256 columns, 256 slices: 4.9 us with
+// the pass over the rows, by eight warps 5.4.)
 __global__ void __launch_bounds__(32 * kJoinWarps) dense_bias_kernel(const float *sums, int slices, int wide, void *out, bool bf16) {
   __shared__ float s[kJoinWarps][32];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = blockIdx.x * 32 + lane;
+  constexpr int kAtOnce = 10;
   float sum = 0.0f;
-  if (n < wide) {
-#pragma unroll 8
-    for (int i = warp; i < slices; i += kJoinWarps) sum += sums[(int64_t)i * wide + n];
+  for (int first = warp; first < slices; first += kJoinWarps * kAtOnce) {
+    float v[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = first + k * kJoinWarps;
+      v[k] = i < slices && n < wide ? sums[(int64_t)i * wide + n] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) sum += v[k];
   }
   s[warp][lane] = sum;
   __syncthreads();
