@@ -47,8 +47,8 @@ constexpr int kJoinedRows = 384;  // at most, whose slices are a cluster
 
 // A column block's slices are neighbours.  Few rows: as many slices as a
 // cluster has blocks, which add them up themselves and save a launch, 3.4 us
-// of the host's, where the device takes 0.8 us longer (333 rows 512 -> 1408:
-// 17.2 us in a graph, 16.4 with the launch; of 1024 rows it would be 11 more).
+// of the host's (in a graph, 128 rows 1024 -> 1024: 13.1 us, 14.4 with the
+// launch; 333 rows 512 -> 1408 16.7 and 16.0; of 1024 rows 11 more).
 struct Slices {
   int columns, slices, rows;  // blocks of columns, of rows, and a slice's rows
   bool joined;
