@@ -349,14 +349,15 @@ __device__ void write_head(const BalanceArgs &p, const Parts &parts) {
 }
 
 // An expert's count and mean score in a sequence, and its share of the loss,
-// from the segments' sums.
-__device__ __forceinline__ float finish_expert(const BalanceArgs &p, int s, int e, int tokens, float prob, int count, int chosen,
-                                               int full) {
+// from the segments' sums.  A sequence may have more choices than 32 bits
+// count, and by indices named twice an expert too: its count stops there.
+__device__ __forceinline__ float finish_expert(const BalanceArgs &p, int s, int e, int tokens, float prob, int64_t count,
+                                               int64_t chosen, int full) {
   const int64_t at = (int64_t)s * p.num_experts + e;
   const float mean = tokens > 0 ? prob / tokens : 0.0f;
   const float share = chosen > 0 ? (float)p.num_experts * count / chosen / full : 0.0f;
   p.probs[at] = mean;
-  p.counts[at] = count;
+  p.counts[at] = (int32_t)min(count, (int64_t)INT32_MAX);
   p.slopes[at] = tokens > 0 ? share / tokens : 0.0f;
   return share * mean;
 }
@@ -600,7 +601,8 @@ Join join_of(const Cut &cut, int E, int S) {
 // Block 0 adds up z too.
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs p, Parts parts, Join join) {
   __shared__ float s_probs[kJoinWarps][32], s_part[kJoinWarps], s_z[kJoinWarps], s_loss;
-  __shared__ int s_counts[kJoinWarps][32], s_chosen[kJoinWarps], s_last;
+  __shared__ int64_t s_counts[kJoinWarps][32], s_chosen[kJoinWarps];
+  __shared__ int s_last;
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int of_block = kJoinWarps / join.warps, sub = warp % join.warps;
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   griddep_launch_dependents();
   const int full = parts.head[0], bad = parts.head[1];
   float prob = 0.0f, z = 0.0f;
-  int count = 0, chosen = 0;
+  int64_t count = 0, chosen = 0;
   for (int i = b0 + sub * 32 + lane; i <= b1; i += join.warps * 32) chosen += parts.chosen[i + s];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < parts.blocks; i += kJoinThreads) z += parts.z[i];
@@ -642,7 +644,9 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   }
   s_probs[warp][lane] = prob;
   s_counts[warp][lane] = count;
-  chosen = __reduce_add_sync(0xffffffffu, chosen);
+  // (by 26 bits: neither half's sum leaves 32)
+  chosen = (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)chosen & 0x3ffffffu) +
+           ((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)(chosen >> 26)) << 26);
   z = lanes_sum<32>(z);
   if (lane == 0) {
     s_chosen[warp] = chosen;

@@ -728,7 +728,8 @@ size_t ep_balance_workspace_bytes(int num_tokens, int num_experts, int num_seque
  * tokens in them:
  *   p         softmax(l), or sigmoid(l) divided by its sum over the experts
  *   counts[s,e]  choices of e: (t, k) with topk_idx[t,k] == e; others, and
- *             indices outside [0, E), count for nobody
+ *             indices outside [0, E), count for nobody (2^31 - 1 where there
+ *             are more; the losses and slopes take them all)
  *   probs[s,e]   the mean of p[t,e], 0 for an empty sequence
  *   balance   1/S' sum_s E sum_e counts[s,e] / C_s * probs[s,e], C_s the
  *             choices of s: 1 when experts or scores are balanced

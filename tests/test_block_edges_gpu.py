@@ -1,0 +1,56 @@
+"""Edges of the block's operators: more choices than 32 bits count.
+"""
+import math
+
+import pytest
+import torch
+
+import combine_ep_get_layout_gb300 as ep
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+
+
+# ------------------------------------------------------------ balance loss
+
+@pytest.mark.parametrize("tokens", [2 ** 28, 2 ** 29, 2 ** 29 + 1000])
+@pytest.mark.parametrize("split", [False, True])
+def test_more_choices_than_32_bits_count(tokens, split):
+    """2^31 choices and more, equal scores: the loss is 1 and every quotient a
+    power of two or near it.  p = 1/8; a sum of it is rounded at each of at
+    most 600 joins of segments."""
+    E = K = 8
+    try:
+        l = torch.zeros((tokens, E), dtype=BF16, device=DEV)
+        idx = torch.arange(K, device=DEV).expand(tokens, K).contiguous()
+    except torch.OutOfMemoryError:
+        pytest.skip("no room")
+    cuts = [0, 3, tokens - 500, tokens] if split else [0, tokens]
+    off = torch.tensor(cuts, dtype=torch.int32, device=DEV)
+    b = ep.ep_balance_loss(l, idx, seq_offsets=off)
+    n = (off[1:] - off[:-1]).double()[:, None]
+    near = 600 * U
+    assert torch.equal(b.counts.double(), n.expand(-1, E))
+    assert ((b.probs.double() - 1 / E).abs() <= near / E).all()
+    assert ((b.slopes.double() * n * (len(cuts) - 1) - 1).abs() <= 8 * U).all()
+    assert abs(float(b.losses[0]) - 1.0) <= 2 * near
+    grad = ep.ep_balance_loss_backward(torch.tensor([1.0, 0.0], device=DEV), l, b, seq_offsets=off)
+    assert float(grad.abs().max()) <= near  # balanced: nothing pulls
+
+
+def test_an_expert_named_more_often_than_32_bits_count():
+    """All choices name one expert: its share is 1, its count stops at the type's end."""
+    T, K, E = 2 ** 28 + 77, 8, 8
+    try:
+        l = torch.zeros((T, E), dtype=BF16, device=DEV)
+        idx = torch.full((T, K), 3, dtype=torch.int64, device=DEV)
+    except torch.OutOfMemoryError:
+        pytest.skip("no room")
+    b = ep.ep_balance_loss(l, idx)
+    want = torch.zeros(E, dtype=torch.int32, device=DEV)
+    want[3] = 2 ** 31 - 1
+    assert torch.equal(b.counts[0], want)
+    assert abs(float(b.losses[0]) - 1.0) <= 1200 * U
+    assert abs(float(b.slopes[0, 3]) * T / E - 1.0) <= 8 * U and float(b.slopes.sum()) == float(b.slopes[0, 3])
