@@ -144,8 +144,10 @@ struct Columns {
       if (WIDE && (past || !there)) *reinterpret_cast<int4 *>(here + i * kThreads * 16) = make_int4(w, w, w, w);
     }
   }
-  // Columns past the last expert read what `clear` put there, or `none`.
-  __device__ void load(const char *here, const char *row, float none, float (&v)[V]) const {
+  // Columns past the last expert read what `clear` put there, or `none`; a row
+  // that is not `there` is not read (its place may be one that another warp
+  // writes, where the gradient goes over the logits).
+  __device__ void load(const char *here, const char *row, bool there, float none, float (&v)[V]) const {
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
       if (WIDE) {
@@ -156,7 +158,8 @@ struct Columns {
           v[i * kPiece + j] = !BF16 ? __int_as_float(w[j % 4]) : j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
       } else {
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) v[i * kPiece + j] = column(i, j) < E ? value_of(row, BF16, column(i, j)) : none;
+        for (int j = 0; j < kPiece; ++j)
+          v[i * kPiece + j] = column(i, j) >= E ? none : there ? value_of(row, BF16, column(i, j)) : 0.0f;
       }
     }
   }
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
     const int r = done + row, behind = done + kRows;
     float l[V];
     if (WIDE) copies_wait<kAhead - 1>();
-    columns.load(mine + slot * kPass, r < count ? from : from - row * apart, kNegInf, l);
+    columns.load(mine + slot * kPass, from, r < count, kNegInf, l);
     if (WIDE) fetch(slot);
     if (++slot == kAhead) slot = 0;
     int now[kChoices];
@@ -762,8 +765,8 @@ __global__ void __launch_bounds__(kThreads, 2) balance_backward_kernel(BalanceBa
     const char *here = mine + slot * 2 * kPass;
     float l[V], add[V];
     if (WIDE) copies_wait<kAhead - 1>();
-    columns.load(here, there ? from : from - row * apart, kNegInf, l);
-    if (p.add != nullptr) columns.load(here + kPass, there ? add_from : add_from - row * packed, 0.0f, add);
+    columns.load(here, from, there, kNegInf, l);
+    if (p.add != nullptr) columns.load(here + kPass, add_from, there, 0.0f, add);
     if (WIDE) fetch(slot);
     if (++slot == kAhead) slot = 0;
     Scores<V, SIGMOID, true> sc;

@@ -1,4 +1,5 @@
-"""Edges of the block's operators: more choices than 32 bits count.
+"""Edges of the block's operators: more choices than 32 bits count, gradients over
+logits that are not of whole 16 bytes.
 """
 import math
 
@@ -54,3 +55,29 @@ def test_an_expert_named_more_often_than_32_bits_count():
     assert torch.equal(b.counts[0], want)
     assert abs(float(b.losses[0]) - 1.0) <= 1200 * U
     assert abs(float(b.slopes[0, 3]) * T / E - 1.0) <= 8 * U and float(b.slopes.sum()) == float(b.slopes[0, 3])
+
+
+def logits_of(T, E, dtype, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    l = (torch.randn((T, E), generator=g, device=DEV) * 1.5).to(dtype)
+    return l, torch.argsort(l.float(), dim=1, descending=True)[:, :min(4, E)].contiguous()
+
+
+@pytest.mark.parametrize("T,E", [(18, 63), (50, 63), (45, 101), (1021, 255), (301, 301), (77, 999), (5, 2047), (40, 9)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_over_logits_off_16_bytes(T, E, dtype, score):
+    """In place, rows that are not of whole 16 bytes, masked first rows: the bits of the call that writes elsewhere."""
+    l, idx = logits_of(T, E, dtype, T)
+    l[::32] = -math.inf
+    b = ep.ep_balance_loss(l, idx, score=score)
+    g = torch.tensor([0.7, 0.3], device=DEV)
+    add = (torch.randn((T, E), device=DEV) * 1e-3).to(dtype)
+    for more in (None, add):
+        want = ep.ep_balance_loss_backward(g, l, b, score=score, add=more)
+        for _ in range(5):
+            mine = l.clone()
+            assert torch.equal(ep.ep_balance_loss_backward(g, mine, b, score=score, add=more, out=mine), want)
+            if more is not None:
+                mine = more.clone()
+                assert torch.equal(ep.ep_balance_loss_backward(g, l, b, score=score, add=mine, out=mine), want)
