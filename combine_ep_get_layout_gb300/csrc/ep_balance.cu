@@ -354,13 +354,14 @@ __device__ void write_head(const BalanceArgs &p, const Parts &parts) {
 // An expert's count and mean score in a sequence, and its share of the loss,
 // from the segments' sums.  A sequence may have more choices than 32 bits
 // count, and by indices named twice an expert too: its count stops there.
-__device__ __forceinline__ float finish_expert(const BalanceArgs &p, int s, int e, int tokens, float prob, int64_t count,
-                                               int64_t chosen, int full) {
+template <typename COUNT>
+__device__ __forceinline__ float finish_expert(const BalanceArgs &p, int s, int e, int tokens, float prob, COUNT count,
+                                               COUNT chosen, int full) {
   const int64_t at = (int64_t)s * p.num_experts + e;
   const float mean = tokens > 0 ? prob / tokens : 0.0f;
   const float share = chosen > 0 ? (float)p.num_experts * count / chosen / full : 0.0f;
   p.probs[at] = mean;
-  p.counts[at] = (int32_t)min(count, (int64_t)INT32_MAX);
+  p.counts[at] = (int32_t)min(count, (COUNT)INT32_MAX);
   p.slopes[at] = tokens > 0 ? share / tokens : 0.0f;
   return share * mean;
 }
@@ -568,6 +569,12 @@ __global__ void __launch_bounds__(kThreads, V > 16 ? 2 : 3) balance_kernel(Balan
   if (parts.joined) join_in_cluster(p, parts, z);
 }
 
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {  // not negative, below 2^52
+  const uint32_t low = (uint32_t)v & 0x3ffffffu, high = (uint32_t)(v >> 26);  // neither one's sum leaves 32 bits
+  return (int64_t)__reduce_add_sync(0xffffffffu, low) + ((int64_t)__reduce_add_sync(0xffffffffu, high) << 26);
+}
+
 constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
 constexpr int kAtOnce = 15;  // segments that a lane reads at once: 480 of a sequence by 32 warps
 
@@ -601,10 +608,12 @@ Join join_of(const Cut &cut, int E, int S) {
   return j;
 }
 
-// Block 0 adds up z too.
+// Block 0 adds up z too.  COUNT: what holds the choices of a sequence, 64 bits
+// where a batch has 2^31 or more (65 536 tokens, 256 experts: 0.7 us longer).
+template <typename COUNT>
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs p, Parts parts, Join join) {
   __shared__ float s_probs[kJoinWarps][32], s_part[kJoinWarps], s_z[kJoinWarps], s_loss;
-  __shared__ int64_t s_counts[kJoinWarps][32], s_chosen[kJoinWarps];
+  __shared__ COUNT s_counts[kJoinWarps][32], s_chosen[kJoinWarps];
   __shared__ int s_last;
   const int E = p.num_experts, T = p.num_tokens, S = p.num_sequences, tiles = (E + 31) / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -624,7 +633,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   griddep_launch_dependents();
   const int full = parts.head[0], bad = parts.head[1];
   float prob = 0.0f, z = 0.0f;
-  int64_t count = 0, chosen = 0;
+  COUNT count = 0, chosen = 0;
   for (int i = b0 + sub * 32 + lane; i <= b1; i += join.warps * 32) chosen += parts.chosen[i + s];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < parts.blocks; i += kJoinThreads) z += parts.z[i];
@@ -647,9 +656,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   }
   s_probs[warp][lane] = prob;
   s_counts[warp][lane] = count;
-  // (by 26 bits: neither half's sum leaves 32)
-  chosen = (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)chosen & 0x3ffffffu) +
-           ((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)(chosen >> 26)) << 26);
+  chosen = warp_sum(chosen);
   z = lanes_sum<32>(z);
   if (lane == 0) {
     s_chosen[warp] = chosen;
@@ -915,9 +922,10 @@ ep_status_t launch_balance(const BalanceArgs &a, cudaStream_t stream) {
     e = a.bf16 ? launch_lanes_of<true>(a, parts, di->device, stream) : launch_lanes_of<false>(a, parts, di->device, stream);
   if (e == cudaSuccess && parts.joined) return EP_OK;
   const Join join = join_of(cut_of(a.num_tokens, a.num_experts, a.num_sequences), a.num_experts, a.num_sequences);
+  const auto kernel = (int64_t)a.num_tokens * a.num_topk > INT32_MAX ? balance_join_kernel<int64_t> : balance_join_kernel<int>;
   if (e == cudaSuccess)
-    e = join.cluster ? launch_clusters(balance_join_kernel, join.blocks, kJoinThreads, 0, stream, join.blocks, a, parts, join)
-                     : launch_kernel(balance_join_kernel, join.blocks, kJoinThreads, 0, stream, false, a, parts, join);
+    e = join.cluster ? launch_clusters(kernel, join.blocks, kJoinThreads, 0, stream, join.blocks, a, parts, join)
+                     : launch_kernel(kernel, join.blocks, kJoinThreads, 0, stream, false, a, parts, join);
   return e == cudaSuccess ? EP_OK : cuda_fail(e, "balance launch");
 }
 
