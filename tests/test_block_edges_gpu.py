@@ -1,5 +1,5 @@
 """Edges of the block's operators: more choices than 32 bits count, gradients over
-logits that are not of whole 16 bytes.
+logits that are not of whole 16 bytes, rows beside masked ones.
 """
 import math
 
@@ -81,3 +81,27 @@ def test_gradient_over_logits_off_16_bytes(T, E, dtype, score):
             if more is not None:
                 mine = more.clone()
                 assert torch.equal(ep.ep_balance_loss_backward(g, l, b, score=score, add=mine, out=mine), want)
+
+
+EDGES = [(8, 8), (18, 60), (50, 64), (45, 100), (77, 200), (50, 256), (37, 300), (40, 512), (20, 1000), (6, 2048)]
+
+
+@pytest.mark.parametrize("T,E", EDGES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_row_does_not_change_with_its_neighbours(T, E, dtype, score):
+    """The same bits beside rows that are masked, NaN or huge.  A sequence a
+    token, so that ``probs`` are one row's scores."""
+    l, idx = logits_of(T, E, dtype, T + E)
+    off = torch.arange(T + 1, dtype=torch.int32, device=DEV)
+    g = torch.tensor([0.7, 0.3], device=DEV)
+    other = l.clone()
+    strange = [i for i in (0, 5, 7, 17, 34, 44, T - 2) if i < T]
+    for i, value in zip(strange, [-math.inf, math.nan, 3e38, -math.inf, -90.0, -math.inf, -math.inf]):
+        other[i] = value
+    keep = [i for i in range(T) if i not in strange]
+    b = ep.ep_balance_loss(l, idx, score=score, seq_offsets=off)
+    c = ep.ep_balance_loss(other, idx, score=score, seq_offsets=off)
+    assert torch.equal(b.probs[keep], c.probs[keep])
+    d, e = (ep.ep_balance_loss_backward(g, x, b, score=score, seq_offsets=off) for x in (l, other))
+    assert torch.equal(d[keep], e[keep])
