@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kMaxWarps * 16, 1) norm_backward_kernel(NormBa
   if (M == kRing) {
     for (int i = 0; i < kAhead; ++i) fetch(i);
   }
-  constexpr bool kKeep = U < 4;  // the weight, and a row's n and g w, stay in registers
+  constexpr bool kKeep = U < 4;  // the weight, and a row's y and h w, stay in registers
   constexpr int kKept = kKeep ? U : 1;
   const Pair zero = pair_of(0.0f, 0.0f);
   Pair w[kKept][4], dw[U][4], db[U][4];
@@ -472,7 +472,14 @@ __global__ void __launch_bounds__(kMaxWarps * 16, 1) norm_backward_kernel(NormBa
     rstd = p.rstd[t];
   }
   for (; t < T; t += step, row += step * packed) {
-    const Pair scale = pair_of(rstd, rstd), shift = pair_of(-mean * rstd, -mean * rstd);
+    // With y = x - mean and h = grad rstd, so n grad = h y:
+    //   grad_x = h w - mean(h w) - y rstd (rstd mean(h w y)) + add,  grad_weight = sum h y
+    // As many instructions as with n, which x rstd - (mean rstd) would give in
+    // one, off by the rounding of mean rstd in a whole row alike.  (Where a row
+    // is read again, g = grad w instead of h w, and rstd at the end: less to do
+    // the second time.)
+    const float factor = rstd;
+    const Pair scale = pair_of(rstd, rstd), minus = pair_of(-mean, -mean);
     if (t + step < T) {  // the next row's, ahead
       mean = p.mean[t + step];
       rstd = p.rstd[t + step];
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(kMaxWarps * 16, 1) norm_backward_kernel(NormBa
                          : static_cast<const char *>(p.add) + row,
                 u, v);
     };
-    Pair n[kKept][4], gw[kKept][4], a = zero, b = zero;  // of this row
+    Pair y[kKept][4], gw[kKept][4], a = zero, b = zero;  // of this row; gw with kKeep times rstd
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       Pair x[4], g[4];
@@ -498,11 +505,12 @@ __global__ void __launch_bounds__(kMaxWarps * 16, 1) norm_backward_kernel(NormBa
       if (!kKeep) at.params(p.weight, p.param_bf16, 1.0f, u, w[k]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        n[k][j] = fma2(x[j], scale, shift);
-        gw[k][j] = mul2(g[j], w[k][j]);
+        const Pair h = mul2(g[j], scale);
+        y[k][j] = add2(x[j], minus);
+        gw[k][j] = mul2(kKeep ? h : g[j], w[k][j]);
         a = add2(a, gw[k][j]);
-        b = fma2(gw[k][j], n[k][j], b);
-        dw[u][j] = fma2(g[j], n[k][j], dw[u][j]);
+        b = fma2(gw[k][j], y[k][j], b);
+        dw[u][j] = fma2(h, y[k][j], dw[u][j]);
         db[u][j] = add2(db[u][j], g[j]);
       }
     }
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kMaxWarps * 16, 1) norm_backward_kernel(NormBa
       row_totals(av, bv, s_sums, turn, shape.warps, at.group);
       turn ^= 1;
       av *= -share;
-      bv *= -share;
+      bv = bv * -share * factor * factor;  // (one after the other: the square alone may not be finite)
       a = pair_of(av, av);
       b = pair_of(bv, bv);
 #pragma unroll
@@ -519,18 +527,21 @@ __global__ void __launch_bounds__(kMaxWarps * 16, 1) norm_backward_kernel(NormBa
         const int k = u % kKept;
         Pair plus[4] = {zero, zero, zero, zero};
         if (!kKeep) {
-          piece(0, u, n[k]);
+          piece(0, u, y[k]);
           piece(1, u, gw[k]);
           at.params(p.weight, p.param_bf16, 1.0f, u, w[k]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            n[k][j] = fma2(n[k][j], scale, shift);
+            y[k][j] = add2(y[k][j], minus);
             gw[k][j] = mul2(gw[k][j], w[k][j]);
           }
         }
         if (added) piece(2, u, plus);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) plus[j] = fma2(add2(fma2(n[k][j], b, gw[k][j]), a), scale, plus[j]);
+        for (int j = 0; j < 4; ++j) {
+          const Pair d = add2(fma2(y[k][j], b, gw[k][j]), a);
+          plus[j] = !kKeep ? fma2(d, scale, plus[j]) : added ? add2(d, plus[j]) : d;
+        }
         at.store(static_cast<char *>(p.grad_x) + row, u, plus);
       }
     }

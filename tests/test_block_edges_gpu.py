@@ -1,5 +1,6 @@
 """Edges of the block's operators: more choices than 32 bits count, gradients over
-logits that are not of whole 16 bytes, rows beside masked ones.
+logits that are not of whole 16 bytes, rows beside masked ones, rows whose mean
+is far above their deviation.
 """
 import math
 
@@ -105,3 +106,58 @@ def test_a_row_does_not_change_with_its_neighbours(T, E, dtype, score):
     assert torch.equal(b.probs[keep], c.probs[keep])
     d, e = (ep.ep_balance_loss_backward(g, x, b, score=score, seq_offsets=off) for x in (l, other))
     assert torch.equal(d[keep], e[keep])
+
+
+# -------------------------------------------------------------- layer norm
+
+NORMS = [(1, 8), (9, 31), (13, 64), (50, 300), (20, 768), (300, 1000), (3, 2047), (200, 4096), (9, 7168), (5, 8200), (40, 10000),
+         (700, 16384)]
+
+
+@pytest.mark.parametrize("T,H", NORMS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_of_constant_rows(T, H, dtype):
+    """n is 0 exactly, whatever the level, so the weight's gradient is too, and
+    grad_x is rstd (g w - mean(g w)): H/32 + 40 roundings of a sum of absolute
+    values.  The last rows' mean times rstd passes fp32's end."""
+    g = torch.Generator(device=DEV).manual_seed(T + H)
+    level = (torch.tensor([1000.1, -7.3, 0.0, 1e6, 1e30], device=DEV).repeat(T // 5 + 1)[:T]).to(dtype)
+    x = level[:, None].expand(T, H).contiguous()
+    grad = torch.randn((T, H), generator=g, device=DEV).to(dtype)
+    w = 1 + 0.2 * torch.randn(H, generator=g, device=DEV)
+    mean = level.float()
+    for eps in (1e-5, 1e-30):
+        rstd = torch.full((T,), eps ** -0.5, device=DEV)
+        dx, dw, db = ep.ep_layer_norm_backward(grad, x, mean, rstd, w)
+        assert (dw == 0).all()
+        gw = grad.double() * w.double()
+        want = rstd.double()[:, None] * (gw - gw.mean(1, keepdim=True))
+        tol = rstd.double()[:, None] * U * ((H / 32 + 40) * gw.abs().mean(1, keepdim=True) + 6 * gw.abs())
+        assert ((dx.double() - want).abs() <= tol + torch.finfo(dtype).eps / 2 * want.abs()).all()
+
+
+@pytest.mark.parametrize("T,H", NORMS)
+@pytest.mark.parametrize("ratio", [30.0, 3e3, 3e5])
+def test_gradients_of_rows_with_a_far_mean(T, H, ratio):
+    """With the statistics as given, n = (x - mean) rstd has the roundings of
+    a difference, a factor and a product: 3 U |n|, however far the mean.  The
+    sums as in the tests of the norm: H/32 + 34 roundings of a row's, of a
+    parameter's T at most (T/8 + 640 from there)."""
+    g = torch.Generator(device=DEV).manual_seed(T + H)
+    x = ratio + torch.randn((T, H), generator=g, device=DEV)
+    grad, w = torch.randn((T, H), generator=g, device=DEV), 1 + 0.2 * torch.randn(H, generator=g, device=DEV)
+    mean, rstd = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    ep.ep_layer_norm(x, w, mean=mean, rstd=rstd)
+    dx, dw, db = ep.ep_layer_norm_backward(grad, x, mean, rstd, w)
+    m, r = mean.double()[:, None], rstd.double()[:, None]
+    n = (x.double() - m) * r
+    gw = grad.double() * w.double()
+    a, b = gw.mean(1, keepdim=True), (gw * n).mean(1, keepdim=True)
+    c = U * (H / 32 + 34)
+    want = r * (gw - a - n * b)
+    off_a = c * gw.abs().mean(1, keepdim=True)
+    off_b = (c + 4 * U) * (gw * n).abs().mean(1, keepdim=True)
+    tol = r * (off_a + off_b * n.abs() + U * (6 * gw.abs() + 6 * a.abs() + 9 * (n * b).abs()))
+    assert ((dx.double() - want).abs() <= 1.01 * tol + U * want.abs()).all()
+    t = U * (min(T, T / 8 + 640) + 6)
+    assert ((dw.double() - (grad.double() * n).sum(0)).abs() <= 1.01 * t * (grad.double() * n).abs().sum(0)).all()
