@@ -75,9 +75,24 @@ ep_status_t check_dense(const char *fn, int T, int H, int width, int act, int64_
   return EP_OK;
 }
 
-// An output that is an operand which others still read.
-ep_status_t check_apart(const char *fn, const char *name, const void *p, const char *of, const void *q) {
-  if (p != nullptr && p == q) return fail(EP_ERR_INVALID_ARG, "%s: %s is %s", fn, name, of);
+// What a call writes or reads (`p` null: not given).
+struct Named {
+  const char *name;
+  const void *p;
+};
+
+// An output that begins where another output or an operand does, which others
+// may still read or write then.
+template <int M, int N>
+ep_status_t check_apart(const char *fn, const Named (&outputs)[M], const Named (&operands)[N]) {
+  for (int i = 0; i < M; ++i) {
+    const Named &out = outputs[i];
+    if (out.p == nullptr) continue;
+    for (int j = i + 1; j < M; ++j)
+      if (outputs[j].p == out.p) return fail(EP_ERR_INVALID_ARG, "%s: %s is %s", fn, out.name, outputs[j].name);
+    for (const Named &in : operands)
+      if (in.p == out.p) return fail(EP_ERR_INVALID_ARG, "%s: %s is %s", fn, out.name, in.name);
+  }
   return EP_OK;
 }
 
@@ -209,10 +224,10 @@ ep_status_t ep_dense_product(const ep_dense_product_args_t *args, ep_stream_t st
   if (any && x.residual == x.out && x.out_type == EP_TYPE_FP32)
     return fail(EP_ERR_INVALID_ARG, "%s: residual (bf16) is out (fp32)", fn);
   if (any) {
-    EP_CHECK(check_apart(fn, "out", x.out, "x", x.x));
-    EP_CHECK(check_apart(fn, "out", x.out, "preact", x.preact));
-    EP_CHECK(check_apart(fn, "preact", x.preact, "x", x.x));
-    EP_CHECK(check_apart(fn, "preact", x.preact, "residual", x.residual));
+    const Named operands[] = {{"x", x.x}, {"w", x.w}, {"bias", x.bias}, {"error_word", x.error_word},
+                              {"residual", x.residual == x.out ? nullptr : x.residual}};
+    const Named outputs[] = {{"out", x.out}, {"preact", x.preact}};
+    EP_CHECK(check_apart(fn, outputs, operands));
   }
   const DenseArgs a{static_cast<const uint16_t *>(x.x), x.row_stride, x.num_rows, x.hidden,
                     static_cast<const uint16_t *>(x.w), x.width, x.bias, x.bias_type == EP_TYPE_BF16, x.activation,
@@ -250,16 +265,13 @@ ep_status_t ep_dense_product_backward(const ep_dense_product_backward_args_t *ar
   EP_CHECK(check_ptr(fn, "error_word", x.error_word, 4, false));
   EP_CHECK(check_workspace(fn, x.workspace, x.workspace_bytes,
                            dense_workspace_bytes(x.num_rows, x.hidden, x.width, x.activation)));
-  if (any) {
-    EP_CHECK(check_apart(fn, "grad_x", x.grad_x, "grad", x.grad));
-    EP_CHECK(check_apart(fn, "grad_x", x.grad_x, "x", x.x));
-    EP_CHECK(check_apart(fn, "grad_x", x.grad_x, "grad_preact", x.grad_preact));
-    EP_CHECK(check_apart(fn, "grad_w", x.grad_w, "w", x.w));
-    EP_CHECK(check_apart(fn, "grad_w", x.grad_w, "x", x.x));
-    EP_CHECK(check_apart(fn, "grad_preact", x.grad_preact, "grad", x.grad));
-    EP_CHECK(check_apart(fn, "grad_preact", x.grad_preact, "preact", x.preact));
-    EP_CHECK(check_apart(fn, "grad_preact", x.grad_preact, "x", x.x));
-  }
+  // (without rows only the parameters' gradients are written)
+  const auto rows = [&](const void *p) { return any ? p : nullptr; };
+  const Named outputs[] = {{"grad_x", rows(x.grad_x)}, {"grad_w", x.grad_w}, {"grad_bias", x.grad_bias},
+                           {"grad_preact", rows(x.grad_preact)}, {"workspace", x.workspace}};
+  const Named operands[] = {{"grad", rows(x.grad)}, {"x", rows(x.x)}, {"w", x.w}, {"preact", rows(x.preact)},
+                            {"error_word", x.error_word}};
+  EP_CHECK(check_apart(fn, outputs, operands));
   const DenseBackwardArgs a{x.grad, x.grad_type == EP_TYPE_BF16, static_cast<const uint16_t *>(x.x), x.row_stride,
                             x.num_rows, x.hidden, static_cast<const uint16_t *>(x.w), x.width, x.activation,
                             static_cast<const uint16_t *>(x.preact), static_cast<uint16_t *>(x.grad_preact),

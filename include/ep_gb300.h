@@ -925,9 +925,9 @@ size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activati
  *          without rows.
  *   workspace >= ep_dense_workspace_bytes(...) bytes, 16-byte aligned; calls
  *          sharing one must be ordered
- * The outputs and grad_preact lie apart from each other and from what is read;
- * where they begin at its first byte the call is refused.  The rest as for
- * ep_dense_product.  The sums run in a fixed order: the same
+ * The outputs, grad_preact and workspace lie apart from each other and from what
+ * is read; where one begins at another's first byte the call is refused.  The
+ * rest as for ep_dense_product.  The sums run in a fixed order: the same
  * inputs give the same bits.
  */
 typedef struct {
