@@ -1144,7 +1144,8 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
     The bias's is computed for a ``bias_dtype`` (or a ``grad_bias`` tensor).
     With an activation ``preact`` is what the forward pass kept;
     ``grad_preact`` (bf16 [T, N], N rounded up to a multiple of 8, allocated
-    when not given) receives its gradient, rounded as the products take it.  A residual's gradient is
+    when not given and needed) receives its gradient, rounded as the products
+    take it.  A residual's gradient is
     ``grad`` itself."""
     act = _DENSE_ACTIVATIONS[activation]
     T, H, apart, width, wide = _dense_sizes(x, w, activation)
@@ -1163,12 +1164,10 @@ def ep_dense_product_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tens
         preact = None
     kept = 0  # bytes of the scratch tensor for grad_preact
     pitch = (wide + 7) // 8 * 8
-    if not ((act or given is not bf or width % 8) and (need_x or need_w)):
-        grad_preact = None
-    elif grad_preact is None:
-        kept = (T * pitch * 2 + 255) // 256 * 256
-    else:
+    if grad_preact is not None:
         _given(grad_preact, "grad_preact", bf, dev, (T, pitch))
+    elif (act or given is not bf or width % 8) and (need_x or need_w):
+        kept = (T * pitch * 2 + 255) // 256 * 256
     x_at = w_at = bias_at = 0
     if need_x:
         grad_x = _target(grad_x, "grad_x", bf, dev, (T, H), stream)

@@ -346,7 +346,7 @@ ep_status_t launch_dense_backward(const DenseBackwardArgs &a, cudaStream_t strea
   const int64_t pitch = made ? up(wide, 8) * 8 : wide;                             // between d's rows
   float *sums = static_cast<float *>(a.workspace);
   cudaError_t e = cudaSuccess;
-  if (a.num_rows > 0 && (a.grad_bias != nullptr || (made && a.grad_preact != nullptr))) {
+  if (a.num_rows > 0 && (a.grad_bias != nullptr || a.grad_preact != nullptr)) {
     const auto kernel = pairs ? (a.grad_bf16 ? dense_gradient_kernel<true, true> : dense_gradient_kernel<true, false>)
                               : (a.grad_bf16 ? dense_gradient_kernel<false, true> : dense_gradient_kernel<false, false>);
     if (any_width)

@@ -919,7 +919,8 @@ size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activati
  *   grad   [T * width] of grad_type (the type of `out`)
  *   preact [T * wide] bf16 (not with EP_ACT_NONE)
  *   grad_preact [T] rows of wide, rounded up to a multiple of 8, bf16: written
- *          (but for what that adds), then read; NULL where d is `grad` itself
+ *          (but for what that adds), then read; may be NULL where d is `grad`
+ *          itself, or without grad_x and grad_w
  *   grad_x [T * hidden], grad_w [wide * hidden] bf16, grad_bias [wide] of
  *          bias_type: NULL: not computed.  grad_w and grad_bias are 0
  *          without rows.

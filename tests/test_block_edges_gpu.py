@@ -1,6 +1,7 @@
 """Edges of the block's operators: more choices than 32 bits count, gradients over
 logits that are not of whole 16 bytes, rows beside masked ones, rows whose mean
-is far above their deviation.
+is far above their deviation, a product's ``grad_preact`` whatever else is
+asked for.
 """
 import math
 
@@ -161,3 +162,29 @@ def test_gradients_of_rows_with_a_far_mean(T, H, ratio):
     assert ((dx.double() - want).abs() <= 1.01 * tol + U * want.abs()).all()
     t = U * (min(T, T / 8 + 640) + 6)
     assert ((dw.double() - (grad.double() * n).sum(0)).abs() <= 1.01 * t * (grad.double() * n).abs().sum(0)).all()
+
+
+# ---------------------------------------------------------- shared product
+
+@pytest.mark.parametrize("width", [16, 12])
+@pytest.mark.parametrize("act", [None, "silu", "swiglu"])
+@pytest.mark.parametrize("grad_type", [BF16, F32])
+def test_grad_preact_is_written_whatever_is_needed(act, grad_type, width):
+    g = torch.Generator(device=DEV).manual_seed(5)
+    wide = width * (2 if act == "swiglu" else 1)
+    pitch = (wide + 7) // 8 * 8
+    x = torch.randn((40, 64), generator=g, device=DEV).to(BF16)
+    w = torch.randn((wide, 64), generator=g, device=DEV).to(BF16)
+    grad = torch.randn((40, width), generator=g, device=DEV).to(grad_type)
+    preact = torch.randn((40, wide), generator=g, device=DEV).to(BF16)
+    z = preact.double().requires_grad_(True)
+    F = torch.nn.functional
+    y = F.silu(z) if act == "silu" else F.silu(z[:, :width]) * z[:, width:] if act else z
+    want, = torch.autograd.grad(y, z, grad.double())
+    for needs in [dict(need_x=False, need_w=False), dict(need_x=False, need_w=False, bias_dtype=F32), dict(need_w=False),
+                  dict(need_x=False), dict(bias_dtype=F32)]:
+        kept = torch.full((40, pitch), math.nan, dtype=BF16, device=DEV)
+        got = ep.ep_dense_product_backward(grad, x, w, activation=act, preact=preact if act else None, grad_preact=kept, **needs)
+        assert [t is not None for t in got] == [needs.get("need_x", True), needs.get("need_w", True), "bias_dtype" in needs]
+        # a sigmoid's 2^-16, and the rounding to bf16
+        assert ((kept[:, :wide].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -14) * want.abs() + 1e-3 * 2.0 ** -14).all()
