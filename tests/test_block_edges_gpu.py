@@ -1,7 +1,7 @@
 """Edges of the block's operators: more choices than 32 bits count, gradients over
 logits that are not of whole 16 bytes, rows beside masked ones, rows whose mean
 is far above their deviation, a product's ``grad_preact`` whatever else is
-asked for.
+asked for, the far tail of GELU.
 """
 import math
 
@@ -188,3 +188,53 @@ def test_grad_preact_is_written_whatever_is_needed(act, grad_type, width):
         assert [t is not None for t in got] == [needs.get("need_x", True), needs.get("need_w", True), "bias_dtype" in needs]
         # a sigmoid's 2^-16, and the rounding to bf16
         assert ((kept[:, :wide].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -14) * want.abs() + 1e-3 * 2.0 ** -14).all()
+
+
+def gelu64(z):
+    """GELU and its derivative, relatively right in the tail: by erfc."""
+    tail = 0.5 * torch.special.erfc(-z * math.sqrt(0.5))
+    density = torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    return z * tail, tail + z * density, density
+
+
+def tail_points():
+    z = torch.cat([torch.linspace(-12.5, 12.5, 1601), torch.tensor([-0.0, 1e-6, -1e-6, -13.0, 13.0, 100.0, -100.0, 1e30, -1e30])])
+    return z.to(BF16).to(DEV)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("params", [None, F32])
+def test_gelu_keeps_its_relative_accuracy_in_the_tail(out_dtype, params):
+    """z itself is exact (one product by 1).  The normal integral's tail is a
+    fit of 2^-22, an exponential of 2^-22, whose argument z^2/2 is rounded
+    twice, and a dozen roundings: 2^-24 (24 + 2 z^2), relative."""
+    z = tail_points()
+    x = torch.zeros((z.numel(), 8), dtype=BF16, device=DEV)
+    x[:, 0] = z
+    w = torch.zeros((3, 8), dtype=BF16, device=DEV)
+    w[:, 0] = 1.0
+    out = ep.ep_dense_product(x, w, None if params is None else torch.zeros(3, device=DEV), activation="gelu", out_dtype=out_dtype)
+    z = z.double()[:, None]
+    want = gelu64(z)[0]
+    tol = (U * (24 + 2 * z ** 2) + torch.finfo(out_dtype).eps / 2) * want.abs() + 1e-37
+    tol = torch.where(torch.isfinite(tol), tol, 0.0)
+    # beyond 13 the density leaves fp32's normal numbers
+    far = z < -13.1
+    err = (out.double() - want).abs()
+    assert (err <= torch.where(far, 1e-36, tol)).all(), float((err / tol)[~far.expand_as(err)].max())
+
+
+@pytest.mark.parametrize("width", [8, 3])
+def test_gelu_derivative_in_the_tail(width):
+    """A row at a time, so that the bias's gradient (fp32) is the derivative:
+    the two terms' bounds as above."""
+    z = tail_points()
+    for i in range(0, z.numel() - width, width):
+        at = z[i:i + width].clone()
+        w = torch.zeros((width, 8), dtype=BF16, device=DEV)
+        x, one = torch.zeros((1, 8), dtype=BF16, device=DEV), torch.ones((1, width), device=DEV)
+        got = ep.ep_dense_product_backward(one, x, w, activation="gelu", preact=at[None], bias_dtype=F32)[2]
+        v = at.double()
+        y, d, density = gelu64(v)
+        tol = U * (24 + 2 * v ** 2) * (torch.where(v != 0, (y / v).abs(), 0.5) + (v * density).abs()) + 1e-36
+        assert ((got.double() - d).abs() <= torch.where(v.abs() > 20, 1e-36, tol)).all()
