@@ -302,9 +302,11 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], Scores<V, SIGMOID
 }
 
 // How the tokens are shared.  Many: by blocks that are all on the SMs at once,
-// two each, or three where a lane has 16 columns or fewer (65 536 tokens, 256
-// experts: 411 blocks 28 us, 293 us at most two an SM 22).  Few, up to five
-// passes of a block's rows: by one cluster, which joins its parts itself and
+// two each of 152, or three where a lane has 16 columns or fewer (65 536
+// tokens, 256 experts: 411 blocks 28 us; 293, at most two an SM, 22).  In fp32
+// that holds up to some 450 experts: at 512 a block takes 118 KB of shared
+// memory, so an SM has one, and the blocks two turns (32 768 tokens, 256 blocks:
+// 25.7 us, floor 10.2).  Few, up to five passes of a block's rows: by one cluster, which joins its parts itself and
 // saves a launch, 3.4 us of the host's (1021 tokens, 64 experts in a graph 6.8
 // us, 7.0 with the launch).
 struct Cut {

@@ -40,10 +40,10 @@ __device__ __forceinline__ float slope_of(int act, float z) {
 // a slice of the rows; a second kernel adds the slices in their order.
 constexpr int kWide = 32 * 8;     // columns of a block
 constexpr int kRowLanes = 8;      // rows of a block at a time
-constexpr int kGradBlocks = 608;  // four an SM
+constexpr int kGradBlocks = 608;  // four an SM (of 152)
 constexpr int kLeastRows = 32;    // of a slice
 
-constexpr int kJoinedRows = 384;  // at most, whose slices are a cluster
+constexpr int kJoinedRows = 384;  // at most, whose slices are a cluster (set for calls outside graphs)
 
 // A column block's slices are neighbours.  Few rows: as many slices as a
 // cluster has blocks, which add them up themselves and save a launch, 3.4 us
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(32 * kRowLanes, 4) dense_gradient_kernel(Dense
   cluster_sync();  // before a block whose sums are read ends
 }
 
-// Rows that are not of whole 16 bytes: a column a thread (64 rows a block).
+// Rows that are not of whole 16 bytes: a column a thread, a slice's rows a
+// block (32 or more).
 template <bool GATED>
 __global__ void __launch_bounds__(kWide) dense_gradient_any_kernel(DenseBackwardArgs p, float *sums, Slices cut, int64_t pitch) {
   const int slice = blockIdx.x % cut.slices, n = blockIdx.x / cut.slices * kWide + threadIdx.x;
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dense_bias_kernel(const float
 // (28 tiles) 42 us, by two segments 35; 512 -> 512 (4 tiles) 38 us, by
 // sixteen 17; 128 -> 128 (one) 37 us, by sixteen 10; 333 rows 512 -> 1408
 // stay whole, 8.5 us.
-constexpr int kPairs = 76;          // that run at once
+constexpr int kPairs = 76;          // that run at once (152 SMs)
 constexpr int kLeastSteps = 8;      // of a segment
 constexpr int kSegmentsCost = 16;   // steps
 

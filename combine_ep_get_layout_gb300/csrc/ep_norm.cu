@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(most_warps(U) * 32, 1) norm_kernel(NormArgs p,
 
 // Rows of the backward pass (x, grad and add of each) in shared memory: up to
 // 48 KB a row of 8192 in bf16, 96 KB in fp32; fp32 rows beyond 8192 come
-// straight from memory.  (Four rows of 7168 in bf16: 83 us instead of 81.6; two
-// of 16 384: 155 instead of 142.)
+// straight from memory.  (Four rows of 7168 in bf16 were slower, 83 us against
+// 81.6, and two of 16 384, 155 against 142.)
 constexpr int backward_ahead(int pieces) { return pieces == 4 ? 1 : 2; }
 
 // grad_x, and this block's part of the parameters' gradients: [block][2][hidden].
@@ -651,7 +651,8 @@ bool wide_rows(const void *p, int64_t stride, bool bf16) {
 
 // Few rows: their gradients are computed by one cluster, which saves the
 // kernel that joins the blocks' sums, 3.4 us of the host's, up to where the
-// device takes 1 to 2 us longer for it (in a graph, one cluster and two
+// device takes 1 to 2 us longer for it, which a graph's replay does not win back
+// (in a graph, one cluster and two
 // kernels: 13 rows of 4096 5.5 and 4.6 us, 48 of 1024 5.1 and 3.5, 8 of 1024
 // 3.1 and 3.4; 96 of 1024 would be 7.1 and 3.7).
 int cluster_rows(int groups) { return 16 + 4 * groups; }
