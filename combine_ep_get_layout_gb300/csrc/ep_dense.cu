@@ -12,12 +12,10 @@ namespace ep {
 
 namespace {
 
-// act'(z)
+// act'(z), but for ReLU
 __device__ __forceinline__ float slope_of(int act, float z) {
   float s;
   switch (act) {
-    case EP_ACT_RELU:
-      return z > 0.0f ? 1.0f : 0.0f;
     case EP_ACT_SILU:
       s = sigmoid_of(z);
       return s * (1.0f + z * (1.0f - s));
@@ -33,6 +31,13 @@ __device__ __forceinline__ float slope_of(int act, float z) {
     default:
       return 1.0f;
   }
+}
+
+// act'(z) grad.  ReLU's is a choice, not a product: what is cut off stays 0
+// whatever came back to it.
+__device__ __forceinline__ float through(int act, float z, float grad) {
+  if (act == EP_ACT_RELU) return z > 0.0f ? grad : 0.0f;
+  return slope_of(act, z) * grad;
 }
 
 // d = act'(z) grad for the products, rounded, and the bias's gradient: one
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(32 * kRowLanes, 4) dense_gradient_kernel(Dense
       } else if (p.activation != EP_ACT_NONE) {
         unpack8(z[i][0], a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] *= slope_of(p.activation, a[j]);
+        for (int j = 0; j < 8; ++j) d[j] = through(p.activation, a[j], d[j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[0][j] += d[j];
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kWide) dense_gradient_any_kernel(DenseBackward
       other += du;
       if (p.grad_preact != nullptr) put(t * pitch + p.width + n, du);
     } else if (p.activation != EP_ACT_NONE) {
-      d *= slope_of(p.activation, load_param(p.preact, true, t * wide + n));
+      d = through(p.activation, load_param(p.preact, true, t * wide + n), d);
     }
     if (p.grad_preact != nullptr) put(t * pitch + n, d);
     sum += d;

@@ -910,7 +910,8 @@ size_t ep_dense_workspace_bytes(int num_rows, int hidden, int width, ep_activati
 
 /*
  * The gradients of ep_dense_product.  With d the gradient of z, act'(z) grad
- * (z as kept in preact; at 0 EP_ACT_RELU has the derivative 0):
+ * (z as kept in preact; where it is not above 0 EP_ACT_RELU gives 0, whatever
+ * grad is):
  *   grad_x[t] = bf16(d[t] w),  grad_w = bf16(sum_t d[t]^T x[t]),
  *   grad_bias = sum_t d[t]     (fp32 sums of d before it is rounded)
  * The two products take d in bf16: `grad` itself for EP_ACT_NONE with a bf16

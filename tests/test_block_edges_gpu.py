@@ -1,7 +1,7 @@
 """Edges of the block's operators: more choices than 32 bits count, gradients over
 logits that are not of whole 16 bytes, rows beside masked ones, rows whose mean
 is far above their deviation, a product's ``grad_preact`` whatever else is
-asked for, the far tail of GELU.
+asked for, the far tail of GELU, what ReLU cuts off.
 """
 import math
 
@@ -238,3 +238,26 @@ def test_gelu_derivative_in_the_tail(width):
         y, d, density = gelu64(v)
         tol = U * (24 + 2 * v ** 2) * (torch.where(v != 0, (y / v).abs(), 0.5) + (v * density).abs()) + 1e-36
         assert ((got.double() - d).abs() <= torch.where(v.abs() > 20, 1e-36, tol)).all()
+
+
+@pytest.mark.parametrize("width", [16, 5])
+@pytest.mark.parametrize("grad_type", [BF16, F32])
+def test_relu_lets_nothing_through_where_it_is_closed(grad_type, width):
+    """Infinities and NaN of the output's gradient in places whose output was cut to 0."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    T, H, pitch = 70, 64, (width + 7) // 8 * 8
+    x = torch.randn((T, H), generator=g, device=DEV).to(BF16)
+    w = torch.randn((width, H), generator=g, device=DEV).to(BF16)
+    preact = torch.randn((T, width), generator=g, device=DEV).to(BF16)
+    preact[3] = 0.0
+    preact[4] = -0.0
+    grad = torch.randn((T, width), generator=g, device=DEV).to(grad_type)
+    closed = preact <= 0
+    clean = torch.where(closed, torch.zeros_like(grad), grad)
+    for value in (math.inf, -math.inf, math.nan):
+        kept = torch.empty((T, pitch), dtype=BF16, device=DEV)
+        given = torch.where(closed, torch.full_like(grad, value), grad)
+        got = ep.ep_dense_product_backward(given, x, w, activation="relu", preact=preact, bias_dtype=F32, grad_preact=kept)
+        want = ep.ep_dense_product_backward(clean, x, w, activation="relu", preact=preact, bias_dtype=F32)
+        assert (kept[:, :width][closed] == 0).all()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
